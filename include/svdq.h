@@ -88,6 +88,9 @@ typedef enum {
 
 typedef enum { SVDQ_INT4 = 0, SVDQ_NVFP4 = 1 } svdq_precision;
 typedef enum { SVDQ_F32 = 0, SVDQ_BF16 = 1 } svdq_dtype;
+/* Gate activations of a gated feed-forward pair: x / (1 + exp(-x)), and the
+ * tanh form of GELU (the formula at svdq_act_quantize_gelu). */
+typedef enum { SVDQ_SILU = 0, SVDQ_GELU = 1 } svdq_act;
 
 /* svdq_quantize_weights flag: lora_down / lora_up are INPUTS (the low-rank
  * split is given, the SVD is skipped); smoothing, residual and quantization
@@ -296,6 +299,82 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
                              int32_t group, const uint8_t* q, const uint16_t* scales,
                              const uint16_t* zeros, const uint16_t* bias, void* Y,
                              svdq_dtype y_dtype, hipStream_t stream);
+
+/* --------------------------------------------------- weight-only operators
+ * Few rows, gated pairs and input gradients on the 4-bit weights above, with
+ * unquantized activations.  They are runtime calls: kernels enqueued on
+ * `stream`, nothing allocated, workspace from the caller (DEVICE, 256-byte
+ * aligned, contents need not be initialised, not overlapping any operand; its
+ * size is the call's *_workspace_bytes, a multiple of 256 and 0 when none is
+ * needed or an argument is invalid).  Calls that may run at the same time need
+ * workspaces of their own.  DEVICE operands are 16-byte aligned (biases: their
+ * element size).  Outputs may not overlap inputs or each other.  M == 0
+ * launches nothing. */
+
+/* The SVDQ layer on few rows with the activations in their own precision
+ * (no 4-bit quantization of X):
+ *   Xh = fl32(X * smooth),  LR = X . lora_down^T  (kept in fp32)
+ *   INT4 : Y = sum_g sW[n,g] sum_{k in g} Xh[m,k] q[n,k] + LR lora_up^T + bias
+ *   NVFP4: Y = ts_w sum_k Xh[m,k] wd[n,k] + LR lora_up^T + bias
+ * For the layers a quantized model calls with a row per image or token
+ * (modulation, time step and pooled projections, decoding), where reading the
+ * weights is the whole cost and quantizing X would only add error.  The
+ * products take Xh as a sum of bf16 terms: two for a bf16 Y (Xh to 2^-17), three
+ * for an fp32 Y (2^-24); sums are fp32.  Other arguments as svdq_linear_w4a4;
+ * w_tensor_scale is read for NVFP4 only.
+ * 0 <= M <= 64 (more rows: SVDQ_ERR_UNSUPPORTED; svdq_linear_w4a4 is the form
+ * for them), K % 64 == 0, N % 16 == 0, rank % 16 == 0, 0 <= rank <= 256. */
+size_t svdq_linear_w4a16_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t rank);
+svdq_status svdq_linear_w4a16(const void* X, svdq_dtype x_dtype, int64_t M, int64_t K,
+                              int64_t N, int32_t rank, svdq_precision prec,
+                              const float* smooth, const uint16_t* lora_down,
+                              const uint16_t* lora_up, const uint8_t* wcodes,
+                              const void* wscales, const float* w_tensor_scale,
+                              const void* bias, svdq_dtype bias_dtype, void* Y,
+                              svdq_dtype y_dtype, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/* A gated feed-forward block's first half on two AWQ layers of the same
+ * shape, both projections, the activation and the product in one pass:
+ *   G = X . wd_gate^T + bias_gate,  U = X . wd_up^T + bias_up,  H = act(G) * U
+ * with wd = bf16((q - z) s) as in awq_linear_w4a16.  G and U are fp32 until H is
+ * rounded to h_dtype.  G_out, U_out: DEVICE bf16 [M, N], both or neither
+ * (NULL); they receive G and U rounded to bf16, as awq_gated_w4a16_grad reads
+ * them.  X bf16 [M, K]; q / scales / zeros as awq_quantize_weights writes them;
+ * biases bf16 [N] or NULL; H [M, N].
+ * M >= 0, N % 16 == 0, group == 64, K % 64 == 0. */
+size_t awq_gated_w4a16_workspace_bytes(int64_t M, int64_t K, int64_t N);
+svdq_status awq_gated_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N, int32_t group,
+                            const uint8_t* q_gate, const uint16_t* scales_gate,
+                            const uint16_t* zeros_gate, const uint16_t* bias_gate,
+                            const uint8_t* q_up, const uint16_t* scales_up,
+                            const uint16_t* zeros_up, const uint16_t* bias_up, svdq_act act,
+                            void* H, svdq_dtype h_dtype, uint16_t* G_out, uint16_t* U_out,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Its backward pass for frozen weights and biases, from dH and the G, U that
+ * the forward call stored (all bf16 [M, N]):
+ *   dU = dH * act(G),  dG = dH * U * act'(G),  dX = dG . wd_gate + dU . wd_up
+ * Outputs bf16: dX [M, K]; dG, dU [M, N] (the gradients at both projections'
+ * outputs, for adapters and biases), each NULL where not wanted.  dG and dU
+ * are rounded to bf16 before the products; those sum in fp32.
+ * Sizes as awq_gated_w4a16. */
+size_t awq_gated_w4a16_grad_workspace_bytes(int64_t M, int64_t K, int64_t N);
+svdq_status awq_gated_w4a16_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                                 int64_t M, int64_t K, int64_t N, int32_t group,
+                                 const uint8_t* q_gate, const uint16_t* scales_gate,
+                                 const uint16_t* zeros_gate, const uint8_t* q_up,
+                                 const uint16_t* scales_up, const uint16_t* zeros_up,
+                                 svdq_act act, uint16_t* dX, uint16_t* dG, uint16_t* dU,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Input gradient of an AWQ layer (frozen weights): dX = dY . wd, dY bf16
+ * [M, N], dX [M, K] of dx_dtype, fp32 sums.  Sizes as awq_linear_w4a16. */
+size_t awq_linear_w4a16_grad_workspace_bytes(int64_t M, int64_t K, int64_t N);
+svdq_status awq_linear_w4a16_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
+                                  int32_t group, const uint8_t* q, const uint16_t* scales,
+                                  const uint16_t* zeros, void* dX, svdq_dtype dx_dtype,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -34,31 +34,6 @@ using namespace svdq_dev;
 
 namespace {
 
-typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
-typedef float f2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 v4bf_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, bf2_t));
-}
-
-// 8 unsigned nibbles (one dword, even k low) -> 8 bf16 values (q - z) s in
-// k order, as 4 dwords.  zs = -z s (exact in fp32).  A byte 0x0q read as
-// FP8-E4M3 is q 2^-9 for every q in 0..15 (a subnormal below 8, exponent
-// field 1 from 8 on), so the scaled conversion with the power of two 2^9
-// gives q exactly, two codes per instruction.
-__device__ __forceinline__ uint4 dequant8(uint32_t w, float s, float zs) {
-  const int e = int(w & 0x0F0F0F0Fu), o = int((w >> 4) & 0x0F0F0F0Fu);
-  const f2_t q02 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 512.0f, false);
-  const f2_t q46 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 512.0f, true);
-  const f2_t q13 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(o, 512.0f, false);
-  const f2_t q57 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(o, 512.0f, true);
-  return make_uint4(pk_bf16(fmaf(q02.x, s, zs), fmaf(q13.x, s, zs)),
-                    pk_bf16(fmaf(q02.y, s, zs), fmaf(q13.y, s, zs)),
-                    pk_bf16(fmaf(q46.x, s, zs), fmaf(q57.x, s, zs)),
-                    pk_bf16(fmaf(q46.y, s, zs), fmaf(q57.y, s, zs)));
-}
-
 __device__ __forceinline__ void store_y(void* Y, bool ybf16, int64_t idx, float v) {
   if (ybf16)
     static_cast<uint16_t*>(Y)[idx] = f32_to_bf16(v);

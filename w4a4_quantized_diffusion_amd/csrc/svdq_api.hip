@@ -496,3 +496,238 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
 }
 
 }  // extern "C"
+
+// ------------------------------------------------- weight-only operators
+namespace {
+
+// a DEVICE operand's extent, for the overlap checks
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool out;
+};
+
+// no output overlaps an operand or another output
+svdq_status check_spans(const Span* v, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!v[i].out || !v[i].p || !v[i].bytes) continue;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(v[i].p), a1 = a0 + v[i].bytes;
+    for (int j = 0; j < n; ++j) {
+      if (j == i || !v[j].p || !v[j].bytes) continue;
+      const uintptr_t b0 = reinterpret_cast<uintptr_t>(v[j].p), b1 = b0 + v[j].bytes;
+      if (a0 < b1 && b0 < a1)
+        return fail(SVDQ_ERR_INVALID_ARG,
+                    "outputs and workspace must not overlap the inputs or each other");
+    }
+  }
+  return SVDQ_OK;
+}
+
+svdq_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!need) return SVDQ_OK;
+  if (have < need)
+    return fail(SVDQ_ERR_INVALID_ARG, "workspace too small: need " + std::to_string(need) + " bytes");
+  return check_ptr(ws, "workspace", 256);
+}
+
+svdq_status check_mkn(int64_t M, int64_t K, int64_t N) {
+  if (M < 0 || M > MAX_DIM) return fail(SVDQ_ERR_INVALID_ARG, "M out of range");
+  if (K <= 0 || K > MAX_DIM || K % 64 != 0)
+    return fail(SVDQ_ERR_INVALID_ARG, "K must be a positive multiple of 64");
+  if (N <= 0 || N > MAX_DIM || N % 16 != 0)
+    return fail(SVDQ_ERR_INVALID_ARG, "N must be a positive multiple of 16");
+  const int64_t most = int64_t(1) << 40;
+  if (M * K > most || M * N > most || N * K > most)
+    return fail(SVDQ_ERR_INVALID_ARG, "M*K, M*N and N*K must be at most 2^40");
+  return SVDQ_OK;
+}
+
+svdq_status check_act(svdq_act a) {
+  if (a != SVDQ_SILU && a != SVDQ_GELU) return fail(SVDQ_ERR_INVALID_ARG, "unknown activation");
+  return SVDQ_OK;
+}
+
+svdq_status check_group(int32_t group) {
+  if (group != 64) return fail(SVDQ_ERR_UNSUPPORTED, "group must be 64");
+  return SVDQ_OK;
+}
+
+svdq_status check_awq(const svdq::AwqWeight& w, const char* which) {
+  TRY(check_ptr(w.q, (std::string("q") + which).c_str()));
+  TRY(check_ptr(w.s, (std::string("scales") + which).c_str()));
+  return check_ptr(w.z, (std::string("zeros") + which).c_str());
+}
+
+size_t elem(svdq_dtype d) { return d == SVDQ_F32 ? 4 : 2; }
+
+constexpr int64_t A16_ROWS = 64;
+
+}  // namespace
+
+extern "C" {
+
+size_t svdq_linear_w4a16_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t rank) {
+  if (check_mkr(M, K, rank) != SVDQ_OK || check_mkn(M, K, N) != SVDQ_OK || M > A16_ROWS) return 0;
+  return svdq::linear_a16_workspace(M, K, N, rank);
+}
+
+svdq_status svdq_linear_w4a16(const void* X, svdq_dtype x_dtype, int64_t M, int64_t K, int64_t N,
+                              int32_t rank, svdq_precision prec, const float* smooth,
+                              const uint16_t* lora_down, const uint16_t* lora_up,
+                              const uint8_t* wcodes, const void* wscales,
+                              const float* w_tensor_scale, const void* bias,
+                              svdq_dtype bias_dtype, void* Y, svdq_dtype y_dtype, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_dtype(x_dtype, "x_dtype"));
+  TRY(check_dtype(y_dtype, "y_dtype"));
+  if (bias) TRY(check_dtype(bias_dtype, "bias_dtype"));
+  TRY(check_prec(prec));
+  TRY(check_mkr(M, K, rank));
+  TRY(check_mkn(M, K, N));
+  if (M > A16_ROWS)
+    return fail(SVDQ_ERR_UNSUPPORTED, "svdq_linear_w4a16 takes at most 64 rows");
+  if (M == 0) return SVDQ_OK;
+  TRY(check_ptr(X, "X"));
+  TRY(check_ptr(smooth, "smooth"));
+  if (rank > 0) {
+    TRY(check_ptr(lora_down, "lora_down"));
+    TRY(check_ptr(lora_up, "lora_up"));
+  }
+  TRY(check_ptr(wcodes, "wcodes"));
+  TRY(check_ptr(wscales, "wscales"));
+  if (prec == SVDQ_NVFP4) TRY(check_ptr(w_tensor_scale, "w_tensor_scale", 4));
+  if (bias) TRY(check_ptr(bias, "bias", elem(bias_dtype)));
+  TRY(check_ptr(Y, "Y"));
+  const size_t need = svdq::linear_a16_workspace(M, K, N, rank);
+  TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t m = M, k = K, n = N, r = rank;
+  const Span spans[] = {{X, m * k * elem(x_dtype), false}, {smooth, k * 4, false},
+                        {rank ? lora_down : nullptr, r * k * 2, false},
+                        {rank ? lora_up : nullptr, r * n * 2, false}, {wcodes, n * k / 2, false},
+                        {wscales, n * k / 16, false}, {bias, n * elem(bias_dtype), false},
+                        {prec == SVDQ_NVFP4 ? w_tensor_scale : nullptr, 4, false},
+                        {Y, m * n * elem(y_dtype), true}, {workspace, need, true}};
+  TRY(check_spans(spans, 10));
+  return svdq::launch_linear_a16(X, x_dtype, M, K, N, rank, prec, smooth, lora_down, lora_up,
+                                 wcodes, wscales, w_tensor_scale, bias, bias_dtype, Y, y_dtype,
+                                 workspace, stream);
+}
+
+size_t awq_gated_w4a16_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (check_mkn(M, K, N) != SVDQ_OK) return 0;
+  return svdq::awq_gated_workspace(M, K, N);
+}
+
+svdq_status awq_gated_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N, int32_t group,
+                            const uint8_t* q_gate, const uint16_t* scales_gate,
+                            const uint16_t* zeros_gate, const uint16_t* bias_gate,
+                            const uint8_t* q_up, const uint16_t* scales_up,
+                            const uint16_t* zeros_up, const uint16_t* bias_up, svdq_act act,
+                            void* H, svdq_dtype h_dtype, uint16_t* G_out, uint16_t* U_out,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_group(group));
+  TRY(check_dtype(h_dtype, "h_dtype"));
+  TRY(check_act(act));
+  TRY(check_mkn(M, K, N));
+  TRY(check_tiles(M, 2 * N));
+  if (M == 0) return SVDQ_OK;
+  const svdq::AwqWeight wg{q_gate, scales_gate, zeros_gate}, wu{q_up, scales_up, zeros_up};
+  TRY(check_ptr(X, "X"));
+  TRY(check_awq(wg, "_gate"));
+  TRY(check_awq(wu, "_up"));
+  if (bias_gate) TRY(check_ptr(bias_gate, "bias_gate", 2));
+  if (bias_up) TRY(check_ptr(bias_up, "bias_up", 2));
+  TRY(check_ptr(H, "H"));
+  if (!G_out != !U_out)
+    return fail(SVDQ_ERR_INVALID_ARG, "G_out and U_out are given together or not at all");
+  if (G_out) {
+    TRY(check_ptr(G_out, "G_out"));
+    TRY(check_ptr(U_out, "U_out"));
+  }
+  const size_t need = svdq::awq_gated_workspace(M, K, N);
+  TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t m = M, k = K, n = N;
+  const Span spans[] = {{X, m * k * 2, false}, {q_gate, n * k / 2, false},
+                        {scales_gate, n * k / 32, false}, {zeros_gate, n * k / 32, false},
+                        {bias_gate, n * 2, false}, {q_up, n * k / 2, false},
+                        {scales_up, n * k / 32, false}, {zeros_up, n * k / 32, false},
+                        {bias_up, n * 2, false}, {H, m * n * elem(h_dtype), true},
+                        {G_out, m * n * 2, true}, {U_out, m * n * 2, true},
+                        {workspace, need, true}};
+  TRY(check_spans(spans, 13));
+  return svdq::launch_awq_gated(X, M, K, N, wg, wu, bias_gate, bias_up, act, H, h_dtype, G_out,
+                                U_out, workspace, stream);
+}
+
+size_t awq_gated_w4a16_grad_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (check_mkn(M, K, N) != SVDQ_OK) return 0;
+  return svdq::awq_gated_grad_workspace(M, K, N);
+}
+
+svdq_status awq_gated_w4a16_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                                 int64_t M, int64_t K, int64_t N, int32_t group,
+                                 const uint8_t* q_gate, const uint16_t* scales_gate,
+                                 const uint16_t* zeros_gate, const uint8_t* q_up,
+                                 const uint16_t* scales_up, const uint16_t* zeros_up,
+                                 svdq_act act, uint16_t* dX, uint16_t* dG, uint16_t* dU,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_group(group));
+  TRY(check_act(act));
+  TRY(check_mkn(M, K, N));
+  TRY(check_tiles(M, K));
+  if (M == 0) return SVDQ_OK;
+  const svdq::AwqWeight wg{q_gate, scales_gate, zeros_gate}, wu{q_up, scales_up, zeros_up};
+  TRY(check_ptr(dH, "dH"));
+  TRY(check_ptr(G, "G"));
+  TRY(check_ptr(U, "U"));
+  TRY(check_awq(wg, "_gate"));
+  TRY(check_awq(wu, "_up"));
+  TRY(check_ptr(dX, "dX"));
+  if (dG) TRY(check_ptr(dG, "dG"));
+  if (dU) TRY(check_ptr(dU, "dU"));
+  const size_t need = svdq::awq_gated_grad_workspace(M, K, N);
+  TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t m = M, k = K, n = N;
+  const Span spans[] = {{dH, m * n * 2, false}, {G, m * n * 2, false}, {U, m * n * 2, false},
+                        {q_gate, n * k / 2, false}, {scales_gate, n * k / 32, false},
+                        {zeros_gate, n * k / 32, false}, {q_up, n * k / 2, false},
+                        {scales_up, n * k / 32, false}, {zeros_up, n * k / 32, false},
+                        {dX, m * k * 2, true}, {dG, m * n * 2, true}, {dU, m * n * 2, true},
+                        {workspace, need, true}};
+  TRY(check_spans(spans, 13));
+  return svdq::launch_awq_gated_grad(dH, G, U, M, K, N, wg, wu, act, dX, dG, dU, workspace, stream);
+}
+
+size_t awq_linear_w4a16_grad_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (check_mkn(M, K, N) != SVDQ_OK) return 0;
+  return svdq::awq_linear_grad_workspace(M, K, N);
+}
+
+svdq_status awq_linear_w4a16_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
+                                  int32_t group, const uint8_t* q, const uint16_t* scales,
+                                  const uint16_t* zeros, void* dX, svdq_dtype dx_dtype,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_group(group));
+  TRY(check_dtype(dx_dtype, "dx_dtype"));
+  TRY(check_mkn(M, K, N));
+  TRY(check_tiles(M, K));
+  if (M == 0) return SVDQ_OK;
+  const svdq::AwqWeight w{q, scales, zeros};
+  TRY(check_ptr(dY, "dY"));
+  TRY(check_awq(w, ""));
+  TRY(check_ptr(dX, "dX"));
+  const size_t need = svdq::awq_linear_grad_workspace(M, K, N);
+  TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t m = M, k = K, n = N;
+  const Span spans[] = {{dY, m * n * 2, false}, {q, n * k / 2, false}, {scales, n * k / 32, false},
+                        {zeros, n * k / 32, false}, {dX, m * k * elem(dx_dtype), true},
+                        {workspace, need, true}};
+  TRY(check_spans(spans, 6));
+  return svdq::launch_awq_linear_grad(dY, M, K, N, w, dX, dx_dtype, workspace, stream);
+}
+
+}  // extern "C"

@@ -20,6 +20,8 @@ LOWRANK_GIVEN = 1
 
 _PREC = {"int4": INT4, "nvfp4": NVFP4, INT4: INT4, NVFP4: NVFP4}
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
+SILU, GELU = 0, 1
+_ACT = {"silu": SILU, "gelu": GELU, SILU: SILU, GELU: GELU}
 
 _lib = None
 
@@ -59,6 +61,30 @@ _SIG = {
     "awq_quantize_weights": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _P, _P, _P]),
     "awq_linear_w4a16": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P,
                                          ctypes.c_int, _P]),
+    "svdq_linear_w4a16_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I32]),
+    # X, x_dtype, M, K, N, rank, prec, smooth, lora_down, lora_up, wcodes,
+    # wscales, w_tensor_scale, bias, bias_dtype, Y, y_dtype, workspace,
+    # workspace_bytes, stream
+    "svdq_linear_w4a16": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I32, ctypes.c_int,
+                                          _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _P,
+                                          ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "awq_gated_w4a16_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    # X, M, K, N, group, gate q / scales / zeros / bias, up q / scales / zeros /
+    # bias, act, H, h_dtype, G_out, U_out, workspace, workspace_bytes, stream
+    "awq_gated_w4a16": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P,
+                                        ctypes.c_int, _P, ctypes.c_int, _P, _P, _P,
+                                        ctypes.c_size_t, _P]),
+    "awq_gated_w4a16_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    # dH, G, U, M, K, N, group, gate q / scales / zeros, up q / scales / zeros,
+    # act, dX, dG, dU, workspace, workspace_bytes, stream
+    "awq_gated_w4a16_grad": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P,
+                                             _P, ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t,
+                                             _P]),
+    "awq_linear_w4a16_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    # dY, M, K, N, group, q, scales, zeros, dX, dx_dtype, workspace,
+    # workspace_bytes, stream
+    "awq_linear_w4a16_grad": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P,
+                                              ctypes.c_int, _P, ctypes.c_size_t, _P]),
 }
 EXPORTS = tuple(_SIG)
 
@@ -331,3 +357,183 @@ def awq_linear_w4a16(X, layer, bias=None, y_dtype=torch.bfloat16, Y=None):
         _p(X), M, K, N, layer["group"], _p(layer["q"]), _p(layer["scales"]),
         _p(layer["zeros"]), _p(bias), _p(Y), _DT[Y.dtype], _stream()))
     return Y
+
+
+# ------------------------------------------------- weight-only operators
+# These check every tensor against the sizes of the call (the kernels read
+# through raw pointers), run on the device their input is on and on that
+# device's current stream, and allocate outputs and workspace there unless
+# given.
+
+def _arg(t, name, shape, dtype, dev):
+    """The address of a tensor after checking it against what the call reads
+    or writes."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(X, name, width):
+    """(M, device index) of a call's first operand [M, width]."""
+    if X.dim() != 2 or X.shape[1] != width:
+        raise ValueError(f"{name} must have shape [M, {width}], got {tuple(X.shape)}")
+    dev = X.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a device tensor")
+    return X.shape[0], dev
+
+
+def _out(Y, name, shape, dtype, X, dev):
+    """(tensor, address) of an output, allocated beside X unless given."""
+    if Y is None:
+        Y = torch.empty(shape, dtype=dtype, device=X.device)
+        return Y, Y.data_ptr()
+    return Y, _arg(Y, name, shape, dtype, dev)
+
+
+def _ws(workspace, need, X, dev):
+    """(tensor, address, bytes) of a workspace of at least `need` bytes."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        return workspace, workspace.data_ptr(), need
+    return workspace, _arg(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel()
+
+
+def _run(dev, fn, *args):
+    """Call fn(*args, stream) on device `dev` and its current stream."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _check(st)
+
+
+def _awq_args(layer, K, N, dev, which=""):
+    if layer["K"] != K or layer["N"] != N:
+        raise ValueError(f"layer{which} is {layer['N']} x {layer['K']}, expected {N} x {K}")
+    g = K // 64
+    return (_arg(layer["q"], "q" + which, (g, N, 32), torch.uint8, dev),
+            _arg(layer["scales"], "scales" + which, (g, N), torch.int16, dev),
+            _arg(layer["zeros"], "zeros" + which, (g, N), torch.int16, dev))
+
+
+def _out_dtype(Y, dtype, name):
+    dtype = dtype if Y is None else Y.dtype
+    if dtype not in _DT:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return dtype
+
+
+def svdq_linear_w4a16_workspace_bytes(M, K, N, rank):
+    return int(lib().svdq_linear_w4a16_workspace_bytes(M, K, N, rank))
+
+
+def svdq_linear_w4a16(X, layer, bias=None, y_dtype=torch.float32, workspace=None, Y=None):
+    """An SVDQ layer on at most 64 rows with X (float32 or bfloat16) kept in
+    its own precision instead of quantized to 4 bits.  Arguments as
+    svdq_linear_w4a4.  Returns Y [M, N]."""
+    l = lib()
+    K, N, rank, pr = layer["K"], layer["N"], layer["rank"], _PREC[layer["prec"]]
+    M, dev = _rows(X, "X", K)
+    if X.dtype not in _DT:
+        raise TypeError(f"X must be float32 or bfloat16, got {X.dtype}")
+    x = _arg(X, "X", X.shape, X.dtype, dev)
+    yt = _out_dtype(Y, y_dtype, "Y")
+    Y, y = _out(Y, "Y", (M, N), yt, X, dev)
+    b = None
+    if bias is not None:
+        if bias.dtype not in _DT:
+            raise TypeError(f"bias must be float32 or bfloat16, got {bias.dtype}")
+        b = _arg(bias, "bias", (N,), bias.dtype, dev)
+    g = K // 64
+    ws_shape, ws_dtype = ((g, N), torch.float32) if pr == INT4 else ((g, N, 4), torch.uint8)
+    keep, ws, nws = _ws(workspace, l.svdq_linear_w4a16_workspace_bytes(M, K, N, rank), X, dev)
+    _run(dev, l.svdq_linear_w4a16, x, _DT[X.dtype], M, K, N, rank, pr,
+         _arg(layer["smooth"], "smooth", (K,), torch.float32, dev),
+         _arg(layer["lora_down"], "lora_down", (rank, K), torch.int16, dev) if rank else None,
+         _arg(layer["lora_up"], "lora_up", (N, rank), torch.int16, dev) if rank else None,
+         _arg(layer["wcodes"], "wcodes", (g, N, 32), torch.uint8, dev),
+         _arg(layer["wscales"], "wscales", ws_shape, ws_dtype, dev),
+         _arg(layer["w_tensor_scale"], "w_tensor_scale", (1,), torch.float32, dev)
+         if pr == NVFP4 else None,
+         b, _DT[bias.dtype] if bias is not None else F32, y, _DT[yt], ws, nws)
+    return Y
+
+
+def awq_gated_w4a16_workspace_bytes(M, K, N):
+    return int(lib().awq_gated_w4a16_workspace_bytes(M, K, N))
+
+
+def awq_gated_w4a16(X, gate, up, act="silu", bias_gate=None, bias_up=None, h_dtype=torch.bfloat16,
+                    save=False, workspace=None, H=None):
+    """act(X gate^T + bias_gate) * (X up^T + bias_up) for two AWQ layers of one
+    shape.  X bf16 [M, K]; act "silu" or "gelu" (tanh form); biases bf16 [N] or
+    None.  Returns H [M, N], or (H, G, U) with the bf16 pre-activations that
+    awq_gated_w4a16_grad reads if save."""
+    l = lib()
+    K, N = gate["K"], gate["N"]
+    M, dev = _rows(X, "X", K)
+    x = _arg(X, "X", X.shape, torch.bfloat16, dev)
+    ht = _out_dtype(H, h_dtype, "H")
+    H, h = _out(H, "H", (M, N), ht, X, dev)
+    G = U = g = u = None
+    if save:
+        G, g = _out(None, "G", (M, N), torch.bfloat16, X, dev)
+        U, u = _out(None, "U", (M, N), torch.bfloat16, X, dev)
+    keep, ws, nws = _ws(workspace, l.awq_gated_w4a16_workspace_bytes(M, K, N), X, dev)
+    bg, bu = (None if b is None else _arg(b, n, (N,), torch.bfloat16, dev)
+              for b, n in ((bias_gate, "bias_gate"), (bias_up, "bias_up")))
+    _run(dev, l.awq_gated_w4a16, x, M, K, N, gate["group"], *_awq_args(gate, K, N, dev, "_gate"), bg,
+         *_awq_args(up, K, N, dev, "_up"), bu, _ACT[act], h, _DT[ht], g, u, ws, nws)
+    return (H, G, U) if save else H
+
+
+def awq_gated_w4a16_grad_workspace_bytes(M, K, N):
+    return int(lib().awq_gated_w4a16_grad_workspace_bytes(M, K, N))
+
+
+def awq_gated_w4a16_grad(dH, G, U, gate, up, act="silu", workspace=None):
+    """The backward pass of awq_gated_w4a16 for frozen weights, from dH and the
+    saved G and U (bf16 [M, N]).  Returns (dX [M, K], dG, dU), bf16."""
+    l = lib()
+    K, N = gate["K"], gate["N"]
+    M, dev = _rows(dH, "dH", N)
+    bf = torch.bfloat16
+    d, g, u = (_arg(t, n, (M, N), bf, dev) for t, n in ((dH, "dH"), (G, "G"), (U, "U")))
+    dX, dx = _out(None, "dX", (M, K), bf, dH, dev)
+    dG, dg = _out(None, "dG", (M, N), bf, dH, dev)
+    dU, du = _out(None, "dU", (M, N), bf, dH, dev)
+    keep, ws, nws = _ws(workspace, l.awq_gated_w4a16_grad_workspace_bytes(M, K, N), dH, dev)
+    _run(dev, l.awq_gated_w4a16_grad, d, g, u, M, K, N, gate["group"],
+         *_awq_args(gate, K, N, dev, "_gate"), *_awq_args(up, K, N, dev, "_up"), _ACT[act],
+         dx, dg, du, ws, nws)
+    return dX, dG, dU
+
+
+def awq_linear_w4a16_grad_workspace_bytes(M, K, N):
+    return int(lib().awq_linear_w4a16_grad_workspace_bytes(M, K, N))
+
+
+def awq_linear_w4a16_grad(dY, layer, dx_dtype=torch.bfloat16, workspace=None, dX=None):
+    """The input gradient of awq_linear_w4a16: dX = dY wd, dY bf16 [M, N].
+    Returns dX [M, K]."""
+    l = lib()
+    K, N = layer["K"], layer["N"]
+    M, dev = _rows(dY, "dY", N)
+    d = _arg(dY, "dY", dY.shape, torch.bfloat16, dev)
+    xt = _out_dtype(dX, dx_dtype, "dX")
+    dX, dx = _out(dX, "dX", (M, K), xt, dY, dev)
+    keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_grad_workspace_bytes(M, K, N), dY, dev)
+    _run(dev, l.awq_linear_w4a16_grad, d, M, K, N, layer["group"], *_awq_args(layer, K, N, dev),
+         dx, _DT[xt], ws, nws)
+    return dX
