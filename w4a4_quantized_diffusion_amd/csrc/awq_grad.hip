@@ -10,7 +10,7 @@
 // with fp32 sums.  dG and dU enter the products rounded to bf16 (the type
 // they are returned in).
 
-#include "w4a16.h"
+#include "gemm_bf16.h"
 
 using namespace svdq_dev;
 
@@ -43,6 +43,31 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restri
     reinterpret_cast<uint4*>(dG)[i] = make_uint4(og[0], og[1], og[2], og[3]);
     reinterpret_cast<uint4*>(dU)[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
   }
+}
+
+// 8 rows n (from row index at = g N + n, n a multiple of 8) and the 8 k of
+// dword j of a group, packed over n: out[i] holds k = 8j + i
+__device__ __forceinline__ void transpose_dequant8(const svdq::AwqWeight& w, int64_t at, int j,
+                                                   uint4 (&out)[8]) {
+  const uint4 s4 = *reinterpret_cast<const uint4*>(w.s + at);
+  const uint4 z4 = *reinterpret_cast<const uint4*>(w.z + at);
+  const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w}, zw[4] = {z4.x, z4.y, z4.z, z4.w};
+  uint32_t o[8][4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float v[2][8];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(w.q + (at + 2 * p + r) * 32 + 4 * j);
+      const float s = __uint_as_float(r ? sw[p] & 0xFFFF0000u : sw[p] << 16);
+      const float zs = -__uint_as_float(r ? zw[p] & 0xFFFF0000u : zw[p] << 16) * s;
+      dequant8_f32(c, s, zs, v[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i][p] = pack_bf16x2(v[0][i], v[1][i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
 }
 
 constexpr int TB = 64;
@@ -119,18 +144,91 @@ __global__ __launch_bounds__(256) void grad_tile_kernel(
   }
 }
 
+// ---------------------------------------------------------- many rows
+// The weights are dequantized once into the workspace, transposed: B [K, ldb]
+// with the n of the first layer, then those of the second, each padded with
+// zeros to a multiple of 64.
+
+// 64 n x 64 k (one group) per wave: lane (o, j) takes 8 rows n and 8 k of
+// each, and writes 8 pieces of 8 n
+__global__ __launch_bounds__(256) void transpose_dequant_kernel(svdq::AwqWeight w, int N,
+                                                                int64_t ldb,
+                                                                uint16_t* __restrict__ B) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int o = lane & 7, j = lane >> 3;
+  const int64_t n0 = int64_t(blockIdx.x) * 256 + 64 * wave;
+  const int g = blockIdx.y;
+  if (n0 >= (int64_t(N) + 63) / 64 * 64) return;
+  const int64_t n = n0 + 8 * o;
+  uint4 out[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
+  if (n < N) transpose_dequant8(w, int64_t(g) * N + n, j, out);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(B + (64 * int64_t(g) + 8 * j + i) * ldb + n) = out[i];
+}
+
+__global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Args p,
+                                                                  void* __restrict__ dX,
+                                                                  bool xbf16) {
+  using namespace svdq_gemm;
+  __shared__ Stage st0, st1;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int64_t m0, b0;
+  tile_origin((p.M + BM - 1) / BM, (p.rows + BN - 1) / BN, BM, BN, m0, b0);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  tile_product(p, m0, b0, st0, st1, acc);
+  const int64_t row0 = m0 + (wave >> 2) * WM, col0 = b0 + (wave & 3) * WN;
+  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * (WN + 4));
+  const float none[CBL] = {0.f, 0.f};
+  if (xbf16)
+    store_wave_tile<RBL, CBL, true>(acc, none, eb, lane, row0, col0, p.M, p.rows, dX);
+  else
+    store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, p.rows, dX);
+}
+
+constexpr int64_t WIDE_ROWS = 512;      // rows from which the weights are dequantized up front
+
+int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
+
+size_t wide_bytes(int64_t M, int64_t K, int64_t N, int layers) {
+  return M < WIDE_ROWS ? 0 : svdq::align256(size_t(K) * size_t(pad64(N)) * 2 * layers);
+}
+
+// dX = A0 wd0 [+ A1 wd1] for M >= WIDE_ROWS, B the workspace
+svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWeight* w,
+                        int layers, int64_t M, int64_t K, int64_t N, void* dX, bool xbf16,
+                        uint16_t* B, hipStream_t s) {
+  const int64_t np = pad64(N), ldb = np * layers;
+  for (int i = 0; i < layers; ++i) {
+    hipLaunchKernelGGL(transpose_dequant_kernel, dim3(unsigned((np + 255) / 256), unsigned(K / 64)),
+                       dim3(256), 0, s, w[i], int(N), ldb, B + i * np);
+    SVDQ_TRY(svdq::check_launch("transpose_dequant"));
+  }
+  svdq_gemm::Args p{{A0, A1}, N, int(np / 64), layers, B, ldb, int(M), int(K)};
+  const int64_t tiles = ((M + 255) / 256) * ((K + 255) / 256);
+  hipLaunchKernelGGL(grad_wide_kernel, dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, s, p, dX,
+                     xbf16);
+  return svdq::check_launch("awq_grad (wide)");
+}
+
 }  // namespace
 
 namespace svdq {
 
-size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N) { return 0; }
+size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N) { return wide_bytes(M, K, N, 1); }
 size_t awq_gated_grad_workspace(int64_t M, int64_t K, int64_t N) {
-  return 2 * align256(size_t(M) * size_t(N) * 2);
+  return 2 * align256(size_t(M) * size_t(N) * 2) + wide_bytes(M, K, N, 2);
 }
 
 svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
                                    AwqWeight w, void* dX, svdq_dtype x_dt, void* ws,
                                    hipStream_t s) {
+  if (M >= WIDE_ROWS)
+    return launch_wide(dY, dY, &w, 1, M, K, N, dX, x_dt == SVDQ_BF16, static_cast<uint16_t*>(ws), s);
   dim3 grid(unsigned(K / 64), unsigned((M + TB - 1) / TB));
   hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, s, dY, w, dY, w, 1, int(M), int(K),
                      int(N), dX, x_dt == SVDQ_BF16);
@@ -149,6 +247,11 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
   auto k = act == SVDQ_SILU ? gate_grad_kernel<SVDQ_SILU> : gate_grad_kernel<SVDQ_GELU>;
   hipLaunchKernelGGL(k, dim3(blocks), dim3(256), 0, s, dH, G, U, n8, dG, dU);
   SVDQ_TRY(check_launch("gate_grad"));
+  if (M >= WIDE_ROWS) {
+    const AwqWeight w[2] = {wg, wu};
+    uint16_t* const B = reinterpret_cast<uint16_t*>(w8 + 2 * align256(size_t(M) * size_t(N) * 2));
+    return launch_wide(dG, dU, w, 2, M, K, N, dX, true, B, s);
+  }
   dim3 grid(unsigned(K / 64), unsigned((M + TB - 1) / TB));
   hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, s, dG, wg, dU, wu, 2, int(M), int(K),
                      int(N), static_cast<void*>(dX), true);

@@ -1,0 +1,145 @@
+// Tiled bf16 product of the weight-only operators on many rows (gfx950):
+//
+//   C[m, b] = sum_r A[m, r] B[b, r]      (fp32 sums)
+//
+// A in one or two segments along r (A0, A1 [M, width], the columns of one after
+// the other's), B [rows, ldb] the weights in bf16, each segment padded with
+// zeros to whole chunks of 64.  256 x 256 tiles, 8 waves of 128 x 64 on
+// v_mfma_f32_32x32x16_bf16, both operands brought to LDS by the load unit
+// (global_load_lds, 16 bytes a lane) one chunk of 64 ahead in two buffers.
+//
+// LDS rows are 128 bytes, 8 slots of 16; slot s of row r holds piece
+// s ^ ((r >> 1) & 7), so that the 16 lanes of one ds_read_b128 phase (rows
+// r..r+15, one piece) touch 16 different groups of 4 banks.  The load unit
+// writes a wave's 64 pieces consecutively, so the permutation is applied to the
+// global addresses.
+#pragma once
+
+#include "w4a16.h"
+
+namespace svdq_gemm {
+
+using namespace svdq_dev;
+
+constexpr int BM = 256, BN = 256;
+constexpr int NT = 512;
+constexpr int WM = 128, WN = 64;
+constexpr int RBL = WM / 32, CBL = WN / 32;
+
+struct Args {
+  const uint16_t* A[2];
+  int64_t width;          // columns of A in one segment (a multiple of 8)
+  int chunks;             // chunks of 64 in one segment
+  int segments;           // 1 or 2
+  const uint16_t* B;
+  int64_t ldb;            // elements: segments * chunks * 64
+  int M, rows;            // rows of A, rows of B
+};
+
+struct __attribute__((aligned(16))) Stage {
+  uint4 a[BM * 8];
+  uint4 b[BN * 8];
+};
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// acc += the tile at (m0, b0), b0 a row of B.  All 512 threads call it.
+__device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t b0, Stage& st0,
+                                             Stage& st1, v16f (&acc)[RBL][CBL]) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int h = lane >> 5, r32 = lane & 31;
+
+  // Wave w brings rows 32 w .. 32 w + 31 of both operands, 8 rows to a
+  // transfer.  Rows past the edge repeat the last row (their products reach
+  // only outputs that are never stored); pieces past A's width repeat its
+  // last piece (the weights there are zeros).
+  int64_t arow[4], boff[4];
+  int apiece[2];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = 32 * wave + 8 * t + (lane >> 3);
+    const int piece = (lane & 7) ^ ((r >> 1) & 7);
+    const int64_t m = m0 + r < p.M ? m0 + r : p.M - 1;
+    const int64_t b = b0 + r < p.rows ? b0 + r : p.rows - 1;
+    arow[t] = m * p.width;
+    boff[t] = b * p.ldb + 8 * piece;
+    if (t < 2) apiece[t] = 8 * piece;
+  }
+  const int total = p.chunks * p.segments;
+  auto dma = [&](int c, Stage& st) __attribute__((always_inline)) {
+    const bool second = c >= p.chunks;
+    const uint16_t* const A = second ? p.A[1] : p.A[0];
+    const int64_t col = 64 * int64_t(second ? c - p.chunks : c);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int64_t k = min(col + apiece[t & 1], p.width - 8);
+      __builtin_amdgcn_global_load_lds(A + arow[t] + k, (lds_ptr_t)&st.a[(32 * wave + 8 * t) * 8],
+                                       16, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      __builtin_amdgcn_global_load_lds(p.B + boff[t] + 64 * int64_t(c),
+                                       (lds_ptr_t)&st.b[(32 * wave + 8 * t) * 8], 16, 0, 0);
+  };
+
+  const int sw = h ^ ((r32 >> 1) & 7);
+  const int abase = (wm * WM + r32) * 8, bbase = (wn * WN + r32) * 8;
+  auto compute = [&](const Stage& st) __attribute__((always_inline)) {
+    v8bf fa[2][RBL], fb[2][CBL];
+    auto frags = [&](int ks, v8bf (&a)[RBL], v8bf (&b)[CBL]) __attribute__((always_inline)) {
+      const int slot = sw ^ (2 * ks);
+#pragma unroll
+      for (int j = 0; j < CBL; ++j)
+        b[j] = __builtin_bit_cast(v8bf, st.b[bbase + 256 * j + slot]);
+#pragma unroll
+      for (int i = 0; i < RBL; ++i)
+        a[i] = __builtin_bit_cast(v8bf, st.a[abase + 256 * i + slot]);
+    };
+    frags(0, fa[0], fb[0]);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks < 3) frags(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+      // keeps the next substep's fragment reads ahead of this substep's MFMAs
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < RBL; ++i)
+#pragma unroll
+        for (int j = 0; j < CBL; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j],
+                                                              acc[i][j], 0, 0, 0);
+    }
+  };
+  // one step: the chunk's data have landed (every wave waits for its own
+  // transfers, then the barrier), the other buffer is free, its transfers go
+  // out and the chunk is computed.  Past the last chunk the transfers repeat
+  // it into a buffer nobody reads.
+  auto step = [&](int c, Stage& cur, Stage& nxt) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    dma(min(c + 1, total - 1), nxt);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(cur);
+  };
+  dma(0, st0);
+  int c = 0;
+  for (; c + 2 <= total; c += 2) {
+    step(c, st0, st1);
+    step(c + 1, st1, st0);
+  }
+  if (c < total) step(c, st0, st1);
+  // the repeated last transfers, before the buffers are used for anything else
+  __syncthreads();
+}
+
+__device__ __forceinline__ void zero_acc(v16f (&acc)[RBL][CBL]) {
+#pragma unroll
+  for (int i = 0; i < RBL; ++i)
+#pragma unroll
+    for (int j = 0; j < CBL; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+}
+
+}  // namespace svdq_gemm

@@ -140,21 +140,32 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return uint16_t(pack_bf16x2(f, 0.f));
 }
 
-// 8 unsigned nibbles of an AWQ layer (one dword, even k low) -> 8 bf16 values
-// (q - z) s in k order, as 4 dwords.  zs = -z s (exact in fp32).  A byte 0x0q
-// read as FP8-E4M3 is q 2^-9 for every q in 0..15 (a subnormal below 8,
+// 8 unsigned nibbles of an AWQ layer (one dword, even k low) -> (q - z) s in k
+// order, in fp32 and rounded to bf16 (4 dwords).  zs = -z s (exact in fp32).  A
+// byte 0x0q read as FP8-E4M3 is q 2^-9 for every q in 0..15 (a subnormal below 8,
 // exponent field 1 from 8 on), so the scaled conversion with the power of two
 // 2^9 gives q exactly, two codes per instruction.
-__device__ __forceinline__ uint4 dequant8(uint32_t w, float s, float zs) {
+__device__ __forceinline__ void dequant8_f32(uint32_t w, float s, float zs, float (&v)[8]) {
   const int e = int(w & 0x0F0F0F0Fu), o = int((w >> 4) & 0x0F0F0F0Fu);
   const v2f32_t q02 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 512.0f, false);
   const v2f32_t q46 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 512.0f, true);
   const v2f32_t q13 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(o, 512.0f, false);
   const v2f32_t q57 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(o, 512.0f, true);
-  return make_uint4(pack_bf16x2(fmaf(q02.x, s, zs), fmaf(q13.x, s, zs)),
-                    pack_bf16x2(fmaf(q02.y, s, zs), fmaf(q13.y, s, zs)),
-                    pack_bf16x2(fmaf(q46.x, s, zs), fmaf(q57.x, s, zs)),
-                    pack_bf16x2(fmaf(q46.y, s, zs), fmaf(q57.y, s, zs)));
+  v[0] = fmaf(q02.x, s, zs);
+  v[1] = fmaf(q13.x, s, zs);
+  v[2] = fmaf(q02.y, s, zs);
+  v[3] = fmaf(q13.y, s, zs);
+  v[4] = fmaf(q46.x, s, zs);
+  v[5] = fmaf(q57.x, s, zs);
+  v[6] = fmaf(q46.y, s, zs);
+  v[7] = fmaf(q57.y, s, zs);
+}
+
+__device__ __forceinline__ uint4 dequant8(uint32_t w, float s, float zs) {
+  float v[8];
+  dequant8_f32(w, s, zs, v);
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 
 // E4M3 code of a non-negative float: round to nearest even, saturating at
