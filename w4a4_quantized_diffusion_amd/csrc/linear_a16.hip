@@ -71,8 +71,9 @@ __device__ __forceinline__ void load8(const float* f, float (&v)[8]) {
 }
 
 constexpr int WAVES = 8, NT = 64 * WAVES;
-constexpr int D = 4;                     // chunks of weights in flight per wave
+constexpr int D = 2;                     // chunks of weights in flight per wave
 constexpr int LDS_X = 64 << 10;          // LDS for the terms of Xh
+constexpr int MAX_SLICES = 8;            // of K, one workgroup each
 constexpr int LR_STEPS = 4;              // steps of 32 k per wave of LR, all loaded at once
 
 // slices of K over which LR is computed
@@ -196,7 +197,7 @@ __device__ __forceinline__ void lr_block(int block, const void* __restrict__ X, 
 // and serve all waves; every wave streams its own columns' weights through
 // registers, D chunks ahead.  Partial sums go to part [S][M][N].
 template <int PREC, int MT, int T, int CT>
-__global__ __launch_bounds__(NT) void a16_slice_kernel(
+__global__ __launch_bounds__(NT, 4) void a16_slice_kernel(
     const void* __restrict__ X, bool xbf16, int M, int K, int N, int rank, int LS, int lr_blocks,
     int S, int sub, const float* __restrict__ smooth, const uint16_t* __restrict__ down,
     const uint8_t* __restrict__ codes, const uint32_t* __restrict__ scales,
@@ -340,19 +341,17 @@ __global__ __launch_bounds__(256) void a16_sum_kernel(
 #pragma unroll
   for (int e = 0; e < 4; ++e) p[e] = part + int64_t(min(m0 + 4 * j + e, M - 1)) * N + n;
   v4f sum = {0, 0, 0, 0}, low = {0, 0, 0, 0};
-  // (loads of four slices at once; a slice past the last counts as zeros)
-  for (int s0 = 0; s0 < S; s0 += 4) {
-    float v[4][4];
+  // (all loads first; a slice past the last counts as zeros)
+  float v[MAX_SLICES][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < MAX_SLICES; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[q][e] = p[e][int64_t(min(s0 + q, S - 1)) * M * N];
-    __builtin_amdgcn_sched_barrier(0);
+    for (int e = 0; e < 4; ++e) v[q][e] = p[e][int64_t(min(q, S - 1)) * M * N];
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < MAX_SLICES; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += s0 + q < S ? v[q][e] : 0.f;
-  }
+    for (int e = 0; e < 4; ++e) sum[e] += q < S ? v[q][e] : 0.f;
   const float ts = ts_w ? ts_w[0] : 1.f;
   const float bv = !bias   ? 0.f
                    : bbf16 ? bf16_to_f32(static_cast<const uint16_t*>(bias)[n])
@@ -402,9 +401,9 @@ struct Split {
 
 Split split(int64_t K, int64_t N) {
   Split p;
-  p.ct = N >= 4096 ? 2 : 1;
+  p.ct = N >= 8192 ? 2 : 1;
   p.blocks = int((N + 16 * WAVES * p.ct - 1) / (16 * WAVES * p.ct));
-  p.slices = int(std::min<int64_t>(K / 64, std::max<int64_t>(1, 512 / p.blocks)));
+  p.slices = int(std::min<int64_t>({K / 64, MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
   return p;
 }
 
