@@ -132,7 +132,7 @@ def test_workspaces(lib):
                      svdq.awq_gated_w4a16_grad_workspace_bytes(m, k, n),
                      svdq.awq_linear_w4a16_grad_workspace_bytes(m, k, n)):
             assert need % 256 == 0
-        assert svdq.awq_gated_w4a16_grad_workspace_bytes(m, k, n) >= 4 * m * n
+        assert m <= 64 or svdq.awq_gated_w4a16_grad_workspace_bytes(m, k, n) >= 4 * m * n
     assert svdq.svdq_linear_w4a16_workspace_bytes(64, 128, 64, 32) % 256 == 0
     assert svdq.svdq_linear_w4a16_workspace_bytes(65, 128, 64, 32) == 0
     for f in (svdq.awq_gated_w4a16_workspace_bytes, svdq.awq_gated_w4a16_grad_workspace_bytes,

@@ -81,6 +81,187 @@ __global__ __launch_bounds__(256) void gated_tile_kernel(
   }
 }
 
+// ----------------------------------------------------------- few rows
+// Up to 64 rows the time is the weights' way from memory.  A workgroup's 8
+// waves own 16 columns of both weights each, all rows, and one of S slices of
+// K; X's slice is in LDS, the weights stream through registers D chunks ahead.
+// The slices' partial G and U [S][2][M][N] are joined by gated_sum_kernel,
+// which applies bias, activation and product.
+
+constexpr int ROWS = 64;                 // the most rows of this form
+constexpr int WAVES = 8, NT = 64 * WAVES;
+constexpr int D = 2;
+constexpr int LDS_X = 64 << 10;
+constexpr int MAX_SLICES = 8;
+
+struct Split {
+  int blocks, slices;
+};
+
+Split split(int64_t K, int64_t N) {
+  Split p;
+  p.blocks = int((N + 16 * WAVES - 1) / (16 * WAVES));
+  p.slices = int(std::min<int64_t>({K / 64, MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+  return p;
+}
+
+template <int MT>
+__global__ __launch_bounds__(NT, 4) void gated_slice_kernel(
+    const uint16_t* __restrict__ X, int M, int K, int N, svdq::AwqWeight wg, svdq::AwqWeight wu,
+    int S, int sub, float* __restrict__ part) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j = lane >> 4, r = lane & 15;
+  const int G = K / 64;
+  const int slice = blockIdx.x % S;
+  const int g0 = int(int64_t(slice) * G / S), count = int(int64_t(slice + 1) * G / S) - g0;
+  const int64_t n = (int64_t(blockIdx.x / S) * WAVES + wave) * 16 + r;
+  const int64_t nc = min(n, int64_t(N) - 1);
+
+  // lane group j holds the codes k = 16 j .. 16 j + 15 of its row's chunk
+  struct Slot {
+    uint2 w[2];
+    uint32_t s[2], z[2];
+  } ring[D];
+  // every slot is always loaded (past the last chunk with the last one's
+  // data), so that the number of loads in flight is fixed
+  auto fetch = [&](int i, Slot& sl) __attribute__((always_inline)) {
+    const int64_t at = int64_t(g0 + min(i, count - 1)) * N + nc;
+    sl.w[0] = *reinterpret_cast<const uint2*>(wg.q + at * 32 + 8 * j);
+    sl.w[1] = *reinterpret_cast<const uint2*>(wu.q + at * 32 + 8 * j);
+    sl.s[0] = wg.s[at];
+    sl.z[0] = wg.z[at];
+    sl.s[1] = wu.s[at];
+    sl.z[1] = wu.z[at];
+  };
+  v4f acc[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) acc[mt][t] = v4f{0, 0, 0, 0};
+
+  // `sub` chunks of X at a time in LDS: rows of `sub` chunks and 16 bytes, so
+  // that 16 rows start in 16 different groups of 4 banks
+  const int rowb = sub * 128 + 16;
+  int xoff[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) xoff[mt] = min(16 * mt + r, M - 1) * rowb + 32 * j;
+  for (int c0 = 0; c0 < count; c0 += sub) {
+    const int here = min(sub, count - c0);
+    if (c0) __syncthreads();
+    for (int i = tid; i < M * here * 8; i += NT) {
+      const int m = i / (here * 8), o = i - m * (here * 8);
+      *reinterpret_cast<uint4*>(lds + m * rowb + 16 * o) =
+          *reinterpret_cast<const uint4*>(X + int64_t(m) * K + 64 * int64_t(g0 + c0) + 8 * o);
+    }
+    if (c0 == 0)
+#pragma unroll
+      for (int d = 0; d < D; ++d) fetch(d, ring[d]);
+    // (not __syncthreads, which would wait for the weights too)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    for (int c = 0; c < here; c += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        Slot& sl = ring[d];
+        // past the last chunk the scales are zeros
+        const bool live = c + d < here;
+        v8bf b[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float s = live ? __uint_as_float(sl.s[t] << 16) : 0.f;
+          const float zs = -__uint_as_float(sl.z[t] << 16) * s;
+          b[t][0] = __builtin_bit_cast(v8bf, dequant8(sl.w[t].x, s, zs));
+          b[t][1] = __builtin_bit_cast(v8bf, dequant8(sl.w[t].y, s, zs));
+        }
+        const uint8_t* const xc = lds + 128 * min(c + d, here - 1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const v8bf a = *reinterpret_cast<const v8bf*>(xc + xoff[mt] + 16 * h);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              acc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[t][h], acc[mt][t], 0, 0, 0);
+          }
+        fetch(c0 + c + d + D, sl);
+      }
+  }
+  if (n >= N) return;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = 16 * mt + 4 * j + e;
+        if (m < M) part[((int64_t(slice) * 2 + t) * M + m) * N + n] = acc[mt][t][e];
+      }
+}
+
+// 4 columns per thread
+template <int ACT>
+__global__ __launch_bounds__(64) void gated_sum_kernel(
+    const float* __restrict__ part, int S, int M, int N, const uint16_t* __restrict__ bg,
+    const uint16_t* __restrict__ bu, void* __restrict__ H, bool hbf16, uint16_t* __restrict__ Gs,
+    uint16_t* __restrict__ Us) {
+  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x, total = int64_t(M) * N / 4;
+  if (i >= total) return;
+  const int64_t n = 4 * i % N;
+  // all loads first; a slice past the last counts as zeros
+  v4f v[MAX_SLICES][2];
+#pragma unroll
+  for (int q = 0; q < MAX_SLICES; ++q)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      v[q][t] = reinterpret_cast<const v4f*>(part)[(2 * int64_t(min(q, S - 1)) + t) * total + i];
+  uint2 b[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+  if (bg) b[0] = *reinterpret_cast<const uint2*>(bg + n);
+  if (bu) b[1] = *reinterpret_cast<const uint2*>(bu + n);
+  __builtin_amdgcn_sched_barrier(0);
+  v4f p[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    p[t] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < MAX_SLICES; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[t][e] += q < S ? v[q][t][e] : 0.f;
+    p[t][0] += __uint_as_float(b[t].x << 16);
+    p[t][1] += __uint_as_float(b[t].x & 0xFFFF0000u);
+    p[t][2] += __uint_as_float(b[t].y << 16);
+    p[t][3] += __uint_as_float(b[t].y & 0xFFFF0000u);
+  }
+  v4f h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = gate_act<ACT>(p[0][e]) * p[1][e];
+  auto pack = [](v4f x) { return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])); };
+  if (hbf16)
+    static_cast<uint2*>(H)[i] = pack(h);
+  else
+    static_cast<v4f*>(H)[i] = h;
+  if (Gs) {
+    reinterpret_cast<uint2*>(Gs)[i] = pack(p[0]);
+    reinterpret_cast<uint2*>(Us)[i] = pack(p[1]);
+  }
+}
+
+template <int MT>
+svdq_status run_rows(const uint16_t* X, int64_t M, int64_t K, int64_t N, svdq::AwqWeight wg,
+                     svdq::AwqWeight wu, float* part, hipStream_t s) {
+  const Split p = split(K, N);
+  // chunks of X that fit LDS, a multiple of D (64 rows: 7 chunks of 128 bytes)
+  const int most = int((LDS_X / M - 16) / 128 / D * D);
+  const int len = int((K / 64 + p.slices - 1) / p.slices);
+  const int sub = std::min(most, (len + D - 1) / D * D);
+  hipLaunchKernelGGL(gated_slice_kernel<MT>, dim3(unsigned(p.blocks * p.slices)), dim3(NT),
+                     size_t(M) * (sub * 128 + 16), s, X, int(M), int(K), int(N), wg, wu, p.slices,
+                     sub, part);
+  return svdq::check_launch("gated_slice");
+}
+
 // ---------------------------------------------------------- many rows
 // The weights are dequantized once into the workspace, 32 rows of Wg and the
 // 32 rows of Wu with the same n alternating, so that one wave's two column
@@ -167,6 +348,7 @@ int64_t pair_rows(int64_t N) { return (N + 31) / 32 * 64; }
 namespace svdq {
 
 size_t awq_gated_workspace(int64_t M, int64_t K, int64_t N) {
+  if (M <= ROWS) return align256(size_t(split(K, N).slices) * 2 * size_t(M) * size_t(N) * 4);
   return M < WIDE_ROWS ? 0 : align256(size_t(pair_rows(N)) * size_t(K) * 2);
 }
 
@@ -175,6 +357,19 @@ svdq_status launch_awq_gated(const uint16_t* X, int64_t M, int64_t K, int64_t N,
                              void* H, svdq_dtype h_dt, uint16_t* G, uint16_t* U, void* ws,
                              hipStream_t s) {
   const bool hb = h_dt == SVDQ_BF16;
+  if (M <= ROWS) {
+    float* const part = static_cast<float*>(ws);
+    switch ((M + 15) / 16) {
+      case 1: SVDQ_TRY(run_rows<1>(X, M, K, N, wg, wu, part, s)); break;
+      case 2: SVDQ_TRY(run_rows<2>(X, M, K, N, wg, wu, part, s)); break;
+      case 3: SVDQ_TRY(run_rows<3>(X, M, K, N, wg, wu, part, s)); break;
+      default: SVDQ_TRY(run_rows<4>(X, M, K, N, wg, wu, part, s)); break;
+    }
+    auto k = act == SVDQ_SILU ? gated_sum_kernel<SVDQ_SILU> : gated_sum_kernel<SVDQ_GELU>;
+    hipLaunchKernelGGL(k, dim3(unsigned((M * N / 4 + 63) / 64)), dim3(64), 0, s, part,
+                       split(K, N).slices, int(M), int(N), bg, bu, H, hb, G, U);
+    return check_launch("gated_sum");
+  }
   if (M >= WIDE_ROWS) {
     uint16_t* const B = static_cast<uint16_t*>(ws);
     hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((N + 31) / 32), unsigned(K / 64)),

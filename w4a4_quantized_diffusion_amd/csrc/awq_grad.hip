@@ -144,6 +144,232 @@ __global__ __launch_bounds__(256) void grad_tile_kernel(
   }
 }
 
+// ----------------------------------------------------------- few rows
+// Up to 64 rows the time is the weights' way from memory.  A workgroup takes
+// 128 columns of dX (two groups) and one of S slices of the reduction, counted
+// in steps of 32 n (a gated pair's steps run over both layers); its 8 waves
+// take the steps in turn and meet in LDS.  Lane (j, r) of a wave dequantizes
+// 8 k of the 8 rows n = 8 j .. 8 j + 7: column t of the 16 x 16 product t is
+// k = 64 (r / 8) + 8 (r % 8) + t, so a lane's 8 products are 8 consecutive k.
+// The rows' own operand (dY, or dG and dU computed here from dH, G and U) is
+// in LDS.  Partial sums [S][M][K] are joined by grad_sum_kernel.
+
+constexpr int ROWS = 64;                 // the most rows of this form
+constexpr int WAVES = 8, NT = 64 * WAVES;
+constexpr int LDS_A = 64 << 10;
+constexpr int MAX_SLICES = 16;
+
+struct Split {
+  int blocks, slices;
+};
+
+Split split(int64_t K, int64_t N, int layers) {
+  Split p;
+  p.blocks = int((K + 127) / 128);
+  const int64_t steps = (N + 31) / 32 * layers;
+  p.slices = int(std::min<int64_t>({(steps + WAVES - 1) / WAVES, MAX_SLICES,
+                                    std::max<int64_t>(1, 512 / p.blocks)}));
+  return p;
+}
+
+// what a few-row kernel reads: dY, or dH, G, U of a gated pair with where dG
+// and dU go
+struct Rows {
+  const uint16_t *d, *G, *U;
+  uint16_t *dG, *dU;
+};
+
+// 8 values of the pair's dG (layer 0) or dU (layer 1)
+template <int ACT>
+__device__ __forceinline__ uint4 pair_grad8(const uint4 h, const uint4 g, const uint4 u, int layer) {
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, gw[4] = {g.x, g.y, g.z, g.w},
+                 uw[4] = {u.x, u.y, u.z, u.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a0, d0, a1, d1;
+    gate_act_grad<ACT>(__uint_as_float(gw[j] << 16), a0, d0);
+    gate_act_grad<ACT>(__uint_as_float(gw[j] & 0xFFFF0000u), a1, d1);
+    const float h0 = __uint_as_float(hw[j] << 16), h1 = __uint_as_float(hw[j] & 0xFFFF0000u);
+    const float u0 = __uint_as_float(uw[j] << 16), u1 = __uint_as_float(uw[j] & 0xFFFF0000u);
+    o[j] = layer ? pack_bf16x2(h0 * a0, h1 * a1) : pack_bf16x2(h0 * u0 * d0, h1 * u1 * d1);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ACT < 0: one layer
+template <int MT, int ACT>
+__global__ __launch_bounds__(NT, 2) void grad_slice_kernel(Rows in, svdq::AwqWeight wa,
+                                                           svdq::AwqWeight wb, int M, int K, int N,
+                                                           int S, int sub,
+                                                           float* __restrict__ part) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int LAYERS = ACT < 0 ? 1 : 2;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j = lane >> 4, r = lane & 15;
+  const int slice = blockIdx.x % S, block = blockIdx.x / S;
+  const int per = (N + 31) / 32, steps = per * LAYERS;
+  const int s0 = int(int64_t(slice) * steps / S), s1 = int(int64_t(slice + 1) * steps / S);
+  const int g = min(2 * block + (r >> 3), K / 64 - 1);
+
+  v4f acc[MT][8];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) acc[mt][t] = v4f{0, 0, 0, 0};
+
+  struct Slot {
+    uint32_t w[8];
+    uint4 s, z;
+  };
+  // rows n past N (a multiple of 16) repeat the last ones; their scales are
+  // cleared where they are used
+  auto row8 = [&](int s) { return 32 * int64_t(s % per) + 8 * j; };
+  auto fetch = [&](int s, Slot& sl) __attribute__((always_inline)) {
+    const svdq::AwqWeight& w = LAYERS == 2 && s >= per ? wb : wa;
+    const int64_t at = int64_t(g) * N + min(row8(s), int64_t(N) - 8);
+    sl.s = *reinterpret_cast<const uint4*>(w.s + at);
+    sl.z = *reinterpret_cast<const uint4*>(w.z + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sl.w[i] = *reinterpret_cast<const uint32_t*>(w.q + (at + i) * 32 + 4 * (r & 7));
+  };
+
+  // `sub` steps of the rows' operand at a time in LDS, rows of 64 sub + 16 bytes
+  const int rowb = sub * 64 + 16;
+  int aoff[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) aoff[mt] = min(16 * mt + r, M - 1) * rowb + 16 * j;
+  for (int c0 = s0; c0 < s1; c0 += sub) {
+    const int here = min(sub, s1 - c0);
+    if (c0 != s0) __syncthreads();
+    Slot sl;
+    if (wave < here) fetch(c0 + wave, sl);
+    for (int i = tid; i < M * here * 4; i += NT) {
+      const int m = i / (here * 4), o = i - m * (here * 4);
+      const int s = c0 + (o >> 2), layer = LAYERS == 2 && s >= per;
+      const int64_t n = 32 * int64_t(s - layer * per) + 8 * (o & 3), at = int64_t(m) * N + n;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (n < N) {
+        v = *reinterpret_cast<const uint4*>(in.d + at);
+        if constexpr (LAYERS == 2) {
+          const uint4 G = *reinterpret_cast<const uint4*>(in.G + at);
+          const uint4 U = *reinterpret_cast<const uint4*>(in.U + at);
+          v = pair_grad8<ACT>(v, G, U, layer);
+          uint16_t* const out = layer ? in.dU : in.dG;
+          if (block == 0 && out) *reinterpret_cast<uint4*>(out + at) = v;
+        }
+      }
+      *reinterpret_cast<uint4*>(lds + m * rowb + 16 * o) = v;
+    }
+    __syncthreads();
+    for (int c = wave; c < here; c += WAVES) {
+      const bool live = row8(c0 + c) < N;
+      uint32_t o[8][4];
+      const uint32_t sw[4] = {sl.s.x, sl.s.y, sl.s.z, sl.s.w}, zw[4] = {sl.z.x, sl.z.y, sl.z.z, sl.z.w};
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        float v[2][8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float f = __uint_as_float(!live ? 0u : q ? sw[p] & 0xFFFF0000u : sw[p] << 16);
+          const float zs = -__uint_as_float(q ? zw[p] & 0xFFFF0000u : zw[p] << 16) * f;
+          dequant8_f32(sl.w[2 * p + q], f, zs, v[q]);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) o[t][p] = pack_bf16x2(v[0][t], v[1][t]);
+      }
+      if (c + WAVES < here) fetch(c0 + c + WAVES, sl);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const v8bf a = *reinterpret_cast<const v8bf*>(lds + aoff[mt] + 64 * c);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          acc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a, __builtin_bit_cast(v8bf, make_uint4(o[t][0], o[t][1], o[t][2], o[t][3])),
+              acc[mt][t], 0, 0, 0);
+      }
+    }
+  }
+
+  // the waves' sums in order, one block of 16 rows at a time: thread (wave w,
+  // lane) adds the eight sums of product w
+  v4f* const red = reinterpret_cast<v4f*>(lds);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 8; ++t) red[(t * WAVES + wave) * 64 + lane] = acc[mt][t];
+    __syncthreads();
+    v4f v = red[wave * WAVES * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += red[(wave * WAVES + w) * 64 + lane];
+    const int64_t k = 128 * int64_t(block) + 64 * (r >> 3) + 8 * (r & 7) + wave;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int m = 16 * mt + 4 * j + e;
+      if (m < M && k < K) part[(int64_t(slice) * M + m) * K + k] = v[e];
+    }
+  }
+}
+
+// 4 columns per thread
+__global__ __launch_bounds__(64) void grad_sum_kernel(const float* __restrict__ part, int S,
+                                                      int64_t total, void* __restrict__ dX,
+                                                      bool xbf16) {
+  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
+  if (i >= total) return;
+  // all loads first; a slice past the last counts as zeros
+  v4f v[MAX_SLICES], p = {0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < MAX_SLICES; ++q)
+    v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q, S - 1)) * total + i];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int q = 0; q < MAX_SLICES; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] += q < S ? v[q][e] : 0.f;
+  if (xbf16)
+    static_cast<uint2*>(dX)[i] = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+  else
+    static_cast<v4f*>(dX)[i] = p;
+}
+
+template <int MT, int ACT>
+svdq_status run_rows_mt(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
+                        float* part, hipStream_t s) {
+  constexpr int layers = ACT < 0 ? 1 : 2;
+  const Split p = split(K, N, layers);
+  // steps of the rows' operand that fit LDS (64 rows: 15)
+  const int64_t steps = (N + 31) / 32 * layers;
+  const int sub = int(std::min<int64_t>((LDS_A / M - 16) / 64, (steps + p.slices - 1) / p.slices));
+  const size_t shm = std::max(size_t(M) * (sub * 64 + 16), size_t(WAVES) * 8 * 1024);
+  auto k = grad_slice_kernel<MT, ACT>;
+  hipLaunchKernelGGL(k, dim3(unsigned(p.blocks * p.slices)), dim3(NT), shm, s, in, w[0],
+                     w[layers - 1], int(M), int(K), int(N), p.slices, sub, part);
+  return svdq::check_launch("grad_slice");
+}
+
+template <int ACT>
+svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
+                     void* dX, bool xbf16, float* part, hipStream_t s) {
+  switch ((M + 15) / 16) {
+    case 1: SVDQ_TRY((run_rows_mt<1, ACT>(in, M, K, N, w, part, s))); break;
+    case 2: SVDQ_TRY((run_rows_mt<2, ACT>(in, M, K, N, w, part, s))); break;
+    case 3: SVDQ_TRY((run_rows_mt<3, ACT>(in, M, K, N, w, part, s))); break;
+    default: SVDQ_TRY((run_rows_mt<4, ACT>(in, M, K, N, w, part, s))); break;
+  }
+  const int64_t total = M * K / 4;
+  hipLaunchKernelGGL(grad_sum_kernel, dim3(unsigned((total + 63) / 64)), dim3(64), 0, s, part,
+                     split(K, N, ACT < 0 ? 1 : 2).slices, total, dX, xbf16);
+  return svdq::check_launch("grad_sum");
+}
+
+size_t rows_bytes(int64_t M, int64_t K, int64_t N, int layers) {
+  return svdq::align256(size_t(split(K, N, layers).slices) * size_t(M) * size_t(K) * 4);
+}
+
 // ---------------------------------------------------------- many rows
 // The weights are dequantized once into the workspace, transposed: B [K, ldb]
 // with the n of the first layer, then those of the second, each padded with
@@ -219,14 +445,20 @@ svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqW
 
 namespace svdq {
 
-size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N) { return wide_bytes(M, K, N, 1); }
+size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N) {
+  return M <= ROWS ? rows_bytes(M, K, N, 1) : wide_bytes(M, K, N, 1);
+}
 size_t awq_gated_grad_workspace(int64_t M, int64_t K, int64_t N) {
+  if (M <= ROWS) return rows_bytes(M, K, N, 2);
   return 2 * align256(size_t(M) * size_t(N) * 2) + wide_bytes(M, K, N, 2);
 }
 
 svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
                                    AwqWeight w, void* dX, svdq_dtype x_dt, void* ws,
                                    hipStream_t s) {
+  if (M <= ROWS)
+    return run_rows<-1>(Rows{dY, nullptr, nullptr, nullptr, nullptr}, M, K, N, &w, dX,
+                        x_dt == SVDQ_BF16, static_cast<float*>(ws), s);
   if (M >= WIDE_ROWS)
     return launch_wide(dY, dY, &w, 1, M, K, N, dX, x_dt == SVDQ_BF16, static_cast<uint16_t*>(ws), s);
   dim3 grid(unsigned(K / 64), unsigned((M + TB - 1) / TB));
@@ -239,6 +471,13 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
                                   int64_t M, int64_t K, int64_t N, AwqWeight wg, AwqWeight wu,
                                   svdq_act act, uint16_t* dX, uint16_t* dG, uint16_t* dU, void* ws,
                                   hipStream_t s) {
+  if (M <= ROWS) {
+    const Rows in{dH, G, U, dG, dU};
+    const AwqWeight w[2] = {wg, wu};
+    float* const part = static_cast<float*>(ws);
+    return act == SVDQ_SILU ? run_rows<SVDQ_SILU>(in, M, K, N, w, dX, true, part, s)
+                            : run_rows<SVDQ_GELU>(in, M, K, N, w, dX, true, part, s);
+  }
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
   if (!dG) dG = reinterpret_cast<uint16_t*>(w8);
   if (!dU) dU = reinterpret_cast<uint16_t*>(w8 + align256(size_t(M) * size_t(N) * 2));
