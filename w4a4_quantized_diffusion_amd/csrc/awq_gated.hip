@@ -14,71 +14,46 @@ using namespace svdq_dev;
 
 namespace {
 
-// 64 rows x 64 columns of both products per workgroup, 4 waves of 32 x 32;
-// 64 reduction values at a time are staged (weights dequantized) in LDS.
-constexpr int TB = 64;
-constexpr int ROWB = 144;                // 64 bf16 (128 bytes) + 16 pad
-
-template <int ACT>
-__global__ __launch_bounds__(256) void gated_tile_kernel(
-    const uint16_t* __restrict__ X, int M, int K, int N, svdq::AwqWeight wg, svdq::AwqWeight wu,
-    const uint16_t* __restrict__ bg, const uint16_t* __restrict__ bu, void* __restrict__ H,
-    bool hbf16, uint16_t* __restrict__ Gs, uint16_t* __restrict__ Us) {
-  __shared__ __align__(16) uint8_t lds[3][TB * ROWB];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t m0 = int64_t(blockIdx.y) * TB, n0 = int64_t(blockIdx.x) * TB;
-  const int row = tid >> 2, piece = tid & 3;
-  const int64_t mr = m0 + row < M ? m0 + row : M - 1;
-  const int64_t nr = n0 + row < N ? n0 + row : N - 1;
-  v16f ag, au;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) ag[e] = au[e] = 0.f;
-  auto stage_w = [&](const svdq::AwqWeight& w, int g, uint8_t* dst) {
-    const int64_t at = int64_t(g) * N + nr;
-    const uint2 c = *reinterpret_cast<const uint2*>(w.q + at * 32 + piece * 8);
-    const float s = bf16_to_f32(w.s[at]), zs = -bf16_to_f32(w.z[at]) * s;
-    uint4* d = reinterpret_cast<uint4*>(dst + row * ROWB + piece * 32);
-    d[0] = dequant8(c.x, s, zs);
-    d[1] = dequant8(c.y, s, zs);
-  };
-  const int ra = (wave >> 1) * 32 + (lane & 31), rb = (wave & 1) * 32 + (lane & 31);
-  for (int g = 0; g < K / 64; ++g) {
-    const uint4* xp = reinterpret_cast<const uint4*>(X + mr * K + 64 * g + 16 * piece);
-    uint4* d = reinterpret_cast<uint4*>(lds[0] + row * ROWB + piece * 32);
-    d[0] = xp[0];
-    d[1] = xp[1];
-    stage_w(wg, g, lds[1]);
-    stage_w(wu, g, lds[2]);
-    __syncthreads();
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const int o = ks * 32 + (lane >> 5) * 16;
-      const v8bf a = *reinterpret_cast<const v8bf*>(lds[0] + ra * ROWB + o);
-      const v8bf b = *reinterpret_cast<const v8bf*>(lds[1] + rb * ROWB + o);
-      const v8bf c = *reinterpret_cast<const v8bf*>(lds[2] + rb * ROWB + o);
-      ag = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, ag, 0, 0, 0);
-      au = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, c, au, 0, 0, 0);
-    }
-    __syncthreads();
-  }
-  const int64_t n = n0 + rb;
-  if (n >= N) return;
-  const float vg = bg ? bf16_to_f32(bg[n]) : 0.f, vu = bu ? bf16_to_f32(bu[n]) : 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int64_t m = m0 + (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-    if (m >= M) continue;
-    const float G = ag[e] + vg, U = au[e] + vu;
-    const float h = gate_act<ACT>(G) * U;
-    if (hbf16)
-      static_cast<uint16_t*>(H)[m * N + n] = f32_to_bf16(h);
+// The G and U of R blocks of 32 rows and 32 columns in a wave's accumulators:
+// bias, activation, product, and the stores through the wave's LDS buffer `eb`
+// (32 x 36 floats).
+template <int ACT, int R>
+__device__ __forceinline__ void gated_epilogue(v16f (&acc)[R][2], float* eb, int lane, int64_t row0,
+                                               int64_t col0, int M, int N,
+                                               const uint16_t* __restrict__ bg,
+                                               const uint16_t* __restrict__ bu, void* H, bool hbf16,
+                                               uint16_t* Gs, uint16_t* Us) {
+  const int64_t n = col0 + (lane & 31);
+  const float vg = bg && n < N ? bf16_to_f32(bg[n]) : 0.f;
+  const float vu = bu && n < N ? bf16_to_f32(bu[n]) : 0.f;
+  const float none[1] = {0.f};
+  v16f o[R][1];
+  auto store = [&](void* Y, bool b16) {
+    if (b16)
+      store_wave_tile<R, 1, true>(o, none, eb, lane, row0, col0, M, N, Y);
     else
-      static_cast<float*>(H)[m * N + n] = h;
-    if (Gs) {
-      Gs[m * N + n] = f32_to_bf16(G);
-      Us[m * N + n] = f32_to_bf16(U);
+      store_wave_tile<R, 1, false>(o, none, eb, lane, row0, col0, M, N, Y);
+  };
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      acc[i][0][e] += vg;
+      acc[i][1][e] += vu;
     }
+  if (Gs) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) o[i][0] = acc[i][0];
+    store(Gs, true);
+#pragma unroll
+    for (int i = 0; i < R; ++i) o[i][0] = acc[i][1];
+    store(Us, true);
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][0][e] = gate_act<ACT>(acc[i][0][e]) * acc[i][1][e];
+  store(H, hbf16);
 }
 
 // ----------------------------------------------------------- few rows
@@ -304,42 +279,83 @@ __global__ __launch_bounds__(svdq_gemm::NT) void gated_wide_kernel(
   zero_acc(acc);
   tile_product(p, m0, b0, st0, st1, acc);
 
-  const int64_t row0 = m0 + wm * WM, col0 = b0 / 2 + wn * 32;
-  const int64_t n = col0 + (lane & 31);
-  const float vg = bg && n < N ? bf16_to_f32(bg[n]) : 0.f;
-  const float vu = bu && n < N ? bf16_to_f32(bu[n]) : 0.f;
-  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * 36);
-  const float none[1] = {0.f};
-  v16f o[RBL][1];
-  auto store = [&](void* Y, bool b16) {
-    if (b16)
-      store_wave_tile<RBL, 1, true>(o, none, eb, lane, row0, col0, p.M, N, Y);
-    else
-      store_wave_tile<RBL, 1, false>(o, none, eb, lane, row0, col0, p.M, N, Y);
-  };
-#pragma unroll
-  for (int i = 0; i < RBL; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      acc[i][0][e] += vg;
-      acc[i][1][e] += vu;
-    }
-  if (Gs) {
-#pragma unroll
-    for (int i = 0; i < RBL; ++i) o[i][0] = acc[i][0];
-    store(Gs, true);
-#pragma unroll
-    for (int i = 0; i < RBL; ++i) o[i][0] = acc[i][1];
-    store(Us, true);
-  }
-#pragma unroll
-  for (int i = 0; i < RBL; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[i][0][e] = gate_act<ACT>(acc[i][0][e]) * acc[i][1][e];
-  store(H, hbf16);
+  gated_epilogue<ACT>(acc, reinterpret_cast<float*>(&st0) + wave * (32 * 36), lane, m0 + wm * WM,
+                      b0 / 2 + wn * 32, p.M, N, bg, bu, H, hbf16, Gs, Us);
 }
 
-constexpr int64_t WIDE_ROWS = 512;      // rows from which the weights are dequantized up front
+// -------------------------------------------------------- medium number of rows
+// B rows of a tile: for each of the two wave columns 32 rows of Wg and the 32
+// rows of Wu with the same n.  Two threads take one row, 32 codes each.
+struct PairWeights {
+  svdq::AwqWeight wg, wu;
+  const uint8_t* q;
+  const uint16_t *s, *z;
+  int64_t nr;
+  int N, row, half;
+  uint4 c;
+  float fs, fz;
+
+  __device__ __forceinline__ PairWeights(const svdq::AwqWeight& g, const svdq::AwqWeight& u, int N,
+                                         int64_t n0)
+      : N(N), row(int(threadIdx.x) >> 1), half(threadIdx.x & 1) {
+    const bool up = row & 32;
+    q = up ? u.q : g.q;
+    s = up ? u.s : g.s;
+    z = up ? u.z : g.z;
+    nr = min(n0 + (row >> 6) * 32 + (row & 31), int64_t(N) - 1);
+  }
+  static __device__ __forceinline__ int slot(int row, int piece) {
+    return row * 8 + (piece ^ ((row >> 1) & 7));
+  }
+  __device__ __forceinline__ void fetch(int chunk) {
+    const int64_t at = int64_t(chunk) * N + nr;
+    c = *reinterpret_cast<const uint4*>(q + at * 32 + 16 * half);
+    fs = bf16_to_f32(s[at]);
+    fz = -bf16_to_f32(z[at]) * fs;
+  }
+  __device__ __forceinline__ void put(uint4* b, int i) {
+    const uint32_t w = i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
+    b[slot(row, 4 * half + i)] = dequant8(w, fs, fz);
+  }
+};
+
+template <int ACT>
+__global__ __launch_bounds__(svdq_mid::NT, 2) void gated_mid_kernel(
+    svdq_mid::Args p, svdq::AwqWeight wg, svdq::AwqWeight wu, int N, int S, int tiles,
+    const uint16_t* __restrict__ bg, const uint16_t* __restrict__ bu, void* __restrict__ H,
+    bool hbf16, uint16_t* __restrict__ Gs, uint16_t* __restrict__ Us, float* __restrict__ part) {
+  using namespace svdq_mid;
+  __shared__ Stage st0, st1;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slice = blockIdx.x / tiles;
+  int64_t m0, n0;
+  tile_origin(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (N + 63) / 64, BM, 64, m0, n0);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  PairWeights w(wg, wu, N, n0);
+  tile_product(p, m0, int(int64_t(slice) * p.chunks / S), int(int64_t(slice + 1) * p.chunks / S), w,
+               st0, st1, acc);
+  const int64_t row0 = m0 + (wave >> 1) * 64, col0 = n0 + (wave & 1) * 32;
+  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * 36);
+  if (S == 1) {
+    gated_epilogue<ACT>(acc, eb, lane, row0, col0, p.M, N, bg, bu, H, hbf16, Gs, Us);
+    return;
+  }
+  const float none[1] = {0.f};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    v16f o[RBL][1];
+#pragma unroll
+    for (int i = 0; i < RBL; ++i) o[i][0] = acc[i][t];
+    store_wave_tile<RBL, 1, false>(o, none, eb, lane, row0, col0, p.M, N,
+                                   part + (int64_t(slice) * 2 + t) * p.M * N);
+  }
+}
+
+constexpr int64_t WIDE_ROWS = 1024;     // rows from which the weights are dequantized up front
+
+int64_t mid_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 63) / 64); }
 
 int64_t pair_rows(int64_t N) { return (N + 31) / 32 * 64; }
 
@@ -349,7 +365,11 @@ namespace svdq {
 
 size_t awq_gated_workspace(int64_t M, int64_t K, int64_t N) {
   if (M <= ROWS) return align256(size_t(split(K, N).slices) * 2 * size_t(M) * size_t(N) * 4);
-  return M < WIDE_ROWS ? 0 : align256(size_t(pair_rows(N)) * size_t(K) * 2);
+  if (M < WIDE_ROWS) {
+    const int S = svdq_mid::slices(mid_tiles(M, N), K / 64);
+    return S == 1 ? 0 : align256(size_t(S) * 2 * size_t(M) * size_t(N) * 4);
+  }
+  return align256(size_t(pair_rows(N)) * size_t(K) * 2);
 }
 
 svdq_status launch_awq_gated(const uint16_t* X, int64_t M, int64_t K, int64_t N, AwqWeight wg,
@@ -357,18 +377,21 @@ svdq_status launch_awq_gated(const uint16_t* X, int64_t M, int64_t K, int64_t N,
                              void* H, svdq_dtype h_dt, uint16_t* G, uint16_t* U, void* ws,
                              hipStream_t s) {
   const bool hb = h_dt == SVDQ_BF16;
+  float* const part = static_cast<float*>(ws);
+  auto sum = [&](int S) {
+    auto k = act == SVDQ_SILU ? gated_sum_kernel<SVDQ_SILU> : gated_sum_kernel<SVDQ_GELU>;
+    hipLaunchKernelGGL(k, dim3(unsigned((M * N / 4 + 63) / 64)), dim3(64), 0, s, part, S, int(M),
+                       int(N), bg, bu, H, hb, G, U);
+    return check_launch("gated_sum");
+  };
   if (M <= ROWS) {
-    float* const part = static_cast<float*>(ws);
     switch ((M + 15) / 16) {
       case 1: SVDQ_TRY(run_rows<1>(X, M, K, N, wg, wu, part, s)); break;
       case 2: SVDQ_TRY(run_rows<2>(X, M, K, N, wg, wu, part, s)); break;
       case 3: SVDQ_TRY(run_rows<3>(X, M, K, N, wg, wu, part, s)); break;
       default: SVDQ_TRY(run_rows<4>(X, M, K, N, wg, wu, part, s)); break;
     }
-    auto k = act == SVDQ_SILU ? gated_sum_kernel<SVDQ_SILU> : gated_sum_kernel<SVDQ_GELU>;
-    hipLaunchKernelGGL(k, dim3(unsigned((M * N / 4 + 63) / 64)), dim3(64), 0, s, part,
-                       split(K, N).slices, int(M), int(N), bg, bu, H, hb, G, U);
-    return check_launch("gated_sum");
+    return sum(split(K, N).slices);
   }
   if (M >= WIDE_ROWS) {
     uint16_t* const B = static_cast<uint16_t*>(ws);
@@ -382,11 +405,14 @@ svdq_status launch_awq_gated(const uint16_t* X, int64_t M, int64_t K, int64_t N,
                        G, U);
     return check_launch("awq_gated (wide)");
   }
-  dim3 grid(unsigned((N + TB - 1) / TB), unsigned((M + TB - 1) / TB));
-  auto k = act == SVDQ_SILU ? gated_tile_kernel<SVDQ_SILU> : gated_tile_kernel<SVDQ_GELU>;
-  hipLaunchKernelGGL(k, grid, dim3(256), 0, s, X, int(M), int(K), int(N), wg, wu, bg, bu, H, hb,
-                     G, U);
-  return check_launch("awq_gated");
+  const int64_t tiles = mid_tiles(M, N);
+  const int S = svdq_mid::slices(tiles, K / 64);
+  svdq_mid::Args p{{X, X}, K, int(K / 64), 1, int(M)};
+  auto k = act == SVDQ_SILU ? gated_mid_kernel<SVDQ_SILU> : gated_mid_kernel<SVDQ_GELU>;
+  hipLaunchKernelGGL(k, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, s, p, wg, wu, int(N), S,
+                     int(tiles), bg, bu, H, hb, G, U, part);
+  SVDQ_TRY(check_launch("awq_gated (mid)"));
+  return S == 1 ? SVDQ_OK : sum(S);
 }
 
 }  // namespace svdq

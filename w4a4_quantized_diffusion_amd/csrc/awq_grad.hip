@@ -70,80 +70,6 @@ __device__ __forceinline__ void transpose_dequant8(const svdq::AwqWeight& w, int
   for (int i = 0; i < 8; ++i) out[i] = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
 }
 
-constexpr int TB = 64;
-constexpr int ROWB = 144;
-
-// 64 rows x one group of 64 columns of dX per workgroup, 64 n at a time.
-__global__ __launch_bounds__(256) void grad_tile_kernel(
-    const uint16_t* __restrict__ dA, svdq::AwqWeight wa, const uint16_t* __restrict__ dB,
-    svdq::AwqWeight wb, int pairs, int M, int K, int N, void* __restrict__ dX, bool xbf16) {
-  __shared__ __align__(16) uint8_t lds[2][TB * ROWB];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int g = blockIdx.x;
-  const int64_t m0 = int64_t(blockIdx.y) * TB;
-  const int row = tid >> 2, piece = tid & 3;
-  const int64_t mr = m0 + row < M ? m0 + row : M - 1;
-  const int oct = tid >> 5, byte = tid & 31;
-  v16f acc;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  const int ra = (wave >> 1) * 32 + (lane & 31), rb = (wave & 1) * 32 + (lane & 31);
-  for (int p = 0; p < pairs; ++p) {
-    const uint16_t* const d = p ? dB : dA;
-    const svdq::AwqWeight w = p ? wb : wa;
-    for (int64_t n0 = 0; n0 < N; n0 += 64) {
-      // rows of the last chunk past N (a multiple of 16) count as zeros on both sides
-      uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0;
-      if (n0 + 16 * piece < N) {
-        const uint4* ap = reinterpret_cast<const uint4*>(d + mr * N + n0 + 16 * piece);
-        a0 = ap[0];
-        a1 = ap[1];
-      }
-      uint4* ad = reinterpret_cast<uint4*>(lds[0] + row * ROWB + piece * 32);
-      ad[0] = a0;
-      ad[1] = a1;
-      float lo[8], hi[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t n = n0 + 8 * oct + i;
-        lo[i] = hi[i] = 0.f;
-        if (n < N) {
-          const int64_t at = int64_t(g) * N + n;
-          const uint32_t c = w.q[at * 32 + byte];
-          const float s = bf16_to_f32(w.s[at]), zs = -bf16_to_f32(w.z[at]) * s;
-          lo[i] = fmaf(float(c & 15), s, zs);
-          hi[i] = fmaf(float(c >> 4), s, zs);
-        }
-      }
-      *reinterpret_cast<uint4*>(lds[1] + (2 * byte) * ROWB + oct * 16) =
-          make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
-                     pack_bf16x2(lo[4], lo[5]), pack_bf16x2(lo[6], lo[7]));
-      *reinterpret_cast<uint4*>(lds[1] + (2 * byte + 1) * ROWB + oct * 16) =
-          make_uint4(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]),
-                     pack_bf16x2(hi[4], hi[5]), pack_bf16x2(hi[6], hi[7]));
-      __syncthreads();
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const int o = ks * 32 + (lane >> 5) * 16;
-        const v8bf a = *reinterpret_cast<const v8bf*>(lds[0] + ra * ROWB + o);
-        const v8bf b = *reinterpret_cast<const v8bf*>(lds[1] + rb * ROWB + o);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
-      }
-      __syncthreads();
-    }
-  }
-  const int64_t k = int64_t(g) * 64 + rb;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int64_t m = m0 + (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-    if (m >= M) continue;
-    if (xbf16)
-      static_cast<uint16_t*>(dX)[m * K + k] = f32_to_bf16(acc[e]);
-    else
-      static_cast<float*>(dX)[m * K + k] = acc[e];
-  }
-}
-
 // ----------------------------------------------------------- few rows
 // Up to 64 rows the time is the weights' way from memory.  A workgroup takes
 // 128 columns of dX (two groups) and one of S slices of the reduction, counted
@@ -156,19 +82,21 @@ __global__ __launch_bounds__(256) void grad_tile_kernel(
 
 constexpr int ROWS = 64;                 // the most rows of this form
 constexpr int WAVES = 8, NT = 64 * WAVES;
-constexpr int LDS_A = 64 << 10;
+constexpr int LDS_A = 64 << 10;          // for the rows' operand of 16 rows, twice that above
 constexpr int MAX_SLICES = 16;
 
 struct Split {
   int blocks, slices;
 };
 
-Split split(int64_t K, int64_t N, int layers) {
+Split split(int64_t M, int64_t K, int64_t N, int layers) {
   Split p;
   p.blocks = int((K + 127) / 128);
   const int64_t steps = (N + 31) / 32 * layers;
+  // one workgroup fits a compute unit, two where the sums of 16 rows are all it holds
+  const int most = M <= 16 ? 512 : 256;
   p.slices = int(std::min<int64_t>({(steps + WAVES - 1) / WAVES, MAX_SLICES,
-                                    std::max<int64_t>(1, 512 / p.blocks)}));
+                                    std::max<int64_t>(1, most / p.blocks)}));
   return p;
 }
 
@@ -336,16 +264,28 @@ __global__ __launch_bounds__(64) void grad_sum_kernel(const float* __restrict__ 
     static_cast<v4f*>(dX)[i] = p;
 }
 
+svdq_status launch_sum(const float* part, int S, int64_t M, int64_t K, void* dX, bool xbf16,
+                       hipStream_t s) {
+  const int64_t total = M * K / 4;
+  hipLaunchKernelGGL(grad_sum_kernel, dim3(unsigned((total + 63) / 64)), dim3(64), 0, s, part, S,
+                     total, dX, xbf16);
+  return svdq::check_launch("grad_sum");
+}
+
 template <int MT, int ACT>
 svdq_status run_rows_mt(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
                         float* part, hipStream_t s) {
   constexpr int layers = ACT < 0 ? 1 : 2;
-  const Split p = split(K, N, layers);
-  // steps of the rows' operand that fit LDS (64 rows: 15)
+  const Split p = split(M, K, N, layers);
+  // steps of the rows' operand that fit LDS (64 rows: 31)
   const int64_t steps = (N + 31) / 32 * layers;
-  const int sub = int(std::min<int64_t>((LDS_A / M - 16) / 64, (steps + p.slices - 1) / p.slices));
+  const int64_t room = MT == 1 ? LDS_A : 2 * LDS_A;
+  const int sub = int(std::min<int64_t>((room / M - 16) / 64, (steps + p.slices - 1) / p.slices));
   const size_t shm = std::max(size_t(M) * (sub * 64 + 16), size_t(WAVES) * 8 * 1024);
   auto k = grad_slice_kernel<MT, ACT>;
+  if (shm > (64 << 10))
+    SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(shm)));
   hipLaunchKernelGGL(k, dim3(unsigned(p.blocks * p.slices)), dim3(NT), shm, s, in, w[0],
                      w[layers - 1], int(M), int(K), int(N), p.slices, sub, part);
   return svdq::check_launch("grad_slice");
@@ -360,14 +300,11 @@ svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq
     case 3: SVDQ_TRY((run_rows_mt<3, ACT>(in, M, K, N, w, part, s))); break;
     default: SVDQ_TRY((run_rows_mt<4, ACT>(in, M, K, N, w, part, s))); break;
   }
-  const int64_t total = M * K / 4;
-  hipLaunchKernelGGL(grad_sum_kernel, dim3(unsigned((total + 63) / 64)), dim3(64), 0, s, part,
-                     split(K, N, ACT < 0 ? 1 : 2).slices, total, dX, xbf16);
-  return svdq::check_launch("grad_sum");
+  return launch_sum(part, split(M, K, N, ACT < 0 ? 1 : 2).slices, M, K, dX, xbf16, s);
 }
 
 size_t rows_bytes(int64_t M, int64_t K, int64_t N, int layers) {
-  return svdq::align256(size_t(split(K, N, layers).slices) * size_t(M) * size_t(K) * 4);
+  return svdq::align256(size_t(split(M, K, N, layers).slices) * size_t(M) * size_t(K) * 4);
 }
 
 // ---------------------------------------------------------- many rows
@@ -416,12 +353,113 @@ __global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Arg
     store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, p.rows, dX);
 }
 
-constexpr int64_t WIDE_ROWS = 512;      // rows from which the weights are dequantized up front
+// -------------------------------------------------------- medium number of rows
+// B rows of a tile: 128 columns k of dX (two groups) over 64 n of one layer.
+// A thread takes 4 rows n and 8 k of each, and writes 8 pieces of 4 n.  The
+// swizzle has two more bits of the row than A's, so that the 8 k (rows 8 j + i)
+// of 8 neighbouring threads fall into 8 different slots.
+struct GradWeights {
+  svdq::AwqWeight wa, wb;
+  int64_t gN;
+  int N, chunks, j, quad, kr;
+  uint32_t c[4];
+  uint2 s2, z2;
+  bool live;
+
+  __device__ __forceinline__ GradWeights(const svdq::AwqWeight& a, const svdq::AwqWeight& b, int K,
+                                         int N, int chunks, int64_t k0)
+      : wa(a), wb(b), N(N), chunks(chunks) {
+    const int t = threadIdx.x;
+    j = t & 7;
+    quad = (t >> 3) & 15;
+    kr = 64 * (t >> 7) + 8 * j;
+    gN = min(k0 / 64 + (t >> 7), int64_t(K) / 64 - 1) * N;
+  }
+  static __device__ __forceinline__ int slot(int row, int piece) {
+    return row * 8 + (piece ^ (((row >> 1) ^ (row >> 4)) & 7));
+  }
+  __device__ __forceinline__ void fetch(int chunk) {
+    const bool second = chunk >= chunks;
+    const svdq::AwqWeight& w = second ? wb : wa;
+    const int64_t n = 64 * int64_t(second ? chunk - chunks : chunk) + 4 * quad;
+    live = n < N;
+    const int64_t at = gN + min(n, int64_t(N) - 4);
+    s2 = *reinterpret_cast<const uint2*>(w.s + at);
+    z2 = *reinterpret_cast<const uint2*>(w.z + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = *reinterpret_cast<const uint32_t*>(w.q + (at + i) * 32 + 4 * j);
+  }
+  // (quarter 3 alone: the four rows are needed together)
+  __device__ __forceinline__ void put(uint4* b, int q) {
+    if (q != 3) return;
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t sw = i < 2 ? s2.x : s2.y, zw = i < 2 ? z2.x : z2.y;
+      const float f = __uint_as_float(!live ? 0u : i & 1 ? sw & 0xFFFF0000u : sw << 16);
+      dequant8_f32(c[i], f, -__uint_as_float(i & 1 ? zw & 0xFFFF0000u : zw << 16) * f, v[i]);
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      reinterpret_cast<uint2*>(b + slot(kr + t, quad >> 1))[quad & 1] =
+          make_uint2(pack_bf16x2(v[0][t], v[1][t]), pack_bf16x2(v[2][t], v[3][t]));
+  }
+};
+
+__global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
+    svdq_mid::Args p, svdq::AwqWeight wa, svdq::AwqWeight wb, int K, int N, int S, int tiles,
+    void* __restrict__ dX, bool xbf16, float* __restrict__ part) {
+  using namespace svdq_mid;
+  __shared__ Stage st0, st1;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slice = blockIdx.x / tiles;
+  int64_t m0, k0;
+  tile_origin(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (K + BN - 1) / BN, BM, BN, m0, k0);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  GradWeights w(wa, wb, K, N, p.chunks, k0);
+  const int64_t total = int64_t(p.chunks) * p.segments;
+  tile_product(p, m0, int(slice * total / S), int((slice + 1) * total / S), w, st0, st1, acc);
+  const int64_t row0 = m0 + (wave >> 1) * 64, col0 = k0 + (wave & 1) * 64;
+  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * 68);
+  const float none[CBL] = {0.f, 0.f};
+  if (S > 1)
+    store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, K,
+                                     part + int64_t(slice) * p.M * K);
+  else if (xbf16)
+    store_wave_tile<RBL, CBL, true>(acc, none, eb, lane, row0, col0, p.M, K, dX);
+  else
+    store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, K, dX);
+}
+
+int mid_slices(int64_t M, int64_t K, int64_t N, int layers) {
+  return svdq_mid::slices((M + 127) / 128 * ((K + 127) / 128), (N + 63) / 64 * layers);
+}
+
+// dX = A0 wd0 [+ A1 wd1]
+svdq_status launch_mid(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWeight* w,
+                       int layers, int64_t M, int64_t K, int64_t N, void* dX, bool xbf16,
+                       float* part, hipStream_t s) {
+  const int64_t tiles = (M + 127) / 128 * ((K + 127) / 128);
+  const int S = mid_slices(M, K, N, layers);
+  svdq_mid::Args p{{A0, A1}, N, int((N + 63) / 64), layers, int(M)};
+  hipLaunchKernelGGL(grad_mid_kernel, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, s, p, w[0],
+                     w[layers - 1], int(K), int(N), S, int(tiles), dX, xbf16, part);
+  SVDQ_TRY(svdq::check_launch("awq_grad (mid)"));
+  return S == 1 ? SVDQ_OK : launch_sum(part, S, M, K, dX, xbf16, s);
+}
+
+constexpr int64_t WIDE_ROWS = 1024;     // rows from which the weights are dequantized up front
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
+// of a call with more than ROWS rows
 size_t wide_bytes(int64_t M, int64_t K, int64_t N, int layers) {
-  return M < WIDE_ROWS ? 0 : svdq::align256(size_t(K) * size_t(pad64(N)) * 2 * layers);
+  if (M >= WIDE_ROWS) return svdq::align256(size_t(K) * size_t(pad64(N)) * 2 * layers);
+  const int S = mid_slices(M, K, N, layers);
+  return S == 1 ? 0 : svdq::align256(size_t(S) * size_t(M) * size_t(K) * 4);
 }
 
 // dX = A0 wd0 [+ A1 wd1] for M >= WIDE_ROWS, B the workspace
@@ -461,10 +499,7 @@ svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int
                         x_dt == SVDQ_BF16, static_cast<float*>(ws), s);
   if (M >= WIDE_ROWS)
     return launch_wide(dY, dY, &w, 1, M, K, N, dX, x_dt == SVDQ_BF16, static_cast<uint16_t*>(ws), s);
-  dim3 grid(unsigned(K / 64), unsigned((M + TB - 1) / TB));
-  hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, s, dY, w, dY, w, 1, int(M), int(K),
-                     int(N), dX, x_dt == SVDQ_BF16);
-  return check_launch("awq_linear_grad");
+  return launch_mid(dY, dY, &w, 1, M, K, N, dX, x_dt == SVDQ_BF16, static_cast<float*>(ws), s);
 }
 
 svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
@@ -486,15 +521,11 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
   auto k = act == SVDQ_SILU ? gate_grad_kernel<SVDQ_SILU> : gate_grad_kernel<SVDQ_GELU>;
   hipLaunchKernelGGL(k, dim3(blocks), dim3(256), 0, s, dH, G, U, n8, dG, dU);
   SVDQ_TRY(check_launch("gate_grad"));
-  if (M >= WIDE_ROWS) {
-    const AwqWeight w[2] = {wg, wu};
-    uint16_t* const B = reinterpret_cast<uint16_t*>(w8 + 2 * align256(size_t(M) * size_t(N) * 2));
-    return launch_wide(dG, dU, w, 2, M, K, N, dX, true, B, s);
-  }
-  dim3 grid(unsigned(K / 64), unsigned((M + TB - 1) / TB));
-  hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, s, dG, wg, dU, wu, 2, int(M), int(K),
-                     int(N), static_cast<void*>(dX), true);
-  return check_launch("awq_gated_grad");
+  const AwqWeight w[2] = {wg, wu};
+  void* const rest = w8 + 2 * align256(size_t(M) * size_t(N) * 2);
+  if (M >= WIDE_ROWS)
+    return launch_wide(dG, dU, w, 2, M, K, N, dX, true, static_cast<uint16_t*>(rest), s);
+  return launch_mid(dG, dU, w, 2, M, K, N, dX, true, static_cast<float*>(rest), s);
 }
 
 }  // namespace svdq

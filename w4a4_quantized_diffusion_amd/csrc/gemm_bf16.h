@@ -116,7 +116,7 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
   // out and the chunk is computed.  Past the last chunk the transfers repeat
   // it into a buffer nobody reads.
   auto step = [&](int c, Stage& cur, Stage& nxt) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070);     // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     dma(min(c + 1, total - 1), nxt);
     __builtin_amdgcn_sched_barrier(0);
@@ -130,16 +130,132 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
   }
   if (c < total) step(c, st0, st1);
   // the repeated last transfers, before the buffers are used for anything else
+  __builtin_amdgcn_s_waitcnt(0x0070);
   __syncthreads();
 }
 
-__device__ __forceinline__ void zero_acc(v16f (&acc)[RBL][CBL]) {
+template <int R, int C>
+__device__ __forceinline__ void zero_acc(v16f (&acc)[R][C]) {
 #pragma unroll
-  for (int i = 0; i < RBL; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < CBL; ++j)
+    for (int j = 0; j < C; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 }
 
 }  // namespace svdq_gemm
+
+// A medium number of rows: 128 x 128 tiles, 4 waves of 64 x 64, two workgroups
+// to a compute unit.  A comes to LDS by the load unit; the weights are
+// dequantized on their way into LDS (once per 128 rows, where a pass of their
+// own would cost more than it saves).  Few tiles are split over the reduction
+// as well, into S slices of whole chunks.
+namespace svdq_mid {
+
+using namespace svdq_dev;
+using svdq_gemm::lds_ptr_t;
+using svdq_gemm::zero_acc;
+
+constexpr int BM = 128, BN = 128;
+constexpr int NT = 256;
+constexpr int RBL = 2, CBL = 2;
+constexpr int MAX_SLICES = 8;
+
+struct Args {
+  const uint16_t* A[2];
+  int64_t width;          // columns of A in one segment (a multiple of 8)
+  int chunks;             // chunks of 64 in one segment
+  int segments;           // 1 or 2
+  int M;
+};
+
+struct __attribute__((aligned(16))) Stage {
+  uint4 a[BM * 8];
+  uint4 b[BN * 8];
+};
+
+// slices of the reduction for a number of tiles
+inline int slices(int64_t tiles, int64_t chunks) {
+  return int(std::min<int64_t>({std::max<int64_t>(1, 512 / tiles), MAX_SLICES,
+                                std::max<int64_t>(1, chunks / 4)}));
+}
+
+// Weights: fetch(chunk) loads this thread's share of a chunk's B rows into
+// registers, put(stage, q) writes quarter q of it to LDS, slot(row, piece) is
+// where piece `piece` of B row `row` lies.
+template <class Weights>
+__device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, int c1, Weights& w,
+                                             Stage& st0, Stage& st1, v16f (&acc)[RBL][CBL]) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int h = lane >> 5, r32 = lane & 31;
+  // wave w brings rows 32 w .. 32 w + 31 of A, 8 rows to a transfer; rows past
+  // the edge repeat the last row, pieces past the width the last piece
+  int64_t arow[4];
+  int apiece[2];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = 32 * wave + 8 * t + (lane >> 3);
+    arow[t] = (m0 + r < p.M ? m0 + r : p.M - 1) * p.width;
+    if (t < 2) apiece[t] = 8 * ((lane & 7) ^ ((r >> 1) & 7));
+  }
+  auto dma = [&](int c, Stage& st) __attribute__((always_inline)) {
+    const bool second = c >= p.chunks;
+    const uint16_t* const A = second ? p.A[1] : p.A[0];
+    const int64_t col = 64 * int64_t(second ? c - p.chunks : c);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int64_t k = min(col + apiece[t & 1], p.width - 8);
+      __builtin_amdgcn_global_load_lds(A + arow[t] + k, (lds_ptr_t)&st.a[(32 * wave + 8 * t) * 8],
+                                       16, 0, 0);
+    }
+  };
+  const int sw = (r32 >> 1) & 7;
+  const int abase = (wm * 64 + r32) * 8;
+  auto step = [&](int c, Stage& cur, Stage& nxt) __attribute__((always_inline)) {
+    // this wave's transfers and LDS writes of chunk c have landed, then everyone's
+    __builtin_amdgcn_s_waitcnt(0x0070);     // vmcnt(0) lgkmcnt(0)
+    __syncthreads();
+    const bool more = c + 1 < c1;
+    if (more) dma(c + 1, nxt);
+    v8bf fa[2][RBL], fb[2][CBL];
+    auto frags = [&](int ks, v8bf (&a)[RBL], v8bf (&b)[CBL]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < CBL; ++j)
+        b[j] = __builtin_bit_cast(v8bf, cur.b[Weights::slot(wn * 64 + 32 * j + r32, 2 * ks + h)]);
+#pragma unroll
+      for (int i = 0; i < RBL; ++i)
+        a[i] = __builtin_bit_cast(v8bf, cur.a[abase + 256 * i + ((2 * ks + h) ^ sw)]);
+    };
+    frags(0, fa[0], fb[0]);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks < 3) frags(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < RBL; ++i)
+#pragma unroll
+        for (int j = 0; j < CBL; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j],
+                                                              acc[i][j], 0, 0, 0);
+      if (more) w.put(nxt.b, ks);
+    }
+    if (c + 2 < c1) w.fetch(c + 2);
+  };
+  w.fetch(c0);
+  dma(c0, st0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w.put(st0.b, q);
+  if (c0 + 1 < c1) w.fetch(c0 + 1);
+  int c = c0;
+  for (; c + 2 <= c1; c += 2) {
+    step(c, st0, st1);
+    step(c + 1, st1, st0);
+  }
+  if (c < c1) step(c, st0, st1);
+  __syncthreads();
+}
+
+}  // namespace svdq_mid

@@ -264,16 +264,19 @@ __device__ __forceinline__ void store_wave_tile(const v16f (&acc)[RBL][CBL],
 // one XCD runs at a time cover about 4 row tiles by 8 column tiles and their
 // A rows and W rows stay in that XCD's L2 (about a third less HBM traffic
 // than a whole column of row tiles at a time).
-__device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bm, int bn,
+__device__ __forceinline__ void tile_origin(int t, int tiles_m, int tiles_n, int bm, int bn,
                                             int64_t& m0, int64_t& n0) {
   constexpr int GN = 8;
   const int total = tiles_m * tiles_n;
-  int t = blockIdx.x;
   if ((total & 7) == 0) t = (t & 7) * (total >> 3) + (t >> 3);
   const int grp = t / (GN * tiles_m), in = t - grp * (GN * tiles_m);
   const int gn = min(GN, tiles_n - grp * GN);
   m0 = int64_t(in / gn) * bm;
   n0 = int64_t(grp * GN + in % gn) * bn;
+}
+__device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bm, int bn,
+                                            int64_t& m0, int64_t& n0) {
+  tile_origin(int(blockIdx.x), tiles_m, tiles_n, bm, bn, m0, n0);
 }
 
 }  // namespace svdq_dev
