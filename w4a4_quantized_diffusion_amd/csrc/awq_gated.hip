@@ -269,7 +269,7 @@ __global__ __launch_bounds__(svdq_gemm::NT) void gated_wide_kernel(
     svdq_gemm::Args p, int N, const uint16_t* __restrict__ bg, const uint16_t* __restrict__ bu,
     void* __restrict__ H, bool hbf16, uint16_t* __restrict__ Gs, uint16_t* __restrict__ Us) {
   using namespace svdq_gemm;
-  __shared__ Stage st0, st1;
+  __shared__ Stage st0, st1, st2, st3, st4;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(svdq_gemm::NT) void gated_wide_kernel(
   tile_origin((p.M + BM - 1) / BM, (p.rows + BN - 1) / BN, BM, BN, m0, b0);
   v16f acc[RBL][CBL];
   zero_acc(acc);
-  tile_product(p, m0, b0, st0, st1, acc);
+  tile_product(p, m0, b0, st0, st1, st2, st3, st4, acc);
 
   gated_epilogue<ACT>(acc, reinterpret_cast<float*>(&st0) + wave * (32 * 36), lane, m0 + wm * WM,
                       b0 / 2 + wn * 32, p.M, N, bg, bu, H, hbf16, Gs, Us);

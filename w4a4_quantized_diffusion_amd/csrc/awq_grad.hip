@@ -336,14 +336,14 @@ __global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Arg
                                                                   void* __restrict__ dX,
                                                                   bool xbf16) {
   using namespace svdq_gemm;
-  __shared__ Stage st0, st1;
+  __shared__ Stage st0, st1, st2, st3, st4;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int64_t m0, b0;
   tile_origin((p.M + BM - 1) / BM, (p.rows + BN - 1) / BN, BM, BN, m0, b0);
   v16f acc[RBL][CBL];
   zero_acc(acc);
-  tile_product(p, m0, b0, st0, st1, acc);
+  tile_product(p, m0, b0, st0, st1, st2, st3, st4, acc);
   const int64_t row0 = m0 + (wave >> 2) * WM, col0 = b0 + (wave & 3) * WN;
   float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * (WN + 4));
   const float none[CBL] = {0.f, 0.f};

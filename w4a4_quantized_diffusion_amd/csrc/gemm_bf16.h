@@ -6,13 +6,16 @@
 // the other's), B [rows, ldb] the weights in bf16, each segment padded with
 // zeros to whole chunks of 64.  256 x 256 tiles, 8 waves of 128 x 64 on
 // v_mfma_f32_32x32x16_bf16, both operands brought to LDS by the load unit
-// (global_load_lds, 16 bytes a lane) one chunk of 64 ahead in two buffers.
+// (global_load_lds, 16 bytes a lane).
 //
-// LDS rows are 128 bytes, 8 slots of 16; slot s of row r holds piece
-// s ^ ((r >> 1) & 7), so that the 16 lanes of one ds_read_b128 phase (rows
-// r..r+15, one piece) touch 16 different groups of 4 banks.  The load unit
-// writes a wave's 64 pieces consecutively, so the permutation is applied to the
-// global addresses.
+// Both operands move in stages of 32 r through a ring of NST buffers, so that
+// NST - 1 stages are on their way while one is used: the tiles of one XCD run in
+// step, so a stage arrives no sooner than its slowest line from HBM, and with one
+// stage ahead the waves waited for that half of the time.  LDS rows are 64 bytes,
+// 4 slots of 16; slot s of row r holds piece s ^ ((r >> 2) & 3), so that the 16
+// lanes of one ds_read_b128 phase (rows r..r+15, one piece) touch 16 different
+// groups of 4 banks.  The load unit writes a wave's 64 pieces consecutively, so
+// the permutation is applied to the global addresses.
 #pragma once
 
 #include "w4a16.h"
@@ -36,99 +39,129 @@ struct Args {
   int M, rows;            // rows of A, rows of B
 };
 
+constexpr int NST = 5;                   // stages in LDS, 32 KB each
+
 struct __attribute__((aligned(16))) Stage {
-  uint4 a[BM * 8];
-  uint4 b[BN * 8];
+  uint4 a[BM * 4];
+  uint4 b[BN * 4];
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-// acc += the tile at (m0, b0), b0 a row of B.  All 512 threads call it.
+// acc += the tile at (m0, b0), b0 a row of B.  All 512 threads call it.  The
+// stages are separate LDS objects, so that the compiler can tell the one a
+// transfer fills apart from the ones that are read.
 __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t b0, Stage& st0,
-                                             Stage& st1, v16f (&acc)[RBL][CBL]) {
+                                             Stage& st1, Stage& st2, Stage& st3, Stage& st4,
+                                             v16f (&acc)[RBL][CBL]) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int h = lane >> 5, r32 = lane & 31;
 
-  // Wave w brings rows 32 w .. 32 w + 31 of both operands, 8 rows to a
+  // Wave w brings rows 32 w .. 32 w + 31 of both operands, 16 rows to a
   // transfer.  Rows past the edge repeat the last row (their products reach
   // only outputs that are never stored); pieces past A's width repeat its
   // last piece (the weights there are zeros).
-  int64_t arow[4], boff[4];
-  int apiece[2];
+  int64_t arow[2], boff[2];
+  const int piece = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int r = 32 * wave + 8 * t + (lane >> 3);
-    const int piece = (lane & 7) ^ ((r >> 1) & 7);
-    const int64_t m = m0 + r < p.M ? m0 + r : p.M - 1;
-    const int64_t b = b0 + r < p.rows ? b0 + r : p.rows - 1;
-    arow[t] = m * p.width;
-    boff[t] = b * p.ldb + 8 * piece;
-    if (t < 2) apiece[t] = 8 * piece;
+  for (int t = 0; t < 2; ++t) {
+    const int r = 32 * wave + 16 * t + (lane >> 2);
+    arow[t] = (m0 + r < p.M ? m0 + r : p.M - 1) * p.width;
+    boff[t] = (b0 + r < p.rows ? b0 + r : p.rows - 1) * p.ldb + piece;
   }
-  const int total = p.chunks * p.segments;
-  auto dma = [&](int c, Stage& st) __attribute__((always_inline)) {
-    const bool second = c >= p.chunks;
+  const int seg = 2 * p.chunks, total = seg * p.segments;
+  // transfer t of stage s: 0, 1 of A, 2, 3 of B
+  const uint16_t* asrc;
+  int64_t bcol;
+  auto dma_at = [&](int s) __attribute__((always_inline)) {
+    s = min(s, total - 1);
+    const bool second = s >= seg;
     const uint16_t* const A = second ? p.A[1] : p.A[0];
-    const int64_t col = 64 * int64_t(second ? c - p.chunks : c);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t k = min(col + apiece[t & 1], p.width - 8);
-      __builtin_amdgcn_global_load_lds(A + arow[t] + k, (lds_ptr_t)&st.a[(32 * wave + 8 * t) * 8],
-                                       16, 0, 0);
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      __builtin_amdgcn_global_load_lds(p.B + boff[t] + 64 * int64_t(c),
-                                       (lds_ptr_t)&st.b[(32 * wave + 8 * t) * 8], 16, 0, 0);
+    asrc = A + min(32 * int64_t(second ? s - seg : s) + piece, p.width - 8);
+    bcol = 32 * int64_t(s);
+  };
+  auto dma = [&](int t, Stage& st) __attribute__((always_inline)) {
+    if (t < 2)
+      __builtin_amdgcn_global_load_lds(asrc + arow[t & 1],
+                                       (lds_ptr_t)&st.a[(32 * wave + 16 * (t & 1)) * 4], 16, 0, 0);
+    else
+      __builtin_amdgcn_global_load_lds(p.B + boff[t & 1] + bcol,
+                                       (lds_ptr_t)&st.b[(32 * wave + 16 * (t & 1)) * 4], 16, 0, 0);
   };
 
-  const int sw = h ^ ((r32 >> 1) & 7);
-  const int abase = (wm * WM + r32) * 8, bbase = (wn * WN + r32) * 8;
-  auto compute = [&](const Stage& st) __attribute__((always_inline)) {
-    v8bf fa[2][RBL], fb[2][CBL];
-    auto frags = [&](int ks, v8bf (&a)[RBL], v8bf (&b)[CBL]) __attribute__((always_inline)) {
-      const int slot = sw ^ (2 * ks);
+  const int sw = h ^ ((r32 >> 2) & 3);
+  const int abase = (wm * WM + r32) * 4, bbase = (wn * WN + r32) * 4;
+  v8bf fa[2][RBL], fb[2][CBL];
+  // fragment n of half ks, in the order in which the MFMAs need them
+  auto frag = [&](const Stage& st, int ks, int n) __attribute__((always_inline)) {
+    const int slot = sw ^ (2 * ks);
+    if (n == 0 || n == 2)
+      fb[ks][n / 2] = __builtin_bit_cast(v8bf, st.b[bbase + 64 * n + slot]);
+    else
+      fa[ks][n == 1 ? 0 : n - 2] =
+          __builtin_bit_cast(v8bf, st.a[abase + 128 * (n == 1 ? 0 : n - 2) + slot]);
+  };
+  auto mfma = [&](int ks, int n) __attribute__((always_inline)) {
+    const int i = n / CBL, j = n % CBL;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks][i], fb[ks][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // One stage.  Its first half's fragments are in registers (or on their way).
+  // LDS reads and transfers go out one at a time between MFMAs: issued in a row
+  // they would hold the matrix core up, since the eight waves queue for LDS
+  // together.  After the first half every wave waits for its own transfers of
+  // the next stage (the NST - 2 stages after that may stay in flight) and for
+  // its LDS reads; past the barrier the next stage is complete, this one's
+  // buffer is free and is filled again, and the next stage's first fragments are
+  // read.  Past the last stage the transfers repeat it.
+  auto step = [&](int s, Stage& cur, Stage& nxt) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < CBL; ++j)
-        b[j] = __builtin_bit_cast(v8bf, st.b[bbase + 256 * j + slot]);
-#pragma unroll
-      for (int i = 0; i < RBL; ++i)
-        a[i] = __builtin_bit_cast(v8bf, st.a[abase + 256 * i + slot]);
-    };
-    frags(0, fa[0], fb[0]);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks < 3) frags(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
-      // keeps the next substep's fragment reads ahead of this substep's MFMAs
+    for (int n = 0; n < 8; ++n) {
+      mfma(0, n);
+      if (n < 6) frag(cur, 1, n);
+      if (n == 6) dma_at(s + NST);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070 | (4 * (NST - 2)));   // vmcnt(4 (NST - 2)) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
 #pragma unroll
-      for (int i = 0; i < RBL; ++i)
-#pragma unroll
-        for (int j = 0; j < CBL; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j],
-                                                              acc[i][j], 0, 0, 0);
+    for (int n = 0; n < 8; ++n) {
+      mfma(1, n);
+      if (n < 6) frag(nxt, 0, n);
+      if (n & 1) dma(n / 2, cur);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // one step: the chunk's data have landed (every wave waits for its own
-  // transfers, then the barrier), the other buffer is free, its transfers go
-  // out and the chunk is computed.  Past the last chunk the transfers repeat
-  // it into a buffer nobody reads.
-  auto step = [&](int c, Stage& cur, Stage& nxt) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0x0070);     // vmcnt(0) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    dma(min(c + 1, total - 1), nxt);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(cur);
+  static_assert(NST == 5, "the unrolled ring");
+  auto fill = [&](int s, Stage& st) __attribute__((always_inline)) {
+    dma_at(s);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) dma(t, st);
   };
-  dma(0, st0);
-  int c = 0;
-  for (; c + 2 <= total; c += 2) {
-    step(c, st0, st1);
-    step(c + 1, st1, st0);
+  fill(0, st0);
+  fill(1, st1);
+  fill(2, st2);
+  fill(3, st3);
+  fill(4, st4);
+  // vmcnt(4 (NST - 1)): its low four bits and, at bit 14, its high two
+  __builtin_amdgcn_s_waitcnt(0x0F70 | ((4 * (NST - 1)) & 15) | ((4 * (NST - 1)) >> 4 << 14));
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int n = 0; n < 6; ++n) frag(st0, 0, n);
+  int s = 0;
+  for (; s + NST <= total; s += NST) {
+    step(s, st0, st1);
+    step(s + 1, st1, st2);
+    step(s + 2, st2, st3);
+    step(s + 3, st3, st4);
+    step(s + 4, st4, st0);
   }
-  if (c < total) step(c, st0, st1);
+  if (s < total) step(s, st0, st1);
+  if (s + 1 < total) step(s + 1, st1, st2);
+  if (s + 2 < total) step(s + 2, st2, st3);
+  if (s + 3 < total) step(s + 3, st3, st4);
   // the repeated last transfers, before the buffers are used for anything else
   __builtin_amdgcn_s_waitcnt(0x0070);
   __syncthreads();
