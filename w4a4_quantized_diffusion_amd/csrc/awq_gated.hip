@@ -292,8 +292,8 @@ struct PairWeights {
   const uint16_t *s, *z;
   int64_t nr;
   int N, row, half;
-  uint4 c;
-  float fs, fz;
+  uint4 c[2];
+  uint16_t cs[2], cz[2];
 
   __device__ __forceinline__ PairWeights(const svdq::AwqWeight& g, const svdq::AwqWeight& u, int N,
                                          int64_t n0)
@@ -307,15 +307,18 @@ struct PairWeights {
   static __device__ __forceinline__ int slot(int row, int piece) {
     return row * 8 + (piece ^ ((row >> 1) & 7));
   }
+  template <int set>
   __device__ __forceinline__ void fetch(int chunk) {
     const int64_t at = int64_t(chunk) * N + nr;
-    c = *reinterpret_cast<const uint4*>(q + at * 32 + 16 * half);
-    fs = bf16_to_f32(s[at]);
-    fz = -bf16_to_f32(z[at]) * fs;
+    c[set] = *reinterpret_cast<const uint4*>(q + at * 32 + 16 * half);
+    cs[set] = s[at];
+    cz[set] = z[at];
   }
-  __device__ __forceinline__ void put(uint4* b, int i) {
-    const uint32_t w = i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
-    b[slot(row, 4 * half + i)] = dequant8(w, fs, fz);
+  template <int set, int i>
+  __device__ __forceinline__ void put(uint4* b) {
+    const uint32_t w = i == 0 ? c[set].x : i == 1 ? c[set].y : i == 2 ? c[set].z : c[set].w;
+    const float f = bf16_to_f32(cs[set]);
+    b[slot(row, 4 * half + i)] = dequant8(w, f, -bf16_to_f32(cz[set]) * f);
   }
 };
 
@@ -325,7 +328,8 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void gated_mid_kernel(
     const uint16_t* __restrict__ bg, const uint16_t* __restrict__ bu, void* __restrict__ H,
     bool hbf16, uint16_t* __restrict__ Gs, uint16_t* __restrict__ Us, float* __restrict__ part) {
   using namespace svdq_mid;
-  __shared__ Stage st0, st1;
+  __shared__ ChunkA a0, a1, a2;
+  __shared__ ChunkB b0, b1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slice = blockIdx.x / tiles;
@@ -335,9 +339,9 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void gated_mid_kernel(
   zero_acc(acc);
   PairWeights w(wg, wu, N, n0);
   tile_product(p, m0, int(int64_t(slice) * p.chunks / S), int(int64_t(slice + 1) * p.chunks / S), w,
-               st0, st1, acc);
+               a0, a1, a2, b0, b1, acc);
   const int64_t row0 = m0 + (wave >> 1) * 64, col0 = n0 + (wave & 1) * 32;
-  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * 36);
+  float* const eb = reinterpret_cast<float*>(wave < 3 ? &a0 : &a1) + (wave % 3) * (32 * 36);
   if (S == 1) {
     gated_epilogue<ACT>(acc, eb, lane, row0, col0, p.M, N, bg, bu, H, hbf16, Gs, Us);
     return;

@@ -358,13 +358,17 @@ __global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Arg
 // A thread takes 4 rows n and 8 k of each, and writes 8 pieces of 4 n.  The
 // swizzle has two more bits of the row than A's, so that the 8 k (rows 8 j + i)
 // of 8 neighbouring threads fall into 8 different slots.
+typedef float v8f __attribute__((ext_vector_type(8)));
+
 struct GradWeights {
   svdq::AwqWeight wa, wb;
   int64_t gN;
   int N, chunks, j, quad, kr;
-  uint32_t c[4];
-  uint2 s2, z2;
-  bool live;
+  uint32_t c[2][4];
+  uint2 s2[2], z2[2];
+  bool live[2];
+  v8f even;
+  v8i o0, o1;               // rows 0, 1 and rows 2, 3
 
   __device__ __forceinline__ GradWeights(const svdq::AwqWeight& a, const svdq::AwqWeight& b, int K,
                                          int N, int chunks, int64_t k0)
@@ -378,32 +382,39 @@ struct GradWeights {
   static __device__ __forceinline__ int slot(int row, int piece) {
     return row * 8 + (piece ^ (((row >> 1) ^ (row >> 4)) & 7));
   }
+  template <int set>
   __device__ __forceinline__ void fetch(int chunk) {
     const bool second = chunk >= chunks;
-    const svdq::AwqWeight& w = second ? wb : wa;
+    const uint8_t* const wq = second ? wb.q : wa.q;
+    const uint16_t* const ws = second ? wb.s : wa.s;
+    const uint16_t* const wz = second ? wb.z : wa.z;
     const int64_t n = 64 * int64_t(second ? chunk - chunks : chunk) + 4 * quad;
-    live = n < N;
+    live[set] = n < N;
     const int64_t at = gN + min(n, int64_t(N) - 4);
-    s2 = *reinterpret_cast<const uint2*>(w.s + at);
-    z2 = *reinterpret_cast<const uint2*>(w.z + at);
+    s2[set] = *reinterpret_cast<const uint2*>(ws + at);
+    z2[set] = *reinterpret_cast<const uint2*>(wz + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      c[i] = *reinterpret_cast<const uint32_t*>(w.q + (at + i) * 32 + 4 * j);
+      c[set][i] = *reinterpret_cast<const uint32_t*>(wq + (at + i) * 32 + 4 * j);
   }
-  // (quarter 3 alone: the four rows are needed together)
-  __device__ __forceinline__ void put(uint4* b, int q) {
-    if (q != 3) return;
-    float v[4][8];
+  // one row per quarter, packed in pairs; the last writes all four
+  template <int set, int q>
+  __device__ __forceinline__ void put(uint4* b) {
+    const uint32_t sw = q < 2 ? s2[set].x : s2[set].y, zw = q < 2 ? z2[set].x : z2[set].y;
+    const float f = __uint_as_float(!live[set] ? 0u : q & 1 ? sw & 0xFFFF0000u : sw << 16);
+    float r[8];
+    dequant8_f32(c[set][q], f, -__uint_as_float(q & 1 ? zw & 0xFFFF0000u : zw << 16) * f, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t sw = i < 2 ? s2.x : s2.y, zw = i < 2 ? z2.x : z2.y;
-      const float f = __uint_as_float(!live ? 0u : i & 1 ? sw & 0xFFFF0000u : sw << 16);
-      dequant8_f32(c[i], f, -__uint_as_float(i & 1 ? zw & 0xFFFF0000u : zw << 16) * f, v[i]);
+    for (int t = 0; t < 8; ++t) {
+      if constexpr (q == 1) o0[t] = int(pack_bf16x2(even[t], r[t]));
+      if constexpr (q == 3) o1[t] = int(pack_bf16x2(even[t], r[t]));
+      if constexpr (!(q & 1)) even[t] = r[t];
     }
+    if constexpr (q == 3)
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-      reinterpret_cast<uint2*>(b + slot(kr + t, quad >> 1))[quad & 1] =
-          make_uint2(pack_bf16x2(v[0][t], v[1][t]), pack_bf16x2(v[2][t], v[3][t]));
+      for (int t = 0; t < 8; ++t)
+        reinterpret_cast<uint2*>(b + slot(kr + t, quad >> 1))[quad & 1] =
+            make_uint2(uint32_t(o0[t]), uint32_t(o1[t]));
   }
 };
 
@@ -411,7 +422,8 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
     svdq_mid::Args p, svdq::AwqWeight wa, svdq::AwqWeight wb, int K, int N, int S, int tiles,
     void* __restrict__ dX, bool xbf16, float* __restrict__ part) {
   using namespace svdq_mid;
-  __shared__ Stage st0, st1;
+  __shared__ ChunkA a0, a1, a2;
+  __shared__ ChunkB b0, b1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slice = blockIdx.x / tiles;
@@ -421,9 +433,12 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
   zero_acc(acc);
   GradWeights w(wa, wb, K, N, p.chunks, k0);
   const int64_t total = int64_t(p.chunks) * p.segments;
-  tile_product(p, m0, int(slice * total / S), int((slice + 1) * total / S), w, st0, st1, acc);
+  tile_product(p, m0, int(slice * total / S), int((slice + 1) * total / S), w, a0, a1, a2, b0, b1, acc);
   const int64_t row0 = m0 + (wave >> 1) * 64, col0 = k0 + (wave & 1) * 64;
-  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * 68);
+  float* const eb = reinterpret_cast<float*>(wave == 0   ? &a0.v
+                                              : wave == 1 ? &a1.v
+                                              : wave == 2 ? &a2.v
+                                                          : &b0.v);
   const float none[CBL] = {0.f, 0.f};
   if (S > 1)
     store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, K,

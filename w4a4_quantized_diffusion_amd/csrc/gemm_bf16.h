@@ -20,6 +20,8 @@
 
 #include "w4a16.h"
 
+#include <type_traits>
+
 namespace svdq_gemm {
 
 using namespace svdq_dev;
@@ -203,9 +205,12 @@ struct Args {
   int M;
 };
 
-struct __attribute__((aligned(16))) Stage {
-  uint4 a[BM * 8];
-  uint4 b[BN * 8];
+// 80 KB: A's chunks in a ring of three, the weights' in two
+struct __attribute__((aligned(16))) ChunkA {
+  uint4 v[BM * 8];
+};
+struct __attribute__((aligned(16))) ChunkB {
+  uint4 v[BN * 8];
 };
 
 // slices of the reduction for a number of tiles
@@ -214,12 +219,19 @@ inline int slices(int64_t tiles, int64_t chunks) {
                                 std::max<int64_t>(1, chunks / 4)}));
 }
 
-// Weights: fetch(chunk) loads this thread's share of a chunk's B rows into
-// registers, put(stage, q) writes quarter q of it to LDS, slot(row, piece) is
-// where piece `piece` of B row `row` lies.
+// Weights: fetch<set>(chunk) loads this thread's share of a chunk's B rows into
+// one of two register sets, put<set, q>(b) dequantizes quarter q of it and (at
+// the latest in quarter 3) writes it to LDS, slot(row, piece) is where piece
+// `piece` of B row `row` lies.
+using I0 = std::integral_constant<int, 0>;
+using I1 = std::integral_constant<int, 1>;
+using I2 = std::integral_constant<int, 2>;
+using I3 = std::integral_constant<int, 3>;
+
 template <class Weights>
 __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, int c1, Weights& w,
-                                             Stage& st0, Stage& st1, v16f (&acc)[RBL][CBL]) {
+                                             ChunkA& a0, ChunkA& a1, ChunkA& a2, ChunkB& b0,
+                                             ChunkB& b1, v16f (&acc)[RBL][CBL]) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -234,60 +246,87 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, 
     arow[t] = (m0 + r < p.M ? m0 + r : p.M - 1) * p.width;
     if (t < 2) apiece[t] = 8 * ((lane & 7) ^ ((r >> 1) & 7));
   }
-  auto dma = [&](int c, Stage& st) __attribute__((always_inline)) {
+  auto dma = [&](int c, ChunkA& st) __attribute__((always_inline)) {
+    c = min(c, c1 - 1);
     const bool second = c >= p.chunks;
     const uint16_t* const A = second ? p.A[1] : p.A[0];
     const int64_t col = 64 * int64_t(second ? c - p.chunks : c);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t k = min(col + apiece[t & 1], p.width - 8);
-      __builtin_amdgcn_global_load_lds(A + arow[t] + k, (lds_ptr_t)&st.a[(32 * wave + 8 * t) * 8],
+      __builtin_amdgcn_global_load_lds(A + arow[t] + k, (lds_ptr_t)&st.v[(32 * wave + 8 * t) * 8],
                                        16, 0, 0);
     }
   };
   const int sw = (r32 >> 1) & 7;
   const int abase = (wm * 64 + r32) * 8;
-  auto step = [&](int c, Stage& cur, Stage& nxt) __attribute__((always_inline)) {
-    // this wave's transfers and LDS writes of chunk c have landed, then everyone's
-    __builtin_amdgcn_s_waitcnt(0x0070);     // vmcnt(0) lgkmcnt(0)
-    __syncthreads();
-    const bool more = c + 1 < c1;
-    if (more) dma(c + 1, nxt);
+  // One chunk: every wave waits for its transfers of it (the four of the next
+  // chunk may stay in flight, nothing is issued after them) and for its LDS
+  // writes; past the barrier the chunk is complete and the buffers of the one
+  // before are free.  The loads two chunks ahead go out, then the MFMAs with
+  // the LDS reads, the next chunk's dequantization and its LDS writes between
+  // them.  Past the last chunk the loads repeat it.
+  auto step = [&](int c, auto SET, const ChunkA& ac, ChunkA& an, const ChunkB& bc, ChunkB& bn)
+      __attribute__((always_inline)) {
+    constexpr int set = decltype(SET)::value;
+    __builtin_amdgcn_s_waitcnt(0x0070 | 4);     // vmcnt(4) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    w.template fetch<set>(min(c + 2, c1 - 1));
+    dma(c + 2, an);
+    __builtin_amdgcn_sched_barrier(0);
     v8bf fa[2][RBL], fb[2][CBL];
-    auto frags = [&](int ks, v8bf (&a)[RBL], v8bf (&b)[CBL]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < CBL; ++j)
-        b[j] = __builtin_bit_cast(v8bf, cur.b[Weights::slot(wn * 64 + 32 * j + r32, 2 * ks + h)]);
-#pragma unroll
-      for (int i = 0; i < RBL; ++i)
-        a[i] = __builtin_bit_cast(v8bf, cur.a[abase + 256 * i + ((2 * ks + h) ^ sw)]);
+    auto frag = [&](int ks, int n) __attribute__((always_inline)) {
+      if (n < 2)
+        fb[ks & 1][n] =
+            __builtin_bit_cast(v8bf, bc.v[Weights::slot(wn * 64 + 32 * n + r32, 2 * ks + h)]);
+      else
+        fa[ks & 1][n - 2] =
+            __builtin_bit_cast(v8bf, ac.v[abase + 256 * (n - 2) + ((2 * ks + h) ^ sw)]);
     };
-    frags(0, fa[0], fb[0]);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks < 3) frags(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int n = 0; n < 4; ++n) frag(0, n);
+    auto quarter = [&](auto KS) __attribute__((always_inline)) {
+      constexpr int ks = decltype(KS)::value;
 #pragma unroll
-      for (int i = 0; i < RBL; ++i)
-#pragma unroll
-        for (int j = 0; j < CBL; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j],
-                                                              acc[i][j], 0, 0, 0);
-      if (more) w.put(nxt.b, ks);
-    }
-    if (c + 2 < c1) w.fetch(c + 2);
+      for (int n = 0; n < 4; ++n) {
+        const int i = n / CBL, j = n % CBL;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j], acc[i][j],
+                                                            0, 0, 0);
+        if (ks < 3) frag(ks + 1, n);
+        if (n == 1) w.template put<(set ^ 1), ks>(bn.v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    quarter(I0{});
+    quarter(I1{});
+    quarter(I2{});
+    quarter(I3{});
   };
-  w.fetch(c0);
-  dma(c0, st0);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) w.put(st0.b, q);
-  if (c0 + 1 < c1) w.fetch(c0 + 1);
+  w.template fetch<0>(c0);
+  w.template fetch<1>(min(c0 + 1, c1 - 1));
+  __builtin_amdgcn_sched_barrier(0);
+  dma(c0, a0);
+  dma(c0 + 1, a1);
+  w.template put<0, 0>(b0.v);
+  w.template put<0, 1>(b0.v);
+  w.template put<0, 2>(b0.v);
+  w.template put<0, 3>(b0.v);
   int c = c0;
-  for (; c + 2 <= c1; c += 2) {
-    step(c, st0, st1);
-    step(c + 1, st1, st0);
+  for (; c + 6 <= c1; c += 6) {
+    step(c, I0{}, a0, a2, b0, b1);
+    step(c + 1, I1{}, a1, a0, b1, b0);
+    step(c + 2, I0{}, a2, a1, b0, b1);
+    step(c + 3, I1{}, a0, a2, b1, b0);
+    step(c + 4, I0{}, a1, a0, b0, b1);
+    step(c + 5, I1{}, a2, a1, b1, b0);
   }
-  if (c < c1) step(c, st0, st1);
+  if (c < c1) step(c, I0{}, a0, a2, b0, b1);
+  if (c + 1 < c1) step(c + 1, I1{}, a1, a0, b1, b0);
+  if (c + 2 < c1) step(c + 2, I0{}, a2, a1, b0, b1);
+  if (c + 3 < c1) step(c + 3, I1{}, a0, a2, b1, b0);
+  if (c + 4 < c1) step(c + 4, I0{}, a1, a0, b0, b1);
+  // the repeated last transfers, before the buffers are used for anything else
+  __builtin_amdgcn_s_waitcnt(0x0070);
   __syncthreads();
 }
 
