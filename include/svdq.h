@@ -355,9 +355,9 @@ svdq_status awq_gated_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
 /* Its backward pass for frozen weights and biases, from dH and the G, U that
  * the forward call stored (all bf16 [M, N]):
  *   dU = dH * act(G),  dG = dH * U * act'(G),  dX = dG . wd_gate + dU . wd_up
- * Outputs bf16: dX [M, K]; dG, dU [M, N] (the gradients at both projections'
- * outputs, for adapters and biases), each NULL where not wanted.  dG and dU
- * are rounded to bf16 before the products; those sum in fp32.
+ * Outputs bf16: dX [M, K]; dG, dU [M, N], the gradients at both projections'
+ * outputs (for adapters and biases too).  dG and dU are rounded to bf16 before
+ * the products; those sum in fp32.
  * Sizes as awq_gated_w4a16. */
 size_t awq_gated_w4a16_grad_workspace_bytes(int64_t M, int64_t K, int64_t N);
 svdq_status awq_gated_w4a16_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,

@@ -15,6 +15,8 @@ Tolerances, per element, from the operators' roundings:
   * a bf16 intermediate (dG, dU) adds 2^-8 sum |dG wd| through the product.
 """
 
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -33,6 +35,7 @@ BF, F32 = torch.bfloat16, torch.float32
 
 # ------------------------------------------------------------- references
 
+@functools.lru_cache(maxsize=16)
 def awq_layer(n, k, seed):
     """(device layer, float64 weights bf16((q - z) s) on the device)."""
     g = np.random.default_rng([seed, n, k])
@@ -223,6 +226,46 @@ def test_gated_gradient_against_differences(act):
     # act'' is at most 0.8 in size: a step of 2^-9 |G| in G moves act' by 0.8 2^-9 |G|
     more = (((dh.double() * (xd @ wu.t()) * (xd @ wg.t())).abs()) @ wg.abs()) * d.abs()
     assert abs(num - got) <= float(scale.sum() * 4 * 2.0 ** -8 + more.sum() * 2.0 ** -9)
+
+
+# several rounds of large tiles, with the rows behind the last full round taken
+# by the few-row form (4099) or the smaller tiles (4300, 4396)
+MANY = [(4099, 2048, 4112), (4396, 4096, 2064), (4099, 4096, 1040), (4300, 4096, 1040)]
+
+
+@pytest.mark.parametrize("m,k,n", MANY)
+def test_many_rows(m, k, n):
+    print(f"many rows {m} {k} {n}", flush=True)
+    gate, wg = awq_layer(n, k, 71)
+    up, wu = awq_layer(n, k, 72)
+    x, bg, bu = bf((m, k), 73), bf((n,), 74, 0.3), bf((n,), 75, 0.3)
+    (g, tg), (u, tu), (h, th) = gated_ref(x, wg, wu, bg, bu, "gelu")
+    H, G, U = svdq.awq_gated_w4a16(x, gate, up, "gelu", bg, bu, save=True)
+    check(H, h, th + round_tol(h, BF) + 1e-30, "H")
+    check(G, g, tg + round_tol(g, BF) + 1e-30, "G")
+    check(U, u, tu + round_tol(u, BF) + 1e-30, "U")
+    buf = torch.full((m * n + 512,), float("nan"), device="cuda")
+    H32 = svdq.awq_gated_w4a16(x, gate, up, "gelu", bg, bu, H=buf[256:256 + m * n].view(m, n))
+    check(H32, h, th + round_tol(h, F32) + 1e-30, "H fp32")
+    assert torch.isnan(buf[:256]).all() and torch.isnan(buf[256 + m * n:]).all()
+    dh = bf((m, n), 76)
+    dX, dG, dU = svdq.awq_gated_w4a16_grad(dh, G, U, gate, up, "gelu")
+    hd, gd, ud = dh.double(), G.double(), U.double()
+    a, da = act64(gd, "gelu")
+    check(dG, hd * ud * da, round_tol(hd * ud * da, BF)
+          + 2.0 ** -20 * (hd * ud).abs() * (1 + gd.abs()) + 1e-30, "dG")
+    check(dU, hd * a, round_tol(hd * a, BF) + 2.0 ** -20 * (hd * gd).abs() + 1e-30, "dU")
+    dx = dG.double() @ wg + dU.double() @ wu
+    check(dX, dx, 2 * (grad_tol(dG.double(), wg) + grad_tol(dU.double(), wu)) + round_tol(dx, BF)
+          + 1e-30, "dX")
+    ref = dh.double() @ wg
+    buf = torch.full((m * k + 512,), float("nan"), device="cuda")
+    d32 = svdq.awq_linear_w4a16_grad(dh, gate, dX=buf[256:256 + m * k].view(m, k))
+    check(d32, ref, grad_tol(dh.double(), wg) + round_tol(ref, F32) + 1e-30, "linear dX")
+    assert torch.isnan(buf[:256]).all() and torch.isnan(buf[256 + m * k:]).all()
+    again = svdq.awq_gated_w4a16_grad(dh, G, U, gate, up, "gelu")
+    assert all(torch.equal(p, q) for p, q in zip((dX, dG, dU), again))
+    assert torch.equal(H32, svdq.awq_gated_w4a16(x, gate, up, "gelu", bg, bu, h_dtype=F32))
 
 
 # --------------------------------------------------- SVDQ layer, few rows

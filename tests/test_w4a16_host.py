@@ -98,7 +98,7 @@ def test_a16_rows_and_rank(lib):
 @pytest.mark.parametrize("call,names", [
     (a16, ("X", "smooth", "down", "up", "wcodes", "wscales", "Y")),
     (gated, ("X", "qg", "sg", "zg", "qu", "su", "zu", "H")),
-    (gated_grad, ("dH", "G", "U", "qg", "sg", "zg", "qu", "su", "zu", "dX")),
+    (gated_grad, ("dH", "G", "U", "qg", "sg", "zg", "qu", "su", "zu", "dX", "dG", "dU")),
     (linear_grad, ("dY", "q", "s", "z", "dX"))])
 def test_null_and_misaligned(lib, call, names):
     for n in names:
@@ -132,7 +132,6 @@ def test_workspaces(lib):
                      svdq.awq_gated_w4a16_grad_workspace_bytes(m, k, n),
                      svdq.awq_linear_w4a16_grad_workspace_bytes(m, k, n)):
             assert need % 256 == 0
-        assert m <= 64 or svdq.awq_gated_w4a16_grad_workspace_bytes(m, k, n) >= 4 * m * n
     assert svdq.svdq_linear_w4a16_workspace_bytes(64, 128, 64, 32) % 256 == 0
     assert svdq.svdq_linear_w4a16_workspace_bytes(65, 128, 64, 32) == 0
     for f in (svdq.awq_gated_w4a16_workspace_bytes, svdq.awq_gated_w4a16_grad_workspace_bytes,

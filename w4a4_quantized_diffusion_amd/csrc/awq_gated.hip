@@ -223,20 +223,6 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
   }
 }
 
-template <int MT>
-svdq_status run_rows(const uint16_t* X, int64_t M, int64_t K, int64_t N, svdq::AwqWeight wg,
-                     svdq::AwqWeight wu, float* part, hipStream_t s) {
-  const Split p = split(K, N);
-  // chunks of X that fit LDS, a multiple of D (64 rows: 7 chunks of 128 bytes)
-  const int most = int((LDS_X / M - 16) / 128 / D * D);
-  const int len = int((K / 64 + p.slices - 1) / p.slices);
-  const int sub = std::min(most, (len + D - 1) / D * D);
-  hipLaunchKernelGGL(gated_slice_kernel<MT>, dim3(unsigned(p.blocks * p.slices)), dim3(NT),
-                     size_t(M) * (sub * 128 + 16), s, X, int(M), int(K), int(N), wg, wu, p.slices,
-                     sub, part);
-  return svdq::check_launch("gated_slice");
-}
-
 // ---------------------------------------------------------- many rows
 // The weights are dequantized once into the workspace, 32 rows of Wg and the
 // 32 rows of Wu with the same n alternating, so that one wave's two column
@@ -248,8 +234,8 @@ __global__ __launch_bounds__(256) void pair_dequant_kernel(svdq::AwqWeight wg, s
                                                            int K, int N,
                                                            uint16_t* __restrict__ B) {
   const int row = threadIdx.x >> 2, piece = threadIdx.x & 3;
-  const int g = blockIdx.y;
-  const int64_t n = int64_t(blockIdx.x) * 32 + (row & 31);
+  const int blocks = (N + 31) / 32, g = blockIdx.x / blocks;
+  const int64_t block = blockIdx.x % blocks, n = block * 32 + (row & 31);
   const svdq::AwqWeight w = row >= 32 ? wu : wg;
   uint4 a = make_uint4(0, 0, 0, 0), b = a;
   if (n < N) {
@@ -259,7 +245,7 @@ __global__ __launch_bounds__(256) void pair_dequant_kernel(svdq::AwqWeight wg, s
     a = dequant8(c.x, s, zs);
     b = dequant8(c.y, s, zs);
   }
-  uint4* d = reinterpret_cast<uint4*>(B + (int64_t(blockIdx.x) * 64 + row) * K + 64 * g + 16 * piece);
+  uint4* d = reinterpret_cast<uint4*>(B + (block * 64 + row) * K + 64 * g + 16 * piece);
   d[0] = a;
   d[1] = b;
 }
@@ -357,66 +343,123 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void gated_mid_kernel(
   }
 }
 
-constexpr int64_t WIDE_ROWS = 1024;     // rows from which the weights are dequantized up front
-
+int64_t pair_rows(int64_t N) { return (N + 31) / 32 * 64; }
 int64_t mid_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 63) / 64); }
 
-int64_t pair_rows(int64_t N) { return (N + 31) / 32 * 64; }
+int64_t wide_rows(int64_t M, int64_t K, int64_t N) {
+  if (M <= ROWS) return 0;
+  return svdq_plan::wide_rows(M, {K / 64, (pair_rows(N) + 255) / 256, (N + 63) / 64, 2 * K * N});
+}
+
+size_t pair_bytes(int64_t K, int64_t N) {
+  return svdq::align256(size_t(pair_rows(N)) * size_t(K) * 2);
+}
+
+// bytes of the partial sums of `rows` rows
+size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
+  if (rows == 0) return 0;
+  const int S = rows <= ROWS ? split(K, N).slices : svdq_mid::slices(mid_tiles(rows, N), K / 64);
+  return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * 2 * size_t(rows) * size_t(N) * 4);
+}
+
+// A call's rows [m0, m0 + M)
+struct Call {
+  const uint16_t* X;
+  int64_t M, K, N;
+  svdq::AwqWeight wg, wu;
+  const uint16_t *bg, *bu;
+  bool silu;
+  void* H;
+  bool hbf16;
+  uint16_t *G, *U;
+  hipStream_t s;
+
+  Call rows(int64_t m0, int64_t m) const {
+    Call c = *this;
+    c.X += m0 * K;
+    c.M = m;
+    c.H = static_cast<uint8_t*>(H) + m0 * N * (hbf16 ? 2 : 4);
+    if (G) {
+      c.G += m0 * N;
+      c.U += m0 * N;
+    }
+    return c;
+  }
+};
+
+svdq_status sum(const Call& c, const float* part, int S) {
+  auto k = c.silu ? gated_sum_kernel<SVDQ_SILU> : gated_sum_kernel<SVDQ_GELU>;
+  hipLaunchKernelGGL(k, dim3(unsigned((c.M * c.N / 4 + 63) / 64)), dim3(64), 0, c.s, part, S,
+                     int(c.M), int(c.N), c.bg, c.bu, c.H, c.hbf16, c.G, c.U);
+  return svdq::check_launch("gated_sum");
+}
+
+template <int MT>
+svdq_status slices(const Call& c, float* part) {
+  const Split p = split(c.K, c.N);
+  // chunks of X that fit LDS, a multiple of D (64 rows: 7 chunks of 128 bytes)
+  const int most = int((LDS_X / c.M - 16) / 128 / D * D);
+  const int len = int((c.K / 64 + p.slices - 1) / p.slices);
+  const int sub = std::min(most, (len + D - 1) / D * D);
+  hipLaunchKernelGGL(gated_slice_kernel<MT>, dim3(unsigned(p.blocks * p.slices)), dim3(NT),
+                     size_t(c.M) * (sub * 128 + 16), c.s, c.X, int(c.M), int(c.K), int(c.N), c.wg,
+                     c.wu, p.slices, sub, part);
+  return svdq::check_launch("gated_slice");
+}
+
+svdq_status few(const Call& c, float* part) {
+  switch ((c.M + 15) / 16) {
+    case 1: SVDQ_TRY(slices<1>(c, part)); break;
+    case 2: SVDQ_TRY(slices<2>(c, part)); break;
+    case 3: SVDQ_TRY(slices<3>(c, part)); break;
+    default: SVDQ_TRY(slices<4>(c, part)); break;
+  }
+  return sum(c, part, split(c.K, c.N).slices);
+}
+
+svdq_status mid(const Call& c, float* part) {
+  const int64_t tiles = mid_tiles(c.M, c.N);
+  const int S = svdq_mid::slices(tiles, c.K / 64);
+  svdq_mid::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, int(c.M)};
+  auto k = c.silu ? gated_mid_kernel<SVDQ_SILU> : gated_mid_kernel<SVDQ_GELU>;
+  hipLaunchKernelGGL(k, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, c.s, p, c.wg, c.wu,
+                     int(c.N), S, int(tiles), c.bg, c.bu, c.H, c.hbf16, c.G, c.U, part);
+  SVDQ_TRY(svdq::check_launch("gated_mid"));
+  return S == 1 ? SVDQ_OK : sum(c, part, S);
+}
+
+svdq_status wide(const Call& c, uint16_t* B) {
+  hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((c.N + 31) / 32 * (c.K / 64))), dim3(256), 0,
+                     c.s, c.wg, c.wu, int(c.K), int(c.N), B);
+  SVDQ_TRY(svdq::check_launch("pair_dequant"));
+  const int64_t rows = pair_rows(c.N), tiles = (c.M + 255) / 256 * ((rows + 255) / 256);
+  svdq_gemm::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, B, c.K, int(c.M), int(rows)};
+  auto k = c.silu ? gated_wide_kernel<SVDQ_SILU> : gated_wide_kernel<SVDQ_GELU>;
+  hipLaunchKernelGGL(k, dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, c.s, p, int(c.N), c.bg, c.bu,
+                     c.H, c.hbf16, c.G, c.U);
+  return svdq::check_launch("gated_wide");
+}
 
 }  // namespace
 
 namespace svdq {
 
 size_t awq_gated_workspace(int64_t M, int64_t K, int64_t N) {
-  if (M <= ROWS) return align256(size_t(split(K, N).slices) * 2 * size_t(M) * size_t(N) * 4);
-  if (M < WIDE_ROWS) {
-    const int S = svdq_mid::slices(mid_tiles(M, N), K / 64);
-    return S == 1 ? 0 : align256(size_t(S) * 2 * size_t(M) * size_t(N) * 4);
-  }
-  return align256(size_t(pair_rows(N)) * size_t(K) * 2);
+  const int64_t w = wide_rows(M, K, N);
+  return (w ? pair_bytes(K, N) : 0) + part_bytes(M - w, K, N);
 }
 
 svdq_status launch_awq_gated(const uint16_t* X, int64_t M, int64_t K, int64_t N, AwqWeight wg,
                              AwqWeight wu, const uint16_t* bg, const uint16_t* bu, svdq_act act,
                              void* H, svdq_dtype h_dt, uint16_t* G, uint16_t* U, void* ws,
                              hipStream_t s) {
-  const bool hb = h_dt == SVDQ_BF16;
-  float* const part = static_cast<float*>(ws);
-  auto sum = [&](int S) {
-    auto k = act == SVDQ_SILU ? gated_sum_kernel<SVDQ_SILU> : gated_sum_kernel<SVDQ_GELU>;
-    hipLaunchKernelGGL(k, dim3(unsigned((M * N / 4 + 63) / 64)), dim3(64), 0, s, part, S, int(M),
-                       int(N), bg, bu, H, hb, G, U);
-    return check_launch("gated_sum");
-  };
-  if (M <= ROWS) {
-    switch ((M + 15) / 16) {
-      case 1: SVDQ_TRY(run_rows<1>(X, M, K, N, wg, wu, part, s)); break;
-      case 2: SVDQ_TRY(run_rows<2>(X, M, K, N, wg, wu, part, s)); break;
-      case 3: SVDQ_TRY(run_rows<3>(X, M, K, N, wg, wu, part, s)); break;
-      default: SVDQ_TRY(run_rows<4>(X, M, K, N, wg, wu, part, s)); break;
-    }
-    return sum(split(K, N).slices);
-  }
-  if (M >= WIDE_ROWS) {
-    uint16_t* const B = static_cast<uint16_t*>(ws);
-    hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((N + 31) / 32), unsigned(K / 64)),
-                       dim3(256), 0, s, wg, wu, int(K), int(N), B);
-    SVDQ_TRY(check_launch("pair_dequant"));
-    svdq_gemm::Args p{{X, X}, K, int(K / 64), 1, B, K, int(M), int(pair_rows(N))};
-    const int64_t tiles = ((M + 255) / 256) * ((pair_rows(N) + 255) / 256);
-    auto k = act == SVDQ_SILU ? gated_wide_kernel<SVDQ_SILU> : gated_wide_kernel<SVDQ_GELU>;
-    hipLaunchKernelGGL(k, dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, s, p, int(N), bg, bu, H, hb,
-                       G, U);
-    return check_launch("awq_gated (wide)");
-  }
-  const int64_t tiles = mid_tiles(M, N);
-  const int S = svdq_mid::slices(tiles, K / 64);
-  svdq_mid::Args p{{X, X}, K, int(K / 64), 1, int(M)};
-  auto k = act == SVDQ_SILU ? gated_mid_kernel<SVDQ_SILU> : gated_mid_kernel<SVDQ_GELU>;
-  hipLaunchKernelGGL(k, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, s, p, wg, wu, int(N), S,
-                     int(tiles), bg, bu, H, hb, G, U, part);
-  SVDQ_TRY(check_launch("awq_gated (mid)"));
-  return S == 1 ? SVDQ_OK : sum(S);
+  const Call c{X, M, K, N, wg, wu, bg, bu, act == SVDQ_SILU, H, h_dt == SVDQ_BF16, G, U, s};
+  const int64_t w = wide_rows(M, K, N), rest = M - w;
+  uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  if (w) SVDQ_TRY(wide(c.rows(0, w), reinterpret_cast<uint16_t*>(w8)));
+  if (!rest) return SVDQ_OK;
+  float* const part = reinterpret_cast<float*>(w8 + (w ? pair_bytes(K, N) : 0));
+  return rest <= ROWS ? few(c.rows(w, rest), part) : mid(c.rows(w, rest), part);
 }
 
 }  // namespace svdq

@@ -186,7 +186,7 @@ __global__ __launch_bounds__(NT, 2) void grad_slice_kernel(Rows in, svdq::AwqWei
           const uint4 U = *reinterpret_cast<const uint4*>(in.U + at);
           v = pair_grad8<ACT>(v, G, U, layer);
           uint16_t* const out = layer ? in.dU : in.dG;
-          if (block == 0 && out) *reinterpret_cast<uint4*>(out + at) = v;
+          if (block == 0) *reinterpret_cast<uint4*>(out + at) = v;
         }
       }
       *reinterpret_cast<uint4*>(lds + m * rowb + 16 * o) = v;
@@ -319,8 +319,8 @@ __global__ __launch_bounds__(256) void transpose_dequant_kernel(svdq::AwqWeight 
                                                                 uint16_t* __restrict__ B) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int o = lane & 7, j = lane >> 3;
-  const int64_t n0 = int64_t(blockIdx.x) * 256 + 64 * wave;
-  const int g = blockIdx.y;
+  const int blocks = ((N + 63) / 64 + 3) / 4, g = blockIdx.x / blocks;
+  const int64_t n0 = int64_t(blockIdx.x % blocks) * 256 + 64 * wave;
   if (n0 >= (int64_t(N) + 63) / 64 * 64) return;
   const int64_t n = n0 + 8 * o;
   uint4 out[8];
@@ -466,24 +466,32 @@ svdq_status launch_mid(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWe
   return S == 1 ? SVDQ_OK : launch_sum(part, S, M, K, dX, xbf16, s);
 }
 
-constexpr int64_t WIDE_ROWS = 1024;     // rows from which the weights are dequantized up front
-
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// of a call with more than ROWS rows
-size_t wide_bytes(int64_t M, int64_t K, int64_t N, int layers) {
-  if (M >= WIDE_ROWS) return svdq::align256(size_t(K) * size_t(pad64(N)) * 2 * layers);
-  const int S = mid_slices(M, K, N, layers);
-  return S == 1 ? 0 : svdq::align256(size_t(S) * size_t(M) * size_t(K) * 4);
+int64_t wide_rows(int64_t M, int64_t K, int64_t N, int layers) {
+  if (M <= ROWS) return 0;
+  return svdq_plan::wide_rows(
+      M, {pad64(N) / 64 * layers, (K + 255) / 256, (K + 127) / 128, layers * K * N});
 }
 
-// dX = A0 wd0 [+ A1 wd1] for M >= WIDE_ROWS, B the workspace
+size_t transposed_bytes(int64_t K, int64_t N, int layers) {
+  return svdq::align256(size_t(K) * size_t(pad64(N)) * 2 * layers);
+}
+
+// bytes of the partial sums of `rows` rows
+size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers) {
+  if (rows == 0) return 0;
+  const int S = rows <= ROWS ? split(rows, K, N, layers).slices : mid_slices(rows, K, N, layers);
+  return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(K) * 4);
+}
+
+// dX = A0 wd0 [+ A1 wd1], B the workspace
 svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWeight* w,
                         int layers, int64_t M, int64_t K, int64_t N, void* dX, bool xbf16,
                         uint16_t* B, hipStream_t s) {
   const int64_t np = pad64(N), ldb = np * layers;
   for (int i = 0; i < layers; ++i) {
-    hipLaunchKernelGGL(transpose_dequant_kernel, dim3(unsigned((np + 255) / 256), unsigned(K / 64)),
+    hipLaunchKernelGGL(transpose_dequant_kernel, dim3(unsigned((np + 255) / 256 * (K / 64))),
                        dim3(256), 0, s, w[i], int(N), ldb, B + i * np);
     SVDQ_TRY(svdq::check_launch("transpose_dequant"));
   }
@@ -491,7 +499,7 @@ svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqW
   const int64_t tiles = ((M + 255) / 256) * ((K + 255) / 256);
   hipLaunchKernelGGL(grad_wide_kernel, dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, s, p, dX,
                      xbf16);
-  return svdq::check_launch("awq_grad (wide)");
+  return svdq::check_launch("grad_wide");
 }
 
 }  // namespace
@@ -499,48 +507,55 @@ svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqW
 namespace svdq {
 
 size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N) {
-  return M <= ROWS ? rows_bytes(M, K, N, 1) : wide_bytes(M, K, N, 1);
+  const int64_t w = wide_rows(M, K, N, 1);
+  return (w ? transposed_bytes(K, N, 1) : 0) + part_bytes(M - w, K, N, 1);
 }
+
 size_t awq_gated_grad_workspace(int64_t M, int64_t K, int64_t N) {
-  if (M <= ROWS) return rows_bytes(M, K, N, 2);
-  return 2 * align256(size_t(M) * size_t(N) * 2) + wide_bytes(M, K, N, 2);
+  const int64_t w = wide_rows(M, K, N, 2);
+  return (w ? transposed_bytes(K, N, 2) : 0) + part_bytes(M - w, K, N, 2);
 }
 
 svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
-                                   AwqWeight w, void* dX, svdq_dtype x_dt, void* ws,
+                                   AwqWeight wt, void* dX, svdq_dtype x_dt, void* ws,
                                    hipStream_t s) {
-  if (M <= ROWS)
-    return run_rows<-1>(Rows{dY, nullptr, nullptr, nullptr, nullptr}, M, K, N, &w, dX,
-                        x_dt == SVDQ_BF16, static_cast<float*>(ws), s);
-  if (M >= WIDE_ROWS)
-    return launch_wide(dY, dY, &w, 1, M, K, N, dX, x_dt == SVDQ_BF16, static_cast<uint16_t*>(ws), s);
-  return launch_mid(dY, dY, &w, 1, M, K, N, dX, x_dt == SVDQ_BF16, static_cast<float*>(ws), s);
+  const int64_t w = wide_rows(M, K, N, 1), rest = M - w;
+  const bool xb = x_dt == SVDQ_BF16;
+  uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  if (w) SVDQ_TRY(launch_wide(dY, dY, &wt, 1, w, K, N, dX, xb, reinterpret_cast<uint16_t*>(w8), s));
+  if (!rest) return SVDQ_OK;
+  float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 1) : 0));
+  const uint16_t* const d = dY + w * N;
+  void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
+  if (rest <= ROWS)
+    return run_rows<-1>(Rows{d, nullptr, nullptr, nullptr, nullptr}, rest, K, N, &wt, x, xb, part, s);
+  return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, s);
 }
 
 svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
                                   int64_t M, int64_t K, int64_t N, AwqWeight wg, AwqWeight wu,
                                   svdq_act act, uint16_t* dX, uint16_t* dG, uint16_t* dU, void* ws,
                                   hipStream_t s) {
-  if (M <= ROWS) {
-    const Rows in{dH, G, U, dG, dU};
-    const AwqWeight w[2] = {wg, wu};
-    float* const part = static_cast<float*>(ws);
-    return act == SVDQ_SILU ? run_rows<SVDQ_SILU>(in, M, K, N, w, dX, true, part, s)
-                            : run_rows<SVDQ_GELU>(in, M, K, N, w, dX, true, part, s);
-  }
+  const AwqWeight wt[2] = {wg, wu};
+  const int64_t w = wide_rows(M, K, N, 2), rest = M - w, tiled = rest <= ROWS ? w : M;
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
-  if (!dG) dG = reinterpret_cast<uint16_t*>(w8);
-  if (!dU) dU = reinterpret_cast<uint16_t*>(w8 + align256(size_t(M) * size_t(N) * 2));
-  const int64_t n8 = M * N / 8;
+  float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 2) : 0));
+  // few rows form their own dG and dU
+  if (rest && rest <= ROWS) {
+    const Rows in{dH + w * N, G + w * N, U + w * N, dG + w * N, dU + w * N};
+    SVDQ_TRY(act == SVDQ_SILU
+                 ? run_rows<SVDQ_SILU>(in, rest, K, N, wt, dX + w * K, true, part, s)
+                 : run_rows<SVDQ_GELU>(in, rest, K, N, wt, dX + w * K, true, part, s));
+  }
+  if (!tiled) return SVDQ_OK;
+  const int64_t n8 = tiled * N / 8;
   const unsigned blocks = unsigned(std::min<int64_t>((n8 + 255) / 256, 16384));
   auto k = act == SVDQ_SILU ? gate_grad_kernel<SVDQ_SILU> : gate_grad_kernel<SVDQ_GELU>;
   hipLaunchKernelGGL(k, dim3(blocks), dim3(256), 0, s, dH, G, U, n8, dG, dU);
   SVDQ_TRY(check_launch("gate_grad"));
-  const AwqWeight w[2] = {wg, wu};
-  void* const rest = w8 + 2 * align256(size_t(M) * size_t(N) * 2);
-  if (M >= WIDE_ROWS)
-    return launch_wide(dG, dU, w, 2, M, K, N, dX, true, static_cast<uint16_t*>(rest), s);
-  return launch_mid(dG, dU, w, 2, M, K, N, dX, true, static_cast<float*>(rest), s);
+  if (w) SVDQ_TRY(launch_wide(dG, dU, wt, 2, w, K, N, dX, true, reinterpret_cast<uint16_t*>(w8), s));
+  if (rest <= ROWS) return SVDQ_OK;
+  return launch_mid(dG + w * N, dU + w * N, wt, 2, rest, K, N, dX + w * K, true, part, s);
 }
 
 }  // namespace svdq

@@ -331,3 +331,57 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, 
 }
 
 }  // namespace svdq_mid
+
+// Which of the forms takes which rows of a call with more than 64: the first
+// `wide` rows the 256 x 256 tiles on weights dequantized up front, the others
+// (up to 64 of them) the few-row form or the 128 x 128 tiles.  The wide form has
+// the higher rate, but pays the dequantization and whole rounds of 256 tiles (one
+// to a compute unit): 4099 rows to 12288 columns over 4096 are 816 tiles, four
+// rounds and 422 us, or 4096 rows in three rounds and 3 rows apart, 372 us; 1000
+// rows of the gated pair 4096 -> 12288 take 237 us in 128 x 128 tiles and 268 us in
+// 256 x 256.  The times below are what the forms measured, in us: a round of 256
+// wide tiles 1.72 a chunk of 64, a round of 512 tiles of 128 x 128 1.25, the
+// dequantization 5.2 TB/s, sums of slices 4.5 TB/s, few rows their weights at
+// 4.5 TB/s; 3 for a launch.
+namespace svdq_plan {
+
+struct Shape {
+  int64_t chunks;         // of the reduction
+  int64_t wide_n, mid_n;  // tiles across
+  int64_t weights;        // 4-bit weights of the call
+};
+
+inline double few_us(const Shape& p) { return 6 + 0.5625 * double(p.weights) / 4.5e6; }
+
+inline double mid_us(int64_t rows, const Shape& p) {
+  const int64_t tiles = (rows + 127) / 128 * p.mid_n;
+  const int S = svdq_mid::slices(tiles, p.chunks);
+  const double t = 3 + 1.25 * double((tiles * S + 511) / 512) * double(p.chunks) / S;
+  return S == 1 ? t : t + 3 + 8.0 * S * double(rows) * double(p.mid_n) * 128 / 4.5e6;
+}
+
+inline double wide_us(int64_t rows, const Shape& p) {
+  const int64_t tiles = (rows + 255) / 256 * p.wide_n;
+  return 6 + 1.72 * double((tiles + 255) / 256) * double(p.chunks) +
+         2.5625 * double(p.weights) / 5.2e6;
+}
+
+inline double rest_us(int64_t rows, const Shape& p) {
+  return rows == 0 ? 0 : rows <= 64 ? few_us(p) : mid_us(rows, p);
+}
+
+// rows of the wide form: 0, all, or whole tiles that leave the last round out
+inline int64_t wide_rows(int64_t M, const Shape& p) {
+  int64_t best = 0;
+  double t = rest_us(M, p);
+  auto consider = [&](int64_t m) {
+    const double u = wide_us(m, p) + rest_us(M - m, p);
+    if (u < t) t = u, best = m;
+  };
+  consider(M);
+  const int64_t whole = M / 256 * 256;
+  for (int64_t i = 0; i < 32 && whole - 256 * i > 0; ++i) consider(whole - 256 * i);
+  return best;
+}
+
+}  // namespace svdq_plan

@@ -686,8 +686,8 @@ svdq_status awq_gated_w4a16_grad(const uint16_t* dH, const uint16_t* G, const ui
   TRY(check_awq(wg, "_gate"));
   TRY(check_awq(wu, "_up"));
   TRY(check_ptr(dX, "dX"));
-  if (dG) TRY(check_ptr(dG, "dG"));
-  if (dU) TRY(check_ptr(dU, "dU"));
+  TRY(check_ptr(dG, "dG"));
+  TRY(check_ptr(dU, "dU"));
   const size_t need = svdq::awq_gated_grad_workspace(M, K, N);
   TRY(check_workspace(workspace, workspace_bytes, need));
   const size_t m = M, k = K, n = N;
