@@ -73,10 +73,14 @@ struct Split {
   int blocks, slices;
 };
 
-Split split(int64_t K, int64_t N) {
+// About 512 workgroups, two to a compute unit.  Above 16 rows the partial sums
+// are more than the weights, so there are at most 4 slices: 33 rows 2048 -> 5456
+// take 14.2 us in 8 and 13.1 in 4 (one row 4096 -> 12288, 15.7 in 5 and 17.6 in 4).
+Split split(int64_t M, int64_t K, int64_t N) {
   Split p;
   p.blocks = int((N + 16 * WAVES - 1) / (16 * WAVES));
-  p.slices = int(std::min<int64_t>({K / 64, MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+  p.slices = int(std::min<int64_t>(
+      {K / 64, M > 16 ? MAX_SLICES / 2 : MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
   return p;
 }
 
@@ -172,7 +176,10 @@ __global__ __launch_bounds__(NT, 4) void gated_slice_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int m = 16 * mt + 4 * j + e;
-        if (m < M) part[((int64_t(slice) * 2 + t) * M + m) * N + n] = acc[mt][t][e];
+        // (read by the next launch, on any XCD: past this one's L2 at once)
+        if (m < M)
+          __builtin_nontemporal_store(acc[mt][t][e],
+                                      part + ((int64_t(slice) * 2 + t) * M + m) * N + n);
       }
 }
 
@@ -358,7 +365,7 @@ size_t pair_bytes(int64_t K, int64_t N) {
 // bytes of the partial sums of `rows` rows
 size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
   if (rows == 0) return 0;
-  const int S = rows <= ROWS ? split(K, N).slices : svdq_mid::slices(mid_tiles(rows, N), K / 64);
+  const int S = rows <= ROWS ? split(rows, K, N).slices : svdq_mid::slices(mid_tiles(rows, N), K / 64);
   return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * 2 * size_t(rows) * size_t(N) * 4);
 }
 
@@ -396,7 +403,7 @@ svdq_status sum(const Call& c, const float* part, int S) {
 
 template <int MT>
 svdq_status slices(const Call& c, float* part) {
-  const Split p = split(c.K, c.N);
+  const Split p = split(c.M, c.K, c.N);
   // chunks of X that fit LDS, a multiple of D (64 rows: 7 chunks of 128 bytes)
   const int most = int((LDS_X / c.M - 16) / 128 / D * D);
   const int len = int((c.K / 64 + p.slices - 1) / p.slices);
@@ -414,7 +421,7 @@ svdq_status few(const Call& c, float* part) {
     case 3: SVDQ_TRY(slices<3>(c, part)); break;
     default: SVDQ_TRY(slices<4>(c, part)); break;
   }
-  return sum(c, part, split(c.K, c.N).slices);
+  return sum(c, part, split(c.M, c.K, c.N).slices);
 }
 
 svdq_status mid(const Call& c, float* part) {

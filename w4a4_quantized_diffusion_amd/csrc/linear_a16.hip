@@ -319,7 +319,9 @@ __global__ __launch_bounds__(NT, 4) void a16_slice_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int m = 16 * mt + 4 * j + e;
-        if (m < M) part[(int64_t(slice) * M + m) * N + n] = acc[mt][t][e];
+        // (read by the next launch, on any XCD: past this one's L2 at once)
+        if (m < M)
+          __builtin_nontemporal_store(acc[mt][t][e], part + (int64_t(slice) * M + m) * N + n);
       }
   }
 }

@@ -365,6 +365,14 @@ def awq_linear_w4a16(X, layer, bias=None, y_dtype=torch.bfloat16, Y=None):
 # device's current stream, and allocate outputs and workspace there unless
 # given.
 
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same handle without building a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _arg(t, name, shape, dtype, dev):
     """The address of a tensor after checking it against what the call reads
     or writes."""
@@ -390,19 +398,19 @@ def _rows(X, name, width):
 
 
 def _out(Y, name, shape, dtype, X, dev):
-    """(tensor, address) of an output, allocated beside X unless given."""
+    """An output, allocated beside X unless given."""
     if Y is None:
-        Y = torch.empty(shape, dtype=dtype, device=X.device)
-        return Y, Y.data_ptr()
-    return Y, _arg(Y, name, shape, dtype, dev)
+        return X.new_empty(shape, dtype=dtype)
+    _arg(Y, name, shape, dtype, dev)
+    return Y
 
 
 def _ws(workspace, need, X, dev):
-    """(tensor, address, bytes) of a workspace of at least `need` bytes."""
+    """A workspace of at least `need` bytes and its (address, size)."""
     if workspace is None:
         if not need:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = X.new_empty(need, dtype=torch.uint8)
         return workspace, workspace.data_ptr(), need
     return workspace, _arg(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel()
 
@@ -410,10 +418,10 @@ def _ws(workspace, need, X, dev):
 def _run(dev, fn, *args):
     """Call fn(*args, stream) on device `dev` and its current stream."""
     if dev == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(dev))
     if st:
         _check(st)
 
@@ -449,7 +457,7 @@ def svdq_linear_w4a16(X, layer, bias=None, y_dtype=torch.float32, workspace=None
         raise TypeError(f"X must be float32 or bfloat16, got {X.dtype}")
     x = _arg(X, "X", X.shape, X.dtype, dev)
     yt = _out_dtype(Y, y_dtype, "Y")
-    Y, y = _out(Y, "Y", (M, N), yt, X, dev)
+    Y = _out(Y, "Y", (M, N), yt, X, dev)
     b = None
     if bias is not None:
         if bias.dtype not in _DT:
@@ -466,7 +474,7 @@ def svdq_linear_w4a16(X, layer, bias=None, y_dtype=torch.float32, workspace=None
          _arg(layer["wscales"], "wscales", ws_shape, ws_dtype, dev),
          _arg(layer["w_tensor_scale"], "w_tensor_scale", (1,), torch.float32, dev)
          if pr == NVFP4 else None,
-         b, _DT[bias.dtype] if bias is not None else F32, y, _DT[yt], ws, nws)
+         b, _DT[bias.dtype] if bias is not None else F32, Y.data_ptr(), _DT[yt], ws, nws)
     return Y
 
 
@@ -485,16 +493,16 @@ def awq_gated_w4a16(X, gate, up, act="silu", bias_gate=None, bias_up=None, h_dty
     M, dev = _rows(X, "X", K)
     x = _arg(X, "X", X.shape, torch.bfloat16, dev)
     ht = _out_dtype(H, h_dtype, "H")
-    H, h = _out(H, "H", (M, N), ht, X, dev)
+    H = _out(H, "H", (M, N), ht, X, dev)
     G = U = g = u = None
     if save:
-        G, g = _out(None, "G", (M, N), torch.bfloat16, X, dev)
-        U, u = _out(None, "U", (M, N), torch.bfloat16, X, dev)
+        G, U = X.new_empty((M, N)), X.new_empty((M, N))
+        g, u = G.data_ptr(), U.data_ptr()
     keep, ws, nws = _ws(workspace, l.awq_gated_w4a16_workspace_bytes(M, K, N), X, dev)
-    bg, bu = (None if b is None else _arg(b, n, (N,), torch.bfloat16, dev)
-              for b, n in ((bias_gate, "bias_gate"), (bias_up, "bias_up")))
+    bg = None if bias_gate is None else _arg(bias_gate, "bias_gate", (N,), torch.bfloat16, dev)
+    bu = None if bias_up is None else _arg(bias_up, "bias_up", (N,), torch.bfloat16, dev)
     _run(dev, l.awq_gated_w4a16, x, M, K, N, gate["group"], *_awq_args(gate, K, N, dev, "_gate"), bg,
-         *_awq_args(up, K, N, dev, "_up"), bu, _ACT[act], h, _DT[ht], g, u, ws, nws)
+         *_awq_args(up, K, N, dev, "_up"), bu, _ACT[act], H.data_ptr(), _DT[ht], g, u, ws, nws)
     return (H, G, U) if save else H
 
 
@@ -509,14 +517,14 @@ def awq_gated_w4a16_grad(dH, G, U, gate, up, act="silu", workspace=None):
     K, N = gate["K"], gate["N"]
     M, dev = _rows(dH, "dH", N)
     bf = torch.bfloat16
-    d, g, u = (_arg(t, n, (M, N), bf, dev) for t, n in ((dH, "dH"), (G, "G"), (U, "U")))
-    dX, dx = _out(None, "dX", (M, K), bf, dH, dev)
-    dG, dg = _out(None, "dG", (M, N), bf, dH, dev)
-    dU, du = _out(None, "dU", (M, N), bf, dH, dev)
+    d = _arg(dH, "dH", (M, N), bf, dev)
+    g = _arg(G, "G", (M, N), bf, dev)
+    u = _arg(U, "U", (M, N), bf, dev)
+    dX, dG, dU = dH.new_empty((M, K)), dH.new_empty((M, N)), dH.new_empty((M, N))
     keep, ws, nws = _ws(workspace, l.awq_gated_w4a16_grad_workspace_bytes(M, K, N), dH, dev)
     _run(dev, l.awq_gated_w4a16_grad, d, g, u, M, K, N, gate["group"],
          *_awq_args(gate, K, N, dev, "_gate"), *_awq_args(up, K, N, dev, "_up"), _ACT[act],
-         dx, dg, du, ws, nws)
+         dX.data_ptr(), dG.data_ptr(), dU.data_ptr(), ws, nws)
     return dX, dG, dU
 
 
@@ -532,8 +540,8 @@ def awq_linear_w4a16_grad(dY, layer, dx_dtype=torch.bfloat16, workspace=None, dX
     M, dev = _rows(dY, "dY", N)
     d = _arg(dY, "dY", dY.shape, torch.bfloat16, dev)
     xt = _out_dtype(dX, dx_dtype, "dX")
-    dX, dx = _out(dX, "dX", (M, K), xt, dY, dev)
+    dX = _out(dX, "dX", (M, K), xt, dY, dev)
     keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_grad_workspace_bytes(M, K, N), dY, dev)
     _run(dev, l.awq_linear_w4a16_grad, d, M, K, N, layer["group"], *_awq_args(layer, K, N, dev),
-         dx, _DT[xt], ws, nws)
+         dX.data_ptr(), _DT[xt], ws, nws)
     return dX
