@@ -57,11 +57,12 @@ __device__ __forceinline__ void gated_epilogue(v16f (&acc)[R][2], float* eb, int
 }
 
 // ----------------------------------------------------------- few rows
-// Up to 64 rows the time is the weights' way from memory.  A workgroup's 8
-// waves own 16 columns of both weights each, all rows, and one of S slices of
-// K; X's slice is in LDS, the weights stream through registers D chunks ahead.
-// The slices' partial G and U [S][2][M][N] are joined by gated_sum_kernel,
-// which applies bias, activation and product.
+// Up to 64 rows the time is the weights' way from memory, and how many launches
+// follow one another.  Small products take one launch (gated_column_kernel).
+// Larger ones take two: a workgroup's 8 waves own 16 columns of both weights each,
+// all rows, and one of S slices of K; X's slice is in LDS, the weights stream
+// through registers D chunks ahead.  The slices' partial G and U [S][2][M][N] are
+// joined by gated_sum_kernel, which applies bias, activation and product.
 
 constexpr int ROWS = 64;                 // the most rows of this form
 constexpr int WAVES = 8, NT = 64 * WAVES;
@@ -75,7 +76,7 @@ struct Split {
 
 // About 512 workgroups, two to a compute unit.  Above 16 rows the partial sums
 // are more than the weights, so there are at most 4 slices: 33 rows 2048 -> 5456
-// take 14.2 us in 8 and 13.1 in 4 (one row 4096 -> 12288, 15.7 in 5 and 17.6 in 4).
+// took 14.2 us in 8 and 13.1 in 4 (one row 4096 -> 12288, 15.7 in 5 and 17.6 in 4).
 Split split(int64_t M, int64_t K, int64_t N) {
   Split p;
   p.blocks = int((N + 16 * WAVES - 1) / (16 * WAVES));
@@ -83,6 +84,12 @@ Split split(int64_t M, int64_t K, int64_t N) {
       {K / 64, M > 16 ? MAX_SLICES / 2 : MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
   return p;
 }
+
+// Whether few rows take one launch (gated_column_kernel), where every 16 columns
+// read all of X: N / 16 times 2 M K bytes from the L2.  Measured: 20 rows
+// 4096 -> 12288 (M N K = 1.0e9) 22 us either way, one row 13.8 against 16.2, 20
+// rows 1024 -> 2048 4.0 against 7.9, but 64 rows 4096 -> 12288 49 against 34.
+bool one_launch(int64_t M, int64_t K, int64_t N) { return M * N <= (int64_t(1) << 30) / K; }
 
 template <int MT>
 __global__ __launch_bounds__(NT, 4) void gated_slice_kernel(
@@ -181,6 +188,106 @@ __global__ __launch_bounds__(NT, 4) void gated_slice_kernel(
           __builtin_nontemporal_store(acc[mt][t][e],
                                       part + ((int64_t(slice) * 2 + t) * M + m) * N + n);
       }
+}
+
+// One launch: a workgroup owns 16 columns of both weights, its 8
+// waves take the chunks of K in turn, each with its own piece of X, and the
+// sums meet in LDS.
+template <int MT, int ACT>
+__global__ __launch_bounds__(NT, MT == 1 ? 6 : 4) void gated_column_kernel(
+    const uint16_t* __restrict__ X, int M, int K, int N, svdq::AwqWeight wg, svdq::AwqWeight wu,
+    const uint16_t* __restrict__ bg, const uint16_t* __restrict__ bu, void* __restrict__ H,
+    bool hbf16, uint16_t* __restrict__ Gs, uint16_t* __restrict__ Us) {
+  __shared__ v4f red[WAVES][2 * MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane >> 4, r = lane & 15;
+  const int64_t n = int64_t(blockIdx.x) * 16 + r;                   // (N is a multiple of 16)
+  const int G = K / 64, count = (G - wave + WAVES - 1) / WAVES;     // chunks of this wave
+  const uint16_t* xrow[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) xrow[mt] = X + int64_t(min(16 * mt + r, M - 1)) * K + 16 * j;
+  struct Slot {
+    uint2 w[2];
+    uint32_t s[2], z[2];
+    uint4 x[MT][2];
+  } ring[D];
+  // every slot is always loaded (past the last chunk with the last one's
+  // data; a wave without chunks loads chunk 0 and never uses it)
+  auto fetch = [&](int i, Slot& sl) __attribute__((always_inline)) {
+    const int c = count > 0 ? wave + WAVES * min(i, count - 1) : 0;
+    const int64_t at = int64_t(c) * N + n;
+    sl.w[0] = *reinterpret_cast<const uint2*>(wg.q + at * 32 + 8 * j);
+    sl.w[1] = *reinterpret_cast<const uint2*>(wu.q + at * 32 + 8 * j);
+    sl.s[0] = wg.s[at];
+    sl.z[0] = wg.z[at];
+    sl.s[1] = wu.s[at];
+    sl.z[1] = wu.z[at];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint4* const x = reinterpret_cast<const uint4*>(xrow[mt] + 64 * int64_t(c));
+      sl.x[mt][0] = x[0];
+      sl.x[mt][1] = x[1];
+    }
+  };
+  v4f acc[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) acc[mt][t] = v4f{0, 0, 0, 0};
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d, ring[d]);
+  for (int c = 0; c < count; c += D)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      Slot& sl = ring[d];
+      // past the last chunk the scales are zeros
+      const bool live = c + d < count;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float s = live ? __uint_as_float(sl.s[t] << 16) : 0.f;
+        const float zs = -__uint_as_float(sl.z[t] << 16) * s;
+        const v8bf b0 = __builtin_bit_cast(v8bf, dequant8(sl.w[t].x, s, zs));
+        const v8bf b1 = __builtin_bit_cast(v8bf, dequant8(sl.w[t].y, s, zs));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          acc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(v8bf, sl.x[mt][0]), b0, acc[mt][t], 0, 0, 0);
+          acc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(v8bf, sl.x[mt][1]), b1, acc[mt][t], 0, 0, 0);
+        }
+      }
+      fetch(c + d + D, sl);
+    }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) red[wave][2 * mt + t][lane] = acc[mt][t];
+  __syncthreads();
+  if (wave >= MT) return;
+  v4f v[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    v[t] = red[0][2 * wave + t][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v[t] += red[w][2 * wave + t][lane];
+    const uint16_t* const b = t ? bu : bg;
+    if (b) v[t] += bf16_to_f32(b[n]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t m = 16 * wave + 4 * j + e;
+    if (m >= M) continue;
+    const float h = gate_act<ACT>(v[0][e]) * v[1][e];
+    if (hbf16)
+      static_cast<uint16_t*>(H)[m * N + n] = f32_to_bf16(h);
+    else
+      static_cast<float*>(H)[m * N + n] = h;
+    if (Gs) {
+      Gs[m * N + n] = f32_to_bf16(v[0][e]);
+      Us[m * N + n] = f32_to_bf16(v[1][e]);
+    }
+  }
 }
 
 // 4 columns per thread
@@ -364,7 +471,7 @@ size_t pair_bytes(int64_t K, int64_t N) {
 
 // bytes of the partial sums of `rows` rows
 size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
-  if (rows == 0) return 0;
+  if (rows == 0 || (rows <= ROWS && one_launch(rows, K, N))) return 0;
   const int S = rows <= ROWS ? split(rows, K, N).slices : svdq_mid::slices(mid_tiles(rows, N), K / 64);
   return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * 2 * size_t(rows) * size_t(N) * 4);
 }
@@ -414,7 +521,21 @@ svdq_status slices(const Call& c, float* part) {
   return svdq::check_launch("gated_slice");
 }
 
+template <int MT>
+svdq_status columns(const Call& c) {
+  auto k = c.silu ? gated_column_kernel<MT, SVDQ_SILU> : gated_column_kernel<MT, SVDQ_GELU>;
+  hipLaunchKernelGGL(k, dim3(unsigned(c.N / 16)), dim3(NT), 0, c.s, c.X, int(c.M), int(c.K),
+                     int(c.N), c.wg, c.wu, c.bg, c.bu, c.H, c.hbf16, c.G, c.U);
+  return svdq::check_launch("gated_column");
+}
+
 svdq_status few(const Call& c, float* part) {
+  if (one_launch(c.M, c.K, c.N)) switch ((c.M + 15) / 16) {
+      case 1: return columns<1>(c);
+      case 2: return columns<2>(c);
+      case 3: return columns<3>(c);
+      default: return columns<4>(c);
+    }
   switch ((c.M + 15) / 16) {
     case 1: SVDQ_TRY(slices<1>(c, part)); break;
     case 2: SVDQ_TRY(slices<2>(c, part)); break;

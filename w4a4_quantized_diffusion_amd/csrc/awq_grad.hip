@@ -81,22 +81,28 @@ __device__ __forceinline__ void transpose_dequant8(const svdq::AwqWeight& w, int
 // in LDS.  Partial sums [S][M][K] are joined by grad_sum_kernel.
 
 constexpr int ROWS = 64;                 // the most rows of this form
-constexpr int WAVES = 8, NT = 64 * WAVES;
 constexpr int LDS_A = 64 << 10;          // for the rows' operand of 16 rows, twice that above
 constexpr int MAX_SLICES = 16;
+constexpr int ONE_SLICE = 32;            // steps up to which 16 waves take them all
 
 struct Split {
-  int blocks, slices;
+  int blocks, slices, waves;
 };
 
 Split split(int64_t M, int64_t K, int64_t N, int layers) {
   Split p;
   p.blocks = int((K + 127) / 128);
   const int64_t steps = (N + 31) / 32 * layers;
+  p.waves = 8;
+  if (M <= 16 && steps <= ONE_SLICE) {
+    p.waves = 16;
+    p.slices = 1;
+    return p;
+  }
   // one workgroup fits a compute unit, two where the sums of 16 rows are all it holds
   const int most = M <= 16 ? 512 : 256;
-  p.slices = int(std::min<int64_t>({(steps + WAVES - 1) / WAVES, MAX_SLICES,
-                                    std::max<int64_t>(1, most / p.blocks)}));
+  p.slices = int(std::min<int64_t>(
+      {(steps + 7) / 8, MAX_SLICES, std::max<int64_t>(1, most / p.blocks)}));
   return p;
 }
 
@@ -126,11 +132,13 @@ __device__ __forceinline__ uint4 pair_grad8(const uint4 h, const uint4 g, const 
 }
 
 // ACT < 0: one layer
-template <int MT, int ACT>
-__global__ __launch_bounds__(NT, 2) void grad_slice_kernel(Rows in, svdq::AwqWeight wa,
-                                                           svdq::AwqWeight wb, int M, int K, int N,
-                                                           int S, int sub,
-                                                           float* __restrict__ part) {
+template <int MT, int ACT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::AwqWeight wa,
+                                                                svdq::AwqWeight wb, int M, int K,
+                                                                int N, int S, int sub,
+                                                                float* __restrict__ part,
+                                                                void* __restrict__ dX, bool xbf16) {
+  constexpr int NT = 64 * WAVES;
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int LAYERS = ACT < 0 ? 1 : 2;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -230,14 +238,21 @@ __global__ __launch_bounds__(NT, 2) void grad_slice_kernel(Rows in, svdq::AwqWei
 #pragma unroll
     for (int t = 0; t < 8; ++t) red[(t * WAVES + wave) * 64 + lane] = acc[mt][t];
     __syncthreads();
+    if (wave >= 8) continue;
     v4f v = red[wave * WAVES * 64 + lane];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += red[(wave * WAVES + w) * 64 + lane];
     const int64_t k = 128 * int64_t(block) + 64 * (r >> 3) + 8 * (r & 7) + wave;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int m = 16 * mt + 4 * j + e;
-      if (m < M && k < K) part[(int64_t(slice) * M + m) * K + k] = v[e];
+      const int64_t m = 16 * mt + 4 * j + e;
+      if (m >= M || k >= K) continue;
+      if (S > 1)
+        part[(slice * int64_t(M) + m) * K + k] = v[e];
+      else if (xbf16)
+        static_cast<uint16_t*>(dX)[m * K + k] = f32_to_bf16(v[e]);
+      else
+        static_cast<float*>(dX)[m * K + k] = v[e];
     }
   }
 }
@@ -272,39 +287,38 @@ svdq_status launch_sum(const float* part, int S, int64_t M, int64_t K, void* dX,
   return svdq::check_launch("grad_sum");
 }
 
-template <int MT, int ACT>
-svdq_status run_rows_mt(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
-                        float* part, hipStream_t s) {
+template <int MT, int ACT, int WAVES>
+svdq_status run_slices(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
+                       const Split& p, float* part, void* dX, bool xbf16, hipStream_t s) {
   constexpr int layers = ACT < 0 ? 1 : 2;
-  const Split p = split(M, K, N, layers);
   // steps of the rows' operand that fit LDS (64 rows: 31)
   const int64_t steps = (N + 31) / 32 * layers;
   const int64_t room = MT == 1 ? LDS_A : 2 * LDS_A;
   const int sub = int(std::min<int64_t>((room / M - 16) / 64, (steps + p.slices - 1) / p.slices));
   const size_t shm = std::max(size_t(M) * (sub * 64 + 16), size_t(WAVES) * 8 * 1024);
-  auto k = grad_slice_kernel<MT, ACT>;
+  auto k = grad_slice_kernel<MT, ACT, WAVES>;
   if (shm > (64 << 10))
     SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, int(shm)));
-  hipLaunchKernelGGL(k, dim3(unsigned(p.blocks * p.slices)), dim3(NT), shm, s, in, w[0],
-                     w[layers - 1], int(M), int(K), int(N), p.slices, sub, part);
+  hipLaunchKernelGGL(k, dim3(unsigned(p.blocks * p.slices)), dim3(64 * WAVES), shm, s, in, w[0],
+                     w[layers - 1], int(M), int(K), int(N), p.slices, sub, part, dX, xbf16);
   return svdq::check_launch("grad_slice");
 }
 
 template <int ACT>
 svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
                      void* dX, bool xbf16, float* part, hipStream_t s) {
+  const Split p = split(M, K, N, ACT < 0 ? 1 : 2);
   switch ((M + 15) / 16) {
-    case 1: SVDQ_TRY((run_rows_mt<1, ACT>(in, M, K, N, w, part, s))); break;
-    case 2: SVDQ_TRY((run_rows_mt<2, ACT>(in, M, K, N, w, part, s))); break;
-    case 3: SVDQ_TRY((run_rows_mt<3, ACT>(in, M, K, N, w, part, s))); break;
-    default: SVDQ_TRY((run_rows_mt<4, ACT>(in, M, K, N, w, part, s))); break;
+    case 1:
+      SVDQ_TRY(p.waves == 16 ? (run_slices<1, ACT, 16>(in, M, K, N, w, p, part, dX, xbf16, s))
+                             : (run_slices<1, ACT, 8>(in, M, K, N, w, p, part, dX, xbf16, s)));
+      break;
+    case 2: SVDQ_TRY((run_slices<2, ACT, 8>(in, M, K, N, w, p, part, dX, xbf16, s))); break;
+    case 3: SVDQ_TRY((run_slices<3, ACT, 8>(in, M, K, N, w, p, part, dX, xbf16, s))); break;
+    default: SVDQ_TRY((run_slices<4, ACT, 8>(in, M, K, N, w, p, part, dX, xbf16, s))); break;
   }
-  return launch_sum(part, split(M, K, N, ACT < 0 ? 1 : 2).slices, M, K, dX, xbf16, s);
-}
-
-size_t rows_bytes(int64_t M, int64_t K, int64_t N, int layers) {
-  return svdq::align256(size_t(split(M, K, N, layers).slices) * size_t(M) * size_t(K) * 4);
+  return p.slices == 1 ? SVDQ_OK : launch_sum(part, p.slices, M, K, dX, xbf16, s);
 }
 
 // ---------------------------------------------------------- many rows
@@ -482,7 +496,7 @@ size_t transposed_bytes(int64_t K, int64_t N, int layers) {
 size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers) {
   if (rows == 0) return 0;
   const int S = rows <= ROWS ? split(rows, K, N, layers).slices : mid_slices(rows, K, N, layers);
-  return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(K) * 4);
+  return S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(K) * 4);
 }
 
 // dX = A0 wd0 [+ A1 wd1], B the workspace
