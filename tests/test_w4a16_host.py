@@ -119,6 +119,8 @@ def test_null_and_misaligned(lib, call, names):
     (linear_grad, ("dY", "q", "s", "z"), ("dX",))])
 def test_overlap(lib, call, ins, outs):
     base = dict(G=at(20), U=at(21)) if call is gated else {}
+    if "ws" in outs and call is gated_grad:
+        base = dict(M=20, N=1024)               # a size that needs a workspace
     for o in outs:
         for i in ins + tuple(p for p in outs if p != o):
             assert call(lib, **{**base, o: at(30), i: at(30)}) == INVALID, (o, i)
@@ -137,9 +139,13 @@ def test_workspaces(lib):
     for f in (svdq.awq_gated_w4a16_workspace_bytes, svdq.awq_gated_w4a16_grad_workspace_bytes,
               svdq.awq_linear_w4a16_grad_workspace_bytes):
         assert f(4, 100, 64) == 0 and f(4, 128, 40) == 0 and f(-1, 128, 64) == 0
-    need = svdq.awq_gated_w4a16_grad_workspace_bytes(4, 128, 64)
-    assert gated_grad(lib, nws=need - 1) == INVALID and "too small" in svdq.svdq_last_error()
-    assert gated_grad(lib, ws=at(12) + 16) == INVALID and "aligned" in svdq.svdq_last_error()
+    need = svdq.awq_gated_w4a16_grad_workspace_bytes(20, 128, 1024)
+    big = dict(M=20, N=1024)
+    assert need > 0
+    assert gated_grad(lib, **big, nws=need - 1) == INVALID
+    assert "too small" in svdq.svdq_last_error()
+    assert gated_grad(lib, **big, ws=at(12) + 16) == INVALID and "aligned" in svdq.svdq_last_error()
+    assert gated_grad(lib, **big, ws=None) == INVALID and "NULL" in svdq.svdq_last_error()
     need = svdq.svdq_linear_w4a16_workspace_bytes(4, 128, 64, 16)
     assert a16(lib, nws=need - 1) == INVALID and "too small" in svdq.svdq_last_error()
 

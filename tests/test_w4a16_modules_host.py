@@ -1,0 +1,65 @@
+"""Modules of the weight-only operators, without a GPU: the gated module and
+a16_rows survive save_quantized / load_quantized, and what they refuse."""
+
+import pytest
+import torch
+from torch import nn
+
+from w4a4_quantized_diffusion_amd import linear as L
+from w4a4_quantized_diffusion_amd import svdq
+from tests.test_linear_format import _awq_layer, _svdq_layer
+
+
+class Block(nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.mod = nn.Linear(128, 256)
+        self.ff = nn.Sequential(nn.Identity(), nn.Linear(256, 128))
+
+
+@pytest.mark.parametrize("biases", [(), ("gate",), ("gate", "up")])
+def test_save_load_gated(tmp_path, biases):
+    g = torch.Generator().manual_seed(3)
+    q = Block()
+    q.mod = L.SVDQLinear(_svdq_layer(256, 128, 16, svdq.INT4, g), None, a16_rows=9)
+    kw = {f"bias_{b}": torch.randn(256, generator=g) for b in biases}
+    q.ff[0] = L.AWQGatedLinear(_awq_layer(256, 128, g), _awq_layer(256, 128, g), act="gelu", **kw)
+    q.ff[1] = L.AWQLinear(_awq_layer(128, 256, g), None)
+    path = str(tmp_path / "b.safetensors")
+    assert sorted(L.save_quantized(q, path)) == ["ff.0", "ff.1", "mod"]
+    fresh = Block()
+    assert sorted(L.load_quantized(fresh, path)) == ["ff.0", "ff.1", "mod"]
+    for name in ("mod", "ff.0", "ff.1"):
+        a, b = q.get_submodule(name), fresh.get_submodule(name)
+        assert type(a) is type(b) and a.extra_repr() == b.extra_repr()
+        for buf, t in a.named_buffers():
+            assert torch.equal(t, getattr(b, buf)), (name, buf)
+    assert fresh.mod.a16_rows == 9 and fresh.ff[0].act == "gelu"
+    assert (fresh.ff[0].bias_up is None) == ("up" not in biases)
+
+
+def test_refusals():
+    g = torch.Generator().manual_seed(4)
+    lay = _svdq_layer(64, 128, 16, svdq.INT4, g)
+    for rows in (-1, 65):
+        with pytest.raises(ValueError, match="a16_rows"):
+            L.SVDQLinear(lay, a16_rows=rows)
+    with pytest.raises(ValueError, match="gelu_input"):
+        L.SVDQLinear(lay, gelu_input=True, a16_rows=4)
+    a, b = _awq_layer(64, 128, g), _awq_layer(64, 192, g)
+    with pytest.raises(ValueError, match="one shape"):
+        L.AWQGatedLinear(a, b)
+    with pytest.raises(ValueError, match="act must"):
+        L.AWQGatedLinear(a, a, act="relu")
+    bad = dict(a, zeros=a["zeros"].float())
+    with pytest.raises(ValueError, match="up_zeros"):
+        L.AWQGatedLinear(a, bad)
+    m = L.AWQGatedLinear(a, a)
+    with pytest.raises(TypeError, match="bf16"):
+        m(torch.zeros(2, 128))
+    with pytest.raises(ValueError, match="input"):
+        m(torch.zeros(2, 64, dtype=torch.bfloat16))
+    lin = L.AWQLinear(a, torch.zeros(64))
+    lin.bias.requires_grad_()
+    with pytest.raises(RuntimeError, match="frozen"):
+        lin(torch.zeros(2, 128, dtype=torch.bfloat16, requires_grad=True))

@@ -10,7 +10,11 @@ Diffusers", Technical Breakdown and Performance Metrics).  Here:
   SVDQLinear      one quantized layer held as device tensors; forward runs
                   svdq_linear_w4a4 (or its GELU-input form) on the current
                   stream.
-  AWQLinear       one AWQ W4A16 layer; forward runs awq_linear_w4a16.
+  AWQLinear       one AWQ W4A16 layer; forward runs awq_linear_w4a16, the
+                  gradient of its input awq_linear_w4a16_grad.
+  AWQGatedLinear  the gate and up projections of a gated feed-forward block
+                  with the activation and the product; forward runs
+                  awq_gated_w4a16, backward awq_gated_w4a16_grad.
   calibrate       per-input-channel max|x| of every nn.Linear's inputs
                   (svdq_act_absmax), for the smoothing step.
   quantize_linears  swaps every eligible nn.Linear of a module in place.
@@ -27,6 +31,7 @@ import json
 
 import torch
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import svdq
 
@@ -38,6 +43,7 @@ VERSION = 2
 _SVDQ_FIELDS = ("smooth", "lora_down", "lora_up", "wcodes", "wscales", "w_tensor_scale",
                 "x_tensor_scale")
 _AWQ_FIELDS = ("q", "scales", "zeros")
+_GATED_FIELDS = tuple(f"{p}_{f}" for p in ("gate", "up") for f in _AWQ_FIELDS)
 _PREC_NAME = {svdq.INT4: "int4", svdq.NVFP4: "nvfp4"}
 
 
@@ -81,10 +87,19 @@ class SVDQLinear(nn.Module):
     x must be bf16).  Inputs of any leading shape [..., K] in fp32 or bf16;
     the output has x's dtype.  The workspace is kept between calls and
     reused on the calling stream: one module must not run on two streams at
-    once."""
+    once.
 
-    def __init__(self, layer, bias=None, gelu_input=False):
+    Inputs of at most `a16_rows` rows (0 to 64, default 0) run
+    svdq_linear_w4a16 instead: the same layer with x kept in its own precision,
+    for the layers that see a row per image or token."""
+
+    def __init__(self, layer, bias=None, gelu_input=False, a16_rows=0):
         super().__init__()
+        self.a16_rows = int(a16_rows)
+        if not 0 <= self.a16_rows <= 64:
+            raise ValueError("a16_rows must be in [0, 64]")
+        if self.a16_rows and gelu_input:
+            raise ValueError("a16_rows does not go with gelu_input")
         self.in_features, self.out_features = int(layer["K"]), int(layer["N"])
         self.rank, self.prec = int(layer["rank"]), int(svdq._PREC[layer["prec"]])
         self.gelu_input = bool(gelu_input)
@@ -103,13 +118,14 @@ class SVDQLinear(nn.Module):
         self._ws = None
 
     @classmethod
-    def from_linear(cls, linear, act_amax=None, rank=32, prec="int4", gelu_input=False):
+    def from_linear(cls, linear, act_amax=None, rank=32, prec="int4", gelu_input=False,
+                    a16_rows=0):
         """Quantize an nn.Linear on its (HIP) device with the library's
         offline quantizer; act_amax is its inputs' per-channel max|x| (None:
         no smoothing)."""
         w = linear.weight.detach().to(torch.float32).contiguous()
         lay = svdq.svdq_quantize_weights(w, act_amax, rank, prec)
-        return cls(lay, linear.bias, gelu_input)
+        return cls(lay, linear.bias, gelu_input, a16_rows)
 
     def layer(self):
         d = {f: getattr(self, f) for f in _SVDQ_FIELDS}
@@ -130,23 +146,80 @@ class SVDQLinear(nn.Module):
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features).contiguous()
         m = x2.shape[0]
-        need = max(svdq.svdq_workspace_bytes(m, self.in_features, self.rank, self.prec), 256)
+        a16 = 0 < m <= self.a16_rows
+        if a16:
+            need = svdq.svdq_linear_w4a16_workspace_bytes(m, self.in_features, self.out_features,
+                                                          self.rank)
+        else:
+            need = svdq.svdq_workspace_bytes(m, self.in_features, self.rank, self.prec)
+        need = max(need, 256)
         if self._ws is None or self._ws.numel() < need or self._ws.device != x2.device:
             self._ws = torch.empty(need, dtype=torch.uint8, device=x2.device)
-        fn = svdq.svdq_linear_w4a4_gelu if self.gelu_input else svdq.svdq_linear_w4a4
+        fn = (svdq.svdq_linear_w4a16 if a16 else
+              svdq.svdq_linear_w4a4_gelu if self.gelu_input else svdq.svdq_linear_w4a4)
         y = fn(x2, self.layer(), self.bias, y_dtype=x2.dtype, workspace=self._ws)
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"rank={self.rank}, prec={_PREC_NAME[self.prec]}, bias={self.bias is not None}, "
-                f"gelu_input={self.gelu_input}")
+                f"gelu_input={self.gelu_input}"
+                + (f", a16_rows={self.a16_rows}" if self.a16_rows else ""))
+
+
+def _grad_rows(dy, width):
+    """An incoming gradient as a contiguous [M, width] matrix (autograd hands on
+    expanded and strided ones)."""
+    return dy.reshape(-1, width).contiguous()
+
+
+class _AWQLinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, q, scales, zeros, bias, dims):
+        ctx.save_for_backward(q, scales, zeros)
+        ctx.dims = dims
+        return svdq.awq_linear_w4a16(x, dict(dims, q=q, scales=scales, zeros=zeros), bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        q, scales, zeros = ctx.saved_tensors
+        lay = dict(ctx.dims, q=q, scales=scales, zeros=zeros)
+        dx = svdq.awq_linear_w4a16_grad(_grad_rows(dy, lay["N"]), lay)
+        return dx, None, None, None, None, None
+
+
+class _AWQGatedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, act, bias_gate, bias_up, dims, *fields):
+        n = len(_AWQ_FIELDS)
+        gate, up = (dict(dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
+        h, g, u = svdq.awq_gated_w4a16(x, gate, up, act, bias_gate, bias_up, save=True)
+        ctx.save_for_backward(g, u, *fields)
+        ctx.act, ctx.dims = act, dims
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        g, u, *fields = ctx.saved_tensors
+        n = len(_AWQ_FIELDS)
+        gate, up = (dict(ctx.dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
+        dx, _, _ = svdq.awq_gated_w4a16_grad(_grad_rows(dh, ctx.dims["N"]), g, u, gate, up, ctx.act)
+        return (dx,) + (None,) * (4 + 2 * n)
+
+
+def _frozen(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise RuntimeError("the weights and biases of a quantized layer are frozen: "
+                               "they have no gradient")
 
 
 class AWQLinear(nn.Module):
     """An AWQ W4A16 layer (asymmetric INT4 weights in groups of 64, bf16
     activations) in place of nn.Linear(K, N).  Inputs bf16 [..., K]; output
-    bf16."""
+    bf16.  Differentiable once in its input; weights and bias are frozen."""
 
     def __init__(self, layer, bias=None):
         super().__init__()
@@ -178,12 +251,80 @@ class AWQLinear(nn.Module):
         x2 = x.reshape(-1, self.in_features).contiguous()
         lay = dict(q=self.q, scales=self.scales, zeros=self.zeros, N=self.out_features,
                    K=self.in_features, group=self.group)
-        y = svdq.awq_linear_w4a16(x2, lay, self._bias.get(self.bias, torch.bfloat16))
+        bias = self._bias.get(self.bias, torch.bfloat16)
+        if torch.is_grad_enabled() and x2.requires_grad:
+            _frozen(self.bias)
+            fields = [lay.pop(f) for f in _AWQ_FIELDS]
+            y = _AWQLinearFn.apply(x2, *fields, bias, lay)
+        else:
+            y = svdq.awq_linear_w4a16(x2, lay, bias)
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"group={self.group}, bias={self.bias is not None}")
+
+
+class AWQGatedLinear(nn.Module):
+    """The first half of a gated feed-forward block on two AWQ layers of one
+    shape: act(x gate^T + bias_gate) * (x up^T + bias_up), in place of the two
+    nn.Linear(K, N), the activation and the product.  act: "silu" or "gelu"
+    (tanh form).  Inputs bf16 [..., K]; output bf16.  Differentiable once in its
+    input (the forward pass then keeps both pre-activations in bf16); weights and
+    biases are frozen.  An AWQLinear(N, K) behind it completes the block."""
+
+    def __init__(self, gate, up, bias_gate=None, bias_up=None, act="silu"):
+        super().__init__()
+        self.in_features, self.out_features = int(gate["K"]), int(gate["N"])
+        self.group = int(gate["group"])
+        if (up["K"], up["N"], up["group"]) != (gate["K"], gate["N"], gate["group"]):
+            raise ValueError("gate and up must have one shape")
+        if act not in ("silu", "gelu"):
+            raise ValueError(f"act must be 'silu' or 'gelu', got {act!r}")
+        self.act = act
+        shapes = _shapes_awq(self.out_features, self.in_features, self.group)
+        for p, lay in (("gate", gate), ("up", up)):
+            for f in _AWQ_FIELDS:
+                t, (shape, dt) = lay[f], shapes[f]
+                if tuple(t.shape) != shape or t.dtype != dt:
+                    raise ValueError(f"{p}_{f}: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
+                self.register_buffer(f"{p}_{f}", t)
+        for p, b in (("gate", bias_gate), ("up", bias_up)):
+            if b is not None:                    # as awq_gated_w4a16 reads it
+                b = b.detach().to(torch.bfloat16).reshape(self.out_features).contiguous()
+            self.register_buffer(f"bias_{p}", b)
+
+    @classmethod
+    def from_linears(cls, gate, up, act="silu", group=64):
+        """Quantize the block's two nn.Linear on their (HIP) device."""
+        lays = [svdq.awq_quantize_weights(l.weight.detach().to(torch.float32).contiguous(), group)
+                for l in (gate, up)]
+        return cls(*lays, gate.bias, up.bias, act)
+
+    def forward(self, x):
+        if x.dtype != torch.bfloat16:
+            raise TypeError("AWQGatedLinear takes bf16 activations")
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
+        lead = x.shape[:-1]
+        x2 = x.reshape(-1, self.in_features).contiguous()
+        dims = dict(N=self.out_features, K=self.in_features, group=self.group)
+        fields = [getattr(self, f) for f in _GATED_FIELDS]
+        bg, bu = (None if b is None else b.to(torch.bfloat16)
+                  for b in (self.bias_gate, self.bias_up))
+        if torch.is_grad_enabled() and x2.requires_grad:
+            _frozen(self.bias_gate, self.bias_up)
+            h = _AWQGatedFn.apply(x2, self.act, bg, bu, dims, *fields)
+        else:
+            n = len(_AWQ_FIELDS)
+            gate, up = (dict(dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
+            h = svdq.awq_gated_w4a16(x2, gate, up, self.act, bg, bu)
+        return h.reshape(*lead, self.out_features)
+
+    def extra_repr(self):
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"group={self.group}, act={self.act}, "
+                f"bias={(self.bias_gate is not None, self.bias_up is not None)}")
 
 
 # ------------------------------------------------------------ patching shim
@@ -231,11 +372,12 @@ def _set_child(root, name, new):
 
 
 def quantize_linears(module, act_amax=None, rank=32, prec="int4", awq=(), gelu_input=(),
-                     skip=()):
+                     skip=(), a16_rows=0):
     """Swap the nn.Linear modules of `module` in place: names in `awq` become
     AWQLinear, names in `skip` stay, the other eligible ones become
     SVDQLinear (gelu_input for names in `gelu_input`).  act_amax: {name:
     amax} from calibrate (a missing name quantizes without smoothing).
+    a16_rows: SVDQLinear's, for the layers without gelu_input.
     Returns {name: kind}."""
     if rank < 0 or rank > 256 or rank % 16:
         raise ValueError("rank must be a multiple of 16 in [0, 256]")
@@ -251,16 +393,22 @@ def quantize_linears(module, act_amax=None, rank=32, prec="int4", awq=(), gelu_i
             _set_child(module, name, AWQLinear.from_linear(lin))
             done[name] = "awq"
         elif eligible(lin, rank):
+            gelu = name in gelu_input
             _set_child(module, name, SVDQLinear.from_linear(lin, act_amax.get(name), rank, prec,
-                                                            name in gelu_input))
+                                                            gelu, 0 if gelu else a16_rows))
             done[name] = "svdq"
     return done
 
 
 # ------------------------------------------------------------- file format
 
+def _biases(mod, *names):
+    return tuple(n for n in names if getattr(mod, n) is not None)
+
+
 def save_quantized(module, path):
-    """Write every SVDQLinear / AWQLinear of `module` to a safetensors file."""
+    """Write every SVDQLinear / AWQLinear / AWQGatedLinear of `module` to a
+    safetensors file."""
     from safetensors.torch import save_file
     tensors, layers = {}, {}
     for name, mod in module.named_modules():
@@ -268,14 +416,21 @@ def save_quantized(module, path):
             layers[name] = {"kind": "svdq", "prec": _PREC_NAME[mod.prec], "rank": mod.rank,
                             "N": mod.out_features, "K": mod.in_features,
                             "gelu_input": mod.gelu_input, "bias": mod.bias is not None}
-            fields = _SVDQ_FIELDS
+            if mod.a16_rows:
+                layers[name]["a16_rows"] = mod.a16_rows
+            fields = _SVDQ_FIELDS + _biases(mod, "bias")
         elif isinstance(mod, AWQLinear):
             layers[name] = {"kind": "awq", "group": mod.group, "N": mod.out_features,
                             "K": mod.in_features, "bias": mod.bias is not None}
-            fields = _AWQ_FIELDS
+            fields = _AWQ_FIELDS + _biases(mod, "bias")
+        elif isinstance(mod, AWQGatedLinear):
+            biases = _biases(mod, "bias_gate", "bias_up")
+            layers[name] = {"kind": "awq_gated", "group": mod.group, "N": mod.out_features,
+                            "K": mod.in_features, "act": mod.act, "biases": list(biases)}
+            fields = _GATED_FIELDS + biases
         else:
             continue
-        for f in fields + (("bias",) if mod.bias is not None else ()):
+        for f in fields:
             tensors[f"{name}.{f}"] = getattr(mod, f).detach().cpu().contiguous()
     meta = {"format": FORMAT, "version": VERSION, "layers": layers}
     save_file(tensors, path, metadata={"svdq": json.dumps(meta)})
@@ -310,11 +465,20 @@ def load_quantized(module, path, device=None):
             if d["kind"] == "svdq":
                 lay = {fld: take(name, fld) for fld in _SVDQ_FIELDS}
                 lay.update(rank=int(d["rank"]), prec=svdq._PREC[d["prec"]], N=n, K=k)
-                new = SVDQLinear(lay, bias, bool(d.get("gelu_input", False)))
+                new = SVDQLinear(lay, bias, bool(d.get("gelu_input", False)),
+                                 int(d.get("a16_rows", 0)))
             elif d["kind"] == "awq":
                 lay = {fld: take(name, fld) for fld in _AWQ_FIELDS}
                 lay.update(N=n, K=k, group=int(d["group"]))
                 new = AWQLinear(lay, bias)
+            elif d["kind"] == "awq_gated":
+                lays = [dict({f: take(name, f"{p}_{f}") for f in _AWQ_FIELDS}, N=n, K=k,
+                             group=int(d["group"])) for p in ("gate", "up")]
+                biases = {b: take(name, b) for b in d["biases"]}
+                for b, t in biases.items():
+                    if tuple(t.shape) != (n,):
+                        raise ValueError(f"{name}.{b}: expected ({n},)")
+                new = AWQGatedLinear(*lays, act=d["act"], **biases)
             else:
                 raise ValueError(f"{path}: unknown layer kind {d['kind']!r}")
             if bias is not None and tuple(bias.shape) != (n,):
