@@ -74,11 +74,14 @@ constexpr int WAVES = 8, NT = 64 * WAVES;
 constexpr int D = 2;                     // chunks of weights in flight per wave
 constexpr int LDS_X = 64 << 10;          // LDS for the terms of Xh
 constexpr int MAX_SLICES = 8;            // of K, one workgroup each
-constexpr int LR_STEPS = 4;              // steps of 32 k per wave of LR, all loaded at once
+constexpr int LR_STEPS = 4;              // steps of 32 k per wave of LR, loaded at once
+constexpr int MAX_LR = 4;
 
-// slices of K over which LR is computed
+// slices of K over which LR is computed: two rounds of loads each (it runs beside
+// the weights' stream, and the second launch waits for every slice's sum)
 int lr_slices(int64_t K) {
-  return int(std::min<int64_t>(16, (K / 32 + WAVES * LR_STEPS - 1) / (WAVES * LR_STEPS)));
+  constexpr int64_t steps = 2 * WAVES * LR_STEPS;
+  return int(std::min<int64_t>(MAX_LR, (K / 32 + steps - 1) / steps));
 }
 
 // Lane group j of a wave holds 8 bytes of a weight row's chunk: for INT4 the
@@ -342,47 +345,59 @@ __global__ __launch_bounds__(256) void a16_sum_kernel(
   const float* p[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) p[e] = part + int64_t(min(m0 + 4 * j + e, M - 1)) * N + n;
-  v4f sum = {0, 0, 0, 0}, low = {0, 0, 0, 0};
-  // (all loads first; a slice past the last counts as zeros)
+  // LR and lora_up for 64 rank indices: halves q of 32
+  uint4 u[2];
+  float l[2][MAX_LR][8];
+  auto load_low = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int i = i0 + 32 * q + 8 * j;
+      u[q] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int s = 0; s < MAX_LR; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) l[q][s][e] = 0.f;
+      if (i < rank) {
+        u[q] = *reinterpret_cast<const uint4*>(up + n * rank + i);
+#pragma unroll
+        for (int s = 0; s < MAX_LR; ++s)
+          if (s < LS) load8(LR + (int64_t(s) * M + ml) * rank + i, l[q][s]);
+      }
+    }
+  };
+  // all loads first; a slice past the last counts as zeros
+  if (rank) load_low(0);
   float v[MAX_SLICES][4];
 #pragma unroll
   for (int q = 0; q < MAX_SLICES; ++q)
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[q][e] = p[e][int64_t(min(q, S - 1)) * M * N];
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int q = 0; q < MAX_SLICES; ++q)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += q < S ? v[q][e] : 0.f;
   const float ts = ts_w ? ts_w[0] : 1.f;
   const float bv = !bias   ? 0.f
                    : bbf16 ? bf16_to_f32(static_cast<const uint16_t*>(bias)[n])
                            : static_cast<const float*>(bias)[n];
-  for (int i0 = 0; i0 < rank; i0 += 32) {
-    const int i = i0 + 8 * j;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    float l[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (i < rank) {
-      u = *reinterpret_cast<const uint4*>(up + n * rank + i);
-      for (int s0 = 0; s0 < LS; s0 += 4) {
-        float v[4][8];
+  __builtin_amdgcn_sched_barrier(0);
+  v4f sum = {0, 0, 0, 0}, low = {0, 0, 0, 0};
+  for (int i0 = 0; i0 < rank; i0 += 64) {
+    if (i0) load_low(i0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          load8(LR + (int64_t(min(s0 + q, LS - 1)) * M + ml) * rank + i, v[q]);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+      for (int s = 1; s < MAX_LR; ++s)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) l[e] += s0 + q < LS ? v[q][e] : 0.f;
-      }
+        for (int e = 0; e < 8; ++e) l[q][0][e] += l[q][s][e];
+      uint4 a[T];
+      split_bf16<T>(l[q][0], a);
+#pragma unroll
+      for (int t = T - 1; t >= 0; --t)
+        low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a[t]),
+                                                      __builtin_bit_cast(v8bf, u[q]), low, 0, 0, 0);
     }
-    uint4 a[T];
-    split_bf16<T>(l, a);
-#pragma unroll
-    for (int t = T - 1; t >= 0; --t)
-      low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a[t]),
-                                                    __builtin_bit_cast(v8bf, u), low, 0, 0, 0);
   }
+#pragma unroll
+  for (int q = 0; q < MAX_SLICES; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += q < S ? v[q][e] : 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int64_t m = m0 + 4 * j + e;
@@ -395,8 +410,10 @@ __global__ __launch_bounds__(256) void a16_sum_kernel(
   }
 }
 
-// Columns per wave and slices of K: about 512 workgroups, two to a compute
-// unit, so that one streams while the other fills its LDS or stores.
+// Columns per wave and slices of K: at most 512 workgroups, two to a compute
+// unit, so that one streams while the other fills its LDS or stores; of the
+// possible numbers the one that leaves the fewest compute units idle (12288
+// columns, 7 rows: 5 slices are 240 workgroups and 13.5 us, 6 are 288 and 16.8).
 struct Split {
   int ct, blocks, slices;
 };
@@ -405,7 +422,14 @@ Split split(int64_t K, int64_t N) {
   Split p;
   p.ct = N >= 8192 ? 2 : 1;
   p.blocks = int((N + 16 * WAVES * p.ct - 1) / (16 * WAVES * p.ct));
-  p.slices = int(std::min<int64_t>({K / 64, MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+  const int most = int(std::min<int64_t>({K / 64, MAX_SLICES, std::max(1, 512 / p.blocks)}));
+  p.slices = 1;
+  double best = 0;
+  for (int S = 1; S <= most; ++S) {
+    const int64_t n = int64_t(p.blocks) * S;
+    const double used = double(n) / double((n + 255) / 256 * 256);
+    if (used >= best) best = used, p.slices = S;
+  }
   return p;
 }
 

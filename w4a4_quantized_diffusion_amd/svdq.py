@@ -400,17 +400,18 @@ def _rows(X, name, width):
 def _out(Y, name, shape, dtype, X, dev):
     """An output, allocated beside X unless given."""
     if Y is None:
-        return X.new_empty(shape, dtype=dtype)
+        return X.new_empty(shape) if X.dtype is dtype else X.new_empty(shape, dtype=dtype)
     _arg(Y, name, shape, dtype, dev)
     return Y
 
 
 def _ws(workspace, need, X, dev):
-    """A workspace of at least `need` bytes and its (address, size)."""
+    """(tensor, address, bytes) of a workspace of at least `need` bytes (a
+    multiple of 256); X is float32 or bfloat16."""
     if workspace is None:
         if not need:
             return None, None, 0
-        workspace = X.new_empty(need, dtype=torch.uint8)
+        workspace = X.new_empty(need >> 1 if X.dtype is torch.bfloat16 else need >> 2)
         return workspace, workspace.data_ptr(), need
     return workspace, _arg(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel()
 
