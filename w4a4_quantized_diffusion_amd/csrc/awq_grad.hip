@@ -85,6 +85,11 @@ constexpr int LDS_A = 64 << 10;          // for the rows' operand of 16 rows, tw
 constexpr int MAX_SLICES = 16;
 constexpr int ONE_SLICE = 32;            // steps up to which 16 waves take them all
 
+// The dG and dU of a gated pair's few rows are formed by every workgroup for its
+// slice of n, so (K / 128) M N times 2; above this many (times 2) a launch of
+// their own costs less.
+constexpr int64_t FUSED_GRADS = 4 << 20;
+
 struct Split {
   int blocks, slices, waves;
 };
@@ -106,8 +111,8 @@ Split split(int64_t M, int64_t K, int64_t N, int layers) {
   return p;
 }
 
-// what a few-row kernel reads: dY, or dH, G, U of a gated pair with where dG
-// and dU go
+// what a few-row kernel reads: dY; or dH, G, U of a gated pair with where dG and
+// dU go; or a pair's dG and dU
 struct Rows {
   const uint16_t *d, *G, *U;
   uint16_t *dG, *dU;
@@ -131,7 +136,11 @@ __device__ __forceinline__ uint4 pair_grad8(const uint4 h, const uint4 g, const 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// ACT < 0: one layer
+// ACT >= 0: a gated pair, whose dG and dU every workgroup forms for itself (those
+// of the first 128 columns store them); PLAIN_PAIR: a pair with dG and dU given;
+// PLAIN: one layer
+constexpr int PLAIN = -1, PLAIN_PAIR = -2;
+
 template <int MT, int ACT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::AwqWeight wa,
                                                                 svdq::AwqWeight wb, int M, int K,
@@ -140,7 +149,7 @@ __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::A
                                                                 void* __restrict__ dX, bool xbf16) {
   constexpr int NT = 64 * WAVES;
   extern __shared__ __align__(16) uint8_t lds[];
-  constexpr int LAYERS = ACT < 0 ? 1 : 2;
+  constexpr int LAYERS = ACT == PLAIN ? 1 : 2;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane >> 4, r = lane & 15;
@@ -188,8 +197,9 @@ __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::A
       const int64_t n = 32 * int64_t(s - layer * per) + 8 * (o & 3), at = int64_t(m) * N + n;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (n < N) {
-        v = *reinterpret_cast<const uint4*>(in.d + at);
-        if constexpr (LAYERS == 2) {
+        const uint16_t* const d = ACT == PLAIN_PAIR ? (layer ? in.dU : in.dG) : in.d;
+        v = *reinterpret_cast<const uint4*>(d + at);
+        if constexpr (ACT >= 0) {
           const uint4 G = *reinterpret_cast<const uint4*>(in.G + at);
           const uint4 U = *reinterpret_cast<const uint4*>(in.U + at);
           v = pair_grad8<ACT>(v, G, U, layer);
@@ -290,7 +300,7 @@ svdq_status launch_sum(const float* part, int S, int64_t M, int64_t K, void* dX,
 template <int MT, int ACT, int WAVES>
 svdq_status run_slices(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
                        const Split& p, float* part, void* dX, bool xbf16, hipStream_t s) {
-  constexpr int layers = ACT < 0 ? 1 : 2;
+  constexpr int layers = ACT == PLAIN ? 1 : 2;
   // steps of the rows' operand that fit LDS (64 rows: 31)
   const int64_t steps = (N + 31) / 32 * layers;
   const int64_t room = MT == 1 ? LDS_A : 2 * LDS_A;
@@ -308,7 +318,7 @@ svdq_status run_slices(const Rows& in, int64_t M, int64_t K, int64_t N, const sv
 template <int ACT>
 svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
                      void* dX, bool xbf16, float* part, hipStream_t s) {
-  const Split p = split(M, K, N, ACT < 0 ? 1 : 2);
+  const Split p = split(M, K, N, ACT == PLAIN ? 1 : 2);
   switch ((M + 15) / 16) {
     case 1:
       SVDQ_TRY(p.waves == 16 ? (run_slices<1, ACT, 16>(in, M, K, N, w, p, part, dX, xbf16, s))
@@ -542,7 +552,7 @@ svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int
   const uint16_t* const d = dY + w * N;
   void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
   if (rest <= ROWS)
-    return run_rows<-1>(Rows{d, nullptr, nullptr, nullptr, nullptr}, rest, K, N, &wt, x, xb, part, s);
+    return run_rows<PLAIN>(Rows{d, nullptr, nullptr, nullptr, nullptr}, rest, K, N, &wt, x, xb, part, s);
   return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, s);
 }
 
@@ -551,16 +561,17 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
                                   svdq_act act, uint16_t* dX, uint16_t* dG, uint16_t* dU, void* ws,
                                   hipStream_t s) {
   const AwqWeight wt[2] = {wg, wu};
-  const int64_t w = wide_rows(M, K, N, 2), rest = M - w, tiled = rest <= ROWS ? w : M;
+  const int64_t w = wide_rows(M, K, N, 2), rest = M - w;
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
   float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 2) : 0));
-  // few rows form their own dG and dU
-  if (rest && rest <= ROWS) {
-    const Rows in{dH + w * N, G + w * N, U + w * N, dG + w * N, dU + w * N};
-    SVDQ_TRY(act == SVDQ_SILU
-                 ? run_rows<SVDQ_SILU>(in, rest, K, N, wt, dX + w * K, true, part, s)
-                 : run_rows<SVDQ_GELU>(in, rest, K, N, wt, dX + w * K, true, part, s));
-  }
+  // few rows form their own dG and dU unless too many columns of dX repeat that
+  const bool fused = rest <= ROWS && rest * N <= FUSED_GRADS / ((K + 127) / 128);
+  const Rows in{dH + w * N, G + w * N, U + w * N, dG + w * N, dU + w * N};
+  uint16_t* const x = dX + w * K;
+  if (rest && fused)
+    SVDQ_TRY(act == SVDQ_SILU ? run_rows<SVDQ_SILU>(in, rest, K, N, wt, x, true, part, s)
+                              : run_rows<SVDQ_GELU>(in, rest, K, N, wt, x, true, part, s));
+  const int64_t tiled = fused ? w : M;
   if (!tiled) return SVDQ_OK;
   const int64_t n8 = tiled * N / 8;
   const unsigned blocks = unsigned(std::min<int64_t>((n8 + 255) / 256, 16384));
@@ -568,8 +579,9 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
   hipLaunchKernelGGL(k, dim3(blocks), dim3(256), 0, s, dH, G, U, n8, dG, dU);
   SVDQ_TRY(check_launch("gate_grad"));
   if (w) SVDQ_TRY(launch_wide(dG, dU, wt, 2, w, K, N, dX, true, reinterpret_cast<uint16_t*>(w8), s));
-  if (rest <= ROWS) return SVDQ_OK;
-  return launch_mid(dG + w * N, dU + w * N, wt, 2, rest, K, N, dX + w * K, true, part, s);
+  if (!rest || fused) return SVDQ_OK;
+  if (rest <= ROWS) return run_rows<PLAIN_PAIR>(in, rest, K, N, wt, x, true, part, s);
+  return launch_mid(in.dG, in.dU, wt, 2, rest, K, N, x, true, part, s);
 }
 
 }  // namespace svdq
