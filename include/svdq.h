@@ -308,8 +308,8 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  * size is the call's *_workspace_bytes, a multiple of 256 and 0 when none is
  * needed or an argument is invalid).  Calls that may run at the same time need
  * workspaces of their own.  DEVICE operands are 16-byte aligned (biases: their
- * element size).  Outputs may not overlap inputs or each other.  M == 0
- * launches nothing. */
+ * element size).  Outputs may not overlap inputs or each other.  K and N are at
+ * most 2^22, M K and M N at most 2^40.  M == 0 launches nothing. */
 
 /* The SVDQ layer on few rows with the activations in their own precision
  * (no 4-bit quantization of X):

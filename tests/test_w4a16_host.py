@@ -66,7 +66,8 @@ def test_sizes(lib, call):
     for kw, msg in ((dict(K=100), "K must"), (dict(K=0), "K must"), (dict(N=40), "N must"),
                     (dict(N=0), "N must"), (dict(N=-16), "N must"), (dict(M=-1), "M out of range"),
                     (dict(M=1 << 27), "M out of range"), (dict(K=1 << 27), "K must"),
-                    (dict(K=(1 << 27) - 64, N=(1 << 27) - 16), "2^40")):
+                    (dict(K=(1 << 22) + 64), "2^22"), (dict(N=(1 << 22) + 16), "2^22"),
+                    (dict(K=1 << 22, N=1 << 22), "2^40")):
         assert call(lib, **kw) == INVALID, kw
         assert msg in svdq.svdq_last_error(), (kw, svdq.svdq_last_error())
 
@@ -74,7 +75,7 @@ def test_sizes(lib, call):
 @pytest.mark.parametrize("call", [gated, gated_grad, linear_grad])
 def test_group_and_large_sizes(lib, call):
     assert call(lib, group=128) == UNSUPPORTED
-    assert call(lib, M=(1 << 27) - 1, N=(1 << 27) - 16) == INVALID
+    assert call(lib, M=(1 << 27) - 1, N=1 << 22) == INVALID
     assert "2^40" in svdq.svdq_last_error()
 
 

@@ -388,9 +388,9 @@ __global__ __launch_bounds__(svdq_gemm::NT) void gated_wide_kernel(
 // rows of Wu with the same n.  Two threads take one row, 32 codes each.
 struct PairWeights {
   svdq::AwqWeight wg, wu;
+  // this thread's row of chunk 0; a chunk further is N rows further
   const uint8_t* q;
   const uint16_t *s, *z;
-  int64_t nr;
   int N, row, half;
   uint4 c[2];
   uint16_t cs[2], cz[2];
@@ -399,18 +399,18 @@ struct PairWeights {
                                          int64_t n0)
       : N(N), row(int(threadIdx.x) >> 1), half(threadIdx.x & 1) {
     const bool up = row & 32;
-    q = up ? u.q : g.q;
-    s = up ? u.s : g.s;
-    z = up ? u.z : g.z;
-    nr = min(n0 + (row >> 6) * 32 + (row & 31), int64_t(N) - 1);
+    const int64_t nr = min(n0 + (row >> 6) * 32 + (row & 31), int64_t(N) - 1);
+    q = (up ? u.q : g.q) + nr * 32 + 16 * half;
+    s = (up ? u.s : g.s) + nr;
+    z = (up ? u.z : g.z) + nr;
   }
   static __device__ __forceinline__ int slot(int row, int piece) {
     return row * 8 + (piece ^ ((row >> 1) & 7));
   }
   template <int set>
   __device__ __forceinline__ void fetch(int chunk) {
-    const int64_t at = int64_t(chunk) * N + nr;
-    c[set] = *reinterpret_cast<const uint4*>(q + at * 32 + 16 * half);
+    const int64_t at = int64_t(chunk) * N;
+    c[set] = *reinterpret_cast<const uint4*>(q + at * 32);
     cs[set] = s[at];
     cz[set] = z[at];
   }

@@ -65,31 +65,38 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
   // transfer.  Rows past the edge repeat the last row (their products reach
   // only outputs that are never stored); pieces past A's width repeat its
   // last piece (the weights there are zeros).
-  int64_t arow[2], boff[2];
-  const int piece = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
+  // The addresses are a uniform base and a lane's 32-bit offset in bytes (rows
+  // and widths are at most 2^22 elements), which costs no vector instruction.
+  const uint32_t piece = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+  uint32_t aoff[2], boff[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r = 32 * wave + 16 * t + (lane >> 2);
-    arow[t] = (m0 + r < p.M ? m0 + r : p.M - 1) * p.width;
-    boff[t] = (b0 + r < p.rows ? b0 + r : p.rows - 1) * p.ldb + piece;
+    aoff[t] = 2 * uint32_t(min(int64_t(r), p.M - 1 - m0)) * uint32_t(p.width);
+    boff[t] = 2 * uint32_t(min(int64_t(r), p.rows - 1 - b0)) * uint32_t(p.ldb) + piece;
   }
   const int seg = 2 * p.chunks, total = seg * p.segments;
+  const uint8_t* const a0 = reinterpret_cast<const uint8_t*>(p.A[0] + m0 * p.width);
+  const uint8_t* const a1 = reinterpret_cast<const uint8_t*>(p.A[1] + m0 * p.width);
+  const uint8_t* const bb = reinterpret_cast<const uint8_t*>(p.B + b0 * p.ldb);
   // transfer t of stage s: 0, 1 of A, 2, 3 of B
-  const uint16_t* asrc;
-  int64_t bcol;
+  const uint8_t *asrc, *bsrc;
+  uint32_t apiece;
   auto dma_at = [&](int s) __attribute__((always_inline)) {
     s = min(s, total - 1);
     const bool second = s >= seg;
-    const uint16_t* const A = second ? p.A[1] : p.A[0];
-    asrc = A + min(32 * int64_t(second ? s - seg : s) + piece, p.width - 8);
-    bcol = 32 * int64_t(s);
+    // pieces that would lie past A's width repeat its last one
+    const int col = min(32 * (second ? s - seg : s), int(p.width) - 8);
+    apiece = min(piece, 2 * uint32_t(int(p.width) - 8 - col));
+    asrc = (second ? a1 : a0) + 2 * col;
+    bsrc = bb + 64 * int64_t(s);
   };
   auto dma = [&](int t, Stage& st) __attribute__((always_inline)) {
     if (t < 2)
-      __builtin_amdgcn_global_load_lds(asrc + arow[t & 1],
+      __builtin_amdgcn_global_load_lds(asrc + (aoff[t & 1] + apiece),
                                        (lds_ptr_t)&st.a[(32 * wave + 16 * (t & 1)) * 4], 16, 0, 0);
     else
-      __builtin_amdgcn_global_load_lds(p.B + boff[t & 1] + bcol,
+      __builtin_amdgcn_global_load_lds(bsrc + boff[t & 1],
                                        (lds_ptr_t)&st.b[(32 * wave + 16 * (t & 1)) * 4], 16, 0, 0);
   };
 
@@ -238,25 +245,26 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, 
   const int h = lane >> 5, r32 = lane & 31;
   // wave w brings rows 32 w .. 32 w + 31 of A, 8 rows to a transfer; rows past
   // the edge repeat the last row, pieces past the width the last piece
-  int64_t arow[4];
-  int apiece[2];
+  // (addresses as in the wide tile: a uniform base and 32-bit offsets in bytes)
+  uint32_t aoff[4], apiece[2];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int r = 32 * wave + 8 * t + (lane >> 3);
-    arow[t] = (m0 + r < p.M ? m0 + r : p.M - 1) * p.width;
-    if (t < 2) apiece[t] = 8 * ((lane & 7) ^ ((r >> 1) & 7));
+    aoff[t] = 2 * uint32_t(min(int64_t(r), p.M - 1 - m0)) * uint32_t(p.width);
+    if (t < 2) apiece[t] = 16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
+  const uint8_t* const base0 = reinterpret_cast<const uint8_t*>(p.A[0] + m0 * p.width);
+  const uint8_t* const base1 = reinterpret_cast<const uint8_t*>(p.A[1] + m0 * p.width);
   auto dma = [&](int c, ChunkA& st) __attribute__((always_inline)) {
     c = min(c, c1 - 1);
     const bool second = c >= p.chunks;
-    const uint16_t* const A = second ? p.A[1] : p.A[0];
-    const int64_t col = 64 * int64_t(second ? c - p.chunks : c);
+    const int col = min(64 * (second ? c - p.chunks : c), int(p.width) - 8);
+    const uint32_t last = 2 * uint32_t(int(p.width) - 8 - col);
+    const uint8_t* const A = (second ? base1 : base0) + 2 * col;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t k = min(col + apiece[t & 1], p.width - 8);
-      __builtin_amdgcn_global_load_lds(A + arow[t] + k, (lds_ptr_t)&st.v[(32 * wave + 8 * t) * 8],
-                                       16, 0, 0);
-    }
+    for (int t = 0; t < 4; ++t)
+      __builtin_amdgcn_global_load_lds(A + (aoff[t] + min(apiece[t & 1], last)),
+                                       (lds_ptr_t)&st.v[(32 * wave + 8 * t) * 8], 16, 0, 0);
   };
   const int sw = (r32 >> 1) & 7;
   const int abase = (wm * 64 + r32) * 8;

@@ -530,12 +530,17 @@ svdq_status check_workspace(const void* ws, size_t have, size_t need) {
   return check_ptr(ws, "workspace", 256);
 }
 
+// the tiled kernels form offsets inside a tile of 256 rows as 32-bit byte counts
+constexpr int64_t MAX_WIDTH = int64_t(1) << 22;
+
 svdq_status check_mkn(int64_t M, int64_t K, int64_t N) {
   if (M < 0 || M > MAX_DIM) return fail(SVDQ_ERR_INVALID_ARG, "M out of range");
   if (K <= 0 || K > MAX_DIM || K % 64 != 0)
     return fail(SVDQ_ERR_INVALID_ARG, "K must be a positive multiple of 64");
   if (N <= 0 || N > MAX_DIM || N % 16 != 0)
     return fail(SVDQ_ERR_INVALID_ARG, "N must be a positive multiple of 16");
+  if (K > MAX_WIDTH || N > MAX_WIDTH)
+    return fail(SVDQ_ERR_INVALID_ARG, "K and N must be at most 2^22");
   const int64_t most = int64_t(1) << 40;
   if (M * K > most || M * N > most || N * K > most)
     return fail(SVDQ_ERR_INVALID_ARG, "M*K, M*N and N*K must be at most 2^40");
