@@ -342,8 +342,9 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
 // 32 rows of Wu with the same n alternating, so that one wave's two column
 // blocks of the product are the G and the U of the same outputs.
 
-// 64 rows of the pair matrix and one group of 64 k per workgroup; rows past N
-// are zeros
+// 64 rows of the pair matrix and one group of 64 k (two stages) per workgroup;
+// rows past N are zeros.  Four lanes take one row, 8 k of each stage, so that a
+// wave stores 1 KB in a row.
 __global__ __launch_bounds__(256) void pair_dequant_kernel(svdq::AwqWeight wg, svdq::AwqWeight wu,
                                                            int K, int N,
                                                            uint16_t* __restrict__ B) {
@@ -351,17 +352,18 @@ __global__ __launch_bounds__(256) void pair_dequant_kernel(svdq::AwqWeight wg, s
   const int blocks = (N + 31) / 32, g = blockIdx.x / blocks;
   const int64_t block = blockIdx.x % blocks, n = block * 32 + (row & 31);
   const svdq::AwqWeight w = row >= 32 ? wu : wg;
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   if (n < N) {
     const int64_t at = int64_t(g) * N + n;
-    const uint2 c = *reinterpret_cast<const uint2*>(w.q + at * 32 + piece * 8);
+    const uint32_t* const c = reinterpret_cast<const uint32_t*>(w.q + at * 32 + piece * 4);
+    const uint32_t c0 = c[0], c1 = c[4];
     const float s = bf16_to_f32(w.s[at]), zs = -bf16_to_f32(w.z[at]) * s;
-    a = dequant8(c.x, s, zs);
-    b = dequant8(c.y, s, zs);
+    v[0] = dequant8(c0, s, zs);
+    v[1] = dequant8(c1, s, zs);
   }
-  uint4* d = reinterpret_cast<uint4*>(B + (block * 64 + row) * K + 64 * g + 16 * piece);
-  d[0] = a;
-  d[1] = b;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    *svdq_gemm::weight_at(B, K / 32, block * 64 + row, 64 * g + 32 * t + 8 * piece) = v[t];
 }
 
 template <int ACT>
@@ -466,7 +468,7 @@ int64_t wide_rows(int64_t M, int64_t K, int64_t N) {
 }
 
 size_t pair_bytes(int64_t K, int64_t N) {
-  return svdq::align256(size_t(pair_rows(N)) * size_t(K) * 2);
+  return svdq_gemm::weight_bytes(pair_rows(N), K / 32);
 }
 
 // bytes of the partial sums of `rows` rows
@@ -561,7 +563,7 @@ svdq_status wide(const Call& c, uint16_t* B) {
                      c.s, c.wg, c.wu, int(c.K), int(c.N), B);
   SVDQ_TRY(svdq::check_launch("pair_dequant"));
   const int64_t rows = pair_rows(c.N), tiles = (c.M + 255) / 256 * ((rows + 255) / 256);
-  svdq_gemm::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, B, c.K, int(c.M), int(rows)};
+  svdq_gemm::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, B, int(c.M), int(rows)};
   auto k = c.silu ? gated_wide_kernel<SVDQ_SILU> : gated_wide_kernel<SVDQ_GELU>;
   hipLaunchKernelGGL(k, dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, c.s, p, int(c.N), c.bg, c.bu,
                      c.H, c.hbf16, c.G, c.U);

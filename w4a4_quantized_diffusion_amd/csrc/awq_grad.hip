@@ -332,15 +332,16 @@ svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq
 }
 
 // ---------------------------------------------------------- many rows
-// The weights are dequantized once into the workspace, transposed: B [K, ldb]
-// with the n of the first layer, then those of the second, each padded with
-// zeros to a multiple of 64.
+// The weights are dequantized once into the workspace, transposed: row k holds
+// the n of the first layer, then those of the second, each padded with zeros to a
+// multiple of 64, in the blocks of gemm_bf16.h.
 
-// 64 n x 64 k (one group) per wave: lane (o, j) takes 8 rows n and 8 k of
-// each, and writes 8 pieces of 8 n
+// 64 n (two stages) x 64 k (one group) per wave: lane (o, j) takes 8 rows n and 8
+// k of each; through the wave's LDS every store then covers 16 rows k in a row
 __global__ __launch_bounds__(256) void transpose_dequant_kernel(svdq::AwqWeight w, int N,
-                                                                int64_t ldb,
+                                                                int64_t stages, int64_t first,
                                                                 uint16_t* __restrict__ B) {
+  __shared__ uint4 lds[4][2][64][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int o = lane & 7, j = lane >> 3;
   const int blocks = ((N + 63) / 64 + 3) / 4, g = blockIdx.x / blocks;
@@ -352,8 +353,18 @@ __global__ __launch_bounds__(256) void transpose_dequant_kernel(svdq::AwqWeight 
   for (int i = 0; i < 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
   if (n < N) transpose_dequant8(w, int64_t(g) * N + n, j, out);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<uint4*>(B + (64 * int64_t(g) + 8 * j + i) * ldb + n) = out[i];
+  for (int i = 0; i < 8; ++i) lds[wave][o >> 2][8 * j + i][o & 3] = out[i];
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 16 * i + (lane >> 2);
+      *svdq_gemm::weight_at(B, stages, 64 * int64_t(g) + k, first + n0 + 32 * t + 8 * (lane & 3)) =
+          lds[wave][t][k][lane & 3];
+    }
 }
 
 __global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Args p,
@@ -499,7 +510,7 @@ int64_t wide_rows(int64_t M, int64_t K, int64_t N, int layers) {
 }
 
 size_t transposed_bytes(int64_t K, int64_t N, int layers) {
-  return svdq::align256(size_t(K) * size_t(pad64(N)) * 2 * layers);
+  return svdq_gemm::weight_bytes(K, pad64(N) / 32 * layers);
 }
 
 // bytes of the partial sums of `rows` rows
@@ -513,13 +524,13 @@ size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers) {
 svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWeight* w,
                         int layers, int64_t M, int64_t K, int64_t N, void* dX, bool xbf16,
                         uint16_t* B, hipStream_t s) {
-  const int64_t np = pad64(N), ldb = np * layers;
+  const int64_t np = pad64(N);
   for (int i = 0; i < layers; ++i) {
     hipLaunchKernelGGL(transpose_dequant_kernel, dim3(unsigned((np + 255) / 256 * (K / 64))),
-                       dim3(256), 0, s, w[i], int(N), ldb, B + i * np);
+                       dim3(256), 0, s, w[i], int(N), np / 32 * layers, i * np, B);
     SVDQ_TRY(svdq::check_launch("transpose_dequant"));
   }
-  svdq_gemm::Args p{{A0, A1}, N, int(np / 64), layers, B, ldb, int(M), int(K)};
+  svdq_gemm::Args p{{A0, A1}, N, int(np / 64), layers, B, int(M), int(K)};
   const int64_t tiles = ((M + 255) / 256) * ((K + 255) / 256);
   hipLaunchKernelGGL(grad_wide_kernel, dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, s, p, dX,
                      xbf16);

@@ -3,8 +3,10 @@
 //   C[m, b] = sum_r A[m, r] B[b, r]      (fp32 sums)
 //
 // A in one or two segments along r (A0, A1 [M, width], the columns of one after
-// the other's), B [rows, ldb] the weights in bf16, each segment padded with
-// zeros to whole chunks of 64.  256 x 256 tiles, 8 waves of 128 x 64 on
+// the other's), B the weights in bf16 as the dequantizing kernels lay them out:
+// for every 256 rows b and every 32 r a block of 16 KB [256][32], each segment
+// padded with zeros to whole chunks of 64 (so a tile's stage is read from
+// consecutive addresses, whatever the row length).  256 x 256 tiles, 8 waves of 128 x 64 on
 // v_mfma_f32_32x32x16_bf16, both operands brought to LDS by the load unit
 // (global_load_lds, 16 bytes a lane).
 //
@@ -31,13 +33,26 @@ constexpr int NT = 512;
 constexpr int WM = 128, WN = 64;
 constexpr int RBL = WM / 32, CBL = WN / 32;
 
+constexpr int BLOCK_BYTES = BN * 64;     // of B: 256 rows, 32 r
+
+// bytes of B for `rows` rows and `stages` stages of 32 r
+inline size_t weight_bytes(int64_t rows, int64_t stages) {
+  return size_t((rows + BN - 1) / BN) * size_t(stages) * BLOCK_BYTES;
+}
+
+// where element (row, r) of B lies, r a multiple of 8
+__device__ __forceinline__ uint4* weight_at(uint16_t* B, int64_t stages, int64_t row, int64_t r) {
+  return reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(B) +
+                                  ((row / BN) * stages + r / 32) * BLOCK_BYTES +
+                                  (row % BN) * 64 + (r % 32) * 2);
+}
+
 struct Args {
   const uint16_t* A[2];
   int64_t width;          // columns of A in one segment (a multiple of 8)
   int chunks;             // chunks of 64 in one segment
   int segments;           // 1 or 2
   const uint16_t* B;
-  int64_t ldb;            // elements: segments * chunks * 64
   int M, rows;            // rows of A, rows of B
 };
 
@@ -73,12 +88,12 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
   for (int t = 0; t < 2; ++t) {
     const int r = 32 * wave + 16 * t + (lane >> 2);
     aoff[t] = 2 * uint32_t(min(int64_t(r), p.M - 1 - m0)) * uint32_t(p.width);
-    boff[t] = 2 * uint32_t(min(int64_t(r), p.rows - 1 - b0)) * uint32_t(p.ldb) + piece;
+    boff[t] = 64 * uint32_t(min(int64_t(r), p.rows - 1 - b0)) + piece;
   }
   const int seg = 2 * p.chunks, total = seg * p.segments;
   const uint8_t* const a0 = reinterpret_cast<const uint8_t*>(p.A[0] + m0 * p.width);
   const uint8_t* const a1 = reinterpret_cast<const uint8_t*>(p.A[1] + m0 * p.width);
-  const uint8_t* const bb = reinterpret_cast<const uint8_t*>(p.B + b0 * p.ldb);
+  const uint8_t* const bb = reinterpret_cast<const uint8_t*>(p.B) + b0 / BN * total * int64_t(BLOCK_BYTES);
   // transfer t of stage s: 0, 1 of A, 2, 3 of B
   const uint8_t *asrc, *bsrc;
   uint32_t apiece;
@@ -89,7 +104,7 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
     const int col = min(32 * (second ? s - seg : s), int(p.width) - 8);
     apiece = min(piece, 2 * uint32_t(int(p.width) - 8 - col));
     asrc = (second ? a1 : a0) + 2 * col;
-    bsrc = bb + 64 * int64_t(s);
+    bsrc = bb + BLOCK_BYTES * int64_t(s);
   };
   auto dma = [&](int t, Stage& st) __attribute__((always_inline)) {
     if (t < 2)
