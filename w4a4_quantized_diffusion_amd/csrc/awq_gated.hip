@@ -342,28 +342,40 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
 // 32 rows of Wu with the same n alternating, so that one wave's two column
 // blocks of the product are the G and the U of the same outputs.
 
-// 64 rows of the pair matrix and one group of 64 k (two stages) per workgroup;
-// rows past N are zeros.  Four lanes take one row, 8 k of each stage, so that a
-// wave stores 1 KB in a row.
+// 64 rows of the pair matrix and four groups of 64 k (two stages each) per
+// workgroup; rows past N are zeros.  Four lanes take one row, 8 k of each stage,
+// so that a wave stores 1 KB in a row.
+constexpr int DEQUANT_GROUPS = 4;
+
 __global__ __launch_bounds__(256) void pair_dequant_kernel(svdq::AwqWeight wg, svdq::AwqWeight wu,
                                                            int K, int N,
                                                            uint16_t* __restrict__ B) {
   const int row = threadIdx.x >> 2, piece = threadIdx.x & 3;
-  const int blocks = (N + 31) / 32, g = blockIdx.x / blocks;
+  const int blocks = (N + 31) / 32, G = K / 64, g0 = blockIdx.x / blocks * DEQUANT_GROUPS;
   const int64_t block = blockIdx.x % blocks, n = block * 32 + (row & 31);
   const svdq::AwqWeight w = row >= 32 ? wu : wg;
-  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (n < N) {
-    const int64_t at = int64_t(g) * N + n;
-    const uint32_t* const c = reinterpret_cast<const uint32_t*>(w.q + at * 32 + piece * 4);
-    const uint32_t c0 = c[0], c1 = c[4];
-    const float s = bf16_to_f32(w.s[at]), zs = -bf16_to_f32(w.z[at]) * s;
-    v[0] = dequant8(c0, s, zs);
-    v[1] = dequant8(c1, s, zs);
+  // (rows past N read the last row and groups past K the last group)
+  const int64_t nc = min(n, int64_t(N) - 1);
+  uint32_t c[DEQUANT_GROUPS][2];
+  uint16_t s[DEQUANT_GROUPS], z[DEQUANT_GROUPS];
+#pragma unroll
+  for (int i = 0; i < DEQUANT_GROUPS; ++i) {
+    const int64_t at = int64_t(min(g0 + i, G - 1)) * N + nc;
+    const uint32_t* const p = reinterpret_cast<const uint32_t*>(w.q + at * 32 + piece * 4);
+    c[i][0] = p[0];
+    c[i][1] = p[4];
+    s[i] = w.s[at];
+    z[i] = w.z[at];
   }
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-    *svdq_gemm::weight_at(B, K / 32, block * 64 + row, 64 * g + 32 * t + 8 * piece) = v[t];
+  for (int i = 0; i < DEQUANT_GROUPS; ++i) {
+    if (g0 + i >= G) break;
+    const float f = n < N ? bf16_to_f32(s[i]) : 0.f, fz = -bf16_to_f32(z[i]) * f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      *svdq_gemm::weight_at(B, K / 32, block * 64 + row, 64 * (g0 + i) + 32 * t + 8 * piece) =
+          dequant8(c[i][t], f, fz);
+  }
 }
 
 template <int ACT>
@@ -559,7 +571,7 @@ svdq_status mid(const Call& c, float* part) {
 }
 
 svdq_status wide(const Call& c, uint16_t* B) {
-  hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((c.N + 31) / 32 * (c.K / 64))), dim3(256), 0,
+  hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((c.N + 31) / 32 * ((c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS))), dim3(256), 0,
                      c.s, c.wg, c.wu, int(c.K), int(c.N), B);
   SVDQ_TRY(svdq::check_launch("pair_dequant"));
   const int64_t rows = pair_rows(c.N), tiles = (c.M + 255) / 256 * ((rows + 255) / 256);
