@@ -385,6 +385,65 @@ def test_a16_agrees_with_the_quantized_layer():
     check(y4, y, tol + lr + round_tol(y, F32), "w4a4")
 
 
+@pytest.mark.parametrize("exponent", [-30, -20, 20, 30])
+def test_linear_a16_over_the_range_of_x(exponent):
+    """X scaled by 10^e: the terms of Xh keep their relative precision (every
+    term and product stays a normal number)."""
+    m, k, n = 5, 256, 64
+    d, parts = svdq_layer(n, k, 16, "int4", 37)
+    g = torch.Generator("cuda").manual_seed(38)
+    x = torch.randn(m, k, generator=g, device="cuda") * 10.0 ** exponent
+    y, tol = a16_ref(x, parts, None, 2.0 ** -24)
+    Y = svdq.svdq_linear_w4a16(x, d)
+    check(Y, y, tol + round_tol(y, F32), f"1e{exponent}")
+
+
+@pytest.mark.parametrize("m", [3, 20, 64, 100, 1100])
+def test_a_row_of_nans_stays_in_its_row(m):
+    """NaN and infinity in one row of the input leave every other row bit for
+    bit as it was, ragged ends of the reduction included."""
+    k, n = 320, 336
+    gate, _ = awq_layer(n, k, 91)
+    up, _ = awq_layer(n, k, 92)
+    d, _ = svdq_layer(n, k, 16, "nvfp4", 93)
+    x, dy = bf((m, k), 94), bf((m, n), 95)
+    calls = [lambda x, dy: svdq.awq_gated_w4a16(x, gate, up),
+             lambda x, dy: svdq.awq_linear_w4a16_grad(dy, gate),
+             lambda x, dy: svdq.awq_gated_w4a16_grad(dy, dy, dy, gate, up)[0]]
+    if m <= 64:
+        calls.append(lambda x, dy: svdq.svdq_linear_w4a16(x, d))
+    ref = [f(x, dy) for f in calls]
+    keep = torch.arange(m, device="cuda") != 1
+    for bad in (float("nan"), float("inf")):
+        x2, dy2 = x.clone(), dy.clone()
+        x2[1], dy2[1] = bad, bad
+        for f, r in zip(calls, ref):
+            assert torch.equal(f(x2, dy2)[keep], r[keep])
+
+
+def test_offsets_past_32_bits():
+    """H and dY of more than 2^31 elements (4.4 GB): the last rows and a sample
+    of the others."""
+    m, k, n = 180007, 64, 12288
+    assert m * n > 1 << 31
+    gate, wg = awq_layer(n, k, 81)
+    up, wu = awq_layer(n, k, 82)
+    x = bf((m, k), 83)
+    rows = torch.cat([torch.arange(0, m, 30011), torch.arange(m - 9, m)]).cuda()
+    H = svdq.awq_gated_w4a16(x, gate, up)
+    _, _, (h, th) = gated_ref(x[rows], wg, wu, None, None, "silu")
+    check(H[rows], h, th + round_tol(h, BF) + 1e-30, "H")
+    dX = svdq.awq_linear_w4a16_grad(H, gate)
+    d = H[rows].double()
+    check(dX[rows], d @ wg, grad_tol(d, wg) + round_tol(d @ wg, BF) + 1e-30, "dX")
+    dX, dG, dU = svdq.awq_gated_w4a16_grad(H, H, H, gate, up)
+    a, da = act64(d, "silu")
+    check(dU[rows], d * a, round_tol(d * a, BF) + 2.0 ** -20 * (d * d).abs() + 1e-30, "dU")
+    dx = dG[rows].double() @ wg + dU[rows].double() @ wu
+    tol = 2 * (grad_tol(dG[rows].double(), wg) + grad_tol(dU[rows].double(), wu))
+    check(dX[rows], dx, tol + round_tol(dx, BF) + 1e-30, "dX of the pair")
+
+
 # ---------------------------------------------- streams, graphs, refusals
 
 def test_zero_rows():

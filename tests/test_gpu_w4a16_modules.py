@@ -184,3 +184,13 @@ def test_svdq_linear_few_rows(prec):
     assert b(x[:0]).shape == (0, 272)
     # alternating sizes reuse one workspace
     assert torch.equal(b(x[:12]), y) and torch.equal(b(x), a(x)) and torch.equal(b(x[:12]), y)
+
+
+def test_shim_hands_a16_rows_on():
+    """quantize_linears(a16_rows=...) reaches the layers without gelu_input."""
+    b = nn.Sequential(linear(128, 256, 8), nn.Linear(256, 128, device="cuda"))
+    done = L.quantize_linears(b, rank=16, gelu_input=("1",), a16_rows=5)
+    assert done == {"0": "svdq", "1": "svdq"}
+    assert b[0].a16_rows == 5 and b[1].a16_rows == 0 and b[1].gelu_input
+    x = torch.randn(4, 128, device="cuda").to(BF)
+    assert torch.equal(b[0](x), svdq.svdq_linear_w4a16(x, b[0].layer(), b[0].bias, y_dtype=BF))
