@@ -16,7 +16,8 @@ using namespace svdq_dev;
 
 namespace {
 
-// dG, dU of 8 elements per thread
+// dG, dU of 8 elements per thread: memory-bound, 503 MB in 76 us (6.6 TB/s, part of
+// it from the Infinity Cache) for 4096 x 12288
 template <int ACT>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restrict__ dH,
                                                         const uint16_t* __restrict__ G,
@@ -79,15 +80,24 @@ __device__ __forceinline__ void transpose_dequant8(const svdq::AwqWeight& w, int
 // k = 64 (r / 8) + 8 (r % 8) + t, so a lane's 8 products are 8 consecutive k.
 // The rows' own operand (dY, or dG and dU computed here from dH, G and U) is
 // in LDS.  Partial sums [S][M][K] are joined by grad_sum_kernel.
+//
+// A dequantized code costs 2.6 vector instructions here, so every compute unit is
+// needed: one row 4096 x 4096 takes 7.5 us in 512 workgroups (6.4 and a launch of 2.6
+// for the sums), and 17 in the 32 that need no second launch.  Twenty rows of the
+// pair 2048 x 5456 take 14 us.
 
 constexpr int ROWS = 64;                 // the most rows of this form
 constexpr int LDS_A = 64 << 10;          // for the rows' operand of 16 rows, twice that above
 constexpr int MAX_SLICES = 16;
-constexpr int ONE_SLICE = 32;            // steps up to which 16 waves take them all
+// Steps up to which the 16 waves of one workgroup take them all, and there is one
+// launch: 512 outputs to 1024 columns 5.1 us against 5.9 in two launches, 1024
+// outputs 6.9 against 6.0, where the host's 3 us for the second launch decide.
+constexpr int ONE_SLICE = 32;
 
 // The dG and dU of a gated pair's few rows are formed by every workgroup for its
 // slice of n, so (K / 128) M N times 2; above this many (times 2) a launch of
-// their own costs less.
+// their own costs less: 40 rows 4096 x 8192 30.5 us against 39, 20 rows 2048 x
+// 5456 14.7 against 14.0.
 constexpr int64_t FUSED_GRADS = 4 << 20;
 
 struct Split {
@@ -338,6 +348,7 @@ svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq
 
 // 64 n (two stages) x 64 k (one group) per wave: lane (o, j) takes 8 rows n and 8
 // k of each; through the wave's LDS every store then covers 16 rows k in a row
+// (12288 x 4096: 129 MB in 24 us, 5.4 TB/s; stores of 64 bytes took 32)
 __global__ __launch_bounds__(256) void transpose_dequant_kernel(svdq::AwqWeight w, int N,
                                                                 int64_t stages, int64_t first,
                                                                 uint16_t* __restrict__ B) {

@@ -6,15 +6,23 @@
 // the other's), B the weights in bf16 as the dequantizing kernels lay them out:
 // for every 256 rows b and every 32 r a block of 16 KB [256][32], each segment
 // padded with zeros to whole chunks of 64 (so a tile's stage is read from
-// consecutive addresses, whatever the row length).  256 x 256 tiles, 8 waves of 128 x 64 on
-// v_mfma_f32_32x32x16_bf16, both operands brought to LDS by the load unit
-// (global_load_lds, 16 bytes a lane).
+// consecutive addresses, whatever the row length: 8% of the time of a 24576-long
+// reduction, where rows are multiples of 4 KB apart).
 //
-// Both operands move in stages of 32 r through a ring of NST buffers, so that
-// NST - 1 stages are on their way while one is used: the tiles of one XCD run in
-// step, so a stage arrives no sooner than its slowest line from HBM, and with one
-// stage ahead the waves waited for that half of the time.  LDS rows are 64 bytes,
-// 4 slots of 16; slot s of row r holds piece s ^ ((r >> 2) & 3), so that the 16
+// 256 x 256 tiles, 8 waves of 128 x 64 on v_mfma_f32_32x32x16_bf16, both operands
+// brought to LDS by the load unit (global_load_lds, 16 bytes a lane) in stages of
+// 32 r, through a ring of NST buffers: NST - 1 stages are on their way while one is
+// used.  LDS reads and transfers are issued one at a time between the MFMAs, which
+// gave 7% over the same ring with the reads in front of them: the eight waves
+// leave a barrier together and queue for LDS together.
+//
+// Measured, 4096 rows: 4096 -> 2 x 12288 columns 640-675 us (1.2-1.3 PFLOP/s),
+// 24576 -> 4096 columns 606-640 us.  The matrix units are busy 74-79% of the cycles
+// and the clock falls to 1.6 GHz: power bounds it, so a schedule with fewer idle
+// cycles gains less than the cycles it saves.  (torch's library product of the same
+// shapes takes 645 and 573 us.)
+//
+// LDS rows are 64 bytes, 4 slots of 16; slot s of row r holds piece s ^ ((r >> 2) & 3), so that the 16
 // lanes of one ds_read_b128 phase (rows r..r+15, one piece) touch 16 different
 // groups of 4 banks.  The load unit writes a wave's 64 pieces consecutively, so
 // the permutation is applied to the global addresses.
@@ -203,6 +211,11 @@ __device__ __forceinline__ void zero_acc(v16f (&acc)[R][C]) {
 
 }  // namespace svdq_gemm
 
+// Measured: gated pair 333 rows 2048 -> 8208 40 us (0.56 PFLOP/s), 1000 rows
+// 4096 -> 12288 225 us (0.90); a copy of the kernel without the dequantization took 29
+// us at 333 rows: its vector instructions and the MFMAs add up on a SIMD instead of
+// overlapping, and 387 tiles leave a quarter of the chip idle in the second half.
+//
 // A medium number of rows: 128 x 128 tiles, 4 waves of 64 x 64, two workgroups
 // to a compute unit.  A comes to LDS by the load unit; the weights are
 // dequantized on their way into LDS (once per 128 rows, where a pass of their
@@ -295,6 +308,7 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, 
     __builtin_amdgcn_s_waitcnt(0x0070 | 4);     // vmcnt(4) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     w.template fetch<set>(min(c + 2, c1 - 1));
+    __builtin_amdgcn_sched_barrier(0);          // the four transfers stay last
     dma(c + 2, an);
     __builtin_amdgcn_sched_barrier(0);
     v8bf fa[2][RBL], fb[2][CBL];

@@ -7,6 +7,13 @@
 // codes with an E4M3 scale per 16) against activations in their own
 // precision: what a pooled vector, a time step or a decoding batch of a
 // quantized model needs, where quantizing the few activations saves nothing.
+//
+// Measured, both launches: one row 4096 -> 24576 INT4 (59 MB) 15 us, of which the
+// first launch takes 11.2 (5.2 TB/s, part of it from the Infinity Cache); 7 rows
+// 4096 -> 12288 NVFP4 13.5 us; 61 rows 2752 -> 10928 in three terms 28 us, shared by
+// the partial sums (9 us), the terms of Xh (4) and the products (5 for the terms
+// beyond the first); 1024 x 1024 one row 6.2 us, two launches and two trips to
+// memory.
 
 #include "w4a16.h"
 
