@@ -194,3 +194,24 @@ def test_shim_hands_a16_rows_on():
     assert b[0].a16_rows == 5 and b[1].a16_rows == 0 and b[1].gelu_input
     x = torch.randn(4, 128, device="cuda").to(BF)
     assert torch.equal(b[0](x), svdq.svdq_linear_w4a16(x, b[0].layer(), b[0].bias, y_dtype=BF))
+
+
+def test_captured_few_rows_outlive_a_larger_call():
+    """A captured call on few rows replays right after eager calls on more rows,
+    and writes to nothing but its own memory."""
+    a = L.SVDQLinear.from_linear(linear(512, 272, 9), rank=16, a16_rows=64)
+    x = torch.randn(2, 512, device="cuda").to(BF)
+    ref = a(x)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = a(x)
+    big = torch.randn(700, 512, device="cuda").to(BF)
+    yb = a(big)
+    fill = [torch.full((n,), 5.0, device="cuda") for n in (64, 1024, 4096, 16384, 1 << 18) * 4]
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref) and torch.equal(a(big), yb)
+    assert all((t == 5.0).all() for t in fill)

@@ -91,7 +91,8 @@ class SVDQLinear(nn.Module):
 
     Inputs of at most `a16_rows` rows (0 to 64, default 0) run
     svdq_linear_w4a16 instead: the same layer with x kept in its own precision,
-    for the layers that see a row per image or token."""
+    for the layers that see a row per image or token (with a workspace of its own
+    for every call)."""
 
     def __init__(self, layer, bias=None, gelu_input=False, a16_rows=0):
         super().__init__()
@@ -146,17 +147,15 @@ class SVDQLinear(nn.Module):
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features).contiguous()
         m = x2.shape[0]
-        a16 = 0 < m <= self.a16_rows
-        if a16:
-            need = svdq.svdq_linear_w4a16_workspace_bytes(m, self.in_features, self.out_features,
-                                                          self.rank)
-        else:
-            need = svdq.svdq_workspace_bytes(m, self.in_features, self.rank, self.prec)
-        need = max(need, 256)
+        if 0 < m <= self.a16_rows:
+            # (a workspace of its own for every call: one captured into a graph must
+            # outlive the larger one that a later call on more rows brings)
+            y = svdq.svdq_linear_w4a16(x2, self.layer(), self.bias, y_dtype=x2.dtype)
+            return y.reshape(*lead, self.out_features)
+        need = max(svdq.svdq_workspace_bytes(m, self.in_features, self.rank, self.prec), 256)
         if self._ws is None or self._ws.numel() < need or self._ws.device != x2.device:
             self._ws = torch.empty(need, dtype=torch.uint8, device=x2.device)
-        fn = (svdq.svdq_linear_w4a16 if a16 else
-              svdq.svdq_linear_w4a4_gelu if self.gelu_input else svdq.svdq_linear_w4a4)
+        fn = svdq.svdq_linear_w4a4_gelu if self.gelu_input else svdq.svdq_linear_w4a4
         y = fn(x2, self.layer(), self.bias, y_dtype=x2.dtype, workspace=self._ws)
         return y.reshape(*lead, self.out_features)
 
