@@ -309,7 +309,10 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  * needed or an argument is invalid).  Calls that may run at the same time need
  * workspaces of their own.  DEVICE operands are 16-byte aligned (biases: their
  * element size).  Outputs may not overlap inputs or each other.  K and N are at
- * most 2^22, M K and M N at most 2^40.  M == 0 launches nothing. */
+ * most 2^22, M K, M N and N K at most 2^40.  M == 0 launches nothing.
+ * An infinity or NaN in a row of the first operand makes that row of the products
+ * infinite or NaN all along (NaN may stand where the formula has an infinity), and
+ * no other row. */
 
 /* The SVDQ layer on few rows with the activations in their own precision
  * (no 4-bit quantization of X):
@@ -320,7 +323,8 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  * (modulation, time step and pooled projections, decoding), where reading the
  * weights is the whole cost and quantizing X would only add error.  The
  * products take Xh as a sum of bf16 terms: two for a bf16 Y (Xh to 2^-17), three
- * for an fp32 Y (2^-24); sums are fp32.  Other arguments as svdq_linear_w4a4;
+ * for an fp32 Y (2^-24); sums are fp32.  |Xh| from 0x1.FFp127 on counts as infinite;
+ * products or sums past fp32's range (before sW or ts_w) give infinities or NaNs.  Other arguments as svdq_linear_w4a4;
  * w_tensor_scale is read for NVFP4 only.
  * 0 <= M <= 64 (more rows: SVDQ_ERR_UNSUPPORTED; svdq_linear_w4a4 is the form
  * for them), K % 64 == 0, N % 16 == 0, rank % 16 == 0, 0 <= rank <= 256. */
@@ -335,7 +339,7 @@ svdq_status svdq_linear_w4a16(const void* X, svdq_dtype x_dtype, int64_t M, int6
                               hipStream_t stream);
 
 /* A gated feed-forward block's first half on two AWQ layers of the same
- * shape, both projections, the activation and the product in one pass:
+ * shape, both projections, the activation and the product in one call:
  *   G = X . wd_gate^T + bias_gate,  U = X . wd_up^T + bias_up,  H = act(G) * U
  * with wd = bf16((q - z) s) as in awq_linear_w4a16.  G and U are fp32 until H is
  * rounded to h_dtype.  G_out, U_out: DEVICE bf16 [M, N], both or neither
@@ -369,7 +373,7 @@ svdq_status awq_gated_w4a16_grad(const uint16_t* dH, const uint16_t* G, const ui
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Input gradient of an AWQ layer (frozen weights): dX = dY . wd, dY bf16
- * [M, N], dX [M, K] of dx_dtype, fp32 sums.  Sizes as awq_linear_w4a16. */
+ * [M, N], dX [M, K] of dx_dtype, fp32 sums.  Sizes as awq_gated_w4a16. */
 size_t awq_linear_w4a16_grad_workspace_bytes(int64_t M, int64_t K, int64_t N);
 svdq_status awq_linear_w4a16_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
                                   int32_t group, const uint8_t* q, const uint16_t* scales,

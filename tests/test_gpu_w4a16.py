@@ -421,6 +421,66 @@ def test_a_row_of_nans_stays_in_its_row(m):
             assert torch.equal(f(x2, dy2)[keep], r[keep])
 
 
+@pytest.mark.parametrize("m,k,n", [(1, 192, 48), (5, 1088, 208), (40, 576, 304), (64, 1856, 5008),
+                                   (70, 192, 80), (600, 320, 272), (1100, 192, 528)])
+def test_infinite_inputs_show_in_every_output(m, k, n):
+    """One infinity in a row makes the whole row of the products infinite or NaN,
+    in every form, wherever it lies; the other rows stay finite."""
+    gate, _ = awq_layer(n, k, 96)
+    up, _ = awq_layer(n, k, 97)
+    for at in (0, -3):
+        x, dy = bf((m, k), 98), bf((m, n), 99)
+        x[m - 1, at], dy[m - 1, at] = float("-inf"), float("inf")
+        H, G, U = svdq.awq_gated_w4a16(x, gate, up, "gelu", save=True)
+        ones = torch.ones_like(dy)
+        out = (H, G, U, svdq.awq_linear_w4a16_grad(dy, gate),
+               svdq.awq_gated_w4a16_grad(dy, ones, ones, gate, up)[0])
+        for t in out:
+            assert not torch.isfinite(t[m - 1]).any() and torch.isfinite(t[:m - 1]).all()
+
+
+@pytest.mark.parametrize("m,k,n", [(1, 192, 48), (17, 1088, 8208), (64, 320, 272)])
+@pytest.mark.parametrize("prec", ["int4", "nvfp4"])
+def test_large_and_infinite_inputs_of_a16(m, k, n, prec):
+    """svdq_linear_w4a16: a row with an infinity is NaN, and leaves a row with a
+    finite value near the top of the range as it is."""
+    d, parts = svdq_layer(n, k, 0, prec, 99)
+    d["smooth"] = torch.ones_like(d["smooth"])
+    x = torch.zeros(m, k, device="cuda")
+    x[m - 1, 1] = 3.0e38
+    if m > 1:
+        x[0, k - 3] = float("inf")
+    w = parts[1]
+    for yt in (F32, BF):
+        Y = svdq.svdq_linear_w4a16(x, d, y_dtype=yt)
+        # 3e38 is a finite bf16 sum of terms; its products are in range before the
+        # scale (INT4) or tensor scale (NVFP4) where the weight's code is 1 at most.
+        # (Beyond that, up to 3e38 x 2688, the products of two terms of opposite
+        # sign overflow both, and fp32 holds no value of the sum.)
+        scale = d["wscales"][0].double() if prec == "int4" else d["w_tensor_scale"].double()
+        fits = w[:, 1].abs() / scale <= 1.001
+        ref = x[m - 1, 1].double() * w[:, 1]
+        assert fits.any()
+        check(Y[m - 1][fits], ref[fits], ref[fits].abs() * 2.0 ** -7, "large")
+        if m > 1:
+            assert torch.isnan(Y[0]).all() and (Y[1:m - 1] == 0).all()
+
+
+def test_gate_gradient_far_out():
+    """act' between -40 and -80, where it is small but no zero (1e-17 to 1e-33)."""
+    m, k, n = 3, 64, 64
+    gate, _ = awq_layer(n, k, 87)
+    up, _ = awq_layer(n, k, 88)
+    G = -torch.linspace(40, 80, m * n, device="cuda").view(m, n).to(BF)
+    ones = torch.ones_like(G)
+    a, da = act64(G.double(), "silu")
+    # exp2's argument is rounded: 2^-24 of 116 moves the result by 116 ln 2 2^-24 < 2^-17,
+    # and 1 + x is 1 / 39 of x at least
+    _, dG, dU = svdq.awq_gated_w4a16_grad(ones, G, ones, gate, up)
+    check(dG, da, da.abs() * 2.0 ** -15 + round_tol(da, BF), "dG")
+    check(dU, a, a.abs() * 2.0 ** -15 + round_tol(a, BF), "dU")
+
+
 def test_offsets_past_32_bits():
     """H and dY of more than 2^31 elements (4.4 GB): the last rows and a sample
     of the others."""

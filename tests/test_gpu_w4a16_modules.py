@@ -182,7 +182,7 @@ def test_svdq_linear_few_rows(prec):
     ref = x[:12].double() @ lin.weight.double().t() + lin.bias.double()
     assert (y.double() - ref).norm() < (a(x[:12]).double() - ref).norm()
     assert b(x[:0]).shape == (0, 272)
-    # alternating sizes reuse one workspace
+    # alternating sizes
     assert torch.equal(b(x[:12]), y) and torch.equal(b(x), a(x)) and torch.equal(b(x[:12]), y)
 
 

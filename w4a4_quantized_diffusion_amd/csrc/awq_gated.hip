@@ -1,4 +1,4 @@
-// Gated feed-forward pair of AWQ W4A16 layers (gfx950), in one kernel:
+// Gated feed-forward pair of AWQ W4A16 layers (gfx950):
 //
 //   G = X Wg^T + bg,  U = X Wu^T + bu,  H = act(G) * U
 //
@@ -245,7 +245,8 @@ __global__ __launch_bounds__(NT, MT == 1 ? 6 : 4) void gated_column_kernel(
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       Slot& sl = ring[d];
-      // past the last chunk the scales are zeros
+      // past the last chunk the scales are zeros (which leaves an infinite X a NaN;
+      // zeros for X too cost 33 rows 2048 -> 5456 0.7 us)
       const bool live = c + d < count;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -348,8 +349,8 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
 
 // 64 rows of the pair matrix and four groups of 64 k (two stages each) per
 // workgroup (2 x 12288 x 4096: 258 MB in 49 us, 5.3 TB/s; one group per workgroup,
-// with fewer loads in flight, took 62); rows past N are zeros.  Four lanes take one row, 8 k of each stage,
-// so that a wave stores 1 KB in a row.
+// with fewer loads in flight, took 62); rows past N are zeros.  Four lanes take
+// one row, 8 k of each stage, so that a wave stores 1 KB in a row.
 constexpr int DEQUANT_GROUPS = 4;
 
 __global__ __launch_bounds__(256) void pair_dequant_kernel(svdq::AwqWeight wg, svdq::AwqWeight wu,
@@ -491,7 +492,8 @@ size_t pair_bytes(int64_t K, int64_t N) {
 // bytes of the partial sums of `rows` rows
 size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
   if (rows == 0 || (rows <= ROWS && one_launch(rows, K, N))) return 0;
-  const int S = rows <= ROWS ? split(rows, K, N).slices : svdq_mid::slices(mid_tiles(rows, N), K / 64);
+  const int S = rows <= ROWS ? split(rows, K, N).slices
+                             : svdq_mid::slices(mid_tiles(rows, N), K / 64);
   return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * 2 * size_t(rows) * size_t(N) * 4);
 }
 
@@ -576,7 +578,8 @@ svdq_status mid(const Call& c, float* part) {
 }
 
 svdq_status wide(const Call& c, uint16_t* B) {
-  hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((c.N + 31) / 32 * ((c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS))), dim3(256), 0,
+  const int64_t quads = (c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS;
+  hipLaunchKernelGGL(pair_dequant_kernel, dim3(unsigned((c.N + 31) / 32 * quads)), dim3(256), 0,
                      c.s, c.wg, c.wu, int(c.K), int(c.N), B);
   SVDQ_TRY(svdq::check_launch("pair_dequant"));
   const int64_t rows = pair_rows(c.N), tiles = (c.M + 255) / 256 * ((rows + 255) / 256);

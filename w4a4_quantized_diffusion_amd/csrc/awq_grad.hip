@@ -130,7 +130,8 @@ struct Rows {
 
 // 8 values of the pair's dG (layer 0) or dU (layer 1)
 template <int ACT>
-__device__ __forceinline__ uint4 pair_grad8(const uint4 h, const uint4 g, const uint4 u, int layer) {
+__device__ __forceinline__ uint4 pair_grad8(const uint4 h, const uint4 g, const uint4 u,
+                                            int layer) {
   const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, gw[4] = {g.x, g.y, g.z, g.w},
                  uw[4] = {u.x, u.y, u.z, u.w};
   uint32_t o[4];
@@ -223,7 +224,8 @@ __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::A
     for (int c = wave; c < here; c += WAVES) {
       const bool live = row8(c0 + c) < N;
       uint32_t o[8][4];
-      const uint32_t sw[4] = {sl.s.x, sl.s.y, sl.s.z, sl.s.w}, zw[4] = {sl.z.x, sl.z.y, sl.z.z, sl.z.w};
+      const uint32_t sw[4] = {sl.s.x, sl.s.y, sl.s.z, sl.s.w};
+      const uint32_t zw[4] = {sl.z.x, sl.z.y, sl.z.z, sl.z.w};
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         float v[2][8];
@@ -479,7 +481,8 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
   zero_acc(acc);
   GradWeights w(wa, wb, K, N, p.chunks, k0);
   const int64_t total = int64_t(p.chunks) * p.segments;
-  tile_product(p, m0, int(slice * total / S), int((slice + 1) * total / S), w, a0, a1, a2, b0, b1, acc);
+  tile_product(p, m0, int(slice * total / S), int((slice + 1) * total / S), w, a0, a1, a2, b0, b1,
+               acc);
   const int64_t row0 = m0 + (wave >> 1) * 64, col0 = k0 + (wave & 1) * 64;
   float* const eb = reinterpret_cast<float*>(wave == 0   ? &a0.v
                                               : wave == 1 ? &a1.v
@@ -573,8 +576,8 @@ svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int
   float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 1) : 0));
   const uint16_t* const d = dY + w * N;
   void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
-  if (rest <= ROWS)
-    return run_rows<PLAIN>(Rows{d, nullptr, nullptr, nullptr, nullptr}, rest, K, N, &wt, x, xb, part, s);
+  const Rows in{d, nullptr, nullptr, nullptr, nullptr};
+  if (rest <= ROWS) return run_rows<PLAIN>(in, rest, K, N, &wt, x, xb, part, s);
   return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, s);
 }
 
@@ -600,7 +603,8 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
   auto k = act == SVDQ_SILU ? gate_grad_kernel<SVDQ_SILU> : gate_grad_kernel<SVDQ_GELU>;
   hipLaunchKernelGGL(k, dim3(blocks), dim3(256), 0, s, dH, G, U, n8, dG, dU);
   SVDQ_TRY(check_launch("gate_grad"));
-  if (w) SVDQ_TRY(launch_wide(dG, dU, wt, 2, w, K, N, dX, true, reinterpret_cast<uint16_t*>(w8), s));
+  if (w)
+    SVDQ_TRY(launch_wide(dG, dU, wt, 2, w, K, N, dX, true, reinterpret_cast<uint16_t*>(w8), s));
   if (!rest || fused) return SVDQ_OK;
   if (rest <= ROWS) return run_rows<PLAIN_PAIR>(in, rest, K, N, wt, x, true, part, s);
   return launch_mid(in.dG, in.dU, wt, 2, rest, K, N, x, true, part, s);

@@ -22,10 +22,11 @@
 // cycles gains less than the cycles it saves.  (torch's library product of the same
 // shapes takes 645 and 573 us.)
 //
-// LDS rows are 64 bytes, 4 slots of 16; slot s of row r holds piece s ^ ((r >> 2) & 3), so that the 16
-// lanes of one ds_read_b128 phase (rows r..r+15, one piece) touch 16 different
-// groups of 4 banks.  The load unit writes a wave's 64 pieces consecutively, so
-// the permutation is applied to the global addresses.
+// LDS rows are 64 bytes, 4 slots of 16; slot s of row r holds piece
+// s ^ ((r >> 2) & 3), so that the 16 lanes of one ds_read_b128 phase (rows
+// r..r+15, one piece) touch 16 different groups of 4 banks.  The load unit writes a
+// wave's 64 pieces consecutively, so the permutation is applied to the global
+// addresses.
 #pragma once
 
 #include "w4a16.h"
@@ -101,7 +102,8 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
   const int seg = 2 * p.chunks, total = seg * p.segments;
   const uint8_t* const a0 = reinterpret_cast<const uint8_t*>(p.A[0] + m0 * p.width);
   const uint8_t* const a1 = reinterpret_cast<const uint8_t*>(p.A[1] + m0 * p.width);
-  const uint8_t* const bb = reinterpret_cast<const uint8_t*>(p.B) + b0 / BN * total * int64_t(BLOCK_BYTES);
+  const uint8_t* const bb =
+      reinterpret_cast<const uint8_t*>(p.B) + b0 / BN * total * int64_t(BLOCK_BYTES);
   // transfer t of stage s: 0, 1 of A, 2, 3 of B
   const uint8_t *asrc, *bsrc;
   uint32_t apiece;

@@ -23,8 +23,9 @@ namespace {
 
 // A float as a sum of T bf16 terms, largest first: two terms hold it to 2^-17,
 // three to 2^-24 (each term is the rounding of what the ones before left; the
-// subtractions are exact).  A value whose rounding overflows keeps an infinite
-// first term.
+// subtractions are exact).  An infinite value, and one from 0x1.FFp127 on, whose
+// rounding overflows, gives an infinity and NaN: their row of Y is NaN.  (Terms that
+// keep the infinity cost the 61-row case its registers, 29 to 38 us.)
 template <int T>
 __device__ __forceinline__ void split_bf16(const float (&x)[8], uint4 (&t)[T]) {
   float r[8];
@@ -459,15 +460,12 @@ struct Call {
 
 template <int PREC, int MT, int T, int CT>
 svdq_status run(const Call& c, const Split& p) {
-  // chunks of Xh that fit LDS (at least D do: 64 rows x 3 terms x (4 x 128 + 16) = 99 KB)
+  // chunks of Xh that fit LDS (at least D do: 64 rows x 3 terms x (2 x 128 + 16) = 52 KB)
   const int most = (LDS_X / (c.M * T) - 16) / 128 / D * D;
   const int len = (c.K / 64 + p.slices - 1) / p.slices;
-  const int sub = std::min(std::max(most, D), (len + D - 1) / D * D);
+  const int sub = std::min(most, (len + D - 1) / D * D);
   const size_t shm = std::max(size_t(c.M) * T * (sub * 128 + 16), size_t(WAVES) * 1024);
   auto k = a16_slice_kernel<PREC, MT, T, CT>;
-  if (shm > (64 << 10))
-    SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(shm)));
   const int LS = lr_slices(c.K), lr_blocks = MT * (c.rank / 16) * LS;
   hipLaunchKernelGGL(k, dim3(unsigned(lr_blocks + p.blocks * p.slices)), dim3(NT), shm, c.s, c.X,
                      c.xbf16, c.M, c.K, c.N, c.rank, LS, lr_blocks, p.slices, sub, c.smooth, c.down,
