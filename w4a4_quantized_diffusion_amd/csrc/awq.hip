@@ -26,7 +26,7 @@
 //    the LDS buffer the MFMAs are not reading, one chunk ahead; one barrier
 //    per chunk.
 
-#include "internal.h"
+#include "w4a16.h"
 
 #include <type_traits>
 

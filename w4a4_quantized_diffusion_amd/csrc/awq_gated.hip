@@ -454,7 +454,7 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void gated_mid_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slice = blockIdx.x / tiles;
   int64_t m0, n0;
-  tile_origin(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (N + 63) / 64, BM, 64, m0, n0);
+  tile_at(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (N + 63) / 64, BM, 64, m0, n0);
   v16f acc[RBL][CBL];
   zero_acc(acc);
   PairWeights w(wg, wu, N, n0);

@@ -476,7 +476,7 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slice = blockIdx.x / tiles;
   int64_t m0, k0;
-  tile_origin(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (K + BN - 1) / BN, BM, BN, m0, k0);
+  tile_at(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (K + BN - 1) / BN, BM, BN, m0, k0);
   v16f acc[RBL][CBL];
   zero_acc(acc);
   GradWeights w(wa, wb, K, N, p.chunks, k0);

@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stddef.h>
-#include <algorithm>
 #include <string>
 
 #include "../../include/svdq.h"
@@ -23,12 +22,6 @@ svdq_status check_launch(const char* what);
     if (e_ != hipSuccess)                                                      \
       return ::svdq::fail(SVDQ_ERR_HIP, std::string(#expr) + ": " +            \
                                             hipGetErrorString(e_));            \
-  } while (0)
-
-#define SVDQ_TRY(x)                       \
-  do {                                    \
-    svdq_status st_ = (x);                \
-    if (st_ != SVDQ_OK) return st_;       \
   } while (0)
 
 constexpr int GROUP = 64;   // INT4 group along K
@@ -79,35 +72,6 @@ svdq_status launch_awq_linear(const uint16_t* X, int64_t M, int64_t K, int64_t N
                               const uint16_t* zeros, const uint16_t* bias, void* Y,
                               svdq_dtype y_dt, hipStream_t s);
 
-// an AWQ layer's weights: q [K/64][N][32 bytes], scales and zeros bf16 [K/64][N]
-struct AwqWeight {
-  const uint8_t* q;
-  const uint16_t* s;
-  const uint16_t* z;
-};
-// Bytes of the caller's workspace for valid sizes (a multiple of 256, 0: none)
-size_t awq_gated_workspace(int64_t M, int64_t K, int64_t N);
-size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N);
-size_t awq_gated_grad_workspace(int64_t M, int64_t K, int64_t N);
-size_t linear_a16_workspace(int64_t M, int64_t K, int64_t N, int rank);
-svdq_status launch_awq_gated(const uint16_t* X, int64_t M, int64_t K, int64_t N, AwqWeight wg,
-                             AwqWeight wu, const uint16_t* bg, const uint16_t* bu, svdq_act act,
-                             void* H, svdq_dtype h_dt, uint16_t* G, uint16_t* U, void* ws,
-                             hipStream_t s);
-svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
-                                   AwqWeight w, void* dX, svdq_dtype x_dt, void* ws,
-                                   hipStream_t s);
-svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
-                                  int64_t M, int64_t K, int64_t N, AwqWeight wg, AwqWeight wu,
-                                  svdq_act act, uint16_t* dX, uint16_t* dG, uint16_t* dU, void* ws,
-                                  hipStream_t s);
-svdq_status launch_linear_a16(const void* X, svdq_dtype x_dt, int64_t M, int64_t K, int64_t N,
-                              int rank, svdq_precision prec, const float* smooth,
-                              const uint16_t* down, const uint16_t* up, const uint8_t* wcodes,
-                              const void* wscales, const float* ts_w, const void* bias,
-                              svdq_dtype bias_dt, void* Y, svdq_dtype y_dt, void* ws,
-                              hipStream_t s);
-
 }  // namespace svdq
 
 // ------------------------------------------------------------ device helpers
@@ -138,34 +102,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return uint16_t(pack_bf16x2(f, 0.f));
-}
-
-// 8 unsigned nibbles of an AWQ layer (one dword, even k low) -> (q - z) s in k
-// order, in fp32 and rounded to bf16 (4 dwords).  zs = -z s (exact in fp32).  A
-// byte 0x0q read as FP8-E4M3 is q 2^-9 for every q in 0..15 (a subnormal below 8,
-// exponent field 1 from 8 on), so the scaled conversion with the power of two
-// 2^9 gives q exactly, two codes per instruction.
-__device__ __forceinline__ void dequant8_f32(uint32_t w, float s, float zs, float (&v)[8]) {
-  const int e = int(w & 0x0F0F0F0Fu), o = int((w >> 4) & 0x0F0F0F0Fu);
-  const v2f32_t q02 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 512.0f, false);
-  const v2f32_t q46 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 512.0f, true);
-  const v2f32_t q13 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(o, 512.0f, false);
-  const v2f32_t q57 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(o, 512.0f, true);
-  v[0] = fmaf(q02.x, s, zs);
-  v[1] = fmaf(q13.x, s, zs);
-  v[2] = fmaf(q02.y, s, zs);
-  v[3] = fmaf(q13.y, s, zs);
-  v[4] = fmaf(q46.x, s, zs);
-  v[5] = fmaf(q57.x, s, zs);
-  v[6] = fmaf(q46.y, s, zs);
-  v[7] = fmaf(q57.y, s, zs);
-}
-
-__device__ __forceinline__ uint4 dequant8(uint32_t w, float s, float zs) {
-  float v[8];
-  dequant8_f32(w, s, zs, v);
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
 }
 
 // E4M3 code of a non-negative float: round to nearest even, saturating at
@@ -264,19 +200,16 @@ __device__ __forceinline__ void store_wave_tile(const v16f (&acc)[RBL][CBL],
 // one XCD runs at a time cover about 4 row tiles by 8 column tiles and their
 // A rows and W rows stay in that XCD's L2 (about a third less HBM traffic
 // than a whole column of row tiles at a time).
-__device__ __forceinline__ void tile_origin(int t, int tiles_m, int tiles_n, int bm, int bn,
+__device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bm, int bn,
                                             int64_t& m0, int64_t& n0) {
   constexpr int GN = 8;
   const int total = tiles_m * tiles_n;
+  int t = blockIdx.x;
   if ((total & 7) == 0) t = (t & 7) * (total >> 3) + (t >> 3);
   const int grp = t / (GN * tiles_m), in = t - grp * (GN * tiles_m);
   const int gn = min(GN, tiles_n - grp * GN);
   m0 = int64_t(in / gn) * bm;
   n0 = int64_t(grp * GN + in % gn) * bn;
-}
-__device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bm, int bn,
-                                            int64_t& m0, int64_t& n0) {
-  tile_origin(int(blockIdx.x), tiles_m, tiles_n, bm, bn, m0, n0);
 }
 
 }  // namespace svdq_dev

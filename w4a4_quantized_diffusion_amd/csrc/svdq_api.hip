@@ -1,7 +1,7 @@
 // C ABI front end: argument validation, workspace layout, dispatch, and the
 // per-thread error message.  Every check runs before any HIP call.
 
-#include "internal.h"
+#include "w4a16.h"
 
 #include <cstdio>
 #include <mutex>
