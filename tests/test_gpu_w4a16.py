@@ -96,7 +96,7 @@ def gated_ref(x, wg, wu, bg, bu, act):
 
 
 GATED = [(1, 64, 16), (1, 1024, 2736), (2, 192, 48), (17, 320, 112), (33, 128, 80), (64, 1024, 272),
-         (65, 64, 16), (100, 640, 400), (130, 256, 144), (257, 448, 528), (300, 1088, 272),
+         (65, 64, 16), (100, 640, 400), (17, 4096, 16), (33, 8192, 272), (64, 4160, 1008), (130, 256, 144), (257, 448, 528), (300, 1088, 272),
          (1030, 512, 768), (2050, 320, 336)]
 
 
@@ -321,7 +321,8 @@ def a16_ref(x, parts, bias, split):
 
 
 A16 = [(1, 64, 16, 0), (1, 1024, 1024, 16), (2, 128, 48, 32), (3, 1088, 208, 48), (16, 512, 272, 32),
-       (17, 640, 400, 0), (33, 192, 144, 256), (48, 2048, 96, 64), (64, 1024, 528, 32)]
+       (17, 640, 400, 0), (33, 192, 144, 256), (48, 2048, 96, 64), (64, 1024, 528, 32),
+       (17, 8256, 16, 16), (54, 7424, 256, 48)]
 
 
 @pytest.mark.parametrize("m,k,n,rank", A16)

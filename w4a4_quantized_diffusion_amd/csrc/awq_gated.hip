@@ -68,7 +68,7 @@ constexpr int ROWS = 64;                 // the most rows of this form
 constexpr int WAVES = 8, NT = 64 * WAVES;
 constexpr int D = 2;
 constexpr int LDS_X = 64 << 10;
-constexpr int MAX_SLICES = 8;
+constexpr int SUM_SLICES = 8;            // slices that the second launch loads at once
 
 // The two-launch form, 64 rows 4096 -> 12288: 34 us (X and the partial sums in the
 // L2 and the dequantization share the time).
@@ -78,20 +78,28 @@ struct Split {
 
 // About 512 workgroups, two to a compute unit.  Above 16 rows the partial sums
 // are more than the weights, so there are at most 4 slices: 33 rows 2048 -> 5456
-// took 14.2 us in 8 and 13.1 in 4 (one row 4096 -> 12288, 15.7 in 5 and 17.6 in 4).
+// took 14.2 us in 8 and 13.1 in 4 (one row 4096 -> 12288, 15.7 in 5 and 17.6 in 4);
+// but narrow layers, where that leaves most of the chip idle, get more, of at least 4
+// chunks, up to 128 workgroups.
 Split split(int64_t M, int64_t K, int64_t N) {
   Split p;
   p.blocks = int((N + 16 * WAVES - 1) / (16 * WAVES));
   p.slices = int(std::min<int64_t>(
-      {K / 64, M > 16 ? MAX_SLICES / 2 : MAX_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+      {K / 64, M > 16 ? SUM_SLICES / 2 : SUM_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+  if (M > 16) p.slices = std::max(p.slices, int(std::min<int64_t>({K / 256, 32, 128 / p.blocks})));
   return p;
 }
 
 // Whether few rows take one launch (gated_column_kernel), where every 16 columns
 // read all of X: N / 16 times 2 M K bytes from the L2.  Measured: 20 rows
 // 4096 -> 12288 (M N K = 1.0e9) 22 us either way, one row 13.8 against 16.2, 20
-// rows 1024 -> 2048 4.0 against 7.9, but 64 rows 4096 -> 12288 49 against 34.
-bool one_launch(int64_t M, int64_t K, int64_t N) { return M * N <= (int64_t(1) << 30) / K; }
+// rows 1024 -> 2048 4.0 against 7.9, but 64 rows 4096 -> 12288 49 against 34.  On
+// more than 16 rows a long K and few columns take too long in the N / 16 workgroups:
+// 33 rows 8192 -> 512 20.9 against 12.3, 64 rows 4096 -> 1024 17.9 against 13.1 (20
+// rows 4096 -> 512 8.6 against 8.8, and 33 rows 4096 -> 2048 stay at 12.1).
+bool one_launch(int64_t M, int64_t K, int64_t N) {
+  return M * N <= (int64_t(1) << 30) / K && !(M > 16 && K >= 4096 && N <= 1024);
+}
 
 template <int MT>
 __global__ __launch_bounds__(NT, 4) void gated_slice_kernel(
@@ -305,9 +313,9 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
   if (i >= total) return;
   const int64_t n = 4 * i % N;
   // all loads first; a slice past the last counts as zeros
-  v4f v[MAX_SLICES][2];
+  v4f v[SUM_SLICES][2];
 #pragma unroll
-  for (int q = 0; q < MAX_SLICES; ++q)
+  for (int q = 0; q < SUM_SLICES; ++q)
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       v[q][t] = reinterpret_cast<const v4f*>(part)[(2 * int64_t(min(q, S - 1)) + t) * total + i];
@@ -320,9 +328,27 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
   for (int t = 0; t < 2; ++t) {
     p[t] = v4f{0, 0, 0, 0};
 #pragma unroll
-    for (int q = 0; q < MAX_SLICES; ++q)
+    for (int q = 0; q < SUM_SLICES; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[t][e] += q < S ? v[q][t][e] : 0.f;
+  }
+  for (int q0 = SUM_SLICES; q0 < S; q0 += SUM_SLICES) {
+#pragma unroll
+    for (int q = 0; q < SUM_SLICES; ++q)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        v[q][t] =
+            reinterpret_cast<const v4f*>(part)[(2 * int64_t(min(q0 + q, S - 1)) + t) * total + i];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int q = 0; q < SUM_SLICES; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[t][e] += q0 + q < S ? v[q][t][e] : 0.f;
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
     p[t][0] += __uint_as_float(b[t].x << 16);
     p[t][1] += __uint_as_float(b[t].x & 0xFFFF0000u);
     p[t][2] += __uint_as_float(b[t].y << 16);

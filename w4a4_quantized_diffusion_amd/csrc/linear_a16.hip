@@ -10,7 +10,7 @@
 //
 // Measured, both launches: one row 4096 -> 24576 INT4 (59 MB) 15 us, of which the
 // first launch takes 11.2 (5.2 TB/s, part of it from the Infinity Cache); 7 rows
-// 4096 -> 12288 NVFP4 13.5 us; 61 rows 2752 -> 10928 in three terms 28 us, shared by
+// 4096 -> 12288 NVFP4 13.5 us; 61 rows 2752 -> 10928 in three terms 27 us, shared by
 // the partial sums (9 us), the terms of Xh (4) and the products (5 for the terms
 // beyond the first); 1024 x 1024 one row 6.2 us, two launches and two trips to
 // memory.
@@ -80,8 +80,11 @@ __device__ __forceinline__ void load8(const float* f, float (&v)[8]) {
 
 constexpr int WAVES = 8, NT = 64 * WAVES;
 constexpr int D = 2;                     // chunks of weights in flight per wave
-constexpr int LDS_X = 64 << 10;          // LDS for the terms of Xh
-constexpr int MAX_SLICES = 8;            // of K, one workgroup each
+// LDS for the terms of Xh; the second where every workgroup has a compute unit to
+// itself (the fewer times the terms are made anew: 61 rows 2752 -> 10928 28.7 to 27.4
+// us, 64 rows 4096 -> 12288 31.6 to 29.5)
+constexpr int LDS_X = 64 << 10, LDS_ALONE = 152 << 10;
+constexpr int SUM_SLICES = 8;            // slices of K that the second launch loads at once
 constexpr int LR_STEPS = 4;              // steps of 32 k per wave of LR, loaded at once
 constexpr int MAX_LR = 4;
 
@@ -375,9 +378,9 @@ __global__ __launch_bounds__(256) void a16_sum_kernel(
   };
   // all loads first; a slice past the last counts as zeros
   if (rank) load_low(0);
-  float v[MAX_SLICES][4];
+  float v[SUM_SLICES][4];
 #pragma unroll
-  for (int q = 0; q < MAX_SLICES; ++q)
+  for (int q = 0; q < SUM_SLICES; ++q)
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[q][e] = p[e][int64_t(min(q, S - 1)) * M * N];
   const float ts = ts_w ? ts_w[0] : 1.f;
@@ -403,9 +406,20 @@ __global__ __launch_bounds__(256) void a16_sum_kernel(
     }
   }
 #pragma unroll
-  for (int q = 0; q < MAX_SLICES; ++q)
+  for (int q = 0; q < SUM_SLICES; ++q)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] += q < S ? v[q][e] : 0.f;
+  for (int q0 = SUM_SLICES; q0 < S; q0 += SUM_SLICES) {
+#pragma unroll
+    for (int q = 0; q < SUM_SLICES; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q][e] = p[e][int64_t(min(q0 + q, S - 1)) * M * N];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < SUM_SLICES; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += q0 + q < S ? v[q][e] : 0.f;
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int64_t m = m0 + 4 * j + e;
@@ -426,11 +440,11 @@ struct Split {
   int ct, blocks, slices;
 };
 
-Split split(int64_t K, int64_t N) {
+Split split(int64_t M, int64_t K, int64_t N) {
   Split p;
   p.ct = N >= 8192 ? 2 : 1;
   p.blocks = int((N + 16 * WAVES * p.ct - 1) / (16 * WAVES * p.ct));
-  const int most = int(std::min<int64_t>({K / 64, MAX_SLICES, std::max(1, 512 / p.blocks)}));
+  const int most = int(std::min<int64_t>({K / 64, SUM_SLICES, std::max(1, 512 / p.blocks)}));
   p.slices = 1;
   double best = 0;
   for (int S = 1; S <= most; ++S) {
@@ -438,6 +452,11 @@ Split split(int64_t K, int64_t N) {
     const double used = double(n) / double((n + 255) / 256 * 256);
     if (used >= best) best = used, p.slices = S;
   }
+  // Narrow layers on more than 16 rows, bound by the products: more slices, of at
+  // least 4 chunks, up to 128 workgroups (54 rows 7424 -> 256: 27.4 us in 8 slices,
+  // 14.9 in 29; but one row 8.0 and 10.6)
+  if (M > 16)
+    p.slices = std::max(p.slices, int(std::min<int64_t>({K / 256, 32, 128 / p.blocks})));
   return p;
 }
 
@@ -461,12 +480,16 @@ struct Call {
 template <int PREC, int MT, int T, int CT>
 svdq_status run(const Call& c, const Split& p) {
   // chunks of Xh that fit LDS (at least D do: 64 rows x 3 terms x (2 x 128 + 16) = 52 KB)
-  const int most = (LDS_X / (c.M * T) - 16) / 128 / D * D;
+  const int LS = lr_slices(c.K), lr_blocks = MT * (c.rank / 16) * LS;
+  const int room = lr_blocks + p.blocks * p.slices <= 256 ? LDS_ALONE : LDS_X;
+  const int most = (room / (c.M * T) - 16) / 128 / D * D;
   const int len = (c.K / 64 + p.slices - 1) / p.slices;
   const int sub = std::min(most, (len + D - 1) / D * D);
   const size_t shm = std::max(size_t(c.M) * T * (sub * 128 + 16), size_t(WAVES) * 1024);
   auto k = a16_slice_kernel<PREC, MT, T, CT>;
-  const int LS = lr_slices(c.K), lr_blocks = MT * (c.rank / 16) * LS;
+  if (shm > (64 << 10))
+    SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(shm)));
   hipLaunchKernelGGL(k, dim3(unsigned(lr_blocks + p.blocks * p.slices)), dim3(NT), shm, c.s, c.X,
                      c.xbf16, c.M, c.K, c.N, c.rank, LS, lr_blocks, p.slices, sub, c.smooth, c.down,
                      c.codes, c.scales, c.LR, c.part);
@@ -494,7 +517,7 @@ svdq_status run_prec(const Call& c, const Split& p) {
 }
 
 size_t part_bytes(int64_t M, int64_t K, int64_t N) {
-  return svdq::align256(size_t(split(K, N).slices) * size_t(M) * size_t(N) * 4);
+  return svdq::align256(size_t(split(M, K, N).slices) * size_t(M) * size_t(N) * 4);
 }
 
 }  // namespace
@@ -515,7 +538,7 @@ svdq_status launch_linear_a16(const void* X, svdq_dtype x_dt, int64_t M, int64_t
                static_cast<const uint32_t*>(wscales), ts_w, bias, bias_dt == SVDQ_BF16, Y,
                y_dt == SVDQ_BF16, static_cast<float*>(ws),
                reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part_bytes(M, K, N)), s};
-  const Split p = split(K, N);
+  const Split p = split(M, K, N);
   return prec == SVDQ_INT4 ? run_prec<SVDQ_INT4>(c, p) : run_prec<SVDQ_NVFP4>(c, p);
 }
 
