@@ -270,7 +270,11 @@ class AWQGatedLinear(nn.Module):
     nn.Linear(K, N), the activation and the product.  act: "silu" or "gelu"
     (tanh form).  Inputs bf16 [..., K]; output bf16.  Differentiable once in its
     input (the forward pass then keeps both pre-activations in bf16); weights and
-    biases are frozen.  An AWQLinear(N, K) behind it completes the block."""
+    biases are frozen.  An AWQLinear(N, K) behind it completes the block.
+
+    Forward and backward can be captured into a graph together.  A backward pass
+    that is captured needs leaves of its own: torch ends the process when an eager
+    graph of the same leaves is still alive then."""
 
     def __init__(self, gate, up, bias_gate=None, bias_up=None, act="silu"):
         super().__init__()
