@@ -555,6 +555,36 @@ def test_captured_and_replayed(m):
         assert all(torch.equal(a, b) for a, b in zip(out, eager)), f"replay {i}"
 
 
+def test_captured_narrow_layers():
+    """The forms with many slices and with most of a compute unit's LDS, captured
+    with workspaces that hold NaN before every replay."""
+    d, _ = svdq_layer(256, 7424, 48, "int4", 71)
+    gate, _ = awq_layer(272, 8192, 72)
+    up, _ = awq_layer(272, 8192, 73)
+    x, x2 = bf((54, 7424), 74), bf((33, 8192), 75)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in
+          (svdq.svdq_linear_w4a16_workspace_bytes(54, 7424, 256, 48),
+           svdq.awq_gated_w4a16_workspace_bytes(33, 8192, 272))]
+
+    def run():
+        return (svdq.svdq_linear_w4a16(x, d, workspace=ws[0]),
+                svdq.awq_gated_w4a16(x2, gate, up, workspace=ws[1]))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in range(3):
+        x.copy_(bf((54, 7424), 76 + i))
+        x2.copy_(bf((33, 8192), 86 + i))
+        eager = run()
+        for w in ws:
+            w.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.isfinite(a).all() and torch.equal(a, b) for a, b in zip(out, eager)), i
+
+
 def test_other_stream_and_dirty_workspace():
     """On another stream than the default, and with workspaces full of NaNs."""
     m, k, n = 37, 256, 320
