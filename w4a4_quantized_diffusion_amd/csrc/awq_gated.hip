@@ -425,7 +425,7 @@ __global__ __launch_bounds__(svdq_gemm::NT) void gated_wide_kernel(
   zero_acc(acc);
   tile_product(p, m0, b0, st0, st1, st2, st3, st4, acc);
 
-  gated_epilogue<ACT>(acc, reinterpret_cast<float*>(&st0) + wave * (32 * 36), lane, m0 + wm * WM,
+  gated_epilogue<ACT>(acc, epilogue_buffer<32 * 36>(wave, st0, st1, st2), lane, m0 + wm * WM,
                       b0 / 2 + wn * 32, p.M, N, bg, bu, H, hbf16, Gs, Us);
 }
 

@@ -393,7 +393,7 @@ __global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Arg
   zero_acc(acc);
   tile_product(p, m0, b0, st0, st1, st2, st3, st4, acc);
   const int64_t row0 = m0 + (wave >> 2) * WM, col0 = b0 + (wave & 3) * WN;
-  float* const eb = reinterpret_cast<float*>(&st0) + wave * (32 * (WN + 4));
+  float* const eb = epilogue_buffer<32 * (WN + 4)>(wave, st0, st1, st2);
   const float none[CBL] = {0.f, 0.f};
   if (xbf16)
     store_wave_tile<RBL, CBL, true>(acc, none, eb, lane, row0, col0, p.M, p.rows, dX);

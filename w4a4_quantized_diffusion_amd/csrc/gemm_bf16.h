@@ -72,6 +72,27 @@ struct __attribute__((aligned(16))) Stage {
   uint4 b[BN * 4];
 };
 
+// The epilogues use the stages' LDS again: each wave FLOATS consecutive floats inside
+// one Stage (the stages are separate objects, in no promised order, and the compiler
+// takes a pointer into one as apart from the others).  Which of st0, st1, st2 and
+// at which float of it:
+constexpr int EPILOGUE_STAGES = 3;
+
+constexpr int epilogue_stage(int floats, int wave) { return wave / (int(sizeof(Stage)) / (4 * floats)); }
+
+constexpr int epilogue_offset(int floats, int wave) {
+  return wave % (int(sizeof(Stage)) / (4 * floats)) * floats;
+}
+
+template <int FLOATS>
+__device__ __forceinline__ float* epilogue_buffer(int wave, Stage& st0, Stage& st1, Stage& st2) {
+  static_assert(FLOATS % 4 == 0 && epilogue_stage(FLOATS, NT / 64 - 1) < EPILOGUE_STAGES,
+                "the waves' buffers fit the stages");
+  const int s = epilogue_stage(FLOATS, wave);
+  return reinterpret_cast<float*>(s == 0 ? &st0 : s == 1 ? &st1 : &st2) +
+         epilogue_offset(FLOATS, wave);
+}
+
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // acc += the tile at (m0, b0), b0 a row of B.  All 512 threads call it.  The
