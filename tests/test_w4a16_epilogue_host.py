@@ -1,6 +1,7 @@
-"""The LDS that the tiled weight-only kernels use again in their epilogues, without a
-GPU: every wave's buffer lies inside one of the kernel's LDS objects and apart
-from the other waves' (the objects are separate, in no promised order)."""
+"""Epilogues of the weight-only kernels, without a GPU: every wave's LDS buffer lies
+inside one of the kernel's LDS objects and apart from the other waves' (the
+objects are separate, in no promised order), and biases, which are aligned to
+their elements only, are read by element."""
 
 import os
 import re
@@ -46,3 +47,10 @@ def test_kernels_take_their_buffers_from_the_stages():
             text = h.read()
         assert not re.search(r"reinterpret_cast<float\s*\*>\(&st\d", text), f
         assert re.search(r"\bepilogue_buffer<", text), f
+
+
+def test_biases_are_read_by_element():
+    for f in ("awq_gated.hip", "linear_a16.hip"):
+        with open(os.path.join(build.CSRC, f)) as h:
+            text = h.read()
+        assert not re.search(r"reinterpret_cast<const (uint\d|float\d|v\w+)\s*\*>\((bg|bu|bias)\b", text), f

@@ -319,9 +319,13 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       v[q][t] = reinterpret_cast<const v4f*>(part)[(2 * int64_t(min(q, S - 1)) + t) * total + i];
-  uint2 b[2] = {make_uint2(0, 0), make_uint2(0, 0)};
-  if (bg) b[0] = *reinterpret_cast<const uint2*>(bg + n);
-  if (bu) b[1] = *reinterpret_cast<const uint2*>(bu + n);
+  // (a bias is aligned to its elements only)
+  uint16_t b[2][4] = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (bg) b[0][e] = bg[n + e];
+    if (bu) b[1][e] = bu[n + e];
+  }
   __builtin_amdgcn_sched_barrier(0);
   v4f p[2];
 #pragma unroll
@@ -348,12 +352,9 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
         for (int e = 0; e < 4; ++e) p[t][e] += q0 + q < S ? v[q][t][e] : 0.f;
   }
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    p[t][0] += __uint_as_float(b[t].x << 16);
-    p[t][1] += __uint_as_float(b[t].x & 0xFFFF0000u);
-    p[t][2] += __uint_as_float(b[t].y << 16);
-    p[t][3] += __uint_as_float(b[t].y & 0xFFFF0000u);
-  }
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[t][e] += bf16_to_f32(b[t][e]);
   v4f h;
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = gate_act<ACT>(p[0][e]) * p[1][e];
