@@ -319,9 +319,12 @@ svdq_status run_slices(const Rows& in, int64_t M, int64_t K, int64_t N, const sv
   const int sub = int(std::min<int64_t>((room / M - 16) / 64, (steps + p.slices - 1) / p.slices));
   const size_t shm = std::max(size_t(M) * (sub * 64 + 16), size_t(WAVES) * 8 * 1024);
   auto k = grad_slice_kernel<MT, ACT, WAVES>;
+  // (the most that any call asks for: the attribute is the function's, and a host
+  // thread with a smaller call must not lower it between another's two steps)
+  static_assert(WAVES * 8 * 1024 <= 2 * LDS_A, "the sums fit");
   if (shm > (64 << 10))
     SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(shm)));
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, 2 * LDS_A));
   hipLaunchKernelGGL(k, dim3(unsigned(p.blocks * p.slices)), dim3(64 * WAVES), shm, s, in, w[0],
                      w[layers - 1], int(M), int(K), int(N), p.slices, sub, part, dX, xbf16);
   return svdq::check_launch("grad_slice");

@@ -487,9 +487,11 @@ svdq_status run(const Call& c, const Split& p) {
   const int sub = std::min(most, (len + D - 1) / D * D);
   const size_t shm = std::max(size_t(c.M) * T * (sub * 128 + 16), size_t(WAVES) * 1024);
   auto k = a16_slice_kernel<PREC, MT, T, CT>;
+  // (the most that any call asks for: the attribute is the function's, and a host
+  // thread with a smaller call must not lower it between another's two steps)
   if (shm > (64 << 10))
     SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(shm)));
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, LDS_ALONE));
   hipLaunchKernelGGL(k, dim3(unsigned(lr_blocks + p.blocks * p.slices)), dim3(NT), shm, c.s, c.X,
                      c.xbf16, c.M, c.K, c.N, c.rank, LS, lr_blocks, p.slices, sub, c.smooth, c.down,
                      c.codes, c.scales, c.LR, c.part);
