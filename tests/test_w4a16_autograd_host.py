@@ -1,0 +1,91 @@
+"""The modules of the weight-only operators under autograd, without a GPU: the
+binding's calls are replaced by the same mathematics in torch on detached values
+(the kernels read raw memory, so nothing of autograd passes through them)."""
+
+import pytest
+import torch
+import torch.autograd.forward_ad as fwAD
+from torch import nn
+
+from w4a4_quantized_diffusion_amd import linear as L
+from w4a4_quantized_diffusion_amd import svdq
+
+BF = torch.bfloat16
+N, K = 64, 128
+
+
+def awq_layer(n, k, seed):
+    g = torch.Generator().manual_seed(seed)
+    bits = lambda t: t.to(BF).view(torch.int16)  # noqa: E731
+    return dict(N=n, K=k, group=64, q=torch.randint(0, 256, (k // 64, n, 32), generator=g, dtype=torch.uint8),
+                scales=bits(torch.rand(k // 64, n, generator=g) / 50 + 0.01),
+                zeros=bits(torch.randint(6, 10, (k // 64, n), generator=g).float()))
+
+
+def weight(lay):
+    n, k = lay["N"], lay["K"]
+    q = torch.stack((lay["q"] & 15, lay["q"] >> 4), -1).reshape(k // 64, n, 64).float()
+    s, z = (lay[f].detach().view(BF).float().unsqueeze(-1) for f in ("scales", "zeros"))
+    return ((q - z) * s).to(BF).float().permute(1, 0, 2).reshape(n, k)
+
+
+def raw(t):
+    """What a kernel sees of a tensor, checked as the library checks it."""
+    if t is None:
+        return 0.0
+    t = fwAD.unpack_dual(t).primal.detach()
+    assert t.is_contiguous() and t.data_ptr() % 16 == 0
+    return t.float()
+
+
+@pytest.fixture(autouse=True)
+def kernels(monkeypatch):
+    def linear(x, lay, bias=None):
+        return (raw(x) @ weight(lay).t() + raw(bias)).to(BF)
+
+    def linear_grad(dy, lay):
+        return (raw(dy) @ weight(lay)).to(BF)
+
+    def gated(x, gate, up, act="silu", bg=None, bu=None, save=False):
+        g, u = raw(x) @ weight(gate).t() + raw(bg), raw(x) @ weight(up).t() + raw(bu)
+        h = (nn.functional.silu(g) * u).to(BF)
+        return (h, g.to(BF), u.to(BF)) if save else h
+
+    def gated_grad(dh, g, u, gate, up, act="silu"):
+        g, u, d = raw(g), raw(u), raw(dh)
+        s = torch.sigmoid(g)
+        dg, du = (d * u * (s + g * s * (1 - s))).to(BF), (d * g * s).to(BF)
+        return (dg.float() @ weight(gate) + du.float() @ weight(up)).to(BF), dg, du
+
+    for name, f in (("awq_linear_w4a16", linear), ("awq_linear_w4a16_grad", linear_grad),
+                    ("awq_gated_w4a16", gated), ("awq_gated_w4a16_grad", gated_grad)):
+        monkeypatch.setattr(svdq, name, torch.no_grad()(f))
+
+
+def modules(bias=None):
+    b = None if bias is None else torch.full((N,), float(bias))
+    return [L.AWQLinear(awq_layer(N, K, 1), b),
+            L.AWQGatedLinear(awq_layer(N, K, 1), awq_layer(N, K, 2), b, b)]
+
+
+def rows(m=3, seed=3):
+    return torch.randn(m, K, generator=torch.Generator().manual_seed(seed)).to(BF)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_forward_mode_is_refused(which):
+    """A tangent of the input is refused, with or without reverse mode beside it, and
+    no call outside forward mode is."""
+    mod, x = modules(0.5)[which], rows()
+    y = mod(x)
+    for leaf in (x, x.clone().requires_grad_()):
+        with fwAD.dual_level():
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                mod(fwAD.make_dual(leaf, torch.ones_like(x)))
+            assert torch.equal(mod(leaf), y)                  # no tangent: as ever
+    with pytest.raises(RuntimeError, match="forward-mode"):
+        torch.func.jvp(mod, (x,), (torch.ones_like(x),))
+    with torch.no_grad():
+        assert torch.equal(mod(x), y)
+    with torch.inference_mode():
+        assert torch.equal(mod(x), y)

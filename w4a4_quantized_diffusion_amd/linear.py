@@ -31,6 +31,7 @@ import json
 
 import torch
 from torch import nn
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import svdq
@@ -215,10 +216,16 @@ def _frozen(*tensors):
                                "they have no gradient")
 
 
+def _reverse_only(x):
+    if unpack_dual(x).tangent is not None:
+        raise RuntimeError("an AWQ layer has no forward-mode derivative")
+
+
 class AWQLinear(nn.Module):
     """An AWQ W4A16 layer (asymmetric INT4 weights in groups of 64, bf16
     activations) in place of nn.Linear(K, N).  Inputs bf16 [..., K]; output
-    bf16.  Differentiable once in its input; weights and bias are frozen."""
+    bf16.  Differentiable once in its input, in reverse mode; weights and bias are
+    frozen."""
 
     def __init__(self, layer, bias=None):
         super().__init__()
@@ -246,6 +253,7 @@ class AWQLinear(nn.Module):
             raise TypeError("AWQLinear takes bf16 activations")
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
+        _reverse_only(x)
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features).contiguous()
         lay = dict(q=self.q, scales=self.scales, zeros=self.zeros, N=self.out_features,
@@ -269,8 +277,8 @@ class AWQGatedLinear(nn.Module):
     shape: act(x gate^T + bias_gate) * (x up^T + bias_up), in place of the two
     nn.Linear(K, N), the activation and the product.  act: "silu" or "gelu"
     (tanh form).  Inputs bf16 [..., K]; output bf16.  Differentiable once in its
-    input (the forward pass then keeps both pre-activations in bf16); weights and
-    biases are frozen.  An AWQLinear(N, K) behind it completes the block.
+    input, in reverse mode (the forward pass then keeps both pre-activations in bf16);
+    weights and biases are frozen.  An AWQLinear(N, K) behind it completes the block.
 
     Forward and backward can be captured into a graph together.  A backward pass
     that is captured needs leaves of its own: torch ends the process when an eager
@@ -309,6 +317,7 @@ class AWQGatedLinear(nn.Module):
             raise TypeError("AWQGatedLinear takes bf16 activations")
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
+        _reverse_only(x)
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features).contiguous()
         dims = dict(N=self.out_features, K=self.in_features, group=self.group)
