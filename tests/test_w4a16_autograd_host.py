@@ -89,3 +89,35 @@ def test_forward_mode_is_refused(which):
         assert torch.equal(mod(x), y)
     with torch.inference_mode():
         assert torch.equal(mod(x), y)
+
+
+@pytest.mark.parametrize("names", [("bias",), ("bias_gate",), ("bias_up",), ("bias_gate", "bias_up")])
+def test_a_bias_that_requires_a_gradient(names):
+    """Biases are frozen.  The call on an input without a gradient runs, and a
+    gradient asked of the bias raises instead of staying away; the values are those
+    of the frozen module, also where they are used in place."""
+    mod, x = modules(0.5)[len(names[0]) > 4], rows()
+    y = mod(x)
+    assert not y.requires_grad
+    for n in names:
+        getattr(mod, n).requires_grad_()
+    for _ in range(2):
+        out = mod(x)
+        assert torch.equal(out, y) and out.requires_grad
+        with pytest.raises(RuntimeError, match="frozen"):
+            out.sum().backward()
+        assert all(getattr(mod, n).grad is None for n in names)
+    out = mod(x)
+    out.add_(1)
+    w = torch.ones(N, requires_grad=True)
+    with pytest.raises(RuntimeError, match="frozen"):
+        (out.float() * w).sum().backward()
+    (g,) = torch.autograd.grad((mod(x).float() * w).sum(), w)        # nothing asked of the bias
+    assert torch.equal(g, y.float().sum(0))
+    with torch.no_grad():
+        assert torch.equal(mod(x), y) and not mod(x).requires_grad
+    with pytest.raises(RuntimeError, match="frozen"):
+        mod(x.clone().requires_grad_())
+    for n in names:
+        getattr(mod, n).requires_grad_(False)
+    assert torch.equal(mod(x), y) and not mod(x).requires_grad

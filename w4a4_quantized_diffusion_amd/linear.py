@@ -74,7 +74,7 @@ class _BiasCache:
             return None
         key = (bias.data_ptr(), bias._version, dtype)
         if self.key != key:
-            self.key, self.value = key, bias.to(dtype).contiguous()
+            self.key, self.value = key, bias.detach().to(dtype).contiguous()
         return self.value
 
 
@@ -209,11 +209,30 @@ class _AWQGatedFn(torch.autograd.Function):
         return (dx,) + (None,) * (4 + 2 * n)
 
 
+_FROZEN = "the weights and biases of a quantized layer are frozen: they have no gradient"
+
+
 def _frozen(*tensors):
     for t in tensors:
         if t is not None and t.requires_grad:
-            raise RuntimeError("the weights and biases of a quantized layer are frozen: "
-                               "they have no gradient")
+            raise RuntimeError(_FROZEN)
+
+
+class _FrozenBiasFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, *biases):
+        ctx.mark_dirty(y)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError(_FROZEN)
+
+
+def _frozen_bias(y, *biases):
+    """y, whose backward pass raises if a bias is to get a gradient from it."""
+    leaves = [b for b in biases if b is not None and b.requires_grad]
+    return _FrozenBiasFn.apply(y, *leaves) if leaves and torch.is_grad_enabled() else y
 
 
 def _reverse_only(x):
@@ -225,7 +244,7 @@ class AWQLinear(nn.Module):
     """An AWQ W4A16 layer (asymmetric INT4 weights in groups of 64, bf16
     activations) in place of nn.Linear(K, N).  Inputs bf16 [..., K]; output
     bf16.  Differentiable once in its input, in reverse mode; weights and bias are
-    frozen."""
+    frozen (a gradient asked of the bias raises)."""
 
     def __init__(self, layer, bias=None):
         super().__init__()
@@ -264,7 +283,7 @@ class AWQLinear(nn.Module):
             fields = [lay.pop(f) for f in _AWQ_FIELDS]
             y = _AWQLinearFn.apply(x2, *fields, bias, lay)
         else:
-            y = svdq.awq_linear_w4a16(x2, lay, bias)
+            y = _frozen_bias(svdq.awq_linear_w4a16(x2, lay, bias), self.bias)
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self):
@@ -278,7 +297,7 @@ class AWQGatedLinear(nn.Module):
     nn.Linear(K, N), the activation and the product.  act: "silu" or "gelu"
     (tanh form).  Inputs bf16 [..., K]; output bf16.  Differentiable once in its
     input, in reverse mode (the forward pass then keeps both pre-activations in bf16);
-    weights and biases are frozen.  An AWQLinear(N, K) behind it completes the block.
+    weights and biases are frozen (a gradient asked of a bias raises).  An AWQLinear(N, K) behind it completes the block.
 
     Forward and backward can be captured into a graph together.  A backward pass
     that is captured needs leaves of its own: torch ends the process when an eager
@@ -322,7 +341,7 @@ class AWQGatedLinear(nn.Module):
         x2 = x.reshape(-1, self.in_features).contiguous()
         dims = dict(N=self.out_features, K=self.in_features, group=self.group)
         fields = [getattr(self, f) for f in _GATED_FIELDS]
-        bg, bu = (None if b is None else b.to(torch.bfloat16)
+        bg, bu = (None if b is None else b.detach().to(torch.bfloat16)
                   for b in (self.bias_gate, self.bias_up))
         if torch.is_grad_enabled() and x2.requires_grad:
             _frozen(self.bias_gate, self.bias_up)
@@ -331,6 +350,7 @@ class AWQGatedLinear(nn.Module):
             n = len(_AWQ_FIELDS)
             gate, up = (dict(dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
             h = svdq.awq_gated_w4a16(x2, gate, up, self.act, bg, bu)
+            h = _frozen_bias(h, self.bias_gate, self.bias_up)
         return h.reshape(*lead, self.out_features)
 
     def extra_repr(self):
