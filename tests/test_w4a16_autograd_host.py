@@ -121,3 +121,33 @@ def test_a_bias_that_requires_a_gradient(names):
     for n in names:
         getattr(mod, n).requires_grad_(False)
     assert torch.equal(mod(x), y) and not mod(x).requires_grad
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_layers_made_under_inference_mode(which):
+    """Layers quantized or loaded under inference mode run outside it, with and
+    without a gradient of the input, and give what other layers give."""
+    ref, x = modules(0.5)[which], rows()
+    with torch.inference_mode():
+        mod = modules(0.5)[which]
+        assert all(b.is_inference() for b in mod.buffers())
+    y = ref(x)
+    with torch.no_grad():
+        assert torch.equal(mod(x), y)
+    assert torch.equal(mod(x), y)
+    a, b = x.clone().requires_grad_(), x.clone().requires_grad_()
+    ref(a).float().square().sum().backward()
+    mod(b).float().square().sum().backward()
+    assert torch.equal(a.grad, b.grad) and a.grad.any()
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_weights_changed_before_the_backward_pass(which):
+    """New weights copied into a layer between a forward pass and its backward pass
+    are noticed, as torch's own layers notice them."""
+    mod, x = modules()[which], rows().requires_grad_()
+    y = mod(x)
+    other = {k: v.clone() for k, v in mod.state_dict().items()}
+    mod.load_state_dict(other)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()

@@ -72,6 +72,8 @@ class _BiasCache:
     def get(self, bias, dtype):
         if bias is None:
             return None
+        if bias.is_inference():                  # has no version to go by
+            return bias.to(dtype).contiguous()
         key = (bias.data_ptr(), bias._version, dtype)
         if self.key != key:
             self.key, self.value = key, bias.detach().to(dtype).contiguous()
@@ -173,17 +175,28 @@ def _grad_rows(dy, width):
     return dy.reshape(-1, width).contiguous()
 
 
+def _save(ctx, *tensors):
+    """save_for_backward, which takes no tensors made under inference mode: those (a
+    layer's, never changed outside it) are kept as they are."""
+    ctx.inference = [t if t.is_inference() else None for t in tensors]
+    ctx.save_for_backward(*(None if t.is_inference() else t for t in tensors))
+
+
+def _saved(ctx):
+    return [t if t is not None else i for t, i in zip(ctx.saved_tensors, ctx.inference)]
+
+
 class _AWQLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, q, scales, zeros, bias, dims):
-        ctx.save_for_backward(q, scales, zeros)
+        _save(ctx, q, scales, zeros)
         ctx.dims = dims
         return svdq.awq_linear_w4a16(x, dict(dims, q=q, scales=scales, zeros=zeros), bias)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        q, scales, zeros = ctx.saved_tensors
+        q, scales, zeros = _saved(ctx)
         lay = dict(ctx.dims, q=q, scales=scales, zeros=zeros)
         dx = svdq.awq_linear_w4a16_grad(_grad_rows(dy, lay["N"]), lay)
         return dx, None, None, None, None, None
@@ -195,14 +208,14 @@ class _AWQGatedFn(torch.autograd.Function):
         n = len(_AWQ_FIELDS)
         gate, up = (dict(dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
         h, g, u = svdq.awq_gated_w4a16(x, gate, up, act, bias_gate, bias_up, save=True)
-        ctx.save_for_backward(g, u, *fields)
+        _save(ctx, g, u, *fields)
         ctx.act, ctx.dims = act, dims
         return h
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh):
-        g, u, *fields = ctx.saved_tensors
+        g, u, *fields = _saved(ctx)
         n = len(_AWQ_FIELDS)
         gate, up = (dict(ctx.dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
         dx, _, _ = svdq.awq_gated_w4a16_grad(_grad_rows(dh, ctx.dims["N"]), g, u, gate, up, ctx.act)
