@@ -2,6 +2,7 @@
 binding's calls are replaced by the same mathematics in torch on detached values
 (the kernels read raw memory, so nothing of autograd passes through them)."""
 
+import numpy as np
 import pytest
 import torch
 import torch.autograd.forward_ad as fwAD
@@ -151,3 +152,20 @@ def test_weights_changed_before_the_backward_pass(which):
     mod.load_state_dict(other)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def test_a_new_bias_at_an_old_address():
+    """The bf16 copy of the bias that AWQLinear keeps belongs to one tensor, not to
+    its address: another tensor that took the freed one's place is read anew."""
+    mod, x = modules(0.0)[0], rows()
+    store = np.zeros(N + 4, dtype=np.float32)
+    store = store[-store.ctypes.data % 16 // 4:][:N]
+    zero = mod(x).float()
+    for v in (4.0, 8.0):
+        store[:] = v
+        mod.bias = torch.from_numpy(store)       # same address and version every time
+        assert torch.equal(mod(x), (raw(x) @ weight(awq_layer(N, K, 1)).t() + v).to(BF))
+        assert torch.equal(mod(x), (raw(x) @ weight(awq_layer(N, K, 1)).t() + v).to(BF))
+    with torch.no_grad():
+        mod.bias.zero_()                         # in place: seen by its version
+    assert torch.equal(mod(x).float(), zero)

@@ -64,19 +64,26 @@ def _shapes_awq(n, k, group):
 
 
 class _BiasCache:
-    """The bias in bf16 (awq_linear_w4a16 reads a bf16 bias)."""
+    """The bias in bf16 (awq_linear_w4a16 reads a bf16 bias).  One copy is kept, for
+    one tensor, its version and the stream that wrote the copy.  Inside a graph
+    capture none is used or left behind: the conversion is captured with the call."""
 
-    def __init__(self):
-        self.key, self.value = None, None
+    source, key, value = None, None, None
 
     def get(self, bias, dtype):
         if bias is None:
             return None
         if bias.is_inference():                  # has no version to go by
             return bias.to(dtype).contiguous()
-        key = (bias.data_ptr(), bias._version, dtype)
-        if self.key != key:
-            self.key, self.value = key, bias.detach().to(dtype).contiguous()
+        stream = None
+        if bias.is_cuda:
+            if torch.cuda.is_current_stream_capturing():
+                return bias.detach().to(dtype).contiguous()
+            stream = svdq._raw_stream(bias.get_device())
+        key = (bias.data_ptr(), bias._version, dtype, stream)
+        if self.source is not bias or self.key != key:
+            self.value = bias.detach().to(dtype).contiguous()
+            self.source, self.key = bias, key
         return self.value
 
 
