@@ -169,3 +169,23 @@ def test_a_new_bias_at_an_old_address():
     with torch.no_grad():
         mod.bias.zero_()                         # in place: seen by its version
     assert torch.equal(mod(x).float(), zero)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("pad", [1, 8])
+def test_rows_at_odd_addresses(which, pad):
+    """Contiguous views that start between 16-byte addresses, as the input (a slice of
+    a flat buffer) and as the gradient (of a concatenation behind an odd number of
+    elements): the library takes aligned rows only, so the modules copy them."""
+    mod, x = modules(0.5)[which], rows()
+    flat = torch.zeros(pad + x.numel(), dtype=BF)
+    flat[pad:] = x.flatten()
+    view = flat[pad:].view_as(x)
+    assert torch.equal(mod(view), mod(x))
+    a, b = x.clone().requires_grad_(), flat.clone().requires_grad_()
+    dy = torch.randn(3, N, generator=torch.Generator().manual_seed(9)).to(BF)
+    mod(a).backward(dy)
+    y = mod(b[pad:].view_as(x))
+    torch.cat((torch.zeros(pad, dtype=BF), y.flatten())).backward(
+        torch.cat((torch.zeros(pad, dtype=BF), dy.flatten())))
+    assert torch.equal(b.grad[pad:].view_as(x), a.grad)

@@ -87,6 +87,13 @@ class _BiasCache:
         return self.value
 
 
+def _rows(x, width):
+    """x as a contiguous [M, width] matrix at a 16-byte address, as the library takes
+    it (autograd hands on expanded and strided gradients, and slices of others)."""
+    x = x.reshape(-1, width).contiguous()
+    return x.clone() if x.data_ptr() % 16 else x
+
+
 class SVDQLinear(nn.Module):
     """An SVDQuant W4A4 layer in place of nn.Linear(K, N).
 
@@ -155,7 +162,7 @@ class SVDQLinear(nn.Module):
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, self.in_features).contiguous()
+        x2 = _rows(x, self.in_features)
         m = x2.shape[0]
         if 0 < m <= self.a16_rows:
             # (a workspace of its own for every call: one captured into a graph must
@@ -174,12 +181,6 @@ class SVDQLinear(nn.Module):
                 f"rank={self.rank}, prec={_PREC_NAME[self.prec]}, bias={self.bias is not None}, "
                 f"gelu_input={self.gelu_input}"
                 + (f", a16_rows={self.a16_rows}" if self.a16_rows else ""))
-
-
-def _grad_rows(dy, width):
-    """An incoming gradient as a contiguous [M, width] matrix (autograd hands on
-    expanded and strided ones)."""
-    return dy.reshape(-1, width).contiguous()
 
 
 def _save(ctx, *tensors):
@@ -205,7 +206,7 @@ class _AWQLinearFn(torch.autograd.Function):
     def backward(ctx, dy):
         q, scales, zeros = _saved(ctx)
         lay = dict(ctx.dims, q=q, scales=scales, zeros=zeros)
-        dx = svdq.awq_linear_w4a16_grad(_grad_rows(dy, lay["N"]), lay)
+        dx = svdq.awq_linear_w4a16_grad(_rows(dy, lay["N"]), lay)
         return dx, None, None, None, None, None
 
 
@@ -225,7 +226,7 @@ class _AWQGatedFn(torch.autograd.Function):
         g, u, *fields = _saved(ctx)
         n = len(_AWQ_FIELDS)
         gate, up = (dict(ctx.dims, **dict(zip(_AWQ_FIELDS, f))) for f in (fields[:n], fields[n:]))
-        dx, _, _ = svdq.awq_gated_w4a16_grad(_grad_rows(dh, ctx.dims["N"]), g, u, gate, up, ctx.act)
+        dx, _, _ = svdq.awq_gated_w4a16_grad(_rows(dh, ctx.dims["N"]), g, u, gate, up, ctx.act)
         return (dx,) + (None,) * (4 + 2 * n)
 
 
@@ -294,7 +295,7 @@ class AWQLinear(nn.Module):
             raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
         _reverse_only(x)
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, self.in_features).contiguous()
+        x2 = _rows(x, self.in_features)
         lay = dict(q=self.q, scales=self.scales, zeros=self.zeros, N=self.out_features,
                    K=self.in_features, group=self.group)
         bias = self._bias.get(self.bias, torch.bfloat16)
@@ -358,7 +359,7 @@ class AWQGatedLinear(nn.Module):
             raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
         _reverse_only(x)
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, self.in_features).contiguous()
+        x2 = _rows(x, self.in_features)
         dims = dict(N=self.out_features, K=self.in_features, group=self.group)
         fields = [getattr(self, f) for f in _GATED_FIELDS]
         bg, bu = (None if b is None else b.detach().to(torch.bfloat16)
