@@ -63,3 +63,16 @@ def test_refusals():
     lin.bias.requires_grad_()
     with pytest.raises(RuntimeError, match="frozen"):
         lin(torch.zeros(2, 128, dtype=torch.bfloat16, requires_grad=True))
+
+
+def test_layers_pickled_before_a16_rows():
+    """An SVDQLinear pickled whole by a version without a16_rows is one with none."""
+    g = torch.Generator().manual_seed(5)
+    m = L.SVDQLinear(_svdq_layer(64, 128, 16, svdq.INT4, g))
+    state = m.__getstate__() if hasattr(m, "__getstate__") else m.__dict__
+    old = {k: v for k, v in dict(state).items() if k != "a16_rows"}
+    new = L.SVDQLinear.__new__(L.SVDQLinear)
+    new.__setstate__(old)
+    assert new.a16_rows == 0 and "a16_rows" not in new.extra_repr()
+    with pytest.raises(ValueError, match="device tensor"):          # as far as a host goes
+        new(torch.zeros(2, 128))

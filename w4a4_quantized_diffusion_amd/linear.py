@@ -111,6 +111,8 @@ class SVDQLinear(nn.Module):
     for the layers that see a row per image or token (with a workspace of its own
     for every call)."""
 
+    a16_rows = 0                # of layers pickled without it
+
     def __init__(self, layer, bias=None, gelu_input=False, a16_rows=0):
         super().__init__()
         self.a16_rows = int(a16_rows)
