@@ -76,3 +76,18 @@ def test_layers_pickled_before_a16_rows():
     assert new.a16_rows == 0 and "a16_rows" not in new.extra_repr()
     with pytest.raises(ValueError, match="device tensor"):          # as far as a host goes
         new(torch.zeros(2, 128))
+
+
+def test_shim_checks_a16_rows_first(monkeypatch):
+    """quantize_linears refuses its arguments before it swaps anything."""
+    g = torch.Generator().manual_seed(6)
+    monkeypatch.setattr(L.AWQLinear, "from_linear",
+                        classmethod(lambda cls, lin: cls(_awq_layer(256, 128, g))))
+    monkeypatch.setattr(svdq, "svdq_quantize_weights",
+                        lambda w, a, r, p: _svdq_layer(w.shape[0], w.shape[1], r, svdq._PREC[p], g))
+    for rows in (-1, 65):
+        b = Block()
+        with pytest.raises(ValueError, match="a16_rows"):
+            L.quantize_linears(b, rank=16, awq=("mod",), a16_rows=rows)
+        assert type(b.mod) is nn.Linear and type(b.ff[1]) is nn.Linear
+    assert L.quantize_linears(Block(), rank=16, awq=("mod",), a16_rows=64) == {"mod": "awq", "ff.1": "svdq"}

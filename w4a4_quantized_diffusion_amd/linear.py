@@ -436,6 +436,8 @@ def quantize_linears(module, act_amax=None, rank=32, prec="int4", awq=(), gelu_i
     Returns {name: kind}."""
     if rank < 0 or rank > 256 or rank % 16:
         raise ValueError("rank must be a multiple of 16 in [0, 256]")
+    if not 0 <= a16_rows <= 64:
+        raise ValueError("a16_rows must be in [0, 64]")
     act_amax = act_amax or {}
     done = {}
     targets = [(n, m) for n, m in module.named_modules() if isinstance(m, nn.Linear)]
