@@ -13,7 +13,7 @@ import torch
 
 from oracle import svdq as O
 from tests.gpu_helpers import gm_codes, gm_int4, t_u8
-from tests.test_gpu_w4a16 import BF, F32, act64, awq_layer, bf, check
+from tests.test_gpu_w4a16 import BF, F32, act64, awq_layer, bf, check, svdq_layer
 from w4a4_quantized_diffusion_amd import svdq
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,20 @@ def test_fp32_low_rank_branch_is_exact(m, k, n, rank, prec):
     x = full_mantissas(m, k, 55)
     assert torch.equal(svdq.svdq_linear_w4a16(x, d).double(), x[:, at[to]].double() * w.double())
 
+
+@pytest.mark.parametrize("m,k,n", [(1, 192, 48), (17, 1088, 8208), (64, 320, 272)])
+@pytest.mark.parametrize("prec", ["int4", "nvfp4"])
+def test_fp32_near_the_top_of_the_range(m, k, n, prec):
+    """A value of 3e38 times weights of size one at most (before their scale): three
+    products summed, the scale and the join with zeros, at most 8 roundings of 2^-24."""
+    d, parts = svdq_layer(n, k, 0, prec, 99)
+    d["smooth"] = torch.ones_like(d["smooth"])
+    x = torch.zeros(m, k, device="cuda")
+    x[m - 1, 1] = 3.0e38
+    scale = d["wscales"][0].double() if prec == "int4" else d["w_tensor_scale"].double()
+    w = parts[1][:, 1]
+    fits = w.abs() / scale <= 1.001
+    assert fits.any()
+    ref = x[m - 1, 1].double() * w
+    Y = svdq.svdq_linear_w4a16(x, d)
+    check(Y[m - 1][fits], ref[fits], ref[fits].abs() * 2.0 ** -21, "large")
