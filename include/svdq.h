@@ -306,7 +306,7 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  * `stream`, nothing allocated, workspace from the caller (DEVICE, 256-byte
  * aligned, contents need not be initialised, not overlapping any operand; its
  * size is the call's *_workspace_bytes, a multiple of 256 and 0 when none is
- * needed or an argument is invalid).  Calls that may run at the same time need
+ * needed or an argument is invalid; it may fall where M grows, so ask for every M).  Calls that may run at the same time need
  * workspaces of their own.  DEVICE operands are 16-byte aligned (biases: their
  * element size).  Outputs may not overlap inputs or each other.  K and N are at
  * most 2^22, M K, M N and N K at most 2^40.  M == 0 launches nothing.
@@ -323,9 +323,10 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  * (modulation, time step and pooled projections, decoding), where reading the
  * weights is the whole cost and quantizing X would only add error.  The
  * products take Xh as a sum of bf16 terms: two for a bf16 Y (Xh to 2^-17), three
- * for an fp32 Y (2^-24); sums are fp32.  |Xh| from 0x1.FFp127 on counts as infinite;
- * products or sums past fp32's range (before sW or ts_w) give infinities or NaNs.  Other arguments as svdq_linear_w4a4;
- * w_tensor_scale is read for NVFP4 only.
+ * for an fp32 Y (2^-24), and X and LR of the low-rank branch likewise (X always
+ * three); sums are fp32.  |Xh|, |X| and |LR| from 0x1.FFp127 on count as infinite;
+ * products or sums past fp32's range (before sW or ts_w) give infinities or NaNs.
+ * Other arguments as svdq_linear_w4a4; w_tensor_scale is read for NVFP4 only.
  * 0 <= M <= 64 (more rows: SVDQ_ERR_UNSUPPORTED; svdq_linear_w4a4 is the form
  * for them), K % 64 == 0, N % 16 == 0, rank % 16 == 0, 0 <= rank <= 256. */
 size_t svdq_linear_w4a16_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t rank);

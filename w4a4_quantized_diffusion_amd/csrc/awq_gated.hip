@@ -559,7 +559,8 @@ svdq_status sum(const Call& c, const float* part, int S) {
 template <int MT>
 svdq_status slices(const Call& c, float* part) {
   const Split p = split(c.M, c.K, c.N);
-  // chunks of X that fit LDS, a multiple of D (64 rows: 7 chunks of 128 bytes)
+  // chunks of X that fit LDS (64 rows: 6 chunks of 128 bytes).  A multiple of D: chunk
+  // c of a piece is in slot c % D of the register ring, which goes on over the pieces.
   const int most = int((LDS_X / c.M - 16) / 128 / D * D);
   const int len = int((c.K / 64 + p.slices - 1) / p.slices);
   const int sub = std::min(most, (len + D - 1) / D * D);

@@ -81,10 +81,12 @@ __device__ __forceinline__ void transpose_dequant8(const svdq::AwqWeight& w, int
 // The rows' own operand (dY, or dG and dU computed here from dH, G and U) is
 // in LDS.  Partial sums [S][M][K] are joined by grad_sum_kernel.
 //
-// A dequantized code costs 2.6 vector instructions here, so every compute unit is
-// needed: one row 4096 x 4096 takes 7.5 us in 512 workgroups (6.4 and a launch of 2.6
-// for the sums), and 17 in the 32 that need no second launch.  Twenty rows of the
-// pair 2048 x 5456 take 14 us.
+// A wave's loads, its two or three steps of products and the workgroup's reduction
+// follow one another and nothing hides them (the dequantization, 2.6 vector
+// instructions a code, is less than 2 us of it), so every compute unit is needed: one
+// row 4096 x 4096 takes 7.5 us in 512 workgroups (6.4 and a launch of 2.6 for the
+// sums), and 17 in the 32 that need no second launch.  Twenty rows of the pair 2048 x
+// 5456 take 14 us.
 
 constexpr int ROWS = 64;                 // the most rows of this form
 constexpr int LDS_A = 64 << 10;          // for the rows' operand of 16 rows, twice that above

@@ -403,6 +403,12 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, 
 // wide tiles 1.72 a chunk of 64, a round of 512 tiles of 128 x 128 1.25, the
 // dequantization 5.2 TB/s, sums of slices 4.5 TB/s, few rows their weights at
 // 4.5 TB/s; 3 for a launch.
+// few_us is the time of a few rows; 64 take about twice that (gated pair 4096 -> 12288:
+// 18.6 here, 15 measured at one row, 28 at 33 and 35 at 64; linear gradient 12288 x
+// 4096: 12.3, 14, 26 and 35).  A factor 1 + rows / 43, which fits them, changes the
+// choice for 0.2% of sizes; on 24 of those it was 0.83 to 1.26 times as fast, 0.998 in
+// the geometric mean (gated 0.96, its backward 0.95, linear gradient 1.06), since the
+// estimates of the other forms are off by as much there.  It is left out.
 namespace svdq_plan {
 
 struct Shape {
