@@ -1,5 +1,6 @@
-"""AWQLinear's bf16 copy of its bias: a first call that is captured, a bias changed
-under a captured call, and first calls on two streams at once."""
+"""What the modules keep between calls: AWQLinear's bf16 copy of its bias (a first call
+that is captured, a bias changed under a captured call, first calls on two streams
+at once) and SVDQLinear's workspace."""
 
 import pytest
 import torch
@@ -70,3 +71,38 @@ def test_first_calls_on_two_streams():
         yb = mod(x)
     torch.cuda.synchronize()
     assert torch.equal(ya, y) and torch.equal(yb, y)
+
+
+@pytest.mark.parametrize("first", ["eager", "captured"])
+@pytest.mark.parametrize("gelu", [False, True])
+def test_captured_svdq_calls_share_nothing(first, gelu):
+    """Two captured calls of one SVDQLinear, replayed beside eager calls on more rows:
+    they keep their own workspaces, and write to nothing else."""
+    a = L.SVDQLinear.from_linear(linear(512, 272, 9), rank=16, gelu_input=gelu)
+    ref = L.SVDQLinear.from_linear(linear(512, 272, 9), rank=16, gelu_input=gelu)
+    xs = [torch.randn(m, 512, device="cuda").to(BF) for m in (100, 200)]
+    big = torch.randn(900, 512, device="cuda").to(BF)
+    want = [ref(x) for x in xs + [big]]
+    if first == "eager":
+        assert torch.equal(a(xs[0]), want[0])
+    torch.cuda.synchronize()
+    outs, graphs = [], [torch.cuda.CUDAGraph() for _ in xs]
+    for g, x in zip(graphs, xs):
+        with torch.cuda.graph(g):
+            outs.append(a(x))
+    yb = a(big)
+    assert torch.equal(yb, want[2])
+    fill = [torch.full((n,), 5.0, device="cuda") for n in (64, 1024, 4096, 16384, 1 << 18) * 4]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for y in outs:
+            y.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        assert torch.equal(a(big), want[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(outs, want))
+    assert all((t == 5.0).all() for t in fill)

@@ -104,7 +104,8 @@ class SVDQLinear(nn.Module):
     x must be bf16).  Inputs of any leading shape [..., K] in fp32 or bf16;
     the output has x's dtype.  The workspace is kept between calls and
     reused on the calling stream: one module must not run on two streams at
-    once.
+    once.  A call captured into a graph has a workspace of its own (the kept one is
+    replaced, and freed, by a later call on more rows).
 
     Inputs of at most `a16_rows` rows (0 to 64, default 0) run
     svdq_linear_w4a16 instead: the same layer with x kept in its own precision,
@@ -171,11 +172,14 @@ class SVDQLinear(nn.Module):
             # outlive the larger one that a later call on more rows brings)
             y = svdq.svdq_linear_w4a16(x2, self.layer(), self.bias, y_dtype=x2.dtype)
             return y.reshape(*lead, self.out_features)
-        need = max(svdq.svdq_workspace_bytes(m, self.in_features, self.rank, self.prec), 256)
-        if self._ws is None or self._ws.numel() < need or self._ws.device != x2.device:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=x2.device)
+        ws = None
+        if not (x2.is_cuda and torch.cuda.is_current_stream_capturing()):
+            need = max(svdq.svdq_workspace_bytes(m, self.in_features, self.rank, self.prec), 256)
+            if self._ws is None or self._ws.numel() < need or self._ws.device != x2.device:
+                self._ws = torch.empty(need, dtype=torch.uint8, device=x2.device)
+            ws = self._ws
         fn = svdq.svdq_linear_w4a4_gelu if self.gelu_input else svdq.svdq_linear_w4a4
-        y = fn(x2, self.layer(), self.bias, y_dtype=x2.dtype, workspace=self._ws)
+        y = fn(x2, self.layer(), self.bias, y_dtype=x2.dtype, workspace=ws)
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self):
