@@ -31,7 +31,7 @@ import json
 
 import torch
 from torch import nn
-from torch.autograd.forward_ad import unpack_dual
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import svdq
@@ -258,12 +258,15 @@ class _FrozenBiasFn(torch.autograd.Function):
 
 def _frozen_bias(y, *biases):
     """y, whose backward pass raises if a bias is to get a gradient from it."""
+    if not torch.is_grad_enabled():
+        return y
     leaves = [b for b in biases if b is not None and b.requires_grad]
-    return _FrozenBiasFn.apply(y, *leaves) if leaves and torch.is_grad_enabled() else y
+    return _FrozenBiasFn.apply(y, *leaves) if leaves else y
 
 
 def _reverse_only(x):
-    if unpack_dual(x).tangent is not None:
+    # (unpack_dual looks at the level too, in 1.5 us)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(x).tangent is not None:
         raise RuntimeError("an AWQ layer has no forward-mode derivative")
 
 
@@ -368,7 +371,7 @@ class AWQGatedLinear(nn.Module):
         x2 = _rows(x, self.in_features)
         dims = dict(N=self.out_features, K=self.in_features, group=self.group)
         fields = [getattr(self, f) for f in _GATED_FIELDS]
-        bg, bu = (None if b is None else b.detach().to(torch.bfloat16)
+        bg, bu = (b if b is None or b.dtype is torch.bfloat16 else b.detach().to(torch.bfloat16)
                   for b in (self.bias_gate, self.bias_up))
         if torch.is_grad_enabled() and x2.requires_grad:
             _frozen(self.bias_gate, self.bias_up)
