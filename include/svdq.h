@@ -306,10 +306,11 @@ svdq_status awq_linear_w4a16(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  * `stream`, nothing allocated, workspace from the caller (DEVICE, 256-byte
  * aligned, contents need not be initialised, not overlapping any operand; its
  * size is the call's *_workspace_bytes, a multiple of 256 and 0 when none is
- * needed or an argument is invalid; it may fall where M grows, so ask for every M).  Calls that may run at the same time need
- * workspaces of their own.  DEVICE operands are 16-byte aligned (biases: their
- * element size).  Outputs may not overlap inputs or each other.  K and N are at
- * most 2^22, M K, M N and N K at most 2^40.  M == 0 launches nothing.
+ * needed or an argument is invalid; it may fall where M grows, so ask for every
+ * M).  Calls that may run at the same time need workspaces of their own.  DEVICE
+ * operands are 16-byte aligned (biases: their element size).  Outputs may not
+ * overlap inputs or each other.  K and N are at most 2^22, M K, M N and N K at
+ * most 2^40.  M == 0 launches nothing.
  * An infinity or NaN in a row of the first operand makes that row of the products
  * infinite or NaN all along (NaN may stand where the formula has an infinity), and
  * no other row. */

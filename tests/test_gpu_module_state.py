@@ -1,6 +1,8 @@
 """What the modules keep between calls: AWQLinear's bf16 copy of its bias (a first call
 that is captured, a bias changed under a captured call, first calls on two streams
-at once) and SVDQLinear's workspace."""
+at once) and SVDQLinear's workspace; and two host threads at once."""
+
+import threading
 
 import pytest
 import torch
@@ -106,3 +108,38 @@ def test_captured_svdq_calls_share_nothing(first, gelu):
         torch.cuda.synchronize()
         assert all(torch.equal(y, w) for y, w in zip(outs, want))
     assert all((t == 5.0).all() for t in fill)
+
+
+def test_two_host_threads():
+    """Calls of two host threads on streams of their own: the same kernels with more
+    and with less LDS at once."""
+    from tests.test_gpu_w4a16 import awq_layer, bf, svdq_layer
+    from w4a4_quantized_diffusion_amd import svdq
+
+    d, _ = svdq_layer(256, 4096, 16, "int4", 61)
+    lay, _ = awq_layer(4096, 512, 62)
+    jobs = []
+    for m in (49, 64):
+        x, dy = bf((m, 4096), 63), bf((m, 4096), 64)
+        jobs.append(lambda x=x, dy=dy: (svdq.svdq_linear_w4a16(x, d), svdq.awq_linear_w4a16_grad(dy, lay)))
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(job, ref):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    out = job()
+                torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(out, ref)):
+                bad.append("differs")
+        except Exception as e:                   # a thread's failure is the test's
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad

@@ -327,7 +327,8 @@ class AWQGatedLinear(nn.Module):
     nn.Linear(K, N), the activation and the product.  act: "silu" or "gelu"
     (tanh form).  Inputs bf16 [..., K]; output bf16.  Differentiable once in its
     input, in reverse mode (the forward pass then keeps both pre-activations in bf16);
-    weights and biases are frozen (a gradient asked of a bias raises).  An AWQLinear(N, K) behind it completes the block.
+    weights and biases are frozen (a gradient asked of a bias raises).  An
+    AWQLinear(N, K) behind it completes the block.
 
     Forward and backward can be captured into a graph together.  A backward pass
     that is captured needs leaves of its own: torch ends the process when an eager
@@ -443,7 +444,7 @@ def quantize_linears(module, act_amax=None, rank=32, prec="int4", awq=(), gelu_i
     Returns {name: kind}."""
     if rank < 0 or rank > 256 or rank % 16:
         raise ValueError("rank must be a multiple of 16 in [0, 256]")
-    if not 0 <= a16_rows <= 64:
+    if not 0 <= int(a16_rows) <= 64:
         raise ValueError("a16_rows must be in [0, 64]")
     act_amax = act_amax or {}
     done = {}
