@@ -1,7 +1,7 @@
 """Epilogues of the weight-only kernels, without a GPU: every wave's LDS buffer lies
 inside one of the kernel's LDS objects and apart from the other waves' (the
 objects are separate, in no promised order), and biases, which are aligned to
-their elements only, are read by element."""
+their elements only, are not read through wider types."""
 
 import os
 import re
@@ -49,7 +49,7 @@ def test_kernels_take_their_buffers_from_the_stages():
         assert re.search(r"\bepilogue_buffer<", text), f
 
 
-def test_biases_are_read_by_element():
+def test_biases_are_not_taken_as_aligned():
     for f in ("awq_gated.hip", "linear_a16.hip"):
         with open(os.path.join(build.CSRC, f)) as h:
             text = h.read()

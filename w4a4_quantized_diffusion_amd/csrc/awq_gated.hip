@@ -319,13 +319,11 @@ __global__ __launch_bounds__(64) void gated_sum_kernel(
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       v[q][t] = reinterpret_cast<const v4f*>(part)[(2 * int64_t(min(q, S - 1)) + t) * total + i];
-  // (a bias is aligned to its elements only)
+  // (a bias is aligned to its elements only: a copy leaves the compiler to choose loads
+  // that the target takes at any address)
   uint16_t b[2][4] = {};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (bg) b[0][e] = bg[n + e];
-    if (bu) b[1][e] = bu[n + e];
-  }
+  if (bg) __builtin_memcpy(b[0], bg + n, 8);
+  if (bu) __builtin_memcpy(b[1], bu + n, 8);
   __builtin_amdgcn_sched_barrier(0);
   v4f p[2];
 #pragma unroll
