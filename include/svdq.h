@@ -91,6 +91,7 @@ typedef enum { SVDQ_F32 = 0, SVDQ_BF16 = 1 } svdq_dtype;
 /* Gate activations of a gated feed-forward pair: x / (1 + exp(-x)), and the
  * tanh form of GELU (the formula at svdq_act_quantize_gelu). */
 typedef enum { SVDQ_SILU = 0, SVDQ_GELU = 1 } svdq_act;
+typedef enum { SVDQ_LAYER_NORM = 0, SVDQ_RMS_NORM = 1 } svdq_norm;
 
 /* svdq_quantize_weights flag: lora_down / lora_up are INPUTS (the low-rank
  * split is given, the SVD is skipped); smoothing, residual and quantization
@@ -381,6 +382,57 @@ svdq_status awq_linear_w4a16_grad(const uint16_t* dY, int64_t M, int64_t K, int6
                                   int32_t group, const uint8_t* q, const uint16_t* scales,
                                   const uint16_t* zeros, void* dX, svdq_dtype dx_dtype,
                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------- norms around a block
+ * What stands between two blocks of a transformer: the residual sum with its
+ * gate, a norm of the block's output before it, and the next block's norm with its
+ * modulation, in one pass over the rows.
+ *   t  = H                            without post
+ *        n(H) * post                  with it
+ *   x' = X + gate * t                 (x' = X without H; gate counts as 1 if absent)
+ *   Y  = n(x') * weight * (1 + scale) + shift      (absent: 1, 0 and 0)
+ * n(v) along a row of D: SVDQ_LAYER_NORM (v - mean v) / sqrt(var v + eps) (var over
+ * D values), SVDQ_RMS_NORM v / sqrt(mean v^2 + eps).  All of it is fp32 until X_out
+ * (x') and Y are rounded, once each; Y comes from the unrounded x'.
+ * X, X_out [M, D] x_dtype, H [M, D] h_dtype, Y [M, D] y_dtype, contiguous, DEVICE,
+ * aligned to their elements (16-byte addresses and D % 8 == 0 run fastest).  H and
+ * X_out are both given or both NULL.  Each vector is NULL or a svdq_vec (HOST struct):
+ * `data` DEVICE, f32 or bf16, aligned to its elements; ld 0: one vector of D for all
+ * rows; else vector i, for rows i M / images .. , starts ld >= D elements after
+ * vector i - 1 (slices of a modulation layer's output).  post and gate need H.
+ * 0 <= M, 1 <= D <= 16384 (more: SVDQ_ERR_UNSUPPORTED), 1 <= images <= 2^20, M a
+ * multiple of images, eps finite and >= 0.  Outputs may not overlap inputs or each
+ * other.  A row whose values are all equal gives zeros for n if eps > 0 (layer
+ * norm); a NaN or infinity stays in its row.  M == 0 launches nothing. */
+typedef struct {
+  const void* data;
+  svdq_dtype dtype;
+  int64_t ld;
+} svdq_vec;
+
+svdq_status svdq_block_norm(const void* X, svdq_dtype x_dtype, const void* H, svdq_dtype h_dtype,
+                            int64_t M, int64_t D, int64_t images, svdq_norm kind, float eps,
+                            const svdq_vec* post, const svdq_vec* gate, const svdq_vec* weight,
+                            const svdq_vec* scale, const svdq_vec* shift, void* X_out, void* Y,
+                            svdq_dtype y_dtype, hipStream_t stream);
+
+/* Its backward pass, from the gradients of Y and of X_out (NULL: zeros) and the
+ * forward call's inputs (statistics and x' are formed again, in fp32 as there).
+ * dX [M, D] x_dtype, dH [M, D] h_dtype (given if H is).  dpost .. dshift: DEVICE fp32,
+ * 16-byte aligned, [images, D] where the vector has ld > 0 and [D] where ld is 0 (the
+ * sum over all rows), NULL if not wanted; a gradient needs its vector.  The sums over
+ * rows have a fixed order.  With M == 0 the vectors' gradients are set to zero.
+ * Workspace as for the weight-only operators (M == 0: none). */
+size_t svdq_block_norm_grad_workspace_bytes(int64_t M, int64_t D, int64_t images);
+svdq_status svdq_block_norm_grad(const void* dY, svdq_dtype y_dtype, const void* dX_out,
+                                 const void* X, svdq_dtype x_dtype, const void* H,
+                                 svdq_dtype h_dtype, int64_t M, int64_t D, int64_t images,
+                                 svdq_norm kind, float eps, const svdq_vec* post,
+                                 const svdq_vec* gate, const svdq_vec* weight,
+                                 const svdq_vec* scale, const svdq_vec* shift, void* dX, void* dH,
+                                 float* dpost, float* dgate, float* dweight, float* dscale,
+                                 float* dshift, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,7 @@
 // C ABI front end: argument validation, workspace layout, dispatch, and the
 // per-thread error message.  Every check runs before any HIP call.
 
-#include "w4a16.h"
+#include "block_norm.h"
 
 #include <cstdio>
 #include <mutex>
@@ -733,6 +733,153 @@ svdq_status awq_linear_w4a16_grad(const uint16_t* dY, int64_t M, int64_t K, int6
                         {workspace, need, true}};
   TRY(check_spans(spans, 6));
   return svdq::launch_awq_linear_grad(dY, M, K, N, w, dX, dx_dtype, workspace, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- norms around a block
+namespace {
+
+// a workgroup holds a row in registers
+constexpr int64_t MAX_NORM = 16384;
+constexpr int64_t MAX_IMAGES = int64_t(1) << 20;
+
+svdq_status check_norm(int64_t M, int64_t D, int64_t images, svdq_norm kind, float eps) {
+  if (M < 0 || M > MAX_DIM) return fail(SVDQ_ERR_INVALID_ARG, "M out of range");
+  if (D <= 0) return fail(SVDQ_ERR_INVALID_ARG, "D must be positive");
+  if (D > MAX_NORM) return fail(SVDQ_ERR_UNSUPPORTED, "D must be at most 16384");
+  if (images <= 0 || images > MAX_IMAGES || M % images != 0)
+    return fail(SVDQ_ERR_INVALID_ARG, "images must be in [1, 2^20] and divide M");
+  if (kind != SVDQ_LAYER_NORM && kind != SVDQ_RMS_NORM)
+    return fail(SVDQ_ERR_INVALID_ARG, "unknown norm");
+  if (!(eps >= 0.f && eps <= 3.4e38f))
+    return fail(SVDQ_ERR_INVALID_ARG, "eps must be finite and not negative");
+  return SVDQ_OK;
+}
+
+// the vector as the kernels take it, and its extent
+svdq_status take_vec(const svdq_vec* v, const char* name, int64_t D, int64_t images, svdq::Vec& out,
+                     Span& span) {
+  out = {nullptr, 0, false};
+  span = {nullptr, 0, false};
+  if (!v) return SVDQ_OK;
+  const std::string n = name;
+  TRY(check_dtype(v->dtype, (n + ".dtype").c_str()));
+  TRY(check_ptr(v->data, (n + ".data").c_str(), elem(v->dtype)));
+  if (v->ld != 0 && (v->ld < D || v->ld > (int64_t(1) << 40) / images))
+    return fail(SVDQ_ERR_INVALID_ARG, n + ".ld must be 0 or at least D");
+  out = {v->data, v->ld, v->dtype == SVDQ_BF16};
+  const int64_t last = v->ld * (images - 1) + D;
+  span = {v->data, size_t(last) * elem(v->dtype), false};
+  return SVDQ_OK;
+}
+
+const char* const VEC_NAMES[] = {"post", "gate", "weight", "scale", "shift"};
+
+svdq_status take_vecs(const svdq_vec* const (&v)[5], bool block, int64_t D, int64_t images,
+                      svdq::BlockNorm& a, Span* spans) {
+  svdq::Vec* const to[] = {&a.post, &a.gate, &a.weight, &a.scale, &a.shift};
+  for (int i = 0; i < 5; ++i) TRY(take_vec(v[i], VEC_NAMES[i], D, images, *to[i], spans[i]));
+  if (!block && (a.post.p || a.gate.p))
+    return fail(SVDQ_ERR_INVALID_ARG, "post and gate go with H");
+  return SVDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_block_norm(const void* X, svdq_dtype x_dtype, const void* H, svdq_dtype h_dtype,
+                            int64_t M, int64_t D, int64_t images, svdq_norm kind, float eps,
+                            const svdq_vec* post, const svdq_vec* gate, const svdq_vec* weight,
+                            const svdq_vec* scale, const svdq_vec* shift, void* X_out, void* Y,
+                            svdq_dtype y_dtype, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_dtype(x_dtype, "x_dtype"));
+  if (H) TRY(check_dtype(h_dtype, "h_dtype"));
+  TRY(check_dtype(y_dtype, "y_dtype"));
+  TRY(check_norm(M, D, images, kind, eps));
+  if (M == 0) return SVDQ_OK;
+  svdq::BlockNorm a{X, H, x_dtype == SVDQ_BF16, h_dtype == SVDQ_BF16, kind == SVDQ_LAYER_NORM, D,
+                    M / images, eps};
+  Span spans[9];
+  TRY(check_ptr(X, "X", elem(x_dtype)));
+  TRY(take_vecs({post, gate, weight, scale, shift}, H != nullptr, D, images, a, spans));
+  if (!H != !X_out)
+    return fail(SVDQ_ERR_INVALID_ARG, "H and X_out are given together or not at all");
+  if (H) {
+    TRY(check_ptr(H, "H", elem(h_dtype)));
+    TRY(check_ptr(X_out, "X_out", elem(x_dtype)));
+  }
+  TRY(check_ptr(Y, "Y", elem(y_dtype)));
+  const size_t n = size_t(M) * size_t(D);
+  spans[5] = {X, n * elem(x_dtype), false};
+  spans[6] = {H, n * elem(h_dtype), false};
+  spans[7] = {X_out, n * elem(x_dtype), true};
+  spans[8] = {Y, n * elem(y_dtype), true};
+  TRY(check_spans(spans, 9));
+  return svdq::launch_block_norm(a, M, X_out, Y, y_dtype, stream);
+}
+
+size_t svdq_block_norm_grad_workspace_bytes(int64_t M, int64_t D, int64_t images) {
+  if (check_norm(M, D, images, SVDQ_RMS_NORM, 0.f) != SVDQ_OK) return 0;
+  return svdq::block_norm_grad_workspace(M, D, images);
+}
+
+svdq_status svdq_block_norm_grad(const void* dY, svdq_dtype y_dtype, const void* dX_out,
+                                 const void* X, svdq_dtype x_dtype, const void* H,
+                                 svdq_dtype h_dtype, int64_t M, int64_t D, int64_t images,
+                                 svdq_norm kind, float eps, const svdq_vec* post,
+                                 const svdq_vec* gate, const svdq_vec* weight,
+                                 const svdq_vec* scale, const svdq_vec* shift, void* dX, void* dH,
+                                 float* dpost, float* dgate, float* dweight, float* dscale,
+                                 float* dshift, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_dtype(y_dtype, "y_dtype"));
+  TRY(check_dtype(x_dtype, "x_dtype"));
+  if (H || dH) TRY(check_dtype(h_dtype, "h_dtype"));
+  TRY(check_norm(M, D, images, kind, eps));
+  svdq::BlockNorm a{X, H, x_dtype == SVDQ_BF16, h_dtype == SVDQ_BF16, kind == SVDQ_LAYER_NORM, D,
+                    M / images, eps};
+  const svdq::BlockNormGrad g{dY, dX_out, dX, dH, y_dtype == SVDQ_BF16};
+  Span spans[17];
+  // (without rows there is no H to go by)
+  TRY(take_vecs({post, gate, weight, scale, shift}, H != nullptr || M == 0, D, images, a, spans));
+  float* const out[5] = {dpost, dgate, dweight, dscale, dshift};
+  const svdq::Vec* const vs[] = {&a.post, &a.gate, &a.weight, &a.scale, &a.shift};
+  for (int i = 0; i < 5; ++i) {
+    spans[5 + i] = {nullptr, 0, true};
+    if (!out[i]) continue;
+    const std::string n = std::string("d") + VEC_NAMES[i];
+    if (!vs[i]->p)
+      return fail(SVDQ_ERR_INVALID_ARG, n + " is asked for without " + VEC_NAMES[i]);
+    TRY(check_ptr(out[i], n.c_str()));
+    spans[5 + i].p = out[i];
+    spans[5 + i].bytes = size_t(vs[i]->ld ? images : 1) * size_t(D) * 4;
+  }
+  const size_t n = size_t(M) * size_t(D), need = svdq::block_norm_grad_workspace(M, D, images);
+  if (M) {
+    TRY(check_ptr(dY, "dY", elem(y_dtype)));
+    TRY(check_ptr(X, "X", elem(x_dtype)));
+    TRY(check_ptr(dX, "dX", elem(x_dtype)));
+    if (!H != !dH) return fail(SVDQ_ERR_INVALID_ARG, "H and dH are given together or not at all");
+    if (H) {
+      TRY(check_ptr(H, "H", elem(h_dtype)));
+      TRY(check_ptr(dH, "dH", elem(h_dtype)));
+    }
+    if (dX_out) TRY(check_ptr(dX_out, "dX_out", elem(x_dtype)));
+    TRY(check_workspace(workspace, workspace_bytes, need));
+  }
+  spans[10] = {dY, n * elem(y_dtype), false};
+  spans[11] = {dX_out, n * elem(x_dtype), false};
+  spans[12] = {X, n * elem(x_dtype), false};
+  spans[13] = {H, n * elem(h_dtype), false};
+  spans[14] = {dX, n * elem(x_dtype), true};
+  spans[15] = {dH, n * elem(h_dtype), true};
+  spans[16] = {workspace, need, true};
+  TRY(check_spans(spans, 17));
+  return svdq::launch_block_norm_grad(a, g, M, images, out, workspace, stream);
 }
 
 }  // extern "C"

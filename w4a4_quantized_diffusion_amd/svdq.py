@@ -22,6 +22,8 @@ _PREC = {"int4": INT4, "nvfp4": NVFP4, INT4: INT4, NVFP4: NVFP4}
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 SILU, GELU = 0, 1
 _ACT = {"silu": SILU, "gelu": GELU, SILU: SILU, GELU: GELU}
+LAYER_NORM, RMS_NORM = 0, 1
+_NORM = {"layer": LAYER_NORM, "rms": RMS_NORM, LAYER_NORM: LAYER_NORM, RMS_NORM: RMS_NORM}
 
 _lib = None
 
@@ -85,6 +87,19 @@ _SIG = {
     # workspace_bytes, stream
     "awq_linear_w4a16_grad": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P,
                                               ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    # X, x_dtype, H, h_dtype, M, D, images, kind, eps, post, gate, weight, scale,
+    # shift, X_out, Y, y_dtype, stream
+    "svdq_block_norm": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int, _I64, _I64, _I64,
+                                        ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P,
+                                        ctypes.c_int, _P]),
+    "svdq_block_norm_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    # dY, y_dtype, dX_out, X, x_dtype, H, h_dtype, M, D, images, kind, eps, post, gate,
+    # weight, scale, shift, dX, dH, dpost, dgate, dweight, dscale, dshift, workspace,
+    # workspace_bytes, stream
+    "svdq_block_norm_grad": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int, _P,
+                                             ctypes.c_int, _I64, _I64, _I64, ctypes.c_int,
+                                             ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                             _P, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 EXPORTS = tuple(_SIG)
 
@@ -546,3 +561,118 @@ def awq_linear_w4a16_grad(dY, layer, dx_dtype=torch.bfloat16, workspace=None, dX
     _run(dev, l.awq_linear_w4a16_grad, d, M, K, N, layer["group"], *_awq_args(layer, K, N, dev),
          dX.data_ptr(), _DT[xt], ws, nws)
     return dX
+
+
+# ------------------------------------------------- norms around a block
+
+class Vec(ctypes.Structure):
+    """svdq_vec"""
+    _fields_ = [("data", _P), ("dtype", ctypes.c_int), ("ld", _I64)]
+
+
+_VECTORS = ("post", "gate", "weight", "scale", "shift")
+
+
+def _vecs(vectors, M, D, dev):
+    """(images, [svdq_vec or None]) of a call's vectors: [D], or [images, D] with the
+    rows at any distance."""
+    images, out = 1, []
+    for name, v in zip(_VECTORS, vectors):
+        if v is None:
+            out.append(None)
+            continue
+        if v.dtype not in _DT:
+            raise TypeError(f"{name} must be float32 or bfloat16, got {v.dtype}")
+        if v.get_device() != dev:
+            raise ValueError(f"{name} is on {v.device}, expected cuda:{dev}")
+        shape = v.shape
+        if not 1 <= len(shape) <= 2 or shape[-1] != D or shape[0] == 0:
+            raise ValueError(f"{name} must have shape [{D}] or [images, {D}], got {tuple(shape)}")
+        if D > 1 and v.stride(-1) != 1:
+            raise ValueError(f"{name}: the values of a row must be adjacent")
+        ld = 0
+        if len(shape) == 2 and shape[0] > 1:
+            n = shape[0]
+            if images != 1 and n != images:
+                raise ValueError(f"{name} has {n} rows, another vector {images}")
+            if M % n:
+                raise ValueError(f"{name} has {n} rows, which do not divide the {M} rows of x")
+            images, ld = n, v.stride(0)
+            if ld < D:
+                raise ValueError(f"{name}: its rows overlap")
+        out.append(Vec(v.data_ptr(), _DT[v.dtype], ld))
+    return images, out
+
+
+def _matrix(t, name, like, dev):
+    """A float32 or bfloat16 operand [M, D] -> (address, dtype)."""
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return _arg(t, name, like, t.dtype, dev), _DT[t.dtype]
+
+
+def svdq_block_norm(x, h=None, kind="layer", eps=1e-6, post=None, gate=None, weight=None,
+                    scale=None, shift=None, y_dtype=torch.bfloat16, X_out=None, Y=None):
+    """The residual sum x' = x + gate * t with t = h or n(h) * post, and the norm
+    n(x') * weight * (1 + scale) + shift behind it.  x, h: float32 or bfloat16 [M, D]
+    (each its own); kind "layer" or "rms"; every vector float32 or bfloat16, [D] or
+    [images, D] (one row for every M / images rows of x, at any row distance).
+    Returns (x', y), x' in x's type, or y alone without h."""
+    l = lib()
+    if x.dim() != 2:
+        raise ValueError(f"x must have shape [M, D], got {tuple(x.shape)}")
+    M, dev = _rows(x, "x", x.shape[1])
+    D = x.shape[1]
+    xp, xt = _matrix(x, "x", x.shape, dev)
+    images, v = _vecs((post, gate, weight, scale, shift), M, D, dev)
+    hp = op = None
+    ht = F32
+    if h is not None:
+        hp, ht = _matrix(h, "h", (M, D), dev)
+        X_out = _out(X_out, "X_out", (M, D), x.dtype, x, dev)
+        op = X_out.data_ptr()
+    elif X_out is not None:
+        raise ValueError("X_out goes with h")
+    yt = _out_dtype(Y, y_dtype, "Y")
+    Y = _out(Y, "Y", (M, D), yt, x, dev)
+    _run(dev, l.svdq_block_norm, xp, xt, hp, ht, M, D, images, _NORM[kind], eps,
+         *(e and ctypes.byref(e) for e in v), op, Y.data_ptr(), _DT[yt])
+    return Y if h is None else (X_out, Y)
+
+
+def svdq_block_norm_grad_workspace_bytes(M, D, images):
+    return int(lib().svdq_block_norm_grad_workspace_bytes(M, D, images))
+
+
+def svdq_block_norm_grad(dy, x, h=None, dx_out=None, kind="layer", eps=1e-6, post=None, gate=None,
+                         weight=None, scale=None, shift=None, workspace=None,
+                         need=(True,) * 5):
+    """The backward pass of svdq_block_norm from the gradients of its outputs (dx_out
+    None: zeros) and its inputs.  Returns (dx, dh, dpost, dgate, dweight, dscale,
+    dshift): dx and dh in the types of x and h, the vectors' gradients float32 in the
+    vectors' shapes; None where there is no input, or `need` (of the five vectors)
+    says no."""
+    l = lib()
+    if x.dim() != 2:
+        raise ValueError(f"x must have shape [M, D], got {tuple(x.shape)}")
+    M, dev = _rows(x, "x", x.shape[1])
+    D = x.shape[1]
+    xp, xt = _matrix(x, "x", x.shape, dev)
+    dyp, dyt = _matrix(dy, "dy", (M, D), dev)
+    vectors = (post, gate, weight, scale, shift)
+    images, v = _vecs(vectors, M, D, dev)
+    hp = dhp = dh = None
+    ht = F32
+    if h is not None:
+        hp, ht = _matrix(h, "h", (M, D), dev)
+        dh = torch.empty_like(h)
+        dhp = dh.data_ptr()
+    dop = None if dx_out is None else _arg(dx_out, "dx_out", (M, D), x.dtype, dev)
+    dx = torch.empty_like(x)
+    grads = [x.new_empty(t.shape, dtype=torch.float32) if t is not None and n else None
+             for t, n in zip(vectors, need)]
+    keep, ws, nws = _ws(workspace, l.svdq_block_norm_grad_workspace_bytes(M, D, images), x, dev)
+    _run(dev, l.svdq_block_norm_grad, dyp, dyt, dop, xp, xt, hp, ht, M, D, images, _NORM[kind], eps,
+         *(e and ctypes.byref(e) for e in v), dx.data_ptr(), dhp,
+         *(None if t is None else t.data_ptr() for t in grads), ws, nws)
+    return (dx, dh, *grads)
