@@ -88,9 +88,9 @@ typedef enum {
 
 typedef enum { SVDQ_INT4 = 0, SVDQ_NVFP4 = 1 } svdq_precision;
 typedef enum { SVDQ_F32 = 0, SVDQ_BF16 = 1 } svdq_dtype;
-/* Gate activations of a gated feed-forward pair: x / (1 + exp(-x)), and the
- * tanh form of GELU (the formula at svdq_act_quantize_gelu). */
-typedef enum { SVDQ_SILU = 0, SVDQ_GELU = 1 } svdq_act;
+/* Activations: x / (1 + exp(-x)), the tanh form of GELU (the formula at
+ * svdq_act_quantize_gelu), and none (for the calls that say so). */
+typedef enum { SVDQ_SILU = 0, SVDQ_GELU = 1, SVDQ_NO_ACT = 2 } svdq_act;
 typedef enum { SVDQ_LAYER_NORM = 0, SVDQ_RMS_NORM = 1 } svdq_norm;
 
 /* svdq_quantize_weights flag: lora_down / lora_up are INPUTS (the low-rank
@@ -433,6 +433,39 @@ svdq_status svdq_block_norm_grad(const void* dY, svdq_dtype y_dtype, const void*
                                  float* dpost, float* dgate, float* dweight, float* dscale,
                                  float* dshift, void* workspace, size_t workspace_bytes,
                                  hipStream_t stream);
+
+/* ------------------------------------ AWQ product with a block's epilogue
+ * A block's output projection with the residual sum behind it, or an up-projection
+ * with its activation, on AWQ weights:
+ *   Z = X . wd^T + bias,  Y = R + gate * act(Z)
+ * with wd as in awq_linear_w4a16; act may be SVDQ_NO_ACT.  Z is fp32 until Y is
+ * rounded, once.  gate: NULL (1) or a svdq_vec of N (see svdq_block_norm: ld 0 for all
+ * rows, else one per image of M / images rows); R [M, N] r_dtype or NULL (0); Z_out:
+ * bf16 [M, N] or NULL, receives Z rounded as awq_linear_w4a16_res_grad reads it.
+ * X bf16 [M, K], bias bf16 [N] or NULL, Y [M, N] y_dtype.  Everything else, sizes
+ * included, as for the weight-only operators; 1 <= images <= 2^20 divides M. */
+size_t awq_linear_w4a16_res_workspace_bytes(int64_t M, int64_t K, int64_t N);
+svdq_status awq_linear_w4a16_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, int32_t group,
+                                 const uint8_t* q, const uint16_t* scales, const uint16_t* zeros,
+                                 const uint16_t* bias, svdq_act act, const svdq_vec* gate,
+                                 int64_t images, const void* R, svdq_dtype r_dtype, void* Y,
+                                 svdq_dtype y_dtype, uint16_t* Z_out, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/* Its backward pass for frozen weights and biases (R's gradient is dY itself):
+ *   dZ = dY * gate * act'(Z),  dX = dZ . wd,  dgate = sum over rows of dY * act(Z)
+ * dY [M, N] dy_dtype; Z bf16 [M, N] as the forward call stored it (may be NULL with
+ * SVDQ_NO_ACT and no dgate); dX bf16 [M, K]; dZ bf16 [M, N], rounded before the product
+ * (it is the gradient at the bias and for adapters too); dgate fp32, [images, N], [N]
+ * for a gate with ld 0, or NULL.  Sums over rows have a fixed order; with M == 0 dgate
+ * is set to zero. */
+size_t awq_linear_w4a16_res_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t images);
+svdq_status awq_linear_w4a16_res_grad(const void* dY, svdq_dtype dy_dtype, const uint16_t* Z,
+                                      int64_t M, int64_t K, int64_t N, int32_t group,
+                                      const uint8_t* q, const uint16_t* scales,
+                                      const uint16_t* zeros, svdq_act act, const svdq_vec* gate,
+                                      int64_t images, uint16_t* dX, uint16_t* dZ, float* dgate,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

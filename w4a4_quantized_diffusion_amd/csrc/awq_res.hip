@@ -1,0 +1,684 @@
+// AWQ W4A16 product with bias, activation, gate and residual in its epilogue (gfx950):
+//
+//   Z = X wd^T + bias,   Y = R + gate * act(Z)
+//
+// wd = bf16((q - z) s) [N, K], X bf16 [M, K], gate one vector of N for all rows or one
+// per image, R [M, N] fp32 or bf16.  Z stays in the fp32 accumulators of the bf16
+// MFMAs; Y is rounded once.  Z can be stored in bf16 for the backward pass
+//
+//   dZ = dY * gate * act'(Z),  dX = dZ wd,  dgate = sum over rows of dY * act(Z)
+//
+// whose first and last part are here, the product in awq_grad.hip.
+
+#include "block.h"
+#include "gemm_bf16.h"
+
+using namespace svdq_dev;
+
+namespace {
+
+using svdq::ResEpilogue;
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float x) {
+  if constexpr (ACT == SVDQ_NO_ACT)
+    return x;
+  else
+    return gate_act<ACT>(x);
+}
+
+// V values at any address that is a multiple of their size (a copy leaves the compiler
+// to choose loads that the target takes there)
+template <int V>
+__device__ __forceinline__ void load_any(const void* p, bool b16, int64_t at, float (&v)[V]) {
+  if (b16) {
+    uint16_t t[V];
+    __builtin_memcpy(t, static_cast<const uint16_t*>(p) + at, 2 * V);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = bf16_to_f32(t[i]);
+  } else {
+    __builtin_memcpy(v, static_cast<const float*>(p) + at, 4 * V);
+  }
+}
+
+__device__ __forceinline__ int64_t gate_at(const ResEpilogue& e, int m, int64_t n) {
+  return (e.gate.ld ? e.gate.ld * (uint32_t(e.first + m) / uint32_t(e.rows)) : 0) + n;
+}
+
+// V (4 or 8) neighbouring outputs of row m from column n on: z = acc + bias
+template <int ACT, int V>
+__device__ __forceinline__ void emit(const ResEpilogue& e, int m, int64_t n, int64_t N,
+                                     float (&z)[V]) {
+  const int64_t at = int64_t(m) * N + n;
+  auto put = [&](void* Y, bool b16, const float (&v)[V]) __attribute__((always_inline)) {
+    if (b16) {
+      uint16_t* const p = static_cast<uint16_t*>(Y) + at;
+      if constexpr (V == 8)
+        __builtin_nontemporal_store(
+            v4i{int(pack_bf16x2(v[0], v[1])), int(pack_bf16x2(v[2], v[3])),
+                int(pack_bf16x2(v[4], v[5])), int(pack_bf16x2(v[6], v[7]))},
+            reinterpret_cast<v4i*>(p));
+      else
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+      float* const p = static_cast<float*>(Y) + at;
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        __builtin_nontemporal_store(v4f{v[i], v[i + 1], v[i + 2], v[i + 3]},
+                                    reinterpret_cast<v4f*>(p + i));
+    }
+  };
+  if (e.Z) put(e.Z, true, z);
+#pragma unroll
+  for (int i = 0; i < V; ++i) z[i] = act_of<ACT>(z[i]);
+  if (e.gate.p) {
+    float g[V];
+    load_any<V>(e.gate.p, e.gate.b16, gate_at(e, m, n), g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] *= g[i];
+  }
+  if (e.R) {
+    float r[V];
+    load_any<V>(e.R, e.r16, at, r);
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] += r[i];
+  }
+  put(e.Y, e.y16, z);
+}
+
+// A wave's RBL x CBL blocks of 32 x 32 in the accumulators, through its LDS buffer
+// `eb` (32 x (32 CBL + 4) floats), so that a lane has 8 neighbouring columns of a row.
+template <int ACT, int RBL, int CBL>
+__device__ __forceinline__ void res_epilogue(const ResEpilogue& e, const v16f (&acc)[RBL][CBL],
+                                             float* eb, int lane, int64_t row0, int64_t col0,
+                                             int M, int N) {
+  constexpr int ER = 32 * CBL + 4, CH = 4 * CBL, RPI = 64 / CH;
+  const int h = lane >> 5, r32 = lane & 31, q = lane % CH;
+  const int64_t n = col0 + 8 * q;
+  float b[8] = {};
+  if (e.bias && n < N) load_any<8>(e.bias, true, n, b);
+#pragma unroll
+  for (int i = 0; i < RBL; ++i) {
+#pragma unroll
+    for (int j = 0; j < CBL; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        eb[(8 * (k >> 2) + 4 * h + (k & 3)) * ER + j * 32 + r32] = acc[i][j][k];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int t = 0; t < 32 / RPI; ++t) {
+      const int rr = lane / CH + RPI * t;
+      const float4 u = *reinterpret_cast<const float4*>(eb + rr * ER + 8 * q);
+      const float4 v = *reinterpret_cast<const float4*>(eb + rr * ER + 8 * q + 4);
+      const int64_t m = row0 + i * 32 + rr;
+      float z[8] = {u.x + b[0], u.y + b[1], u.z + b[2], u.w + b[3],
+                    v.x + b[4], v.y + b[5], v.z + b[6], v.w + b[7]};
+      if (m < M && n < N) emit<ACT, 8>(e, int(m), n, N, z);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// ----------------------------------------------------------- few rows
+// Up to 64 rows the time is the weights' way from memory and how many launches follow
+// one another.  One launch where X is small (res_column_kernel), else slices of K
+// whose partial sums a second launch joins with the epilogue.
+
+constexpr int ROWS = 64;
+constexpr int WAVES = 8, NT = 64 * WAVES;
+constexpr int LDS_X = 64 << 10;
+constexpr int SUM_SLICES = 8;
+
+struct Split {
+  int blocks, slices;
+};
+
+Split split(int64_t M, int64_t K, int64_t N) {
+  Split p;
+  p.blocks = int((N + 16 * WAVES - 1) / (16 * WAVES));
+  p.slices = int(std::min<int64_t>(
+      {K / 64, SUM_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+  return p;
+}
+
+// every 16 columns read all of X in one launch: N / 16 times 2 M K bytes from the L2
+bool one_launch(int64_t M, int64_t K, int64_t N) {
+  return M * N <= (int64_t(1) << 30) / K && !(M > 16 && K >= 4096 && N <= 1024);
+}
+
+// One chunk of 64 k of 16 rows of the weights: lane group j holds the codes
+// k = 16 j .. 16 j + 15 of its row.
+struct Codes {
+  uint2 w;
+  uint32_t s, z;
+};
+
+__device__ __forceinline__ void fetch_codes(Codes& c, const svdq::AwqWeight& w, int64_t at, int j) {
+  c.w = *reinterpret_cast<const uint2*>(w.q + at * 32 + 8 * j);
+  c.s = w.s[at];
+  c.z = w.z[at];
+}
+
+// past the last chunk (not live) the scales are zeros
+__device__ __forceinline__ void operands(const Codes& c, bool live, v8bf (&b)[2]) {
+  const float s = live ? __uint_as_float(c.s << 16) : 0.f;
+  const float zs = -__uint_as_float(c.z << 16) * s;
+  b[0] = __builtin_bit_cast(v8bf, dequant8(c.w.x, s, zs));
+  b[1] = __builtin_bit_cast(v8bf, dequant8(c.w.y, s, zs));
+}
+
+template <int MT>
+__global__ __launch_bounds__(NT, 4) void res_slice_kernel(const uint16_t* __restrict__ X, int M,
+                                                          int K, int N, svdq::AwqWeight w, int S,
+                                                          int sub, float* __restrict__ part) {
+  constexpr int D = 4;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j = lane >> 4, r = lane & 15;
+  const int G = K / 64;
+  const int slice = blockIdx.x % S;
+  const int g0 = int(int64_t(slice) * G / S), count = int(int64_t(slice + 1) * G / S) - g0;
+  const int64_t n = (int64_t(blockIdx.x / S) * WAVES + wave) * 16 + r;
+  const int64_t nc = min(n, int64_t(N) - 1);
+  Codes ring[D];
+  // every slot is always loaded (past the last chunk with the last one's data), so that
+  // the number of loads in flight is fixed
+  auto fetch = [&](int i, Codes& c) __attribute__((always_inline)) {
+    fetch_codes(c, w, int64_t(g0 + min(i, count - 1)) * N + nc, j);
+  };
+  v4f acc[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) acc[mt] = v4f{0, 0, 0, 0};
+  // `sub` chunks of X at a time in LDS: rows of `sub` chunks and 16 bytes, so that 16
+  // rows start in 16 different groups of 4 banks
+  const int rowb = sub * 128 + 16;
+  int xoff[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) xoff[mt] = min(16 * mt + r, M - 1) * rowb + 32 * j;
+  for (int c0 = 0; c0 < count; c0 += sub) {
+    const int here = min(sub, count - c0);
+    if (c0) __syncthreads();
+    for (int i = tid; i < M * here * 8; i += NT) {
+      const int m = i / (here * 8), o = i - m * (here * 8);
+      *reinterpret_cast<uint4*>(lds + m * rowb + 16 * o) =
+          *reinterpret_cast<const uint4*>(X + int64_t(m) * K + 64 * int64_t(g0 + c0) + 8 * o);
+    }
+    if (c0 == 0)
+#pragma unroll
+      for (int d = 0; d < D; ++d) fetch(d, ring[d]);
+    // (not __syncthreads, which would wait for the weights too)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    for (int c = 0; c < here; c += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        v8bf b[2];
+        operands(ring[d], c + d < here, b);
+        const uint8_t* const xc = lds + 128 * min(c + d, here - 1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                *reinterpret_cast<const v8bf*>(xc + xoff[mt] + 16 * h), b[h], acc[mt], 0, 0, 0);
+        fetch(c0 + c + d + D, ring[d]);
+      }
+  }
+  if (n >= N) return;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int m = 16 * mt + 4 * j + e;
+      // (read by the next launch, on any XCD: past this one's L2 at once)
+      if (m < M)
+        __builtin_nontemporal_store(acc[mt][e], part + (int64_t(slice) * M + m) * N + n);
+    }
+}
+
+// 4 columns per thread
+template <int ACT>
+__global__ __launch_bounds__(64) void res_sum_kernel(const float* __restrict__ part, int S, int M,
+                                                     int N, ResEpilogue e) {
+  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x, total = int64_t(M) * N / 4;
+  if (i >= total) return;
+  const int64_t m = 4 * i / N, n = 4 * i - m * N;
+  // all loads first; a slice past the last counts as zeros
+  v4f v[SUM_SLICES];
+#pragma unroll
+  for (int q = 0; q < SUM_SLICES; ++q)
+    v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q, S - 1)) * total + i];
+  float z[4] = {}, b[4] = {};
+  if (e.bias) load_any<4>(e.bias, true, n, b);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int q = 0; q < SUM_SLICES; ++q) z[k] += q < S ? v[q][k] : 0.f;
+    z[k] += b[k];
+  }
+  emit<ACT, 4>(e, int(m), n, N, z);
+}
+
+// One launch: a workgroup owns 16 columns, its 8 waves take the chunks of K in turn,
+// each with its own piece of X, and the sums meet in LDS.
+template <int MT, int ACT>
+__global__ __launch_bounds__(NT, 4) void res_column_kernel(const uint16_t* __restrict__ X, int M,
+                                                           int K, int N, svdq::AwqWeight w,
+                                                           ResEpilogue e) {
+  constexpr int D = MT == 1 ? 4 : 2;
+  __shared__ v4f red[WAVES][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane >> 4, r = lane & 15;
+  const int64_t n = int64_t(blockIdx.x) * 16 + r;                   // (N is a multiple of 16)
+  const int G = K / 64, count = (G - wave + WAVES - 1) / WAVES;     // chunks of this wave
+  const uint16_t* xrow[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) xrow[mt] = X + int64_t(min(16 * mt + r, M - 1)) * K + 16 * j;
+  struct Slot {
+    Codes c;
+    uint4 x[MT][2];
+  } ring[D];
+  // every slot is always loaded (past the last chunk with the last one's
+  // data; a wave without chunks loads chunk 0 and never uses it)
+  auto fetch = [&](int i, Slot& sl) __attribute__((always_inline)) {
+    const int c = count > 0 ? wave + WAVES * min(i, count - 1) : 0;
+    fetch_codes(sl.c, w, int64_t(c) * N + n, j);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint4* const x = reinterpret_cast<const uint4*>(xrow[mt] + 64 * int64_t(c));
+      sl.x[mt][0] = x[0];
+      sl.x[mt][1] = x[1];
+    }
+  };
+  v4f acc[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) acc[mt] = v4f{0, 0, 0, 0};
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d, ring[d]);
+  for (int c = 0; c < count; c += D)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      Slot& sl = ring[d];
+      v8bf b[2];
+      operands(sl.c, c + d < count, b);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, sl.x[mt][h]),
+                                                            b[h], acc[mt], 0, 0, 0);
+      fetch(c + d + D, sl);
+    }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) red[wave][mt][lane] = acc[mt];
+  __syncthreads();
+  // thread (wave w < MT, row t of its 16, columns 4 q ..): the sums from LDS, where
+  // element (row 4 j + e, column r) lies in component e of lane 16 j + r
+  if (wave >= MT) return;
+  const int row = lane >> 2, q = lane & 3, m = 16 * wave + row;
+  if (m >= M) return;
+  float z[4], b[4] = {};
+  const int64_t n0 = int64_t(blockIdx.x) * 16 + 4 * q;
+  if (e.bias) load_any<4>(e.bias, true, n0, b);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int from = 16 * (row >> 2) + 4 * q + k;
+    z[k] = reinterpret_cast<const float*>(&red[0][wave][from])[row & 3];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v)
+      z[k] += reinterpret_cast<const float*>(&red[v][wave][from])[row & 3];
+    z[k] += b[k];
+  }
+  emit<ACT, 4>(e, m, n0, N, z);
+}
+
+// ---------------------------------------------------------- many rows
+// The weights dequantized once into the workspace: 64 rows and four groups of 64 k (two
+// stages each) per workgroup, so that its loads are in flight together; four lanes take
+// one row, 8 k of each stage, so that a wave stores 1 KB in a row.
+constexpr int DEQUANT_GROUPS = 4;
+
+__global__ __launch_bounds__(256) void res_dequant_kernel(svdq::AwqWeight w, int K, int N,
+                                                          uint16_t* __restrict__ B) {
+  const int row = threadIdx.x >> 2, piece = threadIdx.x & 3;
+  const int blocks = (N + 63) / 64, G = K / 64, g0 = blockIdx.x / blocks * DEQUANT_GROUPS;
+  const int64_t n = int64_t(blockIdx.x % blocks) * 64 + row;
+  if (n >= N) return;
+  uint32_t c[DEQUANT_GROUPS][2];
+  uint16_t s[DEQUANT_GROUPS], z[DEQUANT_GROUPS];
+#pragma unroll
+  for (int i = 0; i < DEQUANT_GROUPS; ++i) {
+    const int64_t at = int64_t(min(g0 + i, G - 1)) * N + n;
+    const uint32_t* const p = reinterpret_cast<const uint32_t*>(w.q + at * 32 + piece * 4);
+    c[i][0] = p[0];
+    c[i][1] = p[4];
+    s[i] = w.s[at];
+    z[i] = w.z[at];
+  }
+#pragma unroll
+  for (int i = 0; i < DEQUANT_GROUPS; ++i) {
+    if (g0 + i >= G) break;
+    const float f = bf16_to_f32(s[i]), fz = -bf16_to_f32(z[i]) * f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      *svdq_gemm::weight_at(B, K / 32, n, 64 * (g0 + i) + 32 * t + 8 * piece) =
+          dequant8(c[i][t], f, fz);
+  }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(svdq_gemm::NT) void res_wide_kernel(svdq_gemm::Args p, ResEpilogue e) {
+  using namespace svdq_gemm;
+  __shared__ Stage st0, st1, st2, st3, st4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t m0, b0;
+  tile_origin((p.M + BM - 1) / BM, (p.rows + BN - 1) / BN, BM, BN, m0, b0);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  tile_product(p, m0, b0, st0, st1, st2, st3, st4, acc);
+  res_epilogue<ACT, RBL, CBL>(e, acc, epilogue_buffer<32 * (WN + 4)>(wave, st0, st1, st2), lane,
+                              m0 + (wave >> 2) * WM, b0 + (wave & 3) * WN, p.M, p.rows);
+}
+
+// -------------------------------------------------------- medium number of rows
+// B rows of a tile: 128 rows of the weights, two threads to a row, 32 codes each.
+struct RowWeights {
+  // this thread's row of chunk 0; a chunk further is N rows further
+  const uint8_t* q;
+  const uint16_t *s, *z;
+  int N, row, half;
+  uint4 c[2];
+  uint16_t cs[2], cz[2];
+
+  __device__ __forceinline__ RowWeights(const svdq::AwqWeight& w, int N, int64_t n0)
+      : N(N), row(int(threadIdx.x) >> 1), half(threadIdx.x & 1) {
+    const int64_t nr = min(n0 + row, int64_t(N) - 1);
+    q = w.q + nr * 32 + 16 * half;
+    s = w.s + nr;
+    z = w.z + nr;
+  }
+  static __device__ __forceinline__ int slot(int row, int piece) {
+    return row * 8 + (piece ^ ((row >> 1) & 7));
+  }
+  template <int set>
+  __device__ __forceinline__ void fetch(int chunk) {
+    const int64_t at = int64_t(chunk) * N;
+    c[set] = *reinterpret_cast<const uint4*>(q + at * 32);
+    cs[set] = s[at];
+    cz[set] = z[at];
+  }
+  template <int set, int i>
+  __device__ __forceinline__ void put(uint4* b) {
+    const uint32_t w = i == 0 ? c[set].x : i == 1 ? c[set].y : i == 2 ? c[set].z : c[set].w;
+    const float f = bf16_to_f32(cs[set]);
+    b[slot(row, 4 * half + i)] = dequant8(w, f, -bf16_to_f32(cz[set]) * f);
+  }
+};
+
+template <int ACT>
+__global__ __launch_bounds__(svdq_mid::NT, 2) void res_mid_kernel(svdq_mid::Args p,
+                                                                  svdq::AwqWeight wt, int N, int S,
+                                                                  int tiles, ResEpilogue e,
+                                                                  float* __restrict__ part) {
+  using namespace svdq_mid;
+  __shared__ ChunkA a0, a1, a2;
+  __shared__ ChunkB b0, b1;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slice = blockIdx.x / tiles;
+  int64_t m0, n0;
+  tile_at(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (N + BN - 1) / BN, BM, BN, m0, n0);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  RowWeights w(wt, N, n0);
+  tile_product(p, m0, int(int64_t(slice) * p.chunks / S), int(int64_t(slice + 1) * p.chunks / S), w,
+               a0, a1, a2, b0, b1, acc);
+  const int64_t row0 = m0 + (wave >> 1) * 64, col0 = n0 + (wave & 1) * 64;
+  // 32 x 68 floats, in an LDS object of the wave's own
+  float* const eb = reinterpret_cast<float*>(wave == 0   ? &a0.v
+                                              : wave == 1 ? &a1.v
+                                              : wave == 2 ? &a2.v
+                                                          : &b0.v);
+  if (S == 1) {
+    res_epilogue<ACT, RBL, CBL>(e, acc, eb, lane, row0, col0, p.M, N);
+    return;
+  }
+  const float none[CBL] = {0.f, 0.f};
+  store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, N,
+                                   part + int64_t(slice) * p.M * N);
+}
+
+int64_t mid_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128); }
+
+int64_t wide_rows(int64_t M, int64_t K, int64_t N) {
+  if (M <= ROWS) return 0;
+  return svdq_plan::wide_rows(M, {K / 64, (N + 255) / 256, (N + 127) / 128, K * N});
+}
+
+size_t weight_bytes(int64_t K, int64_t N) { return svdq_gemm::weight_bytes(N, K / 32); }
+
+// bytes of the partial sums of `rows` rows
+size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
+  if (rows == 0 || (rows <= ROWS && one_launch(rows, K, N))) return 0;
+  const int S = rows <= ROWS ? split(rows, K, N).slices
+                             : svdq_mid::slices(mid_tiles(rows, N), K / 64);
+  return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(N) * 4);
+}
+
+// A call's rows [m0, m0 + M); the epilogue's row numbers start at m0 with `e`
+struct Call {
+  const uint16_t* X;
+  int64_t M, K, N;
+  svdq::AwqWeight w;
+  svdq_act act;
+  ResEpilogue e;
+  hipStream_t s;
+};
+
+template <template <int> class Kernel>
+auto by_act(svdq_act a) {
+  return a == SVDQ_SILU ? Kernel<SVDQ_SILU>::get()
+         : a == SVDQ_GELU ? Kernel<SVDQ_GELU>::get()
+                          : Kernel<SVDQ_NO_ACT>::get();
+}
+template <int ACT>
+struct SumKernel {
+  static auto get() { return res_sum_kernel<ACT>; }
+};
+template <int ACT>
+struct MidKernel {
+  static auto get() { return res_mid_kernel<ACT>; }
+};
+template <int ACT>
+struct WideKernel {
+  static auto get() { return res_wide_kernel<ACT>; }
+};
+
+svdq_status sum(const Call& c, const float* part, int S) {
+  hipLaunchKernelGGL(by_act<SumKernel>(c.act), dim3(unsigned((c.M * c.N / 4 + 63) / 64)), dim3(64),
+                     0, c.s, part, S, int(c.M), int(c.N), c.e);
+  return svdq::check_launch("awq_res (sum)");
+}
+
+template <int MT>
+svdq_status few(const Call& c, float* part) {
+  if (one_launch(c.M, c.K, c.N)) {
+    auto k = c.act == SVDQ_SILU   ? res_column_kernel<MT, SVDQ_SILU>
+             : c.act == SVDQ_GELU ? res_column_kernel<MT, SVDQ_GELU>
+                                  : res_column_kernel<MT, SVDQ_NO_ACT>;
+    hipLaunchKernelGGL(k, dim3(unsigned(c.N / 16)), dim3(NT), 0, c.s, c.X, int(c.M), int(c.K),
+                       int(c.N), c.w, c.e);
+    return svdq::check_launch("awq_res (column)");
+  }
+  const Split p = split(c.M, c.K, c.N);
+  // chunks of X that fit LDS, a multiple of the register ring's 4: chunk c of a piece is
+  // in slot c % 4, which goes on over the pieces
+  const int most = int((LDS_X / c.M - 16) / 128 / 4 * 4);
+  const int len = int((c.K / 64 + p.slices - 1) / p.slices);
+  const int sub = std::min(most, (len + 3) / 4 * 4);
+  hipLaunchKernelGGL(res_slice_kernel<MT>, dim3(unsigned(p.blocks * p.slices)), dim3(NT),
+                     size_t(c.M) * (sub * 128 + 16), c.s, c.X, int(c.M), int(c.K), int(c.N), c.w,
+                     p.slices, sub, part);
+  SVDQ_TRY(svdq::check_launch("awq_res (slice)"));
+  return sum(c, part, p.slices);
+}
+
+svdq_status mid(const Call& c, float* part) {
+  const int64_t tiles = mid_tiles(c.M, c.N);
+  const int S = svdq_mid::slices(tiles, c.K / 64);
+  svdq_mid::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, int(c.M)};
+  hipLaunchKernelGGL(by_act<MidKernel>(c.act), dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0,
+                     c.s, p, c.w, int(c.N), S, int(tiles), c.e, part);
+  SVDQ_TRY(svdq::check_launch("awq_res (mid)"));
+  return S == 1 ? SVDQ_OK : sum(c, part, S);
+}
+
+svdq_status wide(const Call& c, uint16_t* B) {
+  const int64_t quads = (c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS;
+  hipLaunchKernelGGL(res_dequant_kernel, dim3(unsigned((c.N + 63) / 64 * quads)), dim3(256), 0, c.s,
+                     c.w, int(c.K), int(c.N), B);
+  SVDQ_TRY(svdq::check_launch("awq_res (dequant)"));
+  const int64_t tiles = (c.M + 255) / 256 * ((c.N + 255) / 256);
+  svdq_gemm::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, B, int(c.M), int(c.N)};
+  hipLaunchKernelGGL(by_act<WideKernel>(c.act), dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, c.s,
+                     p, c.e);
+  return svdq::check_launch("awq_res (wide)");
+}
+
+// ------------------------------------------------------------- backward
+// A wave takes 512 columns, 8 to a lane, and every fourth row of a workgroup's; the
+// workgroup's sums for dgate meet in LDS and, where an image has more workgroups than
+// one, in a second launch in a fixed order.  Memory bound.
+constexpr int GRAD_ROWS = 64;            // rows of a workgroup, at most
+
+template <int ACT>
+__global__ __launch_bounds__(256) void res_grad_kernel(const void* __restrict__ dY, bool dy16,
+                                                       const uint16_t* __restrict__ Z,
+                                                       svdq::Vec gate, int64_t rows, int parts,
+                                                       int N, uint16_t* __restrict__ dZ,
+                                                       float* __restrict__ part) {
+  __shared__ float red[3][8][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int blocks = (N + 511) / 512;
+  const int64_t n = int64_t(blockIdx.x % blocks) * 512 + 8 * lane;
+  const int64_t group = blockIdx.x / blocks, image = group / parts, p = group % parts;
+  const int64_t r0 = image * rows + p * rows / parts, r1 = image * rows + (p + 1) * rows / parts;
+  const bool live = n < N;
+  float g[8], acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = 1.f, acc[i] = 0.f;
+  if (gate.p && live) load_any<8>(gate.p, gate.b16, image * gate.ld + n, g);
+  if (live)
+#pragma unroll 2
+    for (int64_t m = r0 + wave; m < r1; m += 4) {
+      const int64_t at = m * N + n;
+      float d[8], z[8] = {};
+      load_any<8>(dY, dy16, at, d);
+      if (Z) load_any<8>(Z, true, at, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a = z[i], da = 1.f;
+        if constexpr (ACT != SVDQ_NO_ACT) gate_act_grad<ACT>(z[i], a, da);
+        acc[i] = fmaf(d[i], a, acc[i]);
+        d[i] *= g[i] * da;
+      }
+      *reinterpret_cast<uint4*>(dZ + at) =
+          make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
+                     pack_bf16x2(d[6], d[7]));
+    }
+  if (!part) return;
+  if (wave)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[wave - 1][i][lane] = acc[i];
+  __syncthreads();
+  if (wave || !live) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    acc[i] = (acc[i] + red[0][i][lane]) + (red[1][i][lane] + red[2][i][lane]);
+  float4* const o = reinterpret_cast<float4*>(part + group * N + n);
+  o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+template <int ACT>
+struct GradKernel {
+  static auto get() { return res_grad_kernel<ACT>; }
+};
+
+int grad_parts(int64_t rows) { return int(std::max<int64_t>(1, (rows + GRAD_ROWS - 1) / GRAD_ROWS)); }
+
+size_t grad_part_bytes(int64_t M, int64_t N, int64_t images) {
+  const int64_t groups = images * grad_parts(M / images);
+  return groups == 1 ? 0 : svdq::align256(size_t(groups) * size_t(N) * 4);
+}
+
+}  // namespace
+
+namespace svdq {
+
+size_t awq_res_workspace(int64_t M, int64_t K, int64_t N) {
+  const int64_t w = wide_rows(M, K, N);
+  return (w ? weight_bytes(K, N) : 0) + part_bytes(M - w, K, N);
+}
+
+svdq_status launch_awq_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, AwqWeight wt,
+                           svdq_act act, const ResEpilogue& e, void* ws, hipStream_t s) {
+  const int64_t w = wide_rows(M, K, N), rest = M - w;
+  uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  Call c{X, M, K, N, wt, act, e, s};
+  if (w) {
+    c.M = w;
+    SVDQ_TRY(wide(c, reinterpret_cast<uint16_t*>(w8)));
+  }
+  if (!rest) return SVDQ_OK;
+  // the rows behind: every operand from row w on; `first` keeps the images' count
+  c.X = X + w * K;
+  c.M = rest;
+  c.e.first = int(w);
+  c.e.Y = static_cast<uint8_t*>(e.Y) + w * N * (e.y16 ? 2 : 4);
+  if (e.R) c.e.R = static_cast<const uint8_t*>(e.R) + w * N * (e.r16 ? 2 : 4);
+  if (e.Z) c.e.Z = e.Z + w * N;
+  float* const part = reinterpret_cast<float*>(w8 + (w ? weight_bytes(K, N) : 0));
+  if (rest > ROWS) return mid(c, part);
+  switch ((rest + 15) / 16) {
+    case 1: return few<1>(c, part);
+    case 2: return few<2>(c, part);
+    case 3: return few<3>(c, part);
+    default: return few<4>(c, part);
+  }
+}
+
+size_t awq_res_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t images) {
+  return grad_part_bytes(M, N, images) + awq_linear_grad_workspace(M, K, N);
+}
+
+svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, int64_t M, int64_t K,
+                                int64_t N, int64_t images, AwqWeight wt, svdq_act act, Vec gate,
+                                uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s) {
+  const int64_t rows = M / images, each = gate.ld ? images : 1;
+  if (M == 0) return dgate ? launch_join(nullptr, N, 0, each, dgate, s) : SVDQ_OK;
+  const int parts = grad_parts(rows);
+  uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  // one workgroup's sums are the gradient
+  const bool direct = images * parts == each;
+  float* const part = !dgate ? nullptr : direct ? dgate : reinterpret_cast<float*>(w8);
+  hipLaunchKernelGGL(by_act<GradKernel>(act), dim3(unsigned((N + 511) / 512 * images * parts)),
+                     dim3(256), 0, s, dY, dy16, Z, gate, rows, parts, int(N), dZ, part);
+  SVDQ_TRY(check_launch("awq_res_grad"));
+  if (dgate && !direct)
+    SVDQ_TRY(launch_join(part, N, images * parts / each, each, dgate, s));
+  return launch_awq_linear_grad(dZ, M, K, N, wt, dX, SVDQ_BF16,
+                                w8 + grad_part_bytes(M, N, images), s);
+}
+
+}  // namespace svdq

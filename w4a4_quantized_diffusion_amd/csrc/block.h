@@ -1,0 +1,63 @@
+// The operators around a block's layers (norms, residual sums, epilogues): what the C
+// ABI hands on.
+#pragma once
+
+#include "w4a16.h"
+
+namespace svdq {
+
+// a vector of D per image (ld elements apart) or for all rows (ld 0); p NULL: absent
+struct Vec {
+  const void* p;
+  int64_t ld;
+  bool b16;
+};
+
+struct BlockNorm {
+  const void *X, *H;      // [M, D]; H may be NULL
+  bool x16, h16, layer;
+  int64_t D, rows;        // rows of one image
+  float eps;
+  Vec post, gate, weight, scale, shift;
+};
+
+struct BlockNormGrad {
+  const void *dY, *dX_out;
+  void *dX, *dH;
+  bool y16;
+  int64_t parts;          // workgroups an image
+  float* part[5];         // partial sums of the vectors' gradients [workgroups][D]
+};
+
+// out[i][D] = sum over parts i parts .. of part [each parts][D], in a fixed order; zeros
+// for no parts
+svdq_status launch_join(const float* part, int64_t D, int64_t parts, int64_t each, float* out,
+                        hipStream_t s);
+
+// Epilogue of an AWQ product: Y = R + gate * act(Z), Z = the product + bias
+struct ResEpilogue {
+  const uint16_t* bias;   // [N] or NULL
+  Vec gate;
+  int rows, first;        // rows of one image; the image rows before the call's first row
+  const void* R;          // [M, N] or NULL
+  bool r16;
+  void* Y;
+  bool y16;
+  uint16_t* Z;            // [M, N] or NULL
+};
+size_t awq_res_workspace(int64_t M, int64_t K, int64_t N);
+svdq_status launch_awq_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, AwqWeight w,
+                           svdq_act act, const ResEpilogue& e, void* ws, hipStream_t s);
+size_t awq_res_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t images);
+svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, int64_t M, int64_t K,
+                                int64_t N, int64_t images, AwqWeight w, svdq_act act, Vec gate,
+                                uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s);
+
+svdq_status launch_block_norm(const BlockNorm& a, int64_t M, void* X_out, void* Y, svdq_dtype y_dt,
+                              hipStream_t s);
+size_t block_norm_grad_workspace(int64_t M, int64_t D, int64_t images);
+// out: the gradients of post, gate, weight, scale and shift (NULL: not wanted), fp32
+svdq_status launch_block_norm_grad(const BlockNorm& a, BlockNormGrad g, int64_t M, int64_t images,
+                                   float* const (&out)[5], void* ws, hipStream_t s);
+
+}  // namespace svdq

@@ -14,7 +14,7 @@
 // registers, where sum v^2 - mean^2 would lose the digits of a large mean).  x' enters
 // the norm as the fp32 sum, before it is rounded to X's type.
 
-#include "block_norm.h"
+#include "block.h"
 
 using namespace svdq_dev;
 
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(1024) void block_norm_grad_kernel(svdq::BlockNorm a
 }
 
 // out[i] = sum over the parts of image i (all of them where a vector is shared)
-__global__ __launch_bounds__(256) void block_norm_join_kernel(const float* __restrict__ part, int D,
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int D,
                                                               int64_t parts,
                                                               float* __restrict__ out) {
   __shared__ float red[4][64];
@@ -460,6 +460,13 @@ int64_t grad_parts(int64_t M, int64_t images) {
 }  // namespace
 
 namespace svdq {
+
+svdq_status launch_join(const float* part, int64_t D, int64_t parts, int64_t each, float* out,
+                        hipStream_t s) {
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned((D + 63) / 64 * each)), dim3(256), 0, s, part,
+                     int(D), parts, out);
+  return check_launch("join");
+}
 
 svdq_status launch_block_norm(const BlockNorm& a, int64_t M, void* X_out, void* Y, svdq_dtype y_dt,
                               hipStream_t s) {
@@ -513,9 +520,7 @@ svdq_status launch_block_norm_grad(const BlockNorm& a, BlockNormGrad g, int64_t 
   for (int k = 0; k < VECTORS; ++k) {
     if (!out[k] || g.part[k] == out[k]) continue;
     const int64_t each = vs[k]->ld ? images : 1, parts = images * g.parts / each;
-    hipLaunchKernelGGL(block_norm_join_kernel, dim3(unsigned((a.D + 63) / 64 * each)), dim3(256), 0,
-                       s, g.part[k], int(a.D), parts, out[k]);
-    SVDQ_TRY(check_launch("block_norm_join"));
+    SVDQ_TRY(launch_join(g.part[k], a.D, parts, each, out[k], s));
   }
   return SVDQ_OK;
 }

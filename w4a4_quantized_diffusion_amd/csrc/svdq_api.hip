@@ -1,7 +1,7 @@
 // C ABI front end: argument validation, workspace layout, dispatch, and the
 // per-thread error message.  Every check runs before any HIP call.
 
-#include "block_norm.h"
+#include "block.h"
 
 #include <cstdio>
 #include <mutex>
@@ -880,6 +880,122 @@ svdq_status svdq_block_norm_grad(const void* dY, svdq_dtype y_dtype, const void*
   spans[16] = {workspace, need, true};
   TRY(check_spans(spans, 17));
   return svdq::launch_block_norm_grad(a, g, M, images, out, workspace, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------- AWQ product with an epilogue
+namespace {
+
+svdq_status check_act_or_none(svdq_act a) {
+  if (a == SVDQ_NO_ACT) return SVDQ_OK;
+  return check_act(a);
+}
+
+svdq_status check_images(int64_t M, int64_t images) {
+  if (images <= 0 || images > MAX_IMAGES || M % images != 0)
+    return fail(SVDQ_ERR_INVALID_ARG, "images must be in [1, 2^20] and divide M");
+  return SVDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t awq_linear_w4a16_res_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (check_mkn(M, K, N) != SVDQ_OK) return 0;
+  return svdq::awq_res_workspace(M, K, N);
+}
+
+svdq_status awq_linear_w4a16_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, int32_t group,
+                                 const uint8_t* q, const uint16_t* scales, const uint16_t* zeros,
+                                 const uint16_t* bias, svdq_act act, const svdq_vec* gate,
+                                 int64_t images, const void* R, svdq_dtype r_dtype, void* Y,
+                                 svdq_dtype y_dtype, uint16_t* Z_out, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_group(group));
+  TRY(check_act_or_none(act));
+  TRY(check_dtype(y_dtype, "y_dtype"));
+  if (R) TRY(check_dtype(r_dtype, "r_dtype"));
+  TRY(check_mkn(M, K, N));
+  TRY(check_tiles(M, N));
+  TRY(check_images(M, images));
+  if (M == 0) return SVDQ_OK;
+  const svdq::AwqWeight w{q, scales, zeros};
+  Span spans[10];
+  svdq::ResEpilogue e{bias, {}, int(M / images), 0, R, r_dtype == SVDQ_BF16,
+                      Y, y_dtype == SVDQ_BF16, Z_out};
+  TRY(take_vec(gate, "gate", N, images, e.gate, spans[0]));
+  TRY(check_ptr(X, "X"));
+  TRY(check_awq(w, ""));
+  if (bias) TRY(check_ptr(bias, "bias", 2));
+  if (R) TRY(check_ptr(R, "R"));
+  TRY(check_ptr(Y, "Y"));
+  if (Z_out) TRY(check_ptr(Z_out, "Z_out"));
+  const size_t need = svdq::awq_res_workspace(M, K, N);
+  TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t m = M, k = K, n = N;
+  spans[1] = {X, m * k * 2, false};
+  spans[2] = {q, n * k / 2, false};
+  spans[3] = {scales, n * k / 32, false};
+  spans[4] = {zeros, n * k / 32, false};
+  spans[5] = {bias, n * 2, false};
+  spans[6] = {R, m * n * elem(r_dtype), false};
+  spans[7] = {Y, m * n * elem(y_dtype), true};
+  spans[8] = {Z_out, m * n * 2, true};
+  spans[9] = {workspace, need, true};
+  TRY(check_spans(spans, 10));
+  return svdq::launch_awq_res(X, M, K, N, w, act, e, workspace, stream);
+}
+
+size_t awq_linear_w4a16_res_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t images) {
+  if (check_mkn(M, K, N) != SVDQ_OK || check_images(M, images) != SVDQ_OK) return 0;
+  return svdq::awq_res_grad_workspace(M, K, N, images);
+}
+
+svdq_status awq_linear_w4a16_res_grad(const void* dY, svdq_dtype dy_dtype, const uint16_t* Z,
+                                      int64_t M, int64_t K, int64_t N, int32_t group,
+                                      const uint8_t* q, const uint16_t* scales,
+                                      const uint16_t* zeros, svdq_act act, const svdq_vec* gate,
+                                      int64_t images, uint16_t* dX, uint16_t* dZ, float* dgate,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_group(group));
+  TRY(check_act_or_none(act));
+  TRY(check_dtype(dy_dtype, "dy_dtype"));
+  TRY(check_mkn(M, K, N));
+  TRY(check_tiles(M, K));
+  TRY(check_images(M, images));
+  const svdq::AwqWeight w{q, scales, zeros};
+  Span spans[10];
+  svdq::Vec g;
+  TRY(take_vec(gate, "gate", N, images, g, spans[0]));
+  if (dgate) {
+    if (!gate) return fail(SVDQ_ERR_INVALID_ARG, "dgate is asked for without gate");
+    TRY(check_ptr(dgate, "dgate"));
+  }
+  const size_t m = M, k = K, n = N, need = M ? svdq::awq_res_grad_workspace(M, K, N, images) : 0;
+  if (M) {
+    TRY(check_ptr(dY, "dY"));
+    if (Z || act != SVDQ_NO_ACT || dgate) TRY(check_ptr(Z, "Z"));
+    TRY(check_awq(w, ""));
+    TRY(check_ptr(dX, "dX"));
+    TRY(check_ptr(dZ, "dZ"));
+    TRY(check_workspace(workspace, workspace_bytes, need));
+  }
+  spans[1] = {dY, m * n * elem(dy_dtype), false};
+  spans[2] = {Z, m * n * 2, false};
+  spans[3] = {q, n * k / 2, false};
+  spans[4] = {scales, n * k / 32, false};
+  spans[5] = {zeros, n * k / 32, false};
+  spans[6] = {dX, m * k * 2, true};
+  spans[7] = {dZ, m * n * 2, true};
+  spans[8] = {dgate, size_t(g.ld ? images : 1) * n * 4, true};
+  spans[9] = {workspace, need, true};
+  TRY(check_spans(spans, 10));
+  return svdq::launch_awq_res_grad(dY, dy_dtype == SVDQ_BF16, Z, M, K, N, images, w, act, g, dX, dZ,
+                                   dgate, workspace, stream);
 }
 
 }  // extern "C"

@@ -22,6 +22,8 @@ _PREC = {"int4": INT4, "nvfp4": NVFP4, INT4: INT4, NVFP4: NVFP4}
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 SILU, GELU = 0, 1
 _ACT = {"silu": SILU, "gelu": GELU, SILU: SILU, GELU: GELU}
+NO_ACT = 2
+_ACT_OR_NONE = {**_ACT, "none": NO_ACT, None: NO_ACT, NO_ACT: NO_ACT}
 LAYER_NORM, RMS_NORM = 0, 1
 _NORM = {"layer": LAYER_NORM, "rms": RMS_NORM, LAYER_NORM: LAYER_NORM, RMS_NORM: RMS_NORM}
 
@@ -100,6 +102,18 @@ _SIG = {
                                              ctypes.c_int, _I64, _I64, _I64, ctypes.c_int,
                                              ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                              _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "awq_linear_w4a16_res_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    # X, M, K, N, group, q, scales, zeros, bias, act, gate, images, R, r_dtype, Y,
+    # y_dtype, Z_out, workspace, workspace_bytes, stream
+    "awq_linear_w4a16_res": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P,
+                                             ctypes.c_int, _P, _I64, _P, ctypes.c_int, _P,
+                                             ctypes.c_int, _P, _P, ctypes.c_size_t, _P]),
+    "awq_linear_w4a16_res_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
+    # dY, dy_dtype, Z, M, K, N, group, q, scales, zeros, act, gate, images, dX, dZ,
+    # dgate, workspace, workspace_bytes, stream
+    "awq_linear_w4a16_res_grad": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I64, _I64, _I32, _P,
+                                                  _P, _P, ctypes.c_int, _P, _I64, _P, _P, _P, _P,
+                                                  ctypes.c_size_t, _P]),
 }
 EXPORTS = tuple(_SIG)
 
@@ -573,11 +587,11 @@ class Vec(ctypes.Structure):
 _VECTORS = ("post", "gate", "weight", "scale", "shift")
 
 
-def _vecs(vectors, M, D, dev):
+def _vecs(vectors, M, D, dev, names=_VECTORS):
     """(images, [svdq_vec or None]) of a call's vectors: [D], or [images, D] with the
     rows at any distance."""
     images, out = 1, []
-    for name, v in zip(_VECTORS, vectors):
+    for name, v in zip(names, vectors):
         if v is None:
             out.append(None)
             continue
@@ -676,3 +690,62 @@ def svdq_block_norm_grad(dy, x, h=None, dx_out=None, kind="layer", eps=1e-6, pos
          *(e and ctypes.byref(e) for e in v), dx.data_ptr(), dhp,
          *(None if t is None else t.data_ptr() for t in grads), ws, nws)
     return (dx, dh, *grads)
+
+
+# ------------------------------------ AWQ product with a block's epilogue
+
+def awq_linear_w4a16_res_workspace_bytes(M, K, N):
+    return int(lib().awq_linear_w4a16_res_workspace_bytes(M, K, N))
+
+
+def awq_linear_w4a16_res(X, layer, bias=None, act="none", gate=None, residual=None,
+                         y_dtype=torch.bfloat16, save=False, workspace=None, Y=None):
+    """residual + gate * act(X wd^T + bias) on an AWQ layer.  X bf16 [M, K]; bias bf16
+    [N] or None; act "none", "silu" or "gelu" (tanh form); gate float32 or bfloat16, [N]
+    or [images, N] (a row for every M / images rows of X), or None; residual float32 or
+    bfloat16 [M, N] or None.  Returns Y [M, N], or (Y, Z) with the bf16 pre-activations
+    that awq_linear_w4a16_res_grad reads if save."""
+    l = lib()
+    K, N = layer["K"], layer["N"]
+    M, dev = _rows(X, "X", K)
+    x = _arg(X, "X", X.shape, torch.bfloat16, dev)
+    images, (g,) = _vecs((gate,), M, N, dev, ("gate",))
+    r, rt = (None, F32) if residual is None else _matrix(residual, "residual", (M, N), dev)
+    yt = _out_dtype(Y, y_dtype, "Y")
+    Y = _out(Y, "Y", (M, N), yt, X, dev)
+    Z = X.new_empty((M, N)) if save else None
+    b = None if bias is None else _arg(bias, "bias", (N,), torch.bfloat16, dev)
+    keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_res_workspace_bytes(M, K, N), X, dev)
+    _run(dev, l.awq_linear_w4a16_res, x, M, K, N, layer["group"], *_awq_args(layer, K, N, dev), b,
+         _ACT_OR_NONE[act], g and ctypes.byref(g), images, r, rt, Y.data_ptr(), _DT[yt],
+         Z.data_ptr() if save else None, ws, nws)
+    return (Y, Z) if save else Y
+
+
+def awq_linear_w4a16_res_grad_workspace_bytes(M, K, N, images):
+    return int(lib().awq_linear_w4a16_res_grad_workspace_bytes(M, K, N, images))
+
+
+def awq_linear_w4a16_res_grad(dY, Z, layer, act="none", gate=None, workspace=None,
+                              need_dgate=True):
+    """The backward pass of awq_linear_w4a16_res for frozen weights, from dY (float32 or
+    bfloat16 [M, N]) and the saved Z (bf16; None with act "none" where dgate is not
+    needed).  Returns (dX [M, K] bf16, dZ [M, N] bf16, dgate float32 in gate's shape or
+    None); the residual's gradient is dY."""
+    l = lib()
+    K, N = layer["K"], layer["N"]
+    M, dev = _rows(dY, "dY", N)
+    d, dt = _matrix(dY, "dY", dY.shape, dev)
+    z = None if Z is None else _arg(Z, "Z", (M, N), torch.bfloat16, dev)
+    images, (g,) = _vecs((gate,), M, N, dev, ("gate",))
+    bf = torch.bfloat16
+    dX, dZ = dY.new_empty((M, K), dtype=bf), dY.new_empty((M, N), dtype=bf)
+    dgate = None
+    if gate is not None and need_dgate:
+        dgate = dY.new_empty(gate.shape, dtype=torch.float32)
+    keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_res_grad_workspace_bytes(M, K, N, images), dY,
+                        dev)
+    _run(dev, l.awq_linear_w4a16_res_grad, d, dt, z, M, K, N, layer["group"],
+         *_awq_args(layer, K, N, dev), _ACT_OR_NONE[act], g and ctypes.byref(g), images,
+         dX.data_ptr(), dZ.data_ptr(), None if dgate is None else dgate.data_ptr(), ws, nws)
+    return dX, dZ, dgate
