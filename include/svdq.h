@@ -467,6 +467,33 @@ svdq_status awq_linear_w4a16_res_grad(const void* dY, svdq_dtype dy_dtype, const
                                       int64_t images, uint16_t* dX, uint16_t* dZ, float* dgate,
                                       void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------- mixture of experts
+ * A feed-forward layer of E experts, each a gated pair and a down-projection on AWQ
+ * weights, for few tokens, from the router's logits:
+ *   e_1 .. e_top = the experts with the largest logits[t] (equal ones: lower first)
+ *   p_j = softmax(logits[t])[e_j], divided by p_1 + .. + p_top if renorm is not 0
+ *   Y[t] = sum_j p_j . (act(X[t] . wd_gate^T) * (X[t] . wd_up^T)) . wd_down^T  at e_j
+ * Every sum is fp32; the products' input of wd_down is rounded to bf16, and Y once.
+ * X bf16 [T, K], logits [T, E] logits_dtype (f32 or bf16, aligned to its elements), Y
+ * bf16 [T, K].  q / scales / zeros of gate and up: E layers [N, K] as
+ * awq_quantize_weights writes them, one behind the other; of down: E layers [K, N].
+ * ids int32 [T, top] and weights f32 [T, top] receive e_j and p_j (NULL: not wanted).
+ * A logit of -infinity keeps an expert out as long as others are left (its p is 0); a
+ * token whose logits are all -infinity has p = 0, and a NaN counts as the largest
+ * logit and makes its token's p and Y NaN.  An infinity or NaN in X stays in its token.
+ * 0 <= T <= 64, E <= 256, 1 <= top <= min(E, 16) (more: SVDQ_ERR_UNSUPPORTED),
+ * K % 64 == 0, N % 64 == 0, group == 64.  Workspace as for the weight-only operators. */
+size_t awq_moe_w4a16_workspace_bytes(int64_t T, int64_t E, int32_t top, int64_t K, int64_t N);
+svdq_status awq_moe_w4a16(const uint16_t* X, const void* logits, svdq_dtype logits_dtype, int64_t T,
+                          int64_t E, int32_t top, int64_t K, int64_t N, int32_t group,
+                          const uint8_t* q_gate, const uint16_t* scales_gate,
+                          const uint16_t* zeros_gate, const uint8_t* q_up,
+                          const uint16_t* scales_up, const uint16_t* zeros_up,
+                          const uint8_t* q_down, const uint16_t* scales_down,
+                          const uint16_t* zeros_down, svdq_act act, int32_t renorm, uint16_t* Y,
+                          int32_t* ids, float* weights, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

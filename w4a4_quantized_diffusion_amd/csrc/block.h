@@ -53,6 +53,14 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
                                 int64_t N, int64_t images, AwqWeight w, svdq_act act, Vec gate,
                                 uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s);
 
+// Mixture of experts on AWQ weights, expert after expert (every one K N / 64 rows of 32
+// bytes of codes)
+size_t awq_moe_workspace(int64_t T, int64_t top, int64_t N);
+svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int64_t T, int64_t E,
+                           int64_t top, int64_t K, int64_t N, AwqWeight gate, AwqWeight up,
+                           AwqWeight down, svdq_act act, bool renorm, uint16_t* Y, int32_t* ids,
+                           float* weights, void* ws, hipStream_t s);
+
 svdq_status launch_block_norm(const BlockNorm& a, int64_t M, void* X_out, void* Y, svdq_dtype y_dt,
                               hipStream_t s);
 size_t block_norm_grad_workspace(int64_t M, int64_t D, int64_t images);

@@ -999,3 +999,68 @@ svdq_status awq_linear_w4a16_res_grad(const void* dY, svdq_dtype dy_dtype, const
 }
 
 }  // extern "C"
+
+// ------------------------------------------------- mixture of experts
+namespace {
+
+svdq_status check_moe(int64_t T, int64_t E, int32_t top, int64_t K, int64_t N) {
+  TRY(check_mkn(T, K, N));
+  if (N % 64 != 0) return fail(SVDQ_ERR_INVALID_ARG, "N must be a positive multiple of 64");
+  if (T > 64) return fail(SVDQ_ERR_UNSUPPORTED, "awq_moe_w4a16 takes at most 64 tokens");
+  if (E <= 0) return fail(SVDQ_ERR_INVALID_ARG, "E must be positive");
+  if (E > 256) return fail(SVDQ_ERR_UNSUPPORTED, "E must be at most 256");
+  if (top <= 0 || top > E) return fail(SVDQ_ERR_INVALID_ARG, "top must be in [1, E]");
+  if (top > 16) return fail(SVDQ_ERR_UNSUPPORTED, "top must be at most 16");
+  return SVDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t awq_moe_w4a16_workspace_bytes(int64_t T, int64_t E, int32_t top, int64_t K, int64_t N) {
+  if (check_moe(T, E, top, K, N) != SVDQ_OK) return 0;
+  return svdq::awq_moe_workspace(T, top, N);
+}
+
+svdq_status awq_moe_w4a16(const uint16_t* X, const void* logits, svdq_dtype logits_dtype, int64_t T,
+                          int64_t E, int32_t top, int64_t K, int64_t N, int32_t group,
+                          const uint8_t* q_gate, const uint16_t* scales_gate,
+                          const uint16_t* zeros_gate, const uint8_t* q_up,
+                          const uint16_t* scales_up, const uint16_t* zeros_up,
+                          const uint8_t* q_down, const uint16_t* scales_down,
+                          const uint16_t* zeros_down, svdq_act act, int32_t renorm, uint16_t* Y,
+                          int32_t* ids, float* weights, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  svdq::clear_error();
+  TRY(check_group(group));
+  TRY(check_act(act));
+  TRY(check_dtype(logits_dtype, "logits_dtype"));
+  TRY(check_moe(T, E, top, K, N));
+  if (T == 0) return SVDQ_OK;
+  const svdq::AwqWeight g{q_gate, scales_gate, zeros_gate}, u{q_up, scales_up, zeros_up},
+      d{q_down, scales_down, zeros_down};
+  TRY(check_ptr(X, "X"));
+  TRY(check_ptr(logits, "logits", elem(logits_dtype)));
+  TRY(check_awq(g, "_gate"));
+  TRY(check_awq(u, "_up"));
+  TRY(check_awq(d, "_down"));
+  TRY(check_ptr(Y, "Y"));
+  if (ids) TRY(check_ptr(ids, "ids", 4));
+  if (weights) TRY(check_ptr(weights, "weights", 4));
+  const size_t need = svdq::awq_moe_workspace(T, top, N);
+  TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t t = T, e = E, k = K, n = N, c = size_t(T) * size_t(top) * 4;
+  const Span spans[] = {{X, t * k * 2, false}, {logits, t * e * elem(logits_dtype), false},
+                        {q_gate, e * n * k / 2, false}, {scales_gate, e * n * k / 32, false},
+                        {zeros_gate, e * n * k / 32, false}, {q_up, e * n * k / 2, false},
+                        {scales_up, e * n * k / 32, false}, {zeros_up, e * n * k / 32, false},
+                        {q_down, e * n * k / 2, false}, {scales_down, e * n * k / 32, false},
+                        {zeros_down, e * n * k / 32, false}, {Y, t * k * 2, true}, {ids, c, true},
+                        {weights, c, true}, {workspace, need, true}};
+  TRY(check_spans(spans, 15));
+  return svdq::launch_awq_moe(X, logits, logits_dtype == SVDQ_BF16, T, E, top, K, N, g, u, d, act,
+                              renorm != 0, Y, ids, weights, workspace, stream);
+}
+
+}  // extern "C"

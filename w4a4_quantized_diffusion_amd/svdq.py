@@ -114,6 +114,11 @@ _SIG = {
     "awq_linear_w4a16_res_grad": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I64, _I64, _I32, _P,
                                                   _P, _P, ctypes.c_int, _P, _I64, _P, _P, _P, _P,
                                                   ctypes.c_size_t, _P]),
+    "awq_moe_w4a16_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32, _I64, _I64]),
+    # X, logits, logits_dtype, T, E, top, K, N, group, gate q / scales / zeros, up,
+    # down, act, renorm, Y, ids, weights, workspace, workspace_bytes, stream
+    "awq_moe_w4a16": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I64, _I32, _I64, _I64, _I32]
+                      + [_P] * 9 + [ctypes.c_int, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 EXPORTS = tuple(_SIG)
 
@@ -749,3 +754,45 @@ def awq_linear_w4a16_res_grad(dY, Z, layer, act="none", gate=None, workspace=Non
          *_awq_args(layer, K, N, dev), _ACT_OR_NONE[act], g and ctypes.byref(g), images,
          dX.data_ptr(), dZ.data_ptr(), None if dgate is None else dgate.data_ptr(), ws, nws)
     return dX, dZ, dgate
+
+
+# ------------------------------------------------- mixture of experts
+
+def awq_moe_w4a16_workspace_bytes(T, E, top, K, N):
+    return int(lib().awq_moe_w4a16_workspace_bytes(T, E, top, K, N))
+
+
+def _experts_args(lay, E, K, N, dev, which):
+    if lay["E"] != E or lay["K"] != K or lay["N"] != N:
+        raise ValueError(f"{which} is {lay['E']} x {lay['N']} x {lay['K']}, expected "
+                         f"{E} x {N} x {K}")
+    g = K // 64
+    return (_arg(lay["q"], "q_" + which, (E, g, N, 32), torch.uint8, dev),
+            _arg(lay["scales"], "scales_" + which, (E, g, N), torch.int16, dev),
+            _arg(lay["zeros"], "zeros_" + which, (E, g, N), torch.int16, dev))
+
+
+def awq_moe_w4a16(X, logits, gate, up, down, top, act="silu", renorm=True, routing=False,
+                  workspace=None, Y=None):
+    """A mixture-of-experts layer for at most 64 tokens, from the router's logits
+    (float32 or bfloat16 [T, E]).  X bf16 [T, K]; gate, up and down: dicts as an AWQ
+    layer's with a leading dimension of E experts in q, scales and zeros and E beside N, K
+    and group (gate and up N x K, down K x N).  Returns Y [T, K] bf16, or (Y, ids int32,
+    weights float32 [T, top]) if routing."""
+    l = lib()
+    E, K, N = gate["E"], gate["K"], gate["N"]
+    T, dev = _rows(X, "X", K)
+    x = _arg(X, "X", X.shape, torch.bfloat16, dev)
+    lg, lt = _matrix(logits, "logits", (T, E), dev)
+    Y = _out(Y, "Y", (T, K), torch.bfloat16, X, dev)
+    ids = w = ip = wp = None
+    if routing:
+        ids = X.new_empty((T, top), dtype=torch.int32)
+        w = X.new_empty((T, top), dtype=torch.float32)
+        ip, wp = ids.data_ptr(), w.data_ptr()
+    keep, ws, nws = _ws(workspace, l.awq_moe_w4a16_workspace_bytes(T, E, top, K, N), X, dev)
+    _run(dev, l.awq_moe_w4a16, x, lg, lt, T, E, top, K, N, gate["group"],
+         *_experts_args(gate, E, K, N, dev, "gate"), *_experts_args(up, E, K, N, dev, "up"),
+         *_experts_args(down, E, N, K, dev, "down"), _ACT[act], 1 if renorm else 0, Y.data_ptr(),
+         ip, wp, ws, nws)
+    return (Y, ids, w) if routing else Y
