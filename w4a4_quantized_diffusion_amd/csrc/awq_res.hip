@@ -666,7 +666,11 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
                                 int64_t N, int64_t images, AwqWeight wt, svdq_act act, Vec gate,
                                 uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s) {
   const int64_t rows = M / images, each = gate.ld ? images : 1;
-  if (M == 0) return dgate ? launch_join(nullptr, N, 0, each, dgate, s) : SVDQ_OK;
+  Joins j{};
+  if (M == 0) {
+    if (dgate) j.add(nullptr, dgate, N, 0, each);
+    return launch_joins(j, N, s);
+  }
   const int parts = grad_parts(rows);
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
   // one workgroup's sums are the gradient
@@ -675,8 +679,8 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
   hipLaunchKernelGGL(by_act<GradKernel>(act), dim3(unsigned((N + 511) / 512 * images * parts)),
                      dim3(256), 0, s, dY, dy16, Z, gate, rows, parts, int(N), dZ, part);
   SVDQ_TRY(check_launch("awq_res_grad"));
-  if (dgate && !direct)
-    SVDQ_TRY(launch_join(part, N, images * parts / each, each, dgate, s));
+  if (dgate && !direct) j.add(part, dgate, N, images * parts / each, each);
+  SVDQ_TRY(launch_joins(j, N, s));
   return launch_awq_linear_grad(dZ, M, K, N, wt, dX, SVDQ_BF16,
                                 w8 + grad_part_bytes(M, N, images), s);
 }

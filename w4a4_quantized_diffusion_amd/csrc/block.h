@@ -16,7 +16,7 @@ struct Vec {
 struct BlockNorm {
   const void *X, *H;      // [M, D]; H may be NULL
   bool x16, h16, layer;
-  int64_t D, rows;        // rows of one image
+  int64_t D, images, rows;  // rows of one image
   float eps;
   Vec post, gate, weight, scale, shift;
 };
@@ -29,10 +29,22 @@ struct BlockNormGrad {
   float* part[5];         // partial sums of the vectors' gradients [workgroups][D]
 };
 
-// out[i][D] = sum over parts i parts .. of part [each parts][D], in a fixed order; zeros
-// for no parts
-svdq_status launch_join(const float* part, int64_t D, int64_t parts, int64_t each, float* out,
-                        hipStream_t s);
+// Sums of partial results, up to five in one launch: to[i][D] = the sum over parts
+// i parts .. of from [each parts][D], in a fixed order; zeros for no parts
+struct Joins {
+  int count;
+  const float* from[5];
+  float* to[5];
+  int64_t parts[5], blocks[5];
+
+  void add(const float* f, float* t, int64_t D, int64_t p, int64_t each) {
+    from[count] = f;
+    to[count] = t;
+    parts[count] = p;
+    blocks[count++] = (D + 63) / 64 * each;
+  }
+};
+svdq_status launch_joins(const Joins& j, int64_t D, hipStream_t s);
 
 // Epilogue of an AWQ product: Y = R + gate * act(Z), Z = the product + bias
 struct ResEpilogue {

@@ -24,98 +24,163 @@ using svdq::Vec;
 
 constexpr int MAX_WAVES = 16;
 
+// How a row is cut into pieces of V elements: all threads have as many; or not, with the
+// last piece moved back to end with the row where D is no multiple of V, its first
+// elements counting as absent (a branch for a short piece would cost every load: 9216
+// rows of 4096 78 us against 60); or D < V, one thread with element-wise accesses.
+enum Tail { FULL, MOVED, TINY };
+
+// Types of the matrices: bits X16, H16, Y16 if they are known at compile time (loads
+// behind branches on the type wait for one another), ANY if not.
+constexpr int ANY = -1;
+enum { X16 = 1, H16 = 2, Y16 = 4 };
+
+template <int T>
+__device__ __forceinline__ bool type16(int bit, bool b16) {
+  return T == ANY ? b16 : (T & bit) != 0;
+}
+
 // V consecutive elements of a row as they lie in memory, fp32 or bf16.  The loads and
-// the conversion are apart, so that all loads of a row are in flight together although
-// the types are arguments.
+// the conversion are apart, so that all loads of a row are in flight together.  Addresses
+// are multiples of the element only (the target's accesses of 8 and 16 bytes take them).
 template <int V>
-struct Raw;
-template <>
-struct Raw<8> {
-  uint4 a, b;
-};
-template <>
-struct Raw<1> {
-  uint32_t a;
+struct Raw {
+  uint32_t w[V];
 };
 
-__device__ __forceinline__ void load(Raw<8>& r, const void* p, bool b16, int64_t at) {
-  const uint4* const q =
-      reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * (b16 ? 2 : 4));
-  r.a = q[0];
-  if (!b16) r.b = q[1];
-}
-__device__ __forceinline__ void load(Raw<1>& r, const void* p, bool b16, int64_t at) {
-  if (b16)
-    r.a = static_cast<const uint16_t*>(p)[at];
-  else
-    r.a = static_cast<const uint32_t*>(p)[at];
-}
+// A thread's share of a row: C pieces of V columns from col[c] on, of which the first
+// skip[c] are absent (V: all, nothing is loaded or stored)
+template <int V, int C, int TAIL>
+struct Cut {
+  int col[C], skip[C], D;
 
-__device__ __forceinline__ void value(const Raw<8>& r, bool b16, float (&v)[8]) {
-  const uint32_t a[4] = {r.a.x, r.a.y, r.a.z, r.a.w}, b[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
-  if (b16) {
+  __device__ __forceinline__ explicit Cut(int D) : D(D) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    for (int c = 0; c < C; ++c) {
+      col[c] = (c * int(blockDim.x) + int(threadIdx.x)) * V;
+      const int left = D - col[c];
+      skip[c] = left <= 0 ? V : 0;
+      if (TAIL == MOVED && left > 0 && left < V) {
+        skip[c] = V - left;
+        col[c] = D - V;
+      }
+    }
+  }
+  __device__ __forceinline__ bool any(int c) const { return TAIL == FULL || skip[c] < V; }
+  __device__ __forceinline__ bool in(int c, int i) const {
+    return TAIL == FULL ? true : TAIL == MOVED ? i >= skip[c] : col[c] + i < D;
+  }
+};
+
+template <int V, int C, int TAIL>
+__device__ __forceinline__ void load(Raw<V>& r, const Cut<V, C, TAIL>& cut, int c, const void* p,
+                                     bool b16, int64_t first) {
+  if (!cut.any(c)) return;
+  const uint8_t* const q = static_cast<const uint8_t*>(p) + (first + cut.col[c]) * (b16 ? 2 : 4);
+  if (TAIL != TINY) {
+    // (b16 may be known here; if not, the first half is loaded alike for both types)
+    if (__builtin_constant_p(b16) && !b16) {
+      __builtin_memcpy(r.w, q, 4 * V);
+    } else {
+      __builtin_memcpy(r.w, q, 2 * V);
+      if (!b16) __builtin_memcpy(r.w + V / 2, q + 2 * V, 2 * V);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __uint_as_float(a[i]);
-      v[4 + i] = __uint_as_float(b[i]);
+    for (int i = 0; i < V; ++i) {
+      uint32_t v = 0;
+      if (cut.in(c, i)) {
+        if (b16)
+          v = reinterpret_cast<const uint16_t*>(q)[i];
+        else
+          v = reinterpret_cast<const uint32_t*>(q)[i];
+      }
+      if (!b16)
+        r.w[i] = v;
+      else if (i & 1)
+        r.w[i / 2] |= v << 16;
+      else
+        r.w[i / 2] = v;
     }
   }
 }
-__device__ __forceinline__ void value(const Raw<1>& r, bool b16, float (&v)[1]) {
-  v[0] = __uint_as_float(b16 ? r.a << 16 : r.a);
-}
 
-__device__ __forceinline__ void store(void* p, bool b16, int64_t at, const float (&v)[8]) {
+template <int V>
+__device__ __forceinline__ void value(const Raw<V>& r, bool b16, float (&v)[V]) {
   if (b16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      v[i] = __uint_as_float(r.w[i / 2] << 16);
+      v[i + 1] = __uint_as_float(r.w[i / 2] & 0xFFFF0000u);
+    }
   } else {
-    float4* const q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __uint_as_float(r.w[i]);
   }
 }
-__device__ __forceinline__ void store(void* p, bool b16, int64_t at, const float (&v)[1]) {
-  if (b16)
-    static_cast<uint16_t*>(p)[at] = f32_to_bf16(v[0]);
-  else
-    static_cast<float*>(p)[at] = v[0];
+
+template <int V, int C, int TAIL>
+__device__ __forceinline__ void store(const Cut<V, C, TAIL>& cut, int c, void* p, bool b16,
+                                      int64_t first, const float (&v)[V]) {
+  if (!cut.any(c)) return;
+  const int64_t at = first + cut.col[c];
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int i = 0; i < V; i += 2) w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
+  if (TAIL == FULL || (TAIL == MOVED && cut.skip[c] == 0)) {
+    if (b16)
+      __builtin_memcpy(static_cast<uint16_t*>(p) + at, w, 2 * V);
+    else
+      __builtin_memcpy(static_cast<float*>(p) + at, v, 4 * V);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!cut.in(c, i)) continue;
+      if (b16)
+        static_cast<uint16_t*>(p)[at + i] = uint16_t(w[i / 2] >> 16 * (i & 1));
+      else
+        static_cast<float*>(p)[at + i] = v[i];
+    }
+  }
 }
 
-// the sum over a wave, in every lane
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, true));
+}
+
+// the sum over each 16 lanes, in their last one (row_shr 1, 2, 4, 8)
+__device__ __forceinline__ float row_sum(float v) {
+  return add_dpp<0x118>(add_dpp<0x114>(add_dpp<0x112>(add_dpp<0x111>(v))));
+}
+
+// the sum over a wave, in every lane (row_bcast 15 and 31 join the rows)
 __device__ __forceinline__ float wave_sum(float v) {
-  auto add = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
-                                                    decltype(rows)::value, 0xF, true));
-  };
-  using std::integral_constant;
-  add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // row_shr 1
-  add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});   // row_shr 2
-  add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});   // row_shr 4
-  add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});   // row_shr 8
-  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // row_bcast 15
-  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // row_bcast 31
+  v = add_dpp<0x143, 0xC>(add_dpp<0x142, 0xA>(row_sum(v)));
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sums over a workgroup, in every thread.  Each call takes the next of two LDS
-// buffers, so that one barrier a call is enough: a wave can write a buffer again only
-// past the barrier of the call between, which every wave reaches after its reads.
+// Sums over a workgroup, in every thread: of the waves, then of the waves' sums, which 16
+// lanes read.  Each call takes the next of two LDS buffers, so that one barrier a call is
+// enough: a wave can write a buffer again only past the barrier of the call between,
+// which every wave reaches after its reads.
 struct Sums {
   float (*red)[2][MAX_WAVES];
-  int waves, wave, turn;
+  int waves, wave, lane, turn;
 
-  __device__ __forceinline__ Sums(float (*lds)[2][MAX_WAVES])
+  __device__ __forceinline__ explicit Sums(float (*lds)[2][MAX_WAVES])
       : red(lds), waves(int(blockDim.x) >> 6),
-        wave(__builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6)), turn(0) {}
+        wave(__builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6)), lane(int(threadIdx.x) & 63),
+        turn(0) {}
 
+  // lane 15 and lane 31: the sums of the first and the second set
+  __device__ __forceinline__ float read() {
+    const float v = red[turn][(lane >> 4) & 1][lane & 15];
+    return row_sum((lane & 15) < waves ? v : 0.f);
+  }
+  static __device__ __forceinline__ float from(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+  }
   __device__ __forceinline__ void operator()(float& a, float& b) {
     a = wave_sum(a);
     b = wave_sum(b);
@@ -124,11 +189,9 @@ struct Sums {
     red[turn][0][wave] = a;
     red[turn][1][wave] = b;
     __syncthreads();
-    a = b = 0.f;
-    for (int w = 0; w < waves; ++w) {
-      a += red[turn][0][w];
-      b += red[turn][1][w];
-    }
+    const float v = read();
+    a = from(v, 15);
+    b = from(v, 31);
   }
   __device__ __forceinline__ void operator()(float& a) {
     a = wave_sum(a);
@@ -136,20 +199,18 @@ struct Sums {
     turn ^= 1;
     red[turn][0][wave] = a;
     __syncthreads();
-    a = 0.f;
-    for (int w = 0; w < waves; ++w) a += red[turn][0][w];
+    a = from(read(), 15);
   }
 };
 
-// a row's share of a thread: C pieces of V columns, piece c at (c NT + tid) V
 template <int V, int C>
 struct Row {
   float v[C][V];
 };
 
-// v -> n(v); returns 1 / deviation.  Pieces past D hold zeros before and after.
-template <int V, int C>
-__device__ __forceinline__ float normalize(Row<V, C>& r, const bool (&live)[C], bool layer, int D,
+// v -> n(v); returns 1 / deviation.  Elements past D hold zeros before and after.
+template <int V, int C, int TAIL>
+__device__ __forceinline__ float normalize(Row<V, C>& r, const Cut<V, C, TAIL>& cut, bool layer, int D,
                                            float eps, Sums& sum) {
   const float inv = 1.f / float(D);
   if (layer) {
@@ -163,7 +224,7 @@ __device__ __forceinline__ float normalize(Row<V, C>& r, const bool (&live)[C], 
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < V; ++i) r.v[c][i] = live[c] ? r.v[c][i] - mean : 0.f;
+      for (int i = 0; i < V; ++i) r.v[c][i] = cut.in(c, i) ? r.v[c][i] - mean : 0.f;
   }
   float s = 0.f;
 #pragma unroll
@@ -171,7 +232,9 @@ __device__ __forceinline__ float normalize(Row<V, C>& r, const bool (&live)[C], 
 #pragma unroll
     for (int i = 0; i < V; ++i) s = fmaf(r.v[c][i], r.v[c][i], s);
   sum(s);
-  const float rstd = 1.f / sqrtf(fmaf(s, inv, eps));
+  // (the hardware's reciprocal root, 1 ulp, where it is not subnormal)
+  const float var = fmaf(s, inv, eps);
+  const float rstd = var < 0x1p-100f ? 1.f / sqrtf(var) : __builtin_amdgcn_rsqf(var);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -179,41 +242,41 @@ __device__ __forceinline__ float normalize(Row<V, C>& r, const bool (&live)[C], 
   return rstd;
 }
 
-template <int V, int C>
+template <int V, int C, int TAIL, int T>
 __device__ __forceinline__ void norm_row(const svdq::BlockNorm& a, int64_t row, void* X_out,
                                          void* Y, bool y16, Sums& sum) {
-  const int64_t image = row / a.rows;
-  const int NT = blockDim.x, D = int(a.D);
-  bool live[C];
-  int col[C];
+  const int64_t image = a.images > 1 ? row / a.rows : 0;
+  const int D = int(a.D);
+  const Cut<V, C, TAIL> cut(D);
+  const bool x16 = type16<T>(X16, a.x16), h16 = type16<T>(H16, a.h16);
   Raw<V> x[C], h[C], post[C], gate[C], weight[C], scale[C], shift[C];
   auto vec = [&](Raw<V>& r, const Vec& v, int c) __attribute__((always_inline)) {
-    if (v.p && live[c]) load(r, v.p, v.b16, image * v.ld + col[c]);
+    if (v.p) load(r, cut, c, v.p, v.b16, image * v.ld);
   };
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    col[c] = (c * NT + int(threadIdx.x)) * V;
-    live[c] = col[c] < D;
-    if (live[c]) {
-      load(x[c], a.X, a.x16, row * D + col[c]);
-      if (a.H) load(h[c], a.H, a.h16, row * D + col[c]);
-    }
-    vec(post[c], a.post, c);
-    vec(gate[c], a.gate, c);
+  // (all at once while registers last)
+  auto behind = [&](int c) __attribute__((always_inline)) {
     vec(weight[c], a.weight, c);
     vec(scale[c], a.scale, c);
     vec(shift[c], a.shift, c);
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    load(x[c], cut, c, a.X, x16, row * D);
+    if (a.H) load(h[c], cut, c, a.H, h16, row * D);
+    vec(post[c], a.post, c);
+    vec(gate[c], a.gate, c);
+    if (C == 1) behind(c);
   }
   Row<V, C> t, xn;
   if (a.H) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      value(h[c], a.h16, t.v[c]);
+      value(h[c], h16, t.v[c]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) t.v[c][i] = live[c] ? t.v[c][i] : 0.f;
+      for (int i = 0; i < V; ++i) t.v[c][i] = cut.in(c, i) ? t.v[c][i] : 0.f;
     }
     if (a.post.p) {
-      normalize<V, C>(t, live, a.layer, D, a.eps, sum);
+      normalize(t, cut, a.layer, D, a.eps, sum);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float f[V];
@@ -225,7 +288,7 @@ __device__ __forceinline__ void norm_row(const svdq::BlockNorm& a, int64_t row, 
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    value(x[c], a.x16, xn.v[c]);
+    value(x[c], x16, xn.v[c]);
     if (a.H) {
       if (a.gate.p) {
         float f[V];
@@ -236,14 +299,15 @@ __device__ __forceinline__ void norm_row(const svdq::BlockNorm& a, int64_t row, 
 #pragma unroll
         for (int i = 0; i < V; ++i) xn.v[c][i] += t.v[c][i];
       }
-      if (live[c]) store(X_out, a.x16, row * D + col[c], xn.v[c]);
+      store(cut, c, X_out, x16, row * D, xn.v[c]);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) xn.v[c][i] = live[c] ? xn.v[c][i] : 0.f;
+    for (int i = 0; i < V; ++i) xn.v[c][i] = cut.in(c, i) ? xn.v[c][i] : 0.f;
   }
-  normalize<V, C>(xn, live, a.layer, D, a.eps, sum);
+  normalize(xn, cut, a.layer, D, a.eps, sum);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
+    if (C > 1) behind(c);
     float f[V];
     if (a.weight.p) {
       value(weight[c], a.weight.b16, f);
@@ -260,20 +324,20 @@ __device__ __forceinline__ void norm_row(const svdq::BlockNorm& a, int64_t row, 
 #pragma unroll
       for (int i = 0; i < V; ++i) xn.v[c][i] += f[i];
     }
-    if (live[c]) store(Y, y16, row * D + col[c], xn.v[c]);
+    store(cut, c, Y, y16, row * D, xn.v[c]);
   }
 }
 
 // a row a workgroup, and the rows past the grid in turn
 constexpr int64_t MOST_GROUPS = 1 << 20;
 
-template <int V, int C>
+template <int V, int C, int TAIL, int T>
 __global__ __launch_bounds__(1024) void block_norm_kernel(svdq::BlockNorm a, int64_t M, void* X_out,
                                                           void* Y, bool y16) {
-  __shared__ float lds[2][2][MAX_WAVES];
+  __shared__ __align__(16) float lds[2][2][MAX_WAVES];
   Sums sum(lds);
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x)
-    norm_row<V, C>(a, row, X_out, Y, y16, sum);
+    norm_row<V, C, TAIL, T>(a, row, X_out, Y, y16, sum);
 }
 
 // ------------------------------------------------------------- backward
@@ -282,202 +346,286 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(svdq::BlockNorm a, int
 //   dX = g,  dt = gate g,  dH = dt or the same form of dt post at n(H)
 //   dgate = sum g t,  dpost = sum dt n(H),  dweight = sum dY n (1 + scale),
 //   dscale = sum dY n weight,  dshift = sum dY         (sums over the rows)
-// The statistics are formed again from X and H, which costs no traffic.  A
-// workgroup takes rows of one image one after another and sums the vectors' gradients
-// in registers; its sums are joined by a second launch in a fixed order.
+// The statistics are formed again from X and H, which costs no traffic.
+//
+// A workgroup takes rows of one image one after another.  Along them the vectors are
+// constant, so x' and g need only their products weight (1 + scale) and gate post, and
+// three sums a column, A = sum dY n, B = sum g n(H) (or g H) and S = sum dY, hold all
+// five gradients: dweight = (1 + scale) A, dscale = weight A, dgate = post B, dpost =
+// gate B, dshift = S.  The next row's loads are in flight while one is worked on.  The
+// workgroups' gradients are joined by a second launch in a fixed order.
 
 enum { POST, GATE, WEIGHT, SCALE, SHIFT, VECTORS };
 
-template <int V, int C>
-__global__ __launch_bounds__(1024) void block_norm_grad_kernel(svdq::BlockNorm a,
+template <int V, int C, int TAIL>
+__device__ __forceinline__ void vector(const Vec& v, const Cut<V, C, TAIL>& cut, int64_t image, int c,
+                                       float none, float (&out)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = none;
+  if (v.p && cut.any(c)) {
+    Raw<V> raw;
+    load(raw, cut, c, v.p, v.b16, image * v.ld);
+    value(raw, v.b16, out);
+  }
+}
+
+template <int V, int C, int TAIL, int T, bool LAYER, bool POST_NORM>
+__global__ __launch_bounds__(512, C == 1 ? 4 : 2) void block_norm_grad_kernel(svdq::BlockNorm a,
                                                                svdq::BlockNormGrad g) {
-  __shared__ float lds[2][2][MAX_WAVES];
+  __shared__ __align__(16) float lds[2][2][MAX_WAVES];
   Sums sum(lds);
-  const int NT = blockDim.x, D = int(a.D);
+  const int D = int(a.D);
   const int64_t image = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
   const int64_t r0 = image * a.rows + part * a.rows / g.parts;
   const int64_t r1 = image * a.rows + (part + 1) * a.rows / g.parts;
   const float inv = 1.f / float(D);
-  bool live[C];
-  int col[C];
-  float vec[VECTORS][C][V], acc[VECTORS][C][V];
-  const Vec* const vs[VECTORS] = {&a.post, &a.gate, &a.weight, &a.scale, &a.shift};
+  const Cut<V, C, TAIL> cut(D);
+  // B's factor and the norm's: gate post, weight (1 + scale)
+  Row<V, C> gp, wm, accA, accB, accS;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    col[c] = (c * NT + int(threadIdx.x)) * V;
-    live[c] = col[c] < D;
+    float u[V], v[V];
+    vector(a.gate, cut, image, c, 1.f, u);
+    vector(a.post, cut, image, c, 1.f, v);
 #pragma unroll
-    for (int k = 0; k < VECTORS; ++k) {
+    for (int i = 0; i < V; ++i) gp.v[c][i] = u[i] * v[i];
+    vector(a.weight, cut, image, c, 1.f, u);
+    vector(a.scale, cut, image, c, 0.f, v);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        vec[k][c][i] = k == SCALE || k == SHIFT ? 0.f : 1.f;
-        acc[k][c][i] = 0.f;
-      }
-      if (k != SHIFT && vs[k]->p && live[c]) {
-        Raw<V> raw;
-        load(raw, vs[k]->p, vs[k]->b16, image * vs[k]->ld + col[c]);
-        value(raw, vs[k]->b16, vec[k][c]);
-      }
+    for (int i = 0; i < V; ++i) {
+      wm.v[c][i] = u[i] * (1.f + v[i]);
+      accA.v[c][i] = accB.v[c][i] = accS.v[c][i] = 0.f;
     }
   }
-  for (int64_t row = r0; row < r1; ++row) {
-    Raw<V> xr[C], hr[C], dyr[C], dxr[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (live[c]) {
-        const int64_t at = row * D + col[c];
-        load(xr[c], a.X, a.x16, at);
-        if (a.H) load(hr[c], a.H, a.h16, at);
-        load(dyr[c], g.dY, g.y16, at);
-        if (g.dX_out) load(dxr[c], g.dX_out, a.x16, at);
-      }
-    Row<V, C> t, n, dy;
-    float rh = 1.f;
+  const bool x16 = type16<T>(X16, a.x16), h16 = type16<T>(H16, a.h16), y16 = type16<T>(Y16, g.y16);
+  Raw<V> xr[C], hr[C], dyr[C], dxr[C];
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      value(xr[c], a.x16, n.v[c]);
-      value(dyr[c], g.y16, dy.v[c]);
-      if (a.H) value(hr[c], a.h16, t.v[c]);
+      load(xr[c], cut, c, a.X, x16, row * D);
+      if (a.H) load(hr[c], cut, c, a.H, h16, row * D);
+      load(dyr[c], cut, c, g.dY, y16, row * D);
+      if (g.dX_out) load(dxr[c], cut, c, g.dX_out, x16, row * D);
+    }
+  };
+  // (with four pieces a thread the registers do not hold two rows)
+  constexpr bool AHEAD = C <= 2;
+  if (AHEAD) fetch(r0);
+  for (int64_t row = r0; row < r1; ++row) {
+    if (!AHEAD) fetch(row);
+    Row<V, C> t, n, dy, d;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      value(xr[c], x16, n.v[c]);
+      value(dyr[c], y16, dy.v[c]);
+      if (a.H)
+        value(hr[c], h16, t.v[c]);
+      else
+#pragma unroll
+        for (int i = 0; i < V; ++i) t.v[c][i] = 0.f;
+      if (g.dX_out)
+        value(dxr[c], x16, d.v[c]);
+      else
+#pragma unroll
+        for (int i = 0; i < V; ++i) d.v[c][i] = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        t.v[c][i] = a.H && live[c] ? t.v[c][i] : 0.f;
-        n.v[c][i] = live[c] ? n.v[c][i] : 0.f;
-        dy.v[c][i] = live[c] ? dy.v[c][i] : 0.f;
+        const bool in = cut.in(c, i);
+        t.v[c][i] = in ? t.v[c][i] : 0.f;
+        n.v[c][i] = in ? n.v[c][i] : 0.f;
+        dy.v[c][i] = in ? dy.v[c][i] : 0.f;
+        d.v[c][i] = in ? d.v[c][i] : 0.f;
       }
     }
-    if (a.H && a.post.p) rh = normalize<V, C>(t, live, a.layer, D, a.eps, sum);
-    if (a.H)
+    if (AHEAD) fetch(min(row + 1, r1 - 1));
+    float rh = 1.f;
+    if (POST_NORM) rh = normalize(t, cut, LAYER, D, a.eps, sum);
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          n.v[c][i] = fmaf(vec[GATE][c][i], t.v[c][i] * vec[POST][c][i], n.v[c][i]);
-    const float r = normalize<V, C>(n, live, a.layer, D, a.eps, sum);
+      for (int i = 0; i < V; ++i) n.v[c][i] = fmaf(gp.v[c][i], t.v[c][i], n.v[c][i]);
+    const float r = normalize(n, cut, LAYER, D, a.eps, sum);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float d = dy.v[c][i], dn = d * n.v[c][i];
-        const float w = vec[WEIGHT][c][i], m = 1.f + vec[SCALE][c][i];
-        acc[SHIFT][c][i] += d;
-        acc[WEIGHT][c][i] = fmaf(dn, m, acc[WEIGHT][c][i]);
-        acc[SCALE][c][i] = fmaf(dn, w, acc[SCALE][c][i]);
-        dy.v[c][i] = d * w * m;
+        accS.v[c][i] += dy.v[c][i];
+        accA.v[c][i] = fmaf(dy.v[c][i], n.v[c][i], accA.v[c][i]);
+        dy.v[c][i] *= wm.v[c][i];
         s1 += dy.v[c][i];
         s2 = fmaf(dy.v[c][i], n.v[c][i], s2);
       }
     sum(s1, s2);
-    const float m1 = a.layer ? s1 * inv : 0.f, m2 = s2 * inv;
+    const float m1 = LAYER ? s1 * inv : 0.f, m2 = s2 * inv;
     s1 = s2 = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float d[V];
-      if (g.dX_out)
-        value(dxr[c], a.x16, d);
-      else
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        d[i] = live[c] ? d[i] + r * (dy.v[c][i] - m1 - n.v[c][i] * m2) : 0.f;
-        const float tv = t.v[c][i], dt = vec[GATE][c][i] * d[i];
-        acc[GATE][c][i] = fmaf(d[i], tv * vec[POST][c][i], acc[GATE][c][i]);
-        acc[POST][c][i] = fmaf(dt, tv, acc[POST][c][i]);
-        dy.v[c][i] = dt * vec[POST][c][i];
-        s1 += dy.v[c][i];
-        s2 = fmaf(dy.v[c][i], tv, s2);
+        d.v[c][i] += r * (dy.v[c][i] - m1 - n.v[c][i] * m2);
+        d.v[c][i] = cut.in(c, i) ? d.v[c][i] : 0.f;
+        accB.v[c][i] = fmaf(d.v[c][i], t.v[c][i], accB.v[c][i]);
       }
-      if (live[c]) store(g.dX, a.x16, row * D + col[c], d);
+      store(cut, c, g.dX, x16, row * D, d.v[c]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        d.v[c][i] *= gp.v[c][i];
+        s1 += d.v[c][i];
+        s2 = fmaf(d.v[c][i], t.v[c][i], s2);
+      }
     }
     if (!a.H) continue;
     float k1 = 0.f, k2 = 0.f;
-    if (a.post.p) {
+    if (POST_NORM) {
       sum(s1, s2);
-      k1 = a.layer ? s1 * inv : 0.f;
+      k1 = LAYER ? s1 * inv : 0.f;
       k2 = s2 * inv;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float d[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = rh * (dy.v[c][i] - k1 - t.v[c][i] * k2);
-      if (live[c]) store(g.dH, a.h16, row * D + col[c], d);
+      for (int i = 0; i < V; ++i) d.v[c][i] = rh * (d.v[c][i] - k1 - t.v[c][i] * k2);
+      store(cut, c, g.dH, h16, row * D, d.v[c]);
     }
   }
+  // each gradient: a sum times the vector it shares its product with
+  auto put = [&](int k, const Row<V, C>& acc, const Vec& other, float none, float add)
+      __attribute__((always_inline)) {
+    if (!g.part[k]) return;
 #pragma unroll
-  for (int k = 0; k < VECTORS; ++k)
-    if (g.part[k])
+    for (int c = 0; c < C; ++c) {
+      float f[V];
+      vector(other, cut, image, c, none, f);
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (live[c]) store(g.part[k], false, int64_t(blockIdx.x) * D + col[c], acc[k][c]);
+      for (int i = 0; i < V; ++i) f[i] = acc.v[c][i] * (f[i] + add);
+      store(cut, c, g.part[k], false, int64_t(blockIdx.x) * D, f);
+    }
+  };
+  put(POST, accB, a.gate, 1.f, 0.f);
+  put(GATE, accB, a.post, 1.f, 0.f);
+  put(WEIGHT, accA, a.scale, 0.f, 1.f);
+  put(SCALE, accA, a.weight, 1.f, 0.f);
+  put(SHIFT, accS, Vec{nullptr, 0, false}, 1.f, 0.f);
 }
 
-// out[i] = sum over the parts of image i (all of them where a vector is shared)
-__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int D,
-                                                              int64_t parts,
-                                                              float* __restrict__ out) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int blocks = (D + 63) / 64;
-  const int64_t image = blockIdx.x / blocks;
-  const int col = int(blockIdx.x % blocks) * 64 + lane;
-  const float* const p = part + image * parts * D;
-  float s = 0.f;
-  if (col < D)
-    for (int64_t i = wave; i < parts; i += 4) s += p[i * D + col];
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && col < D)
-    out[image * D + col] = red[0][lane] + red[1][lane] + (red[2][lane] + red[3][lane]);
+// For up to five sums at once: out[i] = the sum over the parts of image i (all of them
+// where a vector is shared).  64 columns and 16 waves a workgroup.
+__global__ __launch_bounds__(1024) void join_kernel(svdq::Joins j, int64_t total, int D) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int across = (D + 63) / 64;
+  for (int64_t block = blockIdx.x; block < total; block += gridDim.x) {
+    int64_t b = block;
+    int k = 0;
+    while (k + 1 < j.count && b >= j.blocks[k]) b -= j.blocks[k++];
+    const int64_t image = b / across, parts = j.parts[k];
+    const int col = int(b % across) * 64 + lane;
+    float s = 0.f;
+    if (col < D) {
+      const float* const p = j.from[k] + image * parts * D + col;
+      int64_t i = wave;
+      for (; i + 48 < parts; i += 64) {
+        const float v0 = p[i * D], v1 = p[(i + 16) * D], v2 = p[(i + 32) * D], v3 = p[(i + 48) * D];
+        s += (v0 + v1) + (v2 + v3);
+      }
+      for (; i < parts; i += 16) s += p[i * D];
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < D) {
+      for (int w = 1; w < 16; ++w) s += red[w][lane];
+      j.to[k][image * D + col] = s;
+    }
+    __syncthreads();
+  }
 }
 
-// threads and pieces of a row.  V = 8 where D and every address allow 16-byte loads
+// threads and pieces of a row: more pieces than one a thread beyond `most` threads
 struct Shape {
-  int V, C, NT;
+  int C, NT;
+  Tail tail;
 };
 
-Shape shape(int64_t D, bool wide) {
-  const int V = wide ? 8 : 1;
+constexpr int V = 8;                     // elements of a piece
+constexpr int NORM_THREADS = 1024, GRAD_THREADS = 512;
+
+Shape shape(int64_t D, int most) {
   const int64_t n = (D + V - 1) / V;
   int C = 1;
-  while (C * int64_t(1024) < n) C *= 2;
-  return {V, C, int((n + C * 64 - 1) / (C * 64) * 64)};
+  while (C * int64_t(most) < n) C *= 2;
+  const int NT = int((n + C * 64 - 1) / (C * 64) * 64);
+  return {C, NT, D < V ? TINY : int64_t(C) * NT * V == D ? FULL : MOVED};
 }
 
-bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-bool vec_wide(const Vec& v) { return !v.p || (on16(v.p) && v.ld % (v.b16 ? 8 : 4) == 0); }
-bool all_wide(const svdq::BlockNorm& a) {
-  return a.D % 8 == 0 && on16(a.X) && on16(a.H) && vec_wide(a.post) && vec_wide(a.gate) &&
-         vec_wide(a.weight) && vec_wide(a.scale) && vec_wide(a.shift);
+// The types that a model's stream meets are known to the kernel: all bf16, an fp32
+// stream with bf16 or fp32 blocks.  Others, and rows too short or long to matter, take ANY.
+template <int TAIL>
+auto norm_of(int C, int types) {
+  if (C > 1) return block_norm_kernel<V, 2, TAIL, ANY>;
+  return types == (X16 | H16) ? block_norm_kernel<V, 1, TAIL, X16 | H16>
+         : types == H16       ? block_norm_kernel<V, 1, TAIL, H16>
+         : types == 0         ? block_norm_kernel<V, 1, TAIL, 0>
+                              : block_norm_kernel<V, 1, TAIL, ANY>;
 }
 
-int64_t grad_parts(int64_t M, int64_t images) {
-  const int64_t rows = M / images;
-  return std::max<int64_t>(1, std::min(rows, 512 / images));
+template <int C, int TAIL, int T>
+auto grad_of(bool layer, bool post) {
+  return layer ? post ? block_norm_grad_kernel<V, C, TAIL, T, true, true>
+                      : block_norm_grad_kernel<V, C, TAIL, T, true, false>
+         : post ? block_norm_grad_kernel<V, C, TAIL, T, false, true>
+                : block_norm_grad_kernel<V, C, TAIL, T, false, false>;
+}
+auto grad_of(const Shape& p, int types, bool layer, bool post) {
+  if (p.C == 4) return grad_of<4, MOVED, ANY>(layer, post);
+  if (p.C == 2)
+    return p.tail == FULL ? grad_of<2, FULL, ANY>(layer, post) : grad_of<2, MOVED, ANY>(layer, post);
+  if (p.tail == TINY) return grad_of<1, TINY, ANY>(layer, post);
+  if (p.tail == MOVED)
+    return types == (X16 | H16 | Y16) ? grad_of<1, MOVED, X16 | H16 | Y16>(layer, post)
+                                      : grad_of<1, MOVED, ANY>(layer, post);
+  return types == (X16 | H16 | Y16) ? grad_of<1, FULL, X16 | H16 | Y16>(layer, post)
+         : types == (H16 | Y16)     ? grad_of<1, FULL, H16 | Y16>(layer, post)
+         : types == Y16             ? grad_of<1, FULL, Y16>(layer, post)
+         : types == 0               ? grad_of<1, FULL, 0>(layer, post)
+                                    : grad_of<1, FULL, ANY>(layer, post);
+}
+
+// (a missing H has X's type: no kernel for it alone)
+int types_of(const svdq::BlockNorm& a, bool y16) {
+  const bool h16 = a.H ? a.h16 : a.x16;
+  return (a.x16 ? X16 : 0) | (h16 ? H16 : 0) | (y16 ? Y16 : 0);
+}
+
+Shape grad_shape(int64_t D) { return shape(D, GRAD_THREADS); }
+
+// Workgroups an image: 16 waves to a compute unit in all
+int64_t grad_parts(int64_t M, int64_t D, int64_t images) {
+  const int64_t rows = M / images, groups = 256 * (1024 / grad_shape(D).NT);
+  return std::max<int64_t>(1, std::min(rows, std::min<int64_t>(groups, 1024) / images));
 }
 
 }  // namespace
 
 namespace svdq {
 
-svdq_status launch_join(const float* part, int64_t D, int64_t parts, int64_t each, float* out,
-                        hipStream_t s) {
-  hipLaunchKernelGGL(join_kernel, dim3(unsigned((D + 63) / 64 * each)), dim3(256), 0, s, part,
-                     int(D), parts, out);
+svdq_status launch_joins(const Joins& j, int64_t D, hipStream_t s) {
+  int64_t blocks = 0;
+  for (int k = 0; k < j.count; ++k) blocks += j.blocks[k];
+  if (!blocks) return SVDQ_OK;
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned(std::min(blocks, MOST_GROUPS))), dim3(1024), 0, s, j,
+                     blocks, int(D));
   return check_launch("join");
 }
 
 svdq_status launch_block_norm(const BlockNorm& a, int64_t M, void* X_out, void* Y, svdq_dtype y_dt,
                               hipStream_t s) {
-  const Shape p = shape(a.D, all_wide(a) && on16(X_out) && on16(Y));
-  void (*k)(BlockNorm, int64_t, void*, void*, bool) =
-      p.V == 8 ? (p.C == 1 ? block_norm_kernel<8, 1> : block_norm_kernel<8, 2>)
-      : p.C == 1 ? block_norm_kernel<1, 1>
-      : p.C == 2 ? block_norm_kernel<1, 2>
-      : p.C == 4 ? block_norm_kernel<1, 4>
-      : p.C == 8 ? block_norm_kernel<1, 8>
-                 : block_norm_kernel<1, 16>;
+  const Shape p = shape(a.D, NORM_THREADS);
+  const int t = types_of(a, false);
+  auto k = p.tail == TINY    ? block_norm_kernel<V, 1, TINY, ANY>
+           : p.tail == MOVED ? norm_of<MOVED>(p.C, t)
+                             : norm_of<FULL>(p.C, t);
   hipLaunchKernelGGL(k, dim3(unsigned(std::min(M, MOST_GROUPS))), dim3(p.NT), 0, s, a, M, X_out, Y,
                      y_dt == SVDQ_BF16);
   return check_launch("block_norm");
@@ -485,14 +633,15 @@ svdq_status launch_block_norm(const BlockNorm& a, int64_t M, void* X_out, void* 
 
 size_t block_norm_grad_workspace(int64_t M, int64_t D, int64_t images) {
   if (M == 0) return 0;
-  return align256(size_t(VECTORS) * size_t(images * grad_parts(M, images)) * size_t(D) * 4);
+  return align256(size_t(VECTORS) * size_t(images * grad_parts(M, D, images)) * size_t(D) * 4);
 }
 
 svdq_status launch_block_norm_grad(const BlockNorm& a, BlockNormGrad g, int64_t M, int64_t images,
                                    float* const (&out)[5], void* ws, hipStream_t s) {
-  g.parts = M ? grad_parts(M, images) : 0;
+  g.parts = M ? grad_parts(M, a.D, images) : 0;
   const Vec* const vs[VECTORS] = {&a.post, &a.gate, &a.weight, &a.scale, &a.shift};
   float* at = static_cast<float*>(ws);
+  Joins j{};
   for (int k = 0; k < VECTORS; ++k) {
     g.part[k] = nullptr;
     if (!out[k]) continue;
@@ -503,26 +652,15 @@ svdq_status launch_block_norm_grad(const BlockNorm& a, BlockNormGrad g, int64_t 
     }
     g.part[k] = at;
     at += images * g.parts * a.D;
+    j.add(g.part[k], out[k], a.D, images * g.parts / each, each);
   }
   if (M) {
-    const Shape p = shape(a.D, all_wide(a) && on16(g.dY) && on16(g.dX_out) && on16(g.dX) &&
-                                   on16(g.dH));
-    void (*k)(BlockNorm, BlockNormGrad) =
-        p.V == 8 ? (p.C == 1 ? block_norm_grad_kernel<8, 1> : block_norm_grad_kernel<8, 2>)
-        : p.C == 1 ? block_norm_grad_kernel<1, 1>
-        : p.C == 2 ? block_norm_grad_kernel<1, 2>
-        : p.C == 4 ? block_norm_grad_kernel<1, 4>
-        : p.C == 8 ? block_norm_grad_kernel<1, 8>
-                   : block_norm_grad_kernel<1, 16>;
+    const Shape p = grad_shape(a.D);
+    auto k = grad_of(p, types_of(a, g.y16), a.layer, a.post.p != nullptr);
     hipLaunchKernelGGL(k, dim3(unsigned(images * g.parts)), dim3(p.NT), 0, s, a, g);
     SVDQ_TRY(check_launch("block_norm_grad"));
   }
-  for (int k = 0; k < VECTORS; ++k) {
-    if (!out[k] || g.part[k] == out[k]) continue;
-    const int64_t each = vs[k]->ld ? images : 1, parts = images * g.parts / each;
-    SVDQ_TRY(launch_join(g.part[k], a.D, parts, each, out[k], s));
-  }
-  return SVDQ_OK;
+  return launch_joins(j, a.D, s);
 }
 
 }  // namespace svdq
