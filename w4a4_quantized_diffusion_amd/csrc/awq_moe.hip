@@ -91,66 +91,112 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// All threads of the workgroup.  16 lanes take a token, expert e in lane e % 16.
-__device__ __forceinline__ void route(const Moe& a, Route& r) {
-  const int tid = threadIdx.x, NT = blockDim.x, l = tid & 15;
-  for (int i = tid; i < 2 * MAX_EXPERTS; i += NT) r.mask[i >> 1][i & 1] = 0;
-  __syncthreads();
-  for (int t = tid >> 4; t < a.T; t += NT >> 4) {
-    uint32_t key[MAX_EXPERTS / 16];
-    float v[MAX_EXPERTS / 16];
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return key == 0xFFFFFFFFu ? NAN : __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// inclusive sum over a wave's lanes
+__device__ __forceinline__ int scan64(int v) {
+#define ADD(ctrl, rows) v += __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xF, true)
+  ADD(0x111, 0xF);                       // row_shr 1, 2, 4, 8
+  ADD(0x112, 0xF);
+  ADD(0x114, 0xF);
+  ADD(0x118, 0xF);
+  ADD(0x142, 0xA);                       // row_bcast 15, 31
+  ADD(0x143, 0xC);
+#undef ADD
+  return v;
+}
+
+// The choices of the tokens, 16 lanes to a token, expert e in lane e % 16; NV values a
+// lane (E <= 16 NV).  A lane keeps the token's choice with its number.
+template <int NV>
+__device__ __forceinline__ void choose(const Moe& a, Route& r) {
+  const int tid = threadIdx.x, l = tid & 15;
+  for (int t = tid >> 4; t < a.T; t += int(blockDim.x) >> 4) {
+    uint32_t key[NV];
+    float v[NV];
 #pragma unroll
-    for (int i = 0; i < MAX_EXPERTS / 16; ++i) {
-      const int e = 16 * i + l;
-      v[i] = -INFINITY;
-      if (16 * i < a.E && e < a.E) {
-        const int at = t * a.E + e;
-        v[i] = a.l16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at])
-                     : static_cast<const float*>(a.logits)[at];
-      }
+    for (int i = 0; i < NV; ++i) {
+      // (past the last expert the last one's, and its key is 0)
+      const int at = t * a.E + min(16 * i + l, a.E - 1);
+      v[i] = a.l16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at])
+                   : static_cast<const float*>(a.logits)[at];
     }
-    float top = -INFINITY, sum = 0.f;
     uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < MAX_EXPERTS / 16; ++i) {
+    for (int i = 0; i < NV; ++i) {
       key[i] = 16 * i + l < a.E ? order_key(v[i]) : 0;
       mine = max(mine, key[i]);
     }
-    const uint32_t most = max16(mine);
-    // (the largest logit again; a NaN stays one)
-    top = most == 0xFFFFFFFFu ? NAN : __uint_as_float(most & 0x80000000u ? most ^ 0x80000000u : ~most);
+    const float top = key_value(max16(mine));
     const bool none = top == -INFINITY;
+    float sum = 0.f, kept = 0.f, p = 0.f;
+    if (!a.renorm) {
 #pragma unroll
-    for (int i = 0; i < MAX_EXPERTS / 16; ++i)
-      if (16 * i < a.E) sum += 16 * i + l < a.E ? expf(v[i] - top) : 0.f;
-    sum = sum16(sum);
-    float kept = 0.f, first = 0.f;
+      for (int i = 0; i < NV; ++i) sum += key[i] ? expf(v[i] - top) : 0.f;
+      sum = sum16(sum);
+    }
+    uint32_t choice = 0;
     for (int j = 0; j < a.top; ++j) {
       uint32_t best = 0, at = 0xFFFFu;
 #pragma unroll
-      for (int i = 0; i < MAX_EXPERTS / 16; ++i)
-        if (16 * i < a.E && key[i] > best) best = key[i], at = 16 * i + l;
+      for (int i = 0; i < NV; ++i)
+        if (key[i] > best) best = key[i], at = 16 * i + l;
       const uint32_t m = max16(best);
       const uint32_t e = min16(best == m ? at : 0xFFFFu);
 #pragma unroll
-      for (int i = 0; i < MAX_EXPERTS / 16; ++i)
+      for (int i = 0; i < NV; ++i)
         if (uint32_t(16 * i + l) == e) key[i] = 0;
-      // the logit's own bits back from its key
-      const float lv = m == 0xFFFFFFFFu ? NAN
-                                        : __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
-      const float x = none ? 0.f : expf(lv - top);
-      kept += x;
-      // lane j % 16 keeps the j-th choice (top <= 16)
-      if (l == j) first = x;
-      if (l == 0) {
-        r.chosen[t * a.top + j] = uint8_t(e);
-        atomicOr(&r.mask[e][t >> 5], 1u << (t & 31));
-      }
+      if (l == j) choice = e, p = expf(key_value(m) - top);
     }
-    if (l < a.top) r.p[t * a.top + l] = none ? 0.f : first / (a.renorm ? kept : sum);
+    if (l >= a.top) p = 0.f;
+    if (a.renorm) sum = sum16(p);
+    p = none ? 0.f : p / sum;
+    if (l >= a.top) continue;
+    const int i = t * a.top + l;
+    r.chosen[i] = uint8_t(choice);
+    r.p[i] = p;
+    if (a.T == 1) {
+      // slots in the order of the choices
+      r.mask[choice][0] = 1;
+      r.mask[choice][1] = 0;
+      r.first[choice] = uint16_t(l);
+      r.active[l] = uint8_t(choice);
+      r.token[l] = 0;
+      r.weight[l] = p;
+    } else {
+      atomicOr(&r.mask[choice][t >> 5], 1u << (t & 31));
+    }
+    if (blockIdx.x == 0) {
+      if (a.ids) a.ids[i] = int(choice);
+      if (a.weights) a.weights[i] = p;
+    }
   }
+}
+
+// All threads of the workgroup
+__device__ __forceinline__ void route(const Moe& a, Route& r) {
+  const int tid = threadIdx.x, NT = blockDim.x;
+  if (a.T > 1) {
+    for (int i = tid; i < 2 * MAX_EXPERTS; i += NT) r.mask[i >> 1][i & 1] = 0;
+    __syncthreads();
+  } else if (tid == 0) {
+    r.actives = a.top;
+  }
+  if (a.E <= 16)
+    choose<1>(a, r);
+  else if (a.E <= 32)
+    choose<2>(a, r);
+  else if (a.E <= 64)
+    choose<4>(a, r);
+  else if (a.E <= 128)
+    choose<8>(a, r);
+  else
+    choose<16>(a, r);
   __syncthreads();
-  // slots by expert: first[] and active[] from one wave's running sums
+  if (a.T == 1) return;
+  // slots by expert: first[] and active[] from one wave's running sums, 4 experts a lane
   if (tid < 64) {
     int count[4], c = 0, n = 0;
 #pragma unroll
@@ -160,11 +206,7 @@ __device__ __forceinline__ void route(const Moe& a, Route& r) {
       c += count[i];
       n += count[i] > 0;
     }
-    int sc = c, sn = n;
-    for (int d = 1; d < 64; d *= 2) {
-      const int pc = __shfl_up(sc, d), pn = __shfl_up(sn, d);
-      if (tid >= d) sc += pc, sn += pn;
-    }
+    int sc = scan64(c), sn = scan64(n);
     if (tid == 63) r.actives = sn;
     sc -= c;
     sn -= n;
@@ -183,223 +225,318 @@ __device__ __forceinline__ void route(const Moe& a, Route& r) {
     const int s = r.first[e] + __popc(r.mask[e][0] & lo) + __popc(r.mask[e][1] & hi);
     r.token[s] = uint8_t(t);
     r.weight[s] = r.p[i];
-    if (blockIdx.x == 0) {
-      if (a.ids) a.ids[i] = e;
-      if (a.weights) a.weights[i] = r.p[i];
-    }
   }
   __syncthreads();
 }
 
-// one chunk of 64 k of 16 rows of weights: lane group j holds k = 16 j .. 16 j + 15
-struct Codes {
-  uint2 w;
-  uint32_t s, z;
-};
-__device__ __forceinline__ void fetch_codes(Codes& c, const svdq::AwqWeight& w, int64_t at, int j) {
-  c.w = *reinterpret_cast<const uint2*>(w.q + at * 32 + 8 * j);
-  c.s = w.s[at];
-  c.z = w.z[at];
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ int tokens_of(const Route& r, int e) {
+  return uniform(__popc(r.mask[e][0]) + __popc(r.mask[e][1]));
 }
-// past the last chunk (not live) the scales are zeros
-__device__ __forceinline__ void operands(const Codes& c, bool live, v8bf (&b)[2]) {
-  const float s = live ? __uint_as_float(c.s << 16) : 0.f;
-  const float zs = -__uint_as_float(c.z << 16) * s;
-  b[0] = __builtin_bit_cast(v8bf, dequant8(c.w.x, s, zs));
-  b[1] = __builtin_bit_cast(v8bf, dequant8(c.w.y, s, zs));
+
+// 8 codes each of k = 16 j .. 16 j + 7 and 16 j + 8 .. 16 j + 15 of a row's chunk, times
+// the row's scale; past the last chunk (not live) the scales are zeros
+__device__ __forceinline__ void operands(uint2 w, uint32_t s16, uint32_t z16, bool live,
+                                         v8bf (&b)[2]) {
+  const float s = live ? __uint_as_float(s16 << 16) : 0.f;
+  const float zs = -__uint_as_float(z16 << 16) * s;
+  b[0] = __builtin_bit_cast(v8bf, dequant8(w.x, s, zs));
+  b[1] = __builtin_bit_cast(v8bf, dequant8(w.y, s, zs));
+}
+
+// a barrier for LDS that leaves the loads from memory in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // ------------------------------------------------------- H = act(G) * U
-// A workgroup's 8 waves own 16 columns of an expert's gate and up projections, take the
-// chunks of K in turn, and their sums meet in LDS.
+// An item is 32 columns of an expert's gate and up projections for 16 MT of its slots.
+// A workgroup's 8 waves take the chunks of K in turn, and their sums meet in LDS.  The
+// workgroups go on from item to item with the next item's loads in flight.
 
 constexpr int UP_WAVES = 8;
 
-// slots s0 .. s0 + count - 1 (count <= 16 MT) of expert e, columns 16 block ..
+template <int MT>
+struct UpCursor {
+  int item, e, block, s0, left, step;
+
+  // (the end of the list leaves the cursor where it is; `item` says that it ended)
+  __device__ __forceinline__ void open(const Route& r, int blocks, int items) {
+    step = 0;
+    if (item >= items) return;
+    e = uniform(r.active[item / blocks]);
+    block = item % blocks;
+    s0 = uniform(r.first[e]);
+    left = tokens_of(r, e);
+  }
+};
+
 template <int MT, int ACT>
-__device__ __forceinline__ void up_tile(const Moe& a, const Route& r, v4f (*red)[64], int e,
-                                        int block, int s0, int count) {
-  constexpr int D = MT == 1 ? 4 : 2;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int j = lane >> 4, c16 = lane & 15;
-  const int64_t n = int64_t(block) * 16 + c16;
-  const int G = a.K / 64, chunks = (G - wave + UP_WAVES - 1) / UP_WAVES;
-  const svdq::AwqWeight wg = a.gate.at(e), wu = a.up.at(e);
-  const uint16_t* xrow[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-    xrow[mt] = a.X + int64_t(r.token[s0 + min(16 * mt + c16, count - 1)]) * a.K + 16 * j;
+__global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
+  constexpr int D = MT == 1 ? 3 : 2;
+  __shared__ Route r;
+  __shared__ float red[UP_WAVES][MT][2][2][4][64];   // [wave][rows][column parity][G, U][e][lane]
+  route(a, r);
+  const int lane = threadIdx.x & 63, j = lane >> 4, c16 = lane & 15;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int G = a.K / 64, steps = (G + UP_WAVES - 1) / UP_WAVES;
+  const int blocks = a.N / 32, items = uniform(r.actives) * blocks;
+  // workgroups are dealt round-robin to the 8 XCDs: each XCD takes a run of items, so that
+  // an expert's rows of X and shared lines of scales meet in one L2
+  int start = blockIdx.x, stride = gridDim.x, end = items;
+  if ((gridDim.x & 7) == 0) {
+    const int per = (items + 7) / 8, xcd = blockIdx.x & 7;
+    start = xcd * per + (blockIdx.x >> 3);
+    end = min(items, (xcd + 1) * per);
+    stride = gridDim.x >> 3;
+  }
+  if (start >= end) return;
+  UpCursor<MT> at, ahead;
+  at.item = start;
+  at.open(r, blocks, end);
+  ahead = at;
+  auto advance = [&](UpCursor<MT>& c) __attribute__((always_inline)) {
+    if (++c.step < steps) return;
+    c.step = 0;
+    if (c.left > 16 * MT) {
+      c.left -= 16 * MT;
+      c.s0 += 16 * MT;
+      return;
+    }
+    c.item += stride;
+    c.open(r, blocks, end);
+  };
   struct Slot {
-    Codes c[2];
+    uint2 w[2][2];                       // gate, up; column parity
+    uint32_t s[2], z[2];                 // of both columns
     uint4 x[MT][2];
   } ring[D];
-  // every slot is always loaded (past the last chunk with the last one's data; a wave
-  // without chunks loads chunk 0 and never uses it)
-  auto fetch = [&](int i, Slot& sl) __attribute__((always_inline)) {
-    const int c = chunks > 0 ? wave + UP_WAVES * min(i, chunks - 1) : 0;
-    const int64_t at = int64_t(c) * a.N + n;
-    fetch_codes(sl.c[0], wg, at, j);
-    fetch_codes(sl.c[1], wu, at, j);
+  const uint16_t* xrow[MT];
+  auto rows = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      xrow[mt] = a.X + int64_t(r.token[ahead.s0 + min(16 * mt + c16, ahead.left - 1)]) * a.K + 16 * j;
+  };
+  rows();
+  // every slot is always loaded (past the last chunk with the last one's data), so that
+  // the number of loads in flight is fixed
+  auto fetch = [&](Slot& sl) __attribute__((always_inline)) {
+    const int c = min(wave + UP_WAVES * ahead.step, G - 1);
+    const int64_t row = ahead.e * a.gate.stride + int64_t(c) * a.N + 32 * ahead.block;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const svdq::AwqWeight& w = t ? a.up.w : a.gate.w;
+      const uint8_t* const q = w.q + row * 32;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        sl.w[t][p] = *reinterpret_cast<const uint2*>(q + uint32_t(64 * c16 + 32 * p + 8 * j));
+      sl.s[t] = reinterpret_cast<const uint32_t*>(w.s + row)[c16];
+      sl.z[t] = reinterpret_cast<const uint32_t*>(w.z + row)[c16];
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const uint4* const x = reinterpret_cast<const uint4*>(xrow[mt] + 64 * int64_t(c));
       sl.x[mt][0] = x[0];
       sl.x[mt][1] = x[1];
     }
+    const int s0 = ahead.s0, item = ahead.item;
+    advance(ahead);
+    if (ahead.s0 != s0 || ahead.item != item) rows();
   };
-  v4f acc[MT][2];
+  v4f acc[MT][2][2];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int t = 0; t < 2; ++t) acc[mt][t] = v4f{0, 0, 0, 0};
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-  for (int d = 0; d < D; ++d) fetch(d, ring[d]);
-  for (int c = 0; c < chunks; c += D)
+        for (int t = 0; t < 2; ++t) acc[mt][p][t] = v4f{0, 0, 0, 0};
+  };
+  clear();
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(ring[d]);
+  while (true) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       Slot& sl = ring[d];
+      const bool live = wave + UP_WAVES * at.step < G;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v8bf b[2];
-        operands(sl.c[t], c + d < chunks, b);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          v8bf b[2];
+          operands(sl.w[t][p], p ? sl.s[t] >> 16 : sl.s[t] & 0xFFFF, p ? sl.z[t] >> 16 : sl.z[t] & 0xFFFF,
+                   live, b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              acc[mt][p][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(v8bf, sl.x[mt][h]), b[h], acc[mt][p][t], 0, 0, 0);
+        }
+      fetch(sl);
+      if (at.step == steps - 1) {
+        // the waves' sums in order
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            acc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(v8bf, sl.x[mt][h]), b[h], acc[mt][t], 0, 0, 0);
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) red[wave][mt][p][t][e][lane] = acc[mt][p][t][e];
+        clear();
+        lds_barrier();
+        // wave e of four: rows 4 j + e, both columns
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int e = wave - 4 * (mt & 1), row = 16 * mt + 4 * j + e;
+          if (e < 0 || e > 3 || row >= at.left) continue;
+          float h[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            float g = red[0][mt][p][0][e][lane], u = red[0][mt][p][1][e][lane];
+#pragma unroll
+            for (int w = 1; w < UP_WAVES; ++w) {
+              g += red[w][mt][p][0][e][lane];
+              u += red[w][mt][p][1][e][lane];
+            }
+            h[p] = gate_act<ACT>(g) * u;
+          }
+          reinterpret_cast<uint32_t*>(a.H + int64_t(at.s0 + row) * a.N + 32 * at.block)[c16] =
+              pack_bf16x2(h[0], h[1]);
+        }
+        lds_barrier();
       }
-      fetch(c + d + D, sl);
+      advance(at);
+      if (at.item >= end) return;
     }
-  __syncthreads();                       // the sums of the tile before have been read
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) red[(wave * MT + mt) * 2 + t][lane] = acc[mt][t];
-  __syncthreads();
-  if (wave >= MT) return;
-  v4f v[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    v[t] = red[2 * wave + t][lane];
-#pragma unroll
-    for (int w = 1; w < UP_WAVES; ++w) v[t] += red[(w * MT + wave) * 2 + t][lane];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = 16 * wave + 4 * j + i;
-    if (s < count)
-      a.H[int64_t(s0 + s) * a.N + n] = f32_to_bf16(gate_act<ACT>(v[0][i]) * v[1][i]);
-  }
-}
-
-template <int ACT>
-__global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
-  __shared__ Route r;
-  __shared__ v4f red[UP_WAVES * 4 * 2][64];
-  route(a, r);
-  const int blocks = a.N / 16, items = r.actives * blocks;
-  for (int i = blockIdx.x; i < items; i += gridDim.x) {
-    const int e = r.active[i / blocks], block = i % blocks;
-    const int count = __popc(r.mask[e][0]) + __popc(r.mask[e][1]), s0 = r.first[e];
-    if (count <= 16)
-      up_tile<1, ACT>(a, r, red, e, block, s0, count);
-    else if (count <= 32)
-      up_tile<2, ACT>(a, r, red, e, block, s0, count);
-    else
-      up_tile<4, ACT>(a, r, red, e, block, s0, count);
   }
 }
 
 // ---------------------------------------------------- the down-projections
 // A workgroup owns 16 columns of Y.  Its 16 waves take the active experts in turn (in
 // parts of the reduction where the experts are few), add each expert's rows to the
-// tokens' sums, a set of them per wave in LDS, and the sets are joined in order.
+// tokens' sums, a set of them per wave in LDS, and the sets are joined in order.  A
+// wave goes on from expert to expert with the next one's loads in flight.
 
 constexpr int DOWN_WAVES = 16;
 
 template <int MT>
-__device__ __forceinline__ void down_tile(const Moe& a, const Route& r, float* out, int e, int64_t n,
-                                          int c0, int c1, int s0, int count) {
-  constexpr int D = MT == 4 ? 2 : 4;
-  const int lane = threadIdx.x & 63, j = lane >> 4, c16 = lane & 15;
-  const svdq::AwqWeight w = a.down.at(e);
-  const uint16_t* hrow[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-    hrow[mt] = a.H + int64_t(s0 + min(16 * mt + c16, count - 1)) * a.N + 16 * j;
-  struct Slot {
-    Codes c;
-    uint4 x[MT][2];
-  } ring[D];
-  auto fetch = [&](int i, Slot& sl) __attribute__((always_inline)) {
-    const int c = min(i, c1 - 1);
-    fetch_codes(sl.c, w, int64_t(c) * a.K + n, j);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const uint4* const x = reinterpret_cast<const uint4*>(hrow[mt] + 64 * int64_t(c));
-      sl.x[mt][0] = x[0];
-      sl.x[mt][1] = x[1];
-    }
-  };
-  v4f acc[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) acc[mt] = v4f{0, 0, 0, 0};
-#pragma unroll
-  for (int d = 0; d < D; ++d) fetch(c0 + d, ring[d]);
-  for (int c = c0; c < c1; c += D)
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      v8bf b[2];
-      operands(ring[d].c, c + d < c1, b);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(v8bf, ring[d].x[mt][h]), b[h], acc[mt], 0, 0, 0);
-      fetch(c + d + D, ring[d]);
-    }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = 16 * mt + 4 * j + i;
-      if (s < count) {
-        float* const o = out + r.token[s0 + s] * 16 + c16;
-        *o = fmaf(r.weight[s0 + s], acc[mt][i], *o);
-      }
-    }
-}
-
 __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe a) {
+  constexpr int D = MT == 1 ? 5 : 3;
   __shared__ Route r;
   extern __shared__ __align__(16) float sums[];     // [wave][T][16]
   route(a, r);
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, j = lane >> 4, c16 = lane & 15;
+  const int wave = uniform(tid >> 6);
   float* const out = sums + wave * a.T * 16;
   for (int i = lane; i < a.T * 16; i += 64) out[i] = 0.f;
-  const int64_t n = int64_t(blockIdx.x) * 16 + (lane & 15);
-  const int G = a.N / 64, actives = r.actives;
-  const int parts = min(G, (DOWN_WAVES + actives - 1) / actives);
-  for (int u = wave; u < actives * parts; u += DOWN_WAVES) {
-    const int e = r.active[u / parts], p = u % parts;
-    const int c0 = p * G / parts, c1 = (p + 1) * G / parts;
-    const int count = __popc(r.mask[e][0]) + __popc(r.mask[e][1]), s0 = r.first[e];
-    if (count <= 16)
-      down_tile<1>(a, r, out, e, n, c0, c1, s0, count);
-    else if (count <= 32)
-      down_tile<2>(a, r, out, e, n, c0, c1, s0, count);
-    else
-      down_tile<4>(a, r, out, e, n, c0, c1, s0, count);
+  int cols = blockIdx.x;
+  if ((gridDim.x & 7) == 0) cols = (cols & 7) * (gridDim.x >> 3) + (cols >> 3);
+  const int G = a.N / 64, actives = uniform(r.actives);
+  const int parts = min(G, (DOWN_WAVES + actives - 1) / actives), units = actives * parts;
+  struct Cursor {
+    int unit, e, s0, left, c, c1;
+  } at, ahead;
+  auto open = [&](Cursor& u) __attribute__((always_inline)) {
+    if (u.unit >= units) return;
+    const int p = u.unit % parts;
+    u.e = uniform(r.active[u.unit / parts]);
+    u.s0 = uniform(r.first[u.e]);
+    u.left = tokens_of(r, u.e);
+    u.c = p * G / parts;
+    u.c1 = (p + 1) * G / parts;
+  };
+  auto advance = [&](Cursor& u) __attribute__((always_inline)) {
+    if (++u.c < u.c1) return;
+    const int p = u.unit % parts;
+    u.c = p * G / parts;
+    if (u.left > 16 * MT) {
+      u.left -= 16 * MT;
+      u.s0 += 16 * MT;
+      return;
+    }
+    u.unit += DOWN_WAVES;
+    open(u);
+  };
+  at.unit = wave;
+  open(at);
+  if (wave < units) {
+    ahead = at;
+    struct Slot {
+      uint2 w;
+      uint32_t s, z;
+      uint4 x[MT][2];
+    } ring[D];
+    const uint16_t* hrow[MT];
+    auto rows = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        hrow[mt] = a.H + int64_t(ahead.s0 + min(16 * mt + c16, ahead.left - 1)) * a.N + 16 * j;
+    };
+    rows();
+    auto fetch = [&](Slot& sl) __attribute__((always_inline)) {
+      const int64_t row = ahead.e * a.down.stride + int64_t(ahead.c) * a.K + 16 * cols;
+      sl.w = *reinterpret_cast<const uint2*>(a.down.w.q + row * 32 + uint32_t(32 * c16 + 8 * j));
+      sl.s = (a.down.w.s + row)[c16];
+      sl.z = (a.down.w.z + row)[c16];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint4* const x = reinterpret_cast<const uint4*>(hrow[mt] + 64 * int64_t(ahead.c));
+        sl.x[mt][0] = x[0];
+        sl.x[mt][1] = x[1];
+      }
+      const int s0 = ahead.s0, unit = ahead.unit;
+      advance(ahead);
+      if (ahead.s0 != s0 || ahead.unit != unit) rows();
+    };
+    v4f acc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(ring[d]);
+    bool more = true;
+    while (more) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (!more) break;
+        v8bf b[2];
+        operands(ring[d].w, ring[d].s, ring[d].z, true, b);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(v8bf, ring[d].x[mt][h]), b[h], acc[mt], 0, 0, 0);
+        fetch(ring[d]);
+        if (at.c == at.c1 - 1) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int s = 16 * mt + 4 * j + i;
+              if (s < at.left) {
+                float* const o = out + r.token[at.s0 + s] * 16 + c16;
+                *o = fmaf(r.weight[at.s0 + s], acc[mt][i], *o);
+              }
+            }
+            acc[mt] = v4f{0, 0, 0, 0};
+          }
+        }
+        advance(at);
+        more = at.unit < units;
+      }
+    }
   }
   __syncthreads();
   if (tid >= a.T * 16) return;
   float v = 0.f;
   for (int w = 0; w < DOWN_WAVES; ++w) v += sums[w * a.T * 16 + tid];
-  a.Y[int64_t(tid >> 4) * a.K + int64_t(blockIdx.x) * 16 + (tid & 15)] = f32_to_bf16(v);
+  a.Y[int64_t(tid >> 4) * a.K + int64_t(cols) * 16 + (tid & 15)] = f32_to_bf16(v);
 }
 
 }  // namespace
@@ -415,17 +552,23 @@ svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int6
   const int64_t rows = K * N / 64;
   const Moe a{X, logits, l16, renorm, int(T), int(E), int(top), int(K), int(N),
               {gate, rows}, {up, rows}, {down, rows}, static_cast<uint16_t*>(ws), Y, ids, weights};
-  const int64_t items = std::min(E, T * top) * (N / 16);
-  auto k = act == SVDQ_SILU ? moe_up_kernel<SVDQ_SILU> : moe_up_kernel<SVDQ_GELU>;
-  hipLaunchKernelGGL(k, dim3(unsigned(std::min<int64_t>(items, 512))), dim3(64 * UP_WAVES), 0, s, a);
+  const int64_t items = std::min(E, T * top) * (N / 32);
+  // 32 rows at a time where that many tokens go to an expert
+  const bool two = T * top > 16 * E;
+  auto up_kernel = act == SVDQ_SILU ? two ? moe_up_kernel<2, SVDQ_SILU> : moe_up_kernel<1, SVDQ_SILU>
+                   : two            ? moe_up_kernel<2, SVDQ_GELU>
+                                    : moe_up_kernel<1, SVDQ_GELU>;
+  hipLaunchKernelGGL(up_kernel, dim3(unsigned(std::min<int64_t>(items, 512))), dim3(64 * UP_WAVES), 0,
+                     s, a);
   SVDQ_TRY(check_launch("awq_moe (up)"));
   const size_t lds = size_t(DOWN_WAVES) * size_t(T) * 16 * 4;
+  auto down_kernel = two ? moe_down_kernel<2> : moe_down_kernel<1>;
   // (the most that any call asks for: the attribute is the function's, and a host
   // thread with fewer tokens must not lower it between another's two steps)
-  SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(moe_down_kernel),
+  SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(down_kernel),
                                      hipFuncAttributeMaxDynamicSharedMemorySize,
                                      DOWN_WAVES * MAX_TOKENS * 16 * 4));
-  hipLaunchKernelGGL(moe_down_kernel, dim3(unsigned(K / 16)), dim3(64 * DOWN_WAVES), lds, s, a);
+  hipLaunchKernelGGL(down_kernel, dim3(unsigned(K / 16)), dim3(64 * DOWN_WAVES), lds, s, a);
   return check_launch("awq_moe (down)");
 }
 
