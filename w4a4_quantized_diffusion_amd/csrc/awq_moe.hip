@@ -33,6 +33,16 @@ struct Experts {
   }
 };
 
+// The routing
+struct __attribute__((aligned(16))) Route {
+  uint32_t mask[MAX_EXPERTS][2];       // the tokens that chose an expert
+  float weight[MAX_SLOTS];             // of a slot
+  uint16_t first[MAX_EXPERTS];         // an expert's first slot
+  uint8_t active[MAX_EXPERTS];         // experts with tokens, in order
+  uint8_t token[MAX_SLOTS];            // of a slot
+  int actives;
+};
+
 struct Moe {
   const uint16_t* X;
   const void* logits;
@@ -43,18 +53,9 @@ struct Moe {
   uint16_t* Y;
   int32_t* ids;           // [T][top] or NULL
   float* weights;         // [T][top] or NULL
-};
-
-// What every workgroup knows of the routing, in LDS
-struct Route {
-  uint32_t mask[MAX_EXPERTS][2];       // the tokens that chose an expert
-  uint16_t first[MAX_EXPERTS];         // an expert's first slot
-  uint8_t active[MAX_EXPERTS];         // experts with tokens, in order
-  uint8_t token[MAX_SLOTS];            // of a slot
-  float weight[MAX_SLOTS];             // of a slot
-  uint8_t chosen[MAX_SLOTS];           // [T][top]
-  float p[MAX_SLOTS];                  // [T][top]
-  int actives;
+  int S;                  // slices of the down-projections
+  float* part;            // their sums [S][T][K], if there are more than one
+  Route* route;           // what the first launch found, for the second
 };
 
 template <int CTRL>
@@ -108,10 +109,23 @@ __device__ __forceinline__ int scan64(int v) {
   return v;
 }
 
+// from LDS to memory, or back
+__device__ __forceinline__ void copy_route(const Route& from, Route& to) {
+  static_assert(sizeof(Route) % 16 == 0, "whole pieces");
+  for (int i = threadIdx.x; i < int(sizeof(Route) / 16); i += blockDim.x)
+    reinterpret_cast<uint4*>(&to)[i] = reinterpret_cast<const uint4*>(&from)[i];
+}
+
+// [T][top]
+struct Choices {
+  uint8_t expert[MAX_SLOTS];
+  float p[MAX_SLOTS];
+};
+
 // The choices of the tokens, 16 lanes to a token, expert e in lane e % 16; NV values a
 // lane (E <= 16 NV).  A lane keeps the token's choice with its number.
 template <int NV>
-__device__ __forceinline__ void choose(const Moe& a, Route& r) {
+__device__ __forceinline__ void choose(const Moe& a, Route& r, Choices& ch) {
   const int tid = threadIdx.x, l = tid & 15;
   for (int t = tid >> 4; t < a.T; t += int(blockDim.x) >> 4) {
     uint32_t key[NV];
@@ -155,8 +169,8 @@ __device__ __forceinline__ void choose(const Moe& a, Route& r) {
     p = none ? 0.f : p / sum;
     if (l >= a.top) continue;
     const int i = t * a.top + l;
-    r.chosen[i] = uint8_t(choice);
-    r.p[i] = p;
+    ch.expert[i] = uint8_t(choice);
+    ch.p[i] = p;
     if (a.T == 1) {
       // slots in the order of the choices
       r.mask[choice][0] = 1;
@@ -176,7 +190,7 @@ __device__ __forceinline__ void choose(const Moe& a, Route& r) {
 }
 
 // All threads of the workgroup
-__device__ __forceinline__ void route(const Moe& a, Route& r) {
+__device__ __forceinline__ void route(const Moe& a, Route& r, Choices& ch) {
   const int tid = threadIdx.x, NT = blockDim.x;
   if (a.T > 1) {
     for (int i = tid; i < 2 * MAX_EXPERTS; i += NT) r.mask[i >> 1][i & 1] = 0;
@@ -185,15 +199,15 @@ __device__ __forceinline__ void route(const Moe& a, Route& r) {
     r.actives = a.top;
   }
   if (a.E <= 16)
-    choose<1>(a, r);
+    choose<1>(a, r, ch);
   else if (a.E <= 32)
-    choose<2>(a, r);
+    choose<2>(a, r, ch);
   else if (a.E <= 64)
-    choose<4>(a, r);
+    choose<4>(a, r, ch);
   else if (a.E <= 128)
-    choose<8>(a, r);
+    choose<8>(a, r, ch);
   else
-    choose<16>(a, r);
+    choose<16>(a, r, ch);
   __syncthreads();
   if (a.T == 1) return;
   // slots by expert: first[] and active[] from one wave's running sums, 4 experts a lane
@@ -219,17 +233,21 @@ __device__ __forceinline__ void route(const Moe& a, Route& r) {
   }
   __syncthreads();
   for (int i = tid; i < a.T * a.top; i += NT) {
-    const int t = i / a.top, e = r.chosen[i];
+    const int t = i / a.top, e = ch.expert[i];
     // tokens below t in the expert's mask
     const uint32_t lo = t < 32 ? (1u << t) - 1 : 0xFFFFFFFFu, hi = t < 32 ? 0 : (1u << (t - 32)) - 1;
     const int s = r.first[e] + __popc(r.mask[e][0] & lo) + __popc(r.mask[e][1] & hi);
     r.token[s] = uint8_t(t);
-    r.weight[s] = r.p[i];
+    r.weight[s] = ch.p[i];
   }
   __syncthreads();
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Keeps a lane's offset apart from the uniform part of an address, which the compiler
+// would fold into a 64-bit sum a lane (no instruction)
+__device__ __forceinline__ void opaque(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 __device__ __forceinline__ int tokens_of(const Route& r, int e) {
   return uniform(__popc(r.mask[e][0]) + __popc(r.mask[e][1]));
@@ -254,32 +272,20 @@ __device__ __forceinline__ void lds_barrier() {
 
 // ------------------------------------------------------- H = act(G) * U
 // An item is 32 columns of an expert's gate and up projections for 16 MT of its slots.
-// A workgroup's 8 waves take the chunks of K in turn, and their sums meet in LDS.  The
-// workgroups go on from item to item with the next item's loads in flight.
+// A workgroup's 8 waves take the chunks of K in turn, D of them at a time, and their sums
+// meet in LDS.  The workgroups go on from item to item with the next item's loads in
+// flight.  (One token runs through the code once: a loop that also unrolled the ends of
+// the items took 12 us instead of X for it, most of it waiting for instructions.)
 
 constexpr int UP_WAVES = 8;
 
-template <int MT>
-struct UpCursor {
-  int item, e, block, s0, left, step;
-
-  // (the end of the list leaves the cursor where it is; `item` says that it ended)
-  __device__ __forceinline__ void open(const Route& r, int blocks, int items) {
-    step = 0;
-    if (item >= items) return;
-    e = uniform(r.active[item / blocks]);
-    block = item % blocks;
-    s0 = uniform(r.first[e]);
-    left = tokens_of(r, e);
-  }
-};
-
 template <int MT, int ACT>
 __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
-  constexpr int D = MT == 1 ? 3 : 2;
+  constexpr int D = MT == 1 ? 4 : 2;
   __shared__ Route r;
+  __shared__ Choices ch;
   __shared__ float red[UP_WAVES][MT][2][2][4][64];   // [wave][rows][column parity][G, U][e][lane]
-  route(a, r);
+  route(a, r, ch);
   const int lane = threadIdx.x & 63, j = lane >> 4, c16 = lane & 15;
   const int wave = uniform(threadIdx.x >> 6);
   const int G = a.K / 64, steps = (G + UP_WAVES - 1) / UP_WAVES;
@@ -293,76 +299,95 @@ __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
     end = min(items, (xcd + 1) * per);
     stride = gridDim.x >> 3;
   }
+  if (blockIdx.x == 0)
+    copy_route(r, *a.route);
   if (start >= end) return;
-  UpCursor<MT> at, ahead;
-  at.item = start;
-  at.open(r, blocks, end);
-  ahead = at;
-  auto advance = [&](UpCursor<MT>& c) __attribute__((always_inline)) {
-    if (++c.step < steps) return;
-    c.step = 0;
-    if (c.left > 16 * MT) {
-      c.left -= 16 * MT;
-      c.s0 += 16 * MT;
-      return;
-    }
-    c.item += stride;
-    c.open(r, blocks, end);
+  // D steps of an item's slots s0 .. s0 + left - 1
+  struct Turn {
+    int item, e, block, s0, left, step;
   };
+  auto open = [&](Turn& t) __attribute__((always_inline)) {
+    t.e = uniform(r.active[t.item / blocks]);
+    t.block = t.item % blocks;
+    t.s0 = uniform(r.first[t.e]);
+    t.left = tokens_of(r, t.e);
+  };
+  // addresses are a uniform base and a lane's 32-bit offset in bytes (X is at most 64 x
+  // 2^22 elements)
+  uint32_t xoff[MT];
+  auto rows = [&](const Turn& t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      xoff[mt] = 2 * uint32_t(r.token[t.s0 + min(16 * mt + c16, t.left - 1)]) * uint32_t(a.K) + 32 * j;
+  };
+  uint32_t woff = 64 * c16 + 8 * j, soff = 4 * c16;
   struct Slot {
     uint2 w[2][2];                       // gate, up; column parity
     uint32_t s[2], z[2];                 // of both columns
     uint4 x[MT][2];
   } ring[D];
-  const uint16_t* xrow[MT];
-  auto rows = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      xrow[mt] = a.X + int64_t(r.token[ahead.s0 + min(16 * mt + c16, ahead.left - 1)]) * a.K + 16 * j;
-  };
-  rows();
   // every slot is always loaded (past the last chunk with the last one's data), so that
   // the number of loads in flight is fixed
-  auto fetch = [&](Slot& sl) __attribute__((always_inline)) {
-    const int c = min(wave + UP_WAVES * ahead.step, G - 1);
-    const int64_t row = ahead.e * a.gate.stride + int64_t(c) * a.N + 32 * ahead.block;
+  auto fetch = [&](const Turn& t, int d, Slot& sl) __attribute__((always_inline)) {
+    const int c = min(wave + UP_WAVES * (t.step + d), G - 1);
+    const int64_t row = t.e * a.gate.stride + int64_t(c) * a.N + 32 * t.block;
+    opaque(woff);
+    opaque(soff);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const svdq::AwqWeight& w = t ? a.up.w : a.gate.w;
+    for (int i = 0; i < 2; ++i) {
+      const svdq::AwqWeight& w = i ? a.up.w : a.gate.w;
       const uint8_t* const q = w.q + row * 32;
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        sl.w[t][p] = *reinterpret_cast<const uint2*>(q + uint32_t(64 * c16 + 32 * p + 8 * j));
-      sl.s[t] = reinterpret_cast<const uint32_t*>(w.s + row)[c16];
-      sl.z[t] = reinterpret_cast<const uint32_t*>(w.z + row)[c16];
+        sl.w[i][p] = *reinterpret_cast<const uint2*>(q + 32 * p + woff);
+      sl.s[i] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(w.s + row) + soff);
+      sl.z[i] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(w.z + row) + soff);
     }
+    const uint8_t* const x = reinterpret_cast<const uint8_t*>(a.X + 64 * int64_t(c));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const uint4* const x = reinterpret_cast<const uint4*>(xrow[mt] + 64 * int64_t(c));
-      sl.x[mt][0] = x[0];
-      sl.x[mt][1] = x[1];
+      sl.x[mt][0] = *reinterpret_cast<const uint4*>(x + xoff[mt]);
+      sl.x[mt][1] = *reinterpret_cast<const uint4*>(x + 16 + xoff[mt]);
     }
-    const int s0 = ahead.s0, item = ahead.item;
-    advance(ahead);
-    if (ahead.s0 != s0 || ahead.item != item) rows();
   };
   v4f acc[MT][2][2];
-  auto clear = [&]() __attribute__((always_inline)) {
+  Turn at;
+  at.item = start;
+  at.step = 0;
+  open(at);
+  rows(at);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+  for (int d = 0; d < D; ++d) {
+    fetch(at, d, ring[d]);
+    // (slot by slot, here and below: the waits count the loads behind a slot's)
+    __builtin_amdgcn_sched_barrier(0);
+  }
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) acc[mt][p][t] = v4f{0, 0, 0, 0};
-  };
-  clear();
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-  for (int d = 0; d < D; ++d) fetch(ring[d]);
+      for (int t = 0; t < 2; ++t) acc[mt][p][t] = v4f{0, 0, 0, 0};
   while (true) {
+    // the turn behind this one: the same slots, the item's next, or the next item's
+    // (none: this one again, whose loads are not used)
+    Turn next = at;
+    const bool last = at.step + D >= steps;
+    next.step = last ? 0 : at.step + D;
+    if (last) {
+      if (at.left > 16 * MT) {
+        next.left -= 16 * MT;
+        next.s0 += 16 * MT;
+      } else {
+        next.item += stride;
+        if (next.item < end) open(next);
+      }
+      rows(next);
+    }
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       Slot& sl = ring[d];
-      const bool live = wave + UP_WAVES * at.step < G;
+      const bool live = wave + UP_WAVES * (at.step + d) < G;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -377,199 +402,306 @@ __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
               acc[mt][p][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                   __builtin_bit_cast(v8bf, sl.x[mt][h]), b[h], acc[mt][p][t], 0, 0, 0);
         }
-      fetch(sl);
-      if (at.step == steps - 1) {
-        // the waves' sums in order
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) red[wave][mt][p][t][e][lane] = acc[mt][p][t][e];
-        clear();
-        lds_barrier();
-        // wave e of four: rows 4 j + e, both columns
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int e = wave - 4 * (mt & 1), row = 16 * mt + 4 * j + e;
-          if (e < 0 || e > 3 || row >= at.left) continue;
-          float h[2];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            float g = red[0][mt][p][0][e][lane], u = red[0][mt][p][1][e][lane];
-#pragma unroll
-            for (int w = 1; w < UP_WAVES; ++w) {
-              g += red[w][mt][p][0][e][lane];
-              u += red[w][mt][p][1][e][lane];
-            }
-            h[p] = gate_act<ACT>(g) * u;
-          }
-          reinterpret_cast<uint32_t*>(a.H + int64_t(at.s0 + row) * a.N + 32 * at.block)[c16] =
-              pack_bf16x2(h[0], h[1]);
-        }
-        lds_barrier();
-      }
-      advance(at);
-      if (at.item >= end) return;
+      fetch(next, d, sl);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (last) {
+      // the waves' sums in order
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[wave][mt][p][t][e][lane] = acc[mt][p][t][e];
+            acc[mt][p][t] = v4f{0, 0, 0, 0};
+          }
+      lds_barrier();
+      // wave e of four (of each tile of rows): rows 4 j + e, both columns
+      const int mt = MT == 1 ? 0 : wave >> 2, e = wave & 3, row = 16 * mt + 4 * j + e;
+      if (wave < 4 * MT && row < at.left) {
+        float h[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float g = red[0][mt][p][0][e][lane], u = red[0][mt][p][1][e][lane];
+#pragma unroll
+          for (int w = 1; w < UP_WAVES; ++w) {
+            g += red[w][mt][p][0][e][lane];
+            u += red[w][mt][p][1][e][lane];
+          }
+          h[p] = gate_act<ACT>(g) * u;
+        }
+        reinterpret_cast<uint32_t*>(a.H + int64_t(at.s0 + row) * a.N + 32 * at.block)[c16] =
+            pack_bf16x2(h[0], h[1]);
+      }
+      if (next.item >= end) return;
+      lds_barrier();
+    }
+    at = next;
   }
 }
 
 // ---------------------------------------------------- the down-projections
-// A workgroup owns 16 columns of Y.  Its 16 waves take the active experts in turn (in
-// parts of the reduction where the experts are few), add each expert's rows to the
-// tokens' sums, a set of them per wave in LDS, and the sets are joined in order.  A
-// wave goes on from expert to expert with the next one's loads in flight.
+// A workgroup owns 16 CT columns of Y and one of S slices of the active experts' chunks.
+// Its 16 waves share them evenly: a wave takes a run of them, D at a time, adds each
+// expert's part to the tokens' sums, a set of them per wave in LDS, and the sets are
+// joined in order.  A wave goes on from expert to expert with the next one's loads in
+// flight.  With S > 1 a third launch adds the slices' sums (the workgroup of a column
+// block that ends last could, but its fences write the L2 back and took 9 us).
 
 constexpr int DOWN_WAVES = 16;
+constexpr int MAX_SLICES = 8;
 
-template <int MT>
+template <int MT, int CT>
 __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe a) {
-  constexpr int D = MT == 1 ? 5 : 3;
+  constexpr int D = MT * CT == 4 ? 2 : MT == 1 && CT == 1 ? 4 : 3;
+  constexpr int W = 16 * CT;
   __shared__ Route r;
-  extern __shared__ __align__(16) float sums[];     // [wave][T][16]
-  route(a, r);
+  extern __shared__ __align__(16) float sums[];     // [wave][T][W]
+  copy_route(*a.route, r);
   const int tid = threadIdx.x, lane = tid & 63, j = lane >> 4, c16 = lane & 15;
   const int wave = uniform(tid >> 6);
-  float* const out = sums + wave * a.T * 16;
-  for (int i = lane; i < a.T * 16; i += 64) out[i] = 0.f;
-  int cols = blockIdx.x;
-  if ((gridDim.x & 7) == 0) cols = (cols & 7) * (gridDim.x >> 3) + (cols >> 3);
-  const int G = a.N / 64, actives = uniform(r.actives);
-  const int parts = min(G, (DOWN_WAVES + actives - 1) / actives), units = actives * parts;
-  struct Cursor {
-    int unit, e, s0, left, c, c1;
-  } at, ahead;
-  auto open = [&](Cursor& u) __attribute__((always_inline)) {
-    if (u.unit >= units) return;
-    const int p = u.unit % parts;
-    u.e = uniform(r.active[u.unit / parts]);
-    u.s0 = uniform(r.first[u.e]);
-    u.left = tokens_of(r, u.e);
-    u.c = p * G / parts;
-    u.c1 = (p + 1) * G / parts;
+  float* const out = sums + wave * a.T * W;
+  for (int i = lane; i < a.T * W; i += 64) out[i] = 0.f;
+  __syncthreads();
+  // the slices of a column block one behind the other, the blocks of an XCD in a run
+  int group = blockIdx.x;
+  if ((gridDim.x & 7) == 0) group = (group & 7) * (gridDim.x >> 3) + (group >> 3);
+  const int slice = group % a.S, cols = group / a.S;
+  const int G = a.N / 64, total = uniform(r.actives) * G, shares = DOWN_WAVES * a.S;
+  const int share = slice * DOWN_WAVES + wave;
+  const int p0 = int(int64_t(share) * total / shares), p1 = int(int64_t(share + 1) * total / shares);
+  // D chunks from c on of a piece c0 .. c1 - 1 of expert number i, slots s0 .. s0 + left -
+  // 1; `rest` chunks lie behind the piece
+  struct Turn {
+    int i, e, s0, left, c0, c, c1, rest;
   };
-  auto advance = [&](Cursor& u) __attribute__((always_inline)) {
-    if (++u.c < u.c1) return;
-    const int p = u.unit % parts;
-    u.c = p * G / parts;
-    if (u.left > 16 * MT) {
-      u.left -= 16 * MT;
-      u.s0 += 16 * MT;
-      return;
-    }
-    u.unit += DOWN_WAVES;
-    open(u);
+  auto open = [&](Turn& t) __attribute__((always_inline)) {
+    t.e = uniform(r.active[t.i]);
+    t.s0 = uniform(r.first[t.e]);
+    t.left = tokens_of(r, t.e);
+    t.c = t.c0;
+    t.c1 = min(G, t.c0 + t.rest);
+    t.rest -= t.c1 - t.c0;
   };
-  at.unit = wave;
-  open(at);
-  if (wave < units) {
-    ahead = at;
+  if (p0 < p1) {
+    Turn at;
+    at.i = p0 / G;
+    at.c0 = p0 - at.i * G;
+    at.rest = p1 - p0;
+    open(at);
     struct Slot {
-      uint2 w;
+      uint2 w[CT];
       uint32_t s, z;
       uint4 x[MT][2];
     } ring[D];
-    const uint16_t* hrow[MT];
-    auto rows = [&]() __attribute__((always_inline)) {
+    // (a piece's rows of H: at most 64 x 2^22 elements)
+    uint32_t hoff[MT];
+    auto rows = [&](const Turn& t) __attribute__((always_inline)) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
-        hrow[mt] = a.H + int64_t(ahead.s0 + min(16 * mt + c16, ahead.left - 1)) * a.N + 16 * j;
+        hoff[mt] = 2 * uint32_t(min(16 * mt + c16, t.left - 1)) * uint32_t(a.N) + 32 * j;
     };
-    rows();
-    auto fetch = [&](Slot& sl) __attribute__((always_inline)) {
-      const int64_t row = ahead.e * a.down.stride + int64_t(ahead.c) * a.K + 16 * cols;
-      sl.w = *reinterpret_cast<const uint2*>(a.down.w.q + row * 32 + uint32_t(32 * c16 + 8 * j));
-      sl.s = (a.down.w.s + row)[c16];
-      sl.z = (a.down.w.z + row)[c16];
+    uint32_t woff = 32 * CT * c16 + 8 * j, soff = 2 * CT * c16;
+    auto fetch = [&](const Turn& t, int d, Slot& sl) __attribute__((always_inline)) {
+      const int c = min(t.c + d, t.c1 - 1);
+      const int64_t row = t.e * a.down.stride + int64_t(c) * a.K + W * cols;
+      opaque(woff);
+      opaque(soff);
+      const uint8_t* const s8 = reinterpret_cast<const uint8_t*>(a.down.w.s + row);
+      const uint8_t* const z8 = reinterpret_cast<const uint8_t*>(a.down.w.z + row);
+#pragma unroll
+      for (int p = 0; p < CT; ++p)
+        sl.w[p] = *reinterpret_cast<const uint2*>(a.down.w.q + row * 32 + 32 * p + woff);
+      if constexpr (CT == 1) {
+        sl.s = *reinterpret_cast<const uint16_t*>(s8 + soff);
+        sl.z = *reinterpret_cast<const uint16_t*>(z8 + soff);
+      } else {
+        sl.s = *reinterpret_cast<const uint32_t*>(s8 + soff);
+        sl.z = *reinterpret_cast<const uint32_t*>(z8 + soff);
+      }
+      const uint8_t* const h = reinterpret_cast<const uint8_t*>(a.H + int64_t(t.s0) * a.N + 64 * int64_t(c));
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const uint4* const x = reinterpret_cast<const uint4*>(hrow[mt] + 64 * int64_t(ahead.c));
-        sl.x[mt][0] = x[0];
-        sl.x[mt][1] = x[1];
+        sl.x[mt][0] = *reinterpret_cast<const uint4*>(h + hoff[mt]);
+        sl.x[mt][1] = *reinterpret_cast<const uint4*>(h + 16 + hoff[mt]);
       }
-      const int s0 = ahead.s0, unit = ahead.unit;
-      advance(ahead);
-      if (ahead.s0 != s0 || ahead.unit != unit) rows();
     };
-    v4f acc[MT];
+    v4f acc[MT][CT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = v4f{0, 0, 0, 0};
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(ring[d]);
-    bool more = true;
-    while (more) {
+      for (int p = 0; p < CT; ++p) acc[mt][p] = v4f{0, 0, 0, 0};
+    rows(at);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      fetch(at, d, ring[d]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    while (true) {
+      // the turn behind this one: the same piece, the expert's next slots, or the next
+      // expert (none: this one again, whose loads are not used)
+      Turn next = at;
+      const bool last = at.c + D >= at.c1;
+      bool more = true;
+      next.c += D;
+      if (last) {
+        next.c = at.c0;
+        if (at.left > 16 * MT) {
+          next.left -= 16 * MT;
+          next.s0 += 16 * MT;
+        } else if (at.rest) {
+          ++next.i;
+          next.c0 = 0;
+          open(next);
+        } else {
+          more = false;
+        }
+        rows(next);
+      }
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (!more) break;
-        v8bf b[2];
-        operands(ring[d].w, ring[d].s, ring[d].z, true, b);
+        Slot& sl = ring[d];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int p = 0; p < CT; ++p) {
+          v8bf b[2];
+          operands(sl.w[p], p ? sl.s >> 16 : sl.s & 0xFFFF, p ? sl.z >> 16 : sl.z & 0xFFFF,
+                   at.c + d < at.c1, b);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(v8bf, ring[d].x[mt][h]), b[h], acc[mt], 0, 0, 0);
-        fetch(ring[d]);
-        if (at.c == at.c1 - 1) {
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int s = 16 * mt + 4 * j + i;
-              if (s < at.left) {
-                float* const o = out + r.token[at.s0 + s] * 16 + c16;
-                *o = fmaf(r.weight[at.s0 + s], acc[mt][i], *o);
-              }
-            }
-            acc[mt] = v4f{0, 0, 0, 0};
-          }
+            for (int h = 0; h < 2; ++h)
+              acc[mt][p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(v8bf, sl.x[mt][h]), b[h], acc[mt][p], 0, 0, 0);
         }
-        advance(at);
-        more = at.unit < units;
+        fetch(next, d, sl);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (last) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          // (all reads first)
+          int to[4];
+          float w[4], o[4][CT];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int s = at.s0 + min(16 * mt + 4 * j + i, at.left - 1);
+            to[i] = r.token[s] * W + CT * c16;
+            w[i] = r.weight[s];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < CT; ++p) o[i][p] = out[to[i] + p];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * mt + 4 * j + i < at.left)
+#pragma unroll
+              for (int p = 0; p < CT; ++p) out[to[i] + p] = fmaf(w[i], acc[mt][p][i], o[i][p]);
+#pragma unroll
+          for (int p = 0; p < CT; ++p) acc[mt][p] = v4f{0, 0, 0, 0};
+        }
+        if (!more) break;
+      }
+      at = next;
     }
   }
   __syncthreads();
-  if (tid >= a.T * 16) return;
-  float v = 0.f;
-  for (int w = 0; w < DOWN_WAVES; ++w) v += sums[w * a.T * 16 + tid];
-  a.Y[int64_t(tid >> 4) * a.K + int64_t(cols) * 16 + (tid & 15)] = f32_to_bf16(v);
+  for (int i = tid; i < a.T * W; i += 64 * DOWN_WAVES) {
+    float v = 0.f;
+    for (int w = 0; w < DOWN_WAVES; ++w) v += sums[w * a.T * W + i];
+    const int64_t at = int64_t(i / W) * a.K + int64_t(cols) * W + i % W;
+    if (a.S == 1)
+      a.Y[at] = f32_to_bf16(v);
+    else
+      a.part[int64_t(slice) * a.T * a.K + at] = v;
+  }
 }
 
+// Y from the slices' sums, in order; 4 columns per thread
+__global__ __launch_bounds__(64) void moe_sum_kernel(const float* __restrict__ part, int S,
+                                                     int64_t total, uint16_t* __restrict__ Y) {
+  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
+  if (i >= total) return;
+  v4f v[MAX_SLICES], p = {0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < MAX_SLICES; ++q)
+    v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q, S - 1)) * total + i];
+#pragma unroll
+  for (int q = 0; q < MAX_SLICES; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] += q < S ? v[q][e] : 0.f;
+  reinterpret_cast<uint2*>(Y)[i] = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+}
+
+struct Plan {
+  bool two_rows, two_columns;
+  int S;
+};
+
+Plan plan(int64_t T, int64_t E, int64_t top, int64_t K, int64_t N) {
+  Plan p{};
+  // 32 rows at a time where that many tokens go to an expert
+  p.two_rows = T * top > 16 * E;
+  p.S = 1;
+  if (std::min(E, T * top) * N >= 16384) {
+    p.two_columns = true;
+    while (p.S < MAX_SLICES && p.S * (K / 32) < 256) p.S *= 2;
+  }
+  return p;
+}
+
+size_t h_bytes(int64_t T, int64_t top, int64_t N) {
+  return svdq::align256(size_t(T) * size_t(top) * size_t(N) * 2);
+}
 }  // namespace
 
 namespace svdq {
 
-size_t awq_moe_workspace(int64_t T, int64_t top, int64_t N) { return align256(size_t(T * top * N * 2)); }
+size_t awq_moe_workspace(int64_t T, int64_t E, int64_t top, int64_t K, int64_t N) {
+  const Plan p = plan(T, E, top, K, N);
+  return align256(sizeof(Route)) + h_bytes(T, top, N) +
+         (p.S == 1 ? 0 : align256(size_t(p.S) * size_t(T) * size_t(K) * 4));
+}
 
 svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int64_t T, int64_t E,
                            int64_t top, int64_t K, int64_t N, AwqWeight gate, AwqWeight up,
                            AwqWeight down, svdq_act act, bool renorm, uint16_t* Y, int32_t* ids,
                            float* weights, void* ws, hipStream_t s) {
   const int64_t rows = K * N / 64;
+  const Plan p = plan(T, E, top, K, N);
+  uint8_t* const h = static_cast<uint8_t*>(ws) + align256(sizeof(Route));
+  float* const part = reinterpret_cast<float*>(h + h_bytes(T, top, N));
   const Moe a{X, logits, l16, renorm, int(T), int(E), int(top), int(K), int(N),
-              {gate, rows}, {up, rows}, {down, rows}, static_cast<uint16_t*>(ws), Y, ids, weights};
+              {gate, rows}, {up, rows}, {down, rows}, reinterpret_cast<uint16_t*>(h), Y, ids,
+              weights, p.S, part, static_cast<Route*>(ws)};
   const int64_t items = std::min(E, T * top) * (N / 32);
-  // 32 rows at a time where that many tokens go to an expert
-  const bool two = T * top > 16 * E;
-  auto up_kernel = act == SVDQ_SILU ? two ? moe_up_kernel<2, SVDQ_SILU> : moe_up_kernel<1, SVDQ_SILU>
-                   : two            ? moe_up_kernel<2, SVDQ_GELU>
-                                    : moe_up_kernel<1, SVDQ_GELU>;
+  auto up_kernel = act == SVDQ_SILU
+                       ? p.two_rows ? moe_up_kernel<2, SVDQ_SILU> : moe_up_kernel<1, SVDQ_SILU>
+                   : p.two_rows ? moe_up_kernel<2, SVDQ_GELU>
+                                : moe_up_kernel<1, SVDQ_GELU>;
   hipLaunchKernelGGL(up_kernel, dim3(unsigned(std::min<int64_t>(items, 512))), dim3(64 * UP_WAVES), 0,
                      s, a);
   SVDQ_TRY(check_launch("awq_moe (up)"));
-  const size_t lds = size_t(DOWN_WAVES) * size_t(T) * 16 * 4;
-  auto down_kernel = two ? moe_down_kernel<2> : moe_down_kernel<1>;
+  const int W = p.two_columns ? 32 : 16;
+  const size_t lds = size_t(DOWN_WAVES) * size_t(T) * size_t(W) * 4;
+  auto down_kernel = p.two_columns
+                         ? p.two_rows ? moe_down_kernel<2, 2> : moe_down_kernel<1, 2>
+                     : p.two_rows ? moe_down_kernel<2, 1>
+                                  : moe_down_kernel<1, 1>;
   // (the most that any call asks for: the attribute is the function's, and a host
   // thread with fewer tokens must not lower it between another's two steps)
   SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(down_kernel),
                                      hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     DOWN_WAVES * MAX_TOKENS * 16 * 4));
-  hipLaunchKernelGGL(down_kernel, dim3(unsigned(K / 16)), dim3(64 * DOWN_WAVES), lds, s, a);
-  return check_launch("awq_moe (down)");
+                                     DOWN_WAVES * MAX_TOKENS * 4 * W));
+  hipLaunchKernelGGL(down_kernel, dim3(unsigned(K / W * p.S)), dim3(64 * DOWN_WAVES), lds, s, a);
+  SVDQ_TRY(check_launch("awq_moe (down)"));
+  if (p.S == 1) return SVDQ_OK;
+  const int64_t quads = T * K / 4;
+  hipLaunchKernelGGL(moe_sum_kernel, dim3(unsigned((quads + 63) / 64)), dim3(64), 0, s, part, p.S,
+                     quads, Y);
+  return check_launch("awq_moe (sum)");
 }
 
 }  // namespace svdq

@@ -67,7 +67,7 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
 
 // Mixture of experts on AWQ weights, expert after expert (every one K N / 64 rows of 32
 // bytes of codes)
-size_t awq_moe_workspace(int64_t T, int64_t top, int64_t N);
+size_t awq_moe_workspace(int64_t T, int64_t E, int64_t top, int64_t K, int64_t N);
 svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int64_t T, int64_t E,
                            int64_t top, int64_t K, int64_t N, AwqWeight gate, AwqWeight up,
                            AwqWeight down, svdq_act act, bool renorm, uint16_t* Y, int32_t* ids,

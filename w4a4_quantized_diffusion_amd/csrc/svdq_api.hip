@@ -1020,7 +1020,7 @@ extern "C" {
 
 size_t awq_moe_w4a16_workspace_bytes(int64_t T, int64_t E, int32_t top, int64_t K, int64_t N) {
   if (check_moe(T, E, top, K, N) != SVDQ_OK) return 0;
-  return svdq::awq_moe_workspace(T, top, N);
+  return svdq::awq_moe_workspace(T, E, top, K, N);
 }
 
 svdq_status awq_moe_w4a16(const uint16_t* X, const void* logits, svdq_dtype logits_dtype, int64_t T,
@@ -1048,7 +1048,7 @@ svdq_status awq_moe_w4a16(const uint16_t* X, const void* logits, svdq_dtype logi
   TRY(check_ptr(Y, "Y"));
   if (ids) TRY(check_ptr(ids, "ids", 4));
   if (weights) TRY(check_ptr(weights, "weights", 4));
-  const size_t need = svdq::awq_moe_workspace(T, top, N);
+  const size_t need = svdq::awq_moe_workspace(T, E, top, K, N);
   TRY(check_workspace(workspace, workspace_bytes, need));
   const size_t t = T, e = E, k = K, n = N, c = size_t(T) * size_t(top) * 4;
   const Span spans[] = {{X, t * k * 2, false}, {logits, t * e * elem(logits_dtype), false},
