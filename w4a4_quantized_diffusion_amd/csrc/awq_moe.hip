@@ -281,7 +281,7 @@ constexpr int UP_WAVES = 8;
 
 template <int MT, int ACT>
 __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
-  constexpr int D = MT == 1 ? 4 : 2;
+  constexpr int D = 2;
   __shared__ Route r;
   __shared__ Choices ch;
   __shared__ float red[UP_WAVES][MT][2][2][4][64];   // [wave][rows][column parity][G, U][e][lane]
@@ -692,9 +692,10 @@ svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int6
                                   : moe_down_kernel<1, 1>;
   // (the most that any call asks for: the attribute is the function's, and a host
   // thread with fewer tokens must not lower it between another's two steps)
-  SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(down_kernel),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     DOWN_WAVES * MAX_TOKENS * 4 * W));
+  if (lds + sizeof(Route) > (64 << 10))
+    SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(down_kernel),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       DOWN_WAVES * MAX_TOKENS * 4 * W));
   hipLaunchKernelGGL(down_kernel, dim3(unsigned(K / W * p.S)), dim3(64 * DOWN_WAVES), lds, s, a);
   SVDQ_TRY(check_launch("awq_moe (down)"));
   if (p.S == 1) return SVDQ_OK;
