@@ -11,10 +11,17 @@ Diffusers", Technical Breakdown and Performance Metrics).  Here:
                   svdq_linear_w4a4 (or its GELU-input form) on the current
                   stream.
   AWQLinear       one AWQ W4A16 layer; forward runs awq_linear_w4a16, the
-                  gradient of its input awq_linear_w4a16_grad.
+                  gradient of its input awq_linear_w4a16_grad.  With an
+                  activation, a gate or a residual it runs awq_linear_w4a16_res
+                  and awq_linear_w4a16_res_grad.
   AWQGatedLinear  the gate and up projections of a gated feed-forward block
                   with the activation and the product; forward runs
                   awq_gated_w4a16, backward awq_gated_w4a16_grad.
+  AWQMoE          the experts of a mixture-of-experts layer; forward runs
+                  awq_moe_w4a16 on the router's logits.
+  BlockNorm       the residual sum behind a block with its gate and post norm,
+                  and the next block's norm with its modulation
+                  (svdq_block_norm, svdq_block_norm_grad).
   calibrate       per-input-channel max|x| of every nn.Linear's inputs
                   (svdq_act_absmax), for the smoothing step.
   quantize_linears  swaps every eligible nn.Linear of a module in place.
@@ -45,6 +52,7 @@ _SVDQ_FIELDS = ("smooth", "lora_down", "lora_up", "wcodes", "wscales", "w_tensor
                 "x_tensor_scale")
 _AWQ_FIELDS = ("q", "scales", "zeros")
 _GATED_FIELDS = tuple(f"{p}_{f}" for p in ("gate", "up") for f in _AWQ_FIELDS)
+_MOE_FIELDS = tuple(f"{p}_{f}" for p in ("gate", "up", "down") for f in _AWQ_FIELDS)
 _PREC_NAME = {svdq.INT4: "int4", svdq.NVFP4: "nvfp4"}
 
 
@@ -267,14 +275,69 @@ def _frozen_bias(y, *biases):
 def _reverse_only(x):
     # (unpack_dual looks at the level too, in 1.5 us)
     if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(x).tangent is not None:
-        raise RuntimeError("an AWQ layer has no forward-mode derivative")
+        raise RuntimeError("this layer has no forward-mode derivative")
+
+
+def _vector(v, name, width):
+    """A modulation vector [D], [images, D] or [images, 1, D] as the library takes it
+    (rows of adjacent values)."""
+    if v is None:
+        return None
+    if v.dim() == 0 or v.shape[-1] != width:
+        raise ValueError(f"{name}: expected [..., {width}], got {tuple(v.shape)}")
+    if v.dim() > 1:
+        v = v.reshape(-1, width)
+    if width > 1 and v.stride(-1) != 1 or v.dim() == 2 and len(v) > 1 and v.stride(0) < width:
+        v = v.contiguous()
+    return v
+
+
+class _AWQResFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, residual, act, bias, y_dtype, dims, q, scales, zeros):
+        lay = dict(dims, q=q, scales=scales, zeros=zeros)
+        ctx.save = act != "none" or (gate is not None and gate.requires_grad)
+        y = svdq.awq_linear_w4a16_res(x, lay, bias, act, gate, residual, y_dtype, save=ctx.save)
+        y, z = y if ctx.save else (y, None)
+        held = [q, scales, zeros] + ([gate] if gate is not None else []) + ([z] if ctx.save else [])
+        _save(ctx, *held)
+        ctx.act, ctx.dims, ctx.gated = act, dims, gate is not None
+        ctx.residual = None if residual is None else residual.dtype
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        q, scales, zeros, *held = _saved(ctx)
+        lay = dict(ctx.dims, q=q, scales=scales, zeros=zeros)
+        gate = held.pop(0) if ctx.gated else None
+        z = held.pop(0) if ctx.save else None
+        need_x, need_gate, need_res = ctx.needs_input_grad[:3]
+        dx = dgate = None
+        if need_x or need_gate:
+            d = _rows(dy, lay["N"])
+            if ctx.act == "none" and gate is None and d.dtype == torch.bfloat16:
+                dx = svdq.awq_linear_w4a16_grad(d, lay)
+            else:
+                dx, _, dgate = svdq.awq_linear_w4a16_res_grad(d, z, lay, ctx.act, gate,
+                                                              need_dgate=need_gate)
+            if dgate is not None:
+                dgate = dgate.to(gate.dtype)
+        dres = dy.to(ctx.residual) if need_res else None
+        return (dx if need_x else None, dgate, dres) + (None,) * 7
 
 
 class AWQLinear(nn.Module):
     """An AWQ W4A16 layer (asymmetric INT4 weights in groups of 64, bf16
     activations) in place of nn.Linear(K, N).  Inputs bf16 [..., K]; output
     bf16.  Differentiable once in its input, in reverse mode; weights and bias are
-    frozen (a gradient asked of the bias raises)."""
+    frozen (a gradient asked of the bias raises).
+
+    forward(x, act, gate, residual) computes residual + gate * act(layer(x)) in the
+    layer's own kernels, each part optional: act "silu" or "gelu" (tanh form), gate [N] or
+    one row per image ([images, N] for x [images, ..., K]), residual of the output's
+    shape in fp32 or bf16, whose type the output then has.  Differentiable in x, gate and
+    residual."""
 
     def __init__(self, layer, bias=None):
         super().__init__()
@@ -297,12 +360,42 @@ class AWQLinear(nn.Module):
         lay = svdq.awq_quantize_weights(linear.weight.detach().to(torch.float32).contiguous(), group)
         return cls(lay, linear.bias)
 
-    def forward(self, x):
+    def _res(self, x, act, gate, residual):
+        lead, n = x.shape[:-1], self.out_features
+        x2 = _rows(x, self.in_features)
+        gate = _vector(gate, "gate", n)
+        y_dtype = torch.bfloat16
+        if residual is not None:
+            if residual.shape != (*lead, n):
+                raise ValueError(f"residual: expected {(*lead, n)}, got {tuple(residual.shape)}")
+            y_dtype = residual.dtype
+            residual = _rows(residual, n)
+        for t in (gate, residual):
+            if t is not None:
+                _reverse_only(t)
+        bias = self._bias.get(self.bias, torch.bfloat16)
+        lay = dict(N=n, K=self.in_features, group=self.group)
+        fields = (self.q, self.scales, self.zeros)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                           for t in (x2, gate, residual)):
+            _frozen(self.bias)
+            y = _AWQResFn.apply(x2, gate, residual, act, bias, y_dtype, lay, *fields)
+        else:
+            lay.update(zip(_AWQ_FIELDS, fields))
+            y = svdq.awq_linear_w4a16_res(x2, lay, bias, act, gate, residual, y_dtype)
+            y = _frozen_bias(y, self.bias)
+        return y.reshape(*lead, n)
+
+    def forward(self, x, act=None, gate=None, residual=None):
         if x.dtype != torch.bfloat16:
             raise TypeError("AWQLinear takes bf16 activations")
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
         _reverse_only(x)
+        if act is not None or gate is not None or residual is not None:
+            if act not in (None, "silu", "gelu"):
+                raise ValueError(f"act must be 'silu' or 'gelu', got {act!r}")
+            return self._res(x, act or "none", gate, residual)
         lead = x.shape[:-1]
         x2 = _rows(x, self.in_features)
         lay = dict(q=self.q, scales=self.scales, zeros=self.zeros, N=self.out_features,
@@ -390,6 +483,185 @@ class AWQGatedLinear(nn.Module):
                 f"bias={(self.bias_gate is not None, self.bias_up is not None)}")
 
 
+class _NoBackwardFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, *inputs):
+        ctx.mark_dirty(y)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError("AWQMoE has no backward pass")
+
+
+class AWQMoE(nn.Module):
+    """The experts of a mixture-of-experts layer, each a gated pair and a
+    down-projection on AWQ weights: `gate`, `up` [E, N x K] and `down` [E, K x N] as
+    svdq.awq_moe_w4a16 takes them.  forward(x, logits): x bf16 [..., K], the router's
+    logits fp32 or bf16 [..., E]; a token goes to the `top` experts of its largest logits
+    (equal ones: the lower expert), weighted by the softmax over all experts (renorm:
+    over the chosen ones).  Up to 64 tokens take one call; more of them run in pieces of
+    64, which each read the weights of their experts.  Not differentiable: a backward
+    pass that reaches it raises."""
+
+    def __init__(self, gate, up, down, top, act="silu", renorm=True):
+        super().__init__()
+        self.experts, self.in_features = int(gate["E"]), int(gate["K"])
+        self.hidden_features, self.group = int(gate["N"]), int(gate["group"])
+        self.top, self.act, self.renorm = int(top), act, bool(renorm)
+        if act not in ("silu", "gelu"):
+            raise ValueError(f"act must be 'silu' or 'gelu', got {act!r}")
+        if not 1 <= self.top <= min(self.experts, 16):
+            raise ValueError(f"top must be in [1, min({self.experts}, 16)], got {self.top}")
+        n, k = self.hidden_features, self.in_features
+        for p, lay, dims in (("gate", gate, (n, k)), ("up", up, (n, k)), ("down", down, (k, n))):
+            if (lay["E"], lay["N"], lay["K"], lay["group"]) != (self.experts, *dims, self.group):
+                raise ValueError(f"{p}: expected {self.experts} experts of {dims[0]} x {dims[1]}")
+            shapes = _shapes_awq(*dims, self.group)
+            for f in _AWQ_FIELDS:
+                t, (shape, dt) = lay[f], shapes[f]
+                if tuple(t.shape) != (self.experts, *shape) or t.dtype != dt:
+                    raise ValueError(f"{p}_{f}: expected {(self.experts, *shape)} {dt}, got "
+                                     f"{tuple(t.shape)} {t.dtype}")
+                self.register_buffer(f"{p}_{f}", t)
+
+    @classmethod
+    def from_linears(cls, gates, ups, downs, top, act="silu", renorm=True, group=64):
+        """Quantize the experts' nn.Linear (lists of one per expert, without biases) on
+        their (HIP) device."""
+        parts = []
+        for lins in (gates, ups, downs):
+            if any(l.bias is not None for l in lins):
+                raise ValueError("experts with biases are not supported")
+            lays = [svdq.awq_quantize_weights(l.weight.detach().to(torch.float32).contiguous(), group)
+                    for l in lins]
+            d = {f: torch.stack([lay[f] for lay in lays]) for f in _AWQ_FIELDS}
+            parts.append(dict(d, E=len(lays), N=lays[0]["N"], K=lays[0]["K"], group=group))
+        return cls(*parts, top, act, renorm)
+
+    def layer(self, which):
+        n, k = self.hidden_features, self.in_features
+        n, k = (k, n) if which == "down" else (n, k)
+        return dict({f: getattr(self, f"{which}_{f}") for f in _AWQ_FIELDS}, E=self.experts, N=n,
+                    K=k, group=self.group)
+
+    def forward(self, x, logits):
+        if x.dtype != torch.bfloat16:
+            raise TypeError("AWQMoE takes bf16 activations")
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"expected [..., {self.in_features}] input, got {tuple(x.shape)}")
+        if logits.shape != (*x.shape[:-1], self.experts):
+            raise ValueError(f"expected {(*x.shape[:-1], self.experts)} logits, got "
+                             f"{tuple(logits.shape)}")
+        for t in (x, logits):
+            _reverse_only(t)
+        x2, l2 = _rows(x, self.in_features), _rows(logits, self.experts)
+        y = torch.empty_like(x2)
+        parts = [self.layer(p) for p in ("gate", "up", "down")]
+        for i in range(0, len(x2), 64):
+            svdq.awq_moe_w4a16(x2[i:i + 64], l2[i:i + 64], *parts, self.top, self.act, self.renorm,
+                               Y=y[i:i + 64])
+        if torch.is_grad_enabled() and (x.requires_grad or logits.requires_grad):
+            y = _NoBackwardFn.apply(y, x2, l2)
+        return y.reshape(x.shape)
+
+    def extra_repr(self):
+        return (f"experts={self.experts}, in_features={self.in_features}, "
+                f"hidden_features={self.hidden_features}, top={self.top}, act={self.act}, "
+                f"renorm={self.renorm}, group={self.group}")
+
+
+class _BlockNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, h, post, gate, weight, scale, shift, kind, eps, y_dtype):
+        out = svdq.svdq_block_norm(x, h, kind, eps, post, gate, weight, scale, shift, y_dtype)
+        given = [t is not None for t in (h, post, gate, weight, scale, shift)]
+        _save(ctx, x, *(t for t in (h, post, gate, weight, scale, shift) if t is not None))
+        ctx.given, ctx.kind, ctx.eps = given, kind, eps
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        x, *held = _saved(ctx)
+        h, *vectors = (held.pop(0) if g else None for g in ctx.given)
+        dx_out, dy = grads if h is not None else (None, grads[0])
+        width = x.shape[1]
+        dx, dh, *dv = svdq.svdq_block_norm_grad(
+            _rows(dy, width), x, h, None if dx_out is None else _rows(dx_out, width), ctx.kind,
+            ctx.eps, *vectors, need=ctx.needs_input_grad[2:7])
+        dv = [d if d is None else d.to(v.dtype) for d, v in zip(dv, vectors)]
+        return (dx, dh, *dv, None, None, None)
+
+
+class BlockNorm(nn.Module):
+    """What stands between two blocks of a transformer: forward(x, h, gate, scale, shift)
+    returns
+
+      x' = x + gate * t        t = h, or n(h) * post with a post norm
+      y  = n(x') * weight * (1 + scale) + shift
+
+    (x', y), or y alone for n(x) without h (the first block's norm, the last one).  n is
+    the layer norm ("layer", without an affine part of its own: `shift` is its bias) or
+    the RMS norm ("rms") over the last dimension of `dim`.  weight and post are given as
+    tensors (or None) and become parameters; gate, scale and shift, each optional, are
+    [dim], or one row per image ([images, dim] or [images, 1, dim] for x [images, ...,
+    dim]; slices of a modulation layer's output are read where they lie).  x and h fp32 or
+    bf16, x' in x's type, y in `y_dtype`.  Differentiable once in everything, in reverse
+    mode.
+
+    Forward and backward can be captured into a graph together.  A backward pass
+    that is captured needs leaves of its own: torch ends the process when an eager
+    graph of the same leaves is still alive then."""
+
+    def __init__(self, dim, kind="layer", eps=1e-6, weight=None, post=None,
+                 y_dtype=torch.bfloat16):
+        super().__init__()
+        if kind not in ("layer", "rms"):
+            raise ValueError(f"kind must be 'layer' or 'rms', got {kind!r}")
+        if not 1 <= dim <= 16384:
+            raise ValueError(f"dim must be in [1, 16384], got {dim}")
+        self.dim, self.kind, self.eps, self.y_dtype = int(dim), kind, float(eps), y_dtype
+        for name, t in (("weight", weight), ("post", post)):
+            if t is not None:
+                if tuple(t.shape) != (self.dim,):
+                    raise ValueError(f"{name}: expected ({self.dim},), got {tuple(t.shape)}")
+                t = t if isinstance(t, nn.Parameter) else nn.Parameter(t.detach())
+            self.register_parameter(name, t)
+
+    def forward(self, x, h=None, gate=None, scale=None, shift=None):
+        if x.shape[-1] != self.dim:
+            raise ValueError(f"expected [..., {self.dim}] input, got {tuple(x.shape)}")
+        if h is None and (gate is not None or self.post is not None):
+            raise ValueError("a gate and a post norm go with h")
+        if h is not None and h.shape != x.shape:
+            raise ValueError(f"h: expected {tuple(x.shape)}, got {tuple(h.shape)}")
+        lead = x.shape
+        x2 = _norm_rows(x, self.dim)
+        h2 = None if h is None else _norm_rows(h, self.dim)
+        vectors = [self.post, _vector(gate, "gate", self.dim), self.weight,
+                   _vector(scale, "scale", self.dim), _vector(shift, "shift", self.dim)]
+        inputs = [t for t in (x2, h2, *vectors) if t is not None]
+        for t in inputs:
+            _reverse_only(t)
+        if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+            out = _BlockNormFn.apply(x2, h2, *vectors, self.kind, self.eps, self.y_dtype)
+        else:
+            out = svdq.svdq_block_norm(x2, h2, self.kind, self.eps, *vectors, self.y_dtype)
+        if h is None:
+            return out.reshape(lead)
+        return out[0].reshape(lead), out[1].reshape(lead)
+
+    def extra_repr(self):
+        return (f"{self.dim}, kind={self.kind}, eps={self.eps}, weight={self.weight is not None}, "
+                f"post={self.post is not None}")
+
+
+def _norm_rows(x, width):
+    """x as a contiguous [M, width] matrix (at any address)."""
+    return x.reshape(-1, width).contiguous()
+
+
 # ------------------------------------------------------------ patching shim
 
 def eligible(linear, rank=0):
@@ -472,7 +744,7 @@ def _biases(mod, *names):
 
 
 def save_quantized(module, path):
-    """Write every SVDQLinear / AWQLinear / AWQGatedLinear of `module` to a
+    """Write every SVDQLinear / AWQLinear / AWQGatedLinear / AWQMoE of `module` to a
     safetensors file."""
     from safetensors.torch import save_file
     tensors, layers = {}, {}
@@ -493,6 +765,11 @@ def save_quantized(module, path):
             layers[name] = {"kind": "awq_gated", "group": mod.group, "N": mod.out_features,
                             "K": mod.in_features, "act": mod.act, "biases": list(biases)}
             fields = _GATED_FIELDS + biases
+        elif isinstance(mod, AWQMoE):
+            layers[name] = {"kind": "awq_moe", "group": mod.group, "E": mod.experts,
+                            "N": mod.hidden_features, "K": mod.in_features, "top": mod.top,
+                            "act": mod.act, "renorm": mod.renorm}
+            fields = _MOE_FIELDS
         else:
             continue
         for f in fields:
@@ -544,6 +821,11 @@ def load_quantized(module, path, device=None):
                     if tuple(t.shape) != (n,):
                         raise ValueError(f"{name}.{b}: expected ({n},)")
                 new = AWQGatedLinear(*lays, act=d["act"], **biases)
+            elif d["kind"] == "awq_moe":
+                lays = [dict({f: take(name, f"{p}_{f}") for f in _AWQ_FIELDS}, E=int(d["E"]),
+                             N=k if p == "down" else n, K=n if p == "down" else k,
+                             group=int(d["group"])) for p in ("gate", "up", "down")]
+                new = AWQMoE(*lays, int(d["top"]), d["act"], bool(d["renorm"]))
             else:
                 raise ValueError(f"{path}: unknown layer kind {d['kind']!r}")
             if bias is not None and tuple(bias.shape) != (n,):
