@@ -10,6 +10,7 @@
 // with fp32 sums.  dG and dU enter the products rounded to bf16 (the type
 // they are returned in).
 
+#include "block.h"
 #include "gemm_bf16.h"
 
 using namespace svdq_dev;
@@ -128,6 +129,9 @@ Split split(int64_t M, int64_t K, int64_t N, int layers) {
 struct Rows {
   const uint16_t *d, *G, *U;
   uint16_t *dG, *dU;
+  // of a layer with an epilogue (RES), whose Z is G and whose dZ goes to dG
+  svdq::Vec gate;
+  int rows;                // of an image
 };
 
 // 8 values of the pair's dG (layer 0) or dU (layer 1)
@@ -152,7 +156,44 @@ __device__ __forceinline__ uint4 pair_grad8(const uint4 h, const uint4 g, const 
 // ACT >= 0: a gated pair, whose dG and dU every workgroup forms for itself (those
 // of the first 128 columns store them); PLAIN_PAIR: a pair with dG and dU given;
 // PLAIN: one layer
-constexpr int PLAIN = -1, PLAIN_PAIR = -2;
+// RES + act: one layer behind whose product stands gate * act(Z); every workgroup forms dZ
+// from dY and Z for itself, as a pair's
+constexpr int PLAIN = -1, PLAIN_PAIR = -2, RES = 16;
+
+constexpr int layers_of(int act) { return act == PLAIN || act >= RES ? 1 : 2; }
+
+// 8 values of dZ = dY gate act'(Z), row m, columns n ..
+template <int ACT>
+__device__ __forceinline__ uint4 res_grad8(const Rows& in, const uint4 d, const uint4 z, int m,
+                                           int64_t n) {
+  const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, zw[4] = {z.x, z.y, z.z, z.w};
+  float g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = 1.f;
+  if (in.gate.p) {
+    const int64_t at = (in.gate.ld ? in.gate.ld * (uint32_t(m) / uint32_t(in.rows)) : 0) + n;
+    if (in.gate.b16) {
+      uint16_t t[8];
+      __builtin_memcpy(t, static_cast<const uint16_t*>(in.gate.p) + at, 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = bf16_to_f32(t[i]);
+    } else {
+      __builtin_memcpy(g, static_cast<const float*>(in.gate.p) + at, 32);
+    }
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, d0 = 1.f, d1 = 1.f;
+    if constexpr (ACT != SVDQ_NO_ACT) {
+      gate_act_grad<ACT>(__uint_as_float(zw[j] << 16), a, d0);
+      gate_act_grad<ACT>(__uint_as_float(zw[j] & 0xFFFF0000u), a, d1);
+    }
+    o[j] = pack_bf16x2(__uint_as_float(dw[j] << 16) * (g[2 * j] * d0),
+                       __uint_as_float(dw[j] & 0xFFFF0000u) * (g[2 * j + 1] * d1));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
 
 template <int MT, int ACT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::AwqWeight wa,
@@ -162,7 +203,7 @@ __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::A
                                                                 void* __restrict__ dX, bool xbf16) {
   constexpr int NT = 64 * WAVES;
   extern __shared__ __align__(16) uint8_t lds[];
-  constexpr int LAYERS = ACT == PLAIN ? 1 : 2;
+  constexpr int LAYERS = layers_of(ACT);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane >> 4, r = lane & 15;
@@ -212,7 +253,12 @@ __global__ __launch_bounds__(64 * WAVES) void grad_slice_kernel(Rows in, svdq::A
       if (n < N) {
         const uint16_t* const d = ACT == PLAIN_PAIR ? (layer ? in.dU : in.dG) : in.d;
         v = *reinterpret_cast<const uint4*>(d + at);
-        if constexpr (ACT >= 0) {
+        if constexpr (ACT >= RES) {
+          uint4 z = make_uint4(0, 0, 0, 0);
+          if constexpr (ACT - RES != SVDQ_NO_ACT) z = *reinterpret_cast<const uint4*>(in.G + at);
+          v = res_grad8<ACT - RES>(in, v, z, m, n);
+          if (block == 0) *reinterpret_cast<uint4*>(in.dG + at) = v;
+        } else if constexpr (ACT >= 0) {
           const uint4 G = *reinterpret_cast<const uint4*>(in.G + at);
           const uint4 U = *reinterpret_cast<const uint4*>(in.U + at);
           v = pair_grad8<ACT>(v, G, U, layer);
@@ -314,7 +360,7 @@ svdq_status launch_sum(const float* part, int S, int64_t M, int64_t K, void* dX,
 template <int MT, int ACT, int WAVES>
 svdq_status run_slices(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
                        const Split& p, float* part, void* dX, bool xbf16, hipStream_t s) {
-  constexpr int layers = ACT == PLAIN ? 1 : 2;
+  constexpr int layers = layers_of(ACT);
   // steps of the rows' operand that fit LDS (64 rows: 31)
   const int64_t steps = (N + 31) / 32 * layers;
   const int64_t room = MT == 1 ? LDS_A : 2 * LDS_A;
@@ -335,7 +381,7 @@ svdq_status run_slices(const Rows& in, int64_t M, int64_t K, int64_t N, const sv
 template <int ACT>
 svdq_status run_rows(const Rows& in, int64_t M, int64_t K, int64_t N, const svdq::AwqWeight* w,
                      void* dX, bool xbf16, float* part, hipStream_t s) {
-  const Split p = split(M, K, N, ACT == PLAIN ? 1 : 2);
+  const Split p = split(M, K, N, layers_of(ACT));
   switch ((M + 15) / 16) {
     case 1:
       SVDQ_TRY(p.waves == 16 ? (run_slices<1, ACT, 16>(in, M, K, N, w, p, part, dX, xbf16, s))
@@ -581,9 +627,23 @@ svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int
   float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 1) : 0));
   const uint16_t* const d = dY + w * N;
   void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
-  const Rows in{d, nullptr, nullptr, nullptr, nullptr};
+  const Rows in{d, nullptr, nullptr, nullptr, nullptr, {}, 1};
   if (rest <= ROWS) return run_rows<PLAIN>(in, rest, K, N, &wt, x, xb, part, s);
   return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, s);
+}
+
+bool awq_res_grad_fused(int64_t M, int64_t K, int64_t N) {
+  return M <= ROWS && M * N <= FUSED_GRADS / ((K + 127) / 128);
+}
+
+svdq_status launch_awq_res_grad_rows(const uint16_t* dY, const uint16_t* Z, int64_t M, int64_t K,
+                                     int64_t N, int64_t images, AwqWeight wt, svdq_act act, Vec gate,
+                                     uint16_t* dX, uint16_t* dZ, void* ws, hipStream_t s) {
+  const Rows in{dY, Z, nullptr, dZ, nullptr, gate, int(M / images)};
+  float* const part = static_cast<float*>(ws);
+  return act == SVDQ_SILU   ? run_rows<RES + SVDQ_SILU>(in, M, K, N, &wt, dX, true, part, s)
+         : act == SVDQ_GELU ? run_rows<RES + SVDQ_GELU>(in, M, K, N, &wt, dX, true, part, s)
+                            : run_rows<RES + SVDQ_NO_ACT>(in, M, K, N, &wt, dX, true, part, s);
 }
 
 svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
@@ -596,7 +656,7 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
   float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 2) : 0));
   // few rows form their own dG and dU unless too many columns of dX repeat that
   const bool fused = rest <= ROWS && rest * N <= FUSED_GRADS / ((K + 127) / 128);
-  const Rows in{dH + w * N, G + w * N, U + w * N, dG + w * N, dU + w * N};
+  const Rows in{dH + w * N, G + w * N, U + w * N, dG + w * N, dU + w * N, {}, 1};
   uint16_t* const x = dX + w * K;
   if (rest && fused)
     SVDQ_TRY(act == SVDQ_SILU ? run_rows<SVDQ_SILU>(in, rest, K, N, wt, x, true, part, s)

@@ -555,13 +555,14 @@ svdq_status wide(const Call& c, uint16_t* B) {
 }
 
 // ------------------------------------------------------------- backward
-// A wave takes 512 columns, 8 to a lane, and every fourth row of a workgroup's; the
-// workgroup's sums for dgate meet in LDS and, where an image has more workgroups than
+// A wave takes 512 columns, 8 to a lane, and every fourth pair of rows of a workgroup's;
+// the workgroup's sums for dgate meet in LDS and, where an image has more workgroups than
 // one, in a second launch in a fixed order.  Memory bound.
-constexpr int GRAD_ROWS = 64;            // rows of a workgroup, at most
 
-template <int ACT>
-__global__ __launch_bounds__(256) void res_grad_kernel(const void* __restrict__ dY, bool dy16,
+constexpr int PAIR = 2;                  // rows whose loads a wave has in flight together
+
+template <int ACT, bool DY16>
+__global__ __launch_bounds__(256) void res_grad_kernel(const void* __restrict__ dY,
                                                        const uint16_t* __restrict__ Z,
                                                        svdq::Vec gate, int64_t rows, int parts,
                                                        int N, uint16_t* __restrict__ dZ,
@@ -579,22 +580,42 @@ __global__ __launch_bounds__(256) void res_grad_kernel(const void* __restrict__ 
   for (int i = 0; i < 8; ++i) g[i] = 1.f, acc[i] = 0.f;
   if (gate.p && live) load_any<8>(gate.p, gate.b16, image * gate.ld + n, g);
   if (live)
-#pragma unroll 2
-    for (int64_t m = r0 + wave; m < r1; m += 4) {
-      const int64_t at = m * N + n;
-      float d[8], z[8] = {};
-      load_any<8>(dY, dy16, at, d);
-      if (Z) load_any<8>(Z, true, at, z);
+    for (int64_t m = r0 + PAIR * wave; m < r1; m += 4 * PAIR) {
+      // (a row past the last is the last one again, and counts for nothing)
+      uint32_t d[PAIR][DY16 ? 4 : 8], z[PAIR][4] = {};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float a = z[i], da = 1.f;
-        if constexpr (ACT != SVDQ_NO_ACT) gate_act_grad<ACT>(z[i], a, da);
-        acc[i] = fmaf(d[i], a, acc[i]);
-        d[i] *= g[i] * da;
+      for (int k = 0; k < PAIR; ++k) {
+        const int64_t at = min(m + k, r1 - 1) * N + n;
+        __builtin_memcpy(d[k], static_cast<const uint8_t*>(dY) + at * (DY16 ? 2 : 4), DY16 ? 16 : 32);
+        if (Z) __builtin_memcpy(z[k], Z + at, 16);
       }
-      *reinterpret_cast<uint4*>(dZ + at) =
-          make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
-                     pack_bf16x2(d[6], d[7]));
+#pragma unroll
+      for (int k = 0; k < PAIR; ++k) {
+        if (m + k >= r1) break;
+        uint32_t o[4];
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t zw = z[k][i / 2];
+          float a = __uint_as_float(i & 1 ? zw & 0xFFFF0000u : zw << 16), da = 1.f;
+          float dv;
+          if constexpr (DY16) {
+            const uint32_t dw = d[k][i / 2];
+            dv = __uint_as_float(i & 1 ? dw & 0xFFFF0000u : dw << 16);
+          } else {
+            dv = __uint_as_float(d[k][i]);
+          }
+          if constexpr (ACT != SVDQ_NO_ACT) {
+            const float x = a;
+            gate_act_grad<ACT>(x, a, da);
+          }
+          acc[i] = fmaf(dv, a, acc[i]);
+          v[i] = dv * (g[i] * da);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<uint4*>(dZ + (m + k) * N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   if (!part) return;
   if (wave)
@@ -612,13 +633,22 @@ __global__ __launch_bounds__(256) void res_grad_kernel(const void* __restrict__ 
 
 template <int ACT>
 struct GradKernel {
-  static auto get() { return res_grad_kernel<ACT>; }
+  static auto get() { return res_grad_kernel<ACT, true>; }
+};
+template <int ACT>
+struct GradKernel32 {
+  static auto get() { return res_grad_kernel<ACT, false>; }
 };
 
-int grad_parts(int64_t rows) { return int(std::max<int64_t>(1, (rows + GRAD_ROWS - 1) / GRAD_ROWS)); }
+// Workgroups an image for each 512 columns: about 1024 in all, of 8 to 64 rows
+int grad_parts(int64_t M, int64_t N, int64_t images) {
+  const int64_t rows = M / images, each = M * ((N + 511) / 512) / 1024;
+  return int((rows + std::min<int64_t>(64, std::max<int64_t>(8, each)) - 1) /
+             std::min<int64_t>(64, std::max<int64_t>(8, each)));
+}
 
 size_t grad_part_bytes(int64_t M, int64_t N, int64_t images) {
-  const int64_t groups = images * grad_parts(M / images);
+  const int64_t groups = images * grad_parts(M, N, images);
   return groups == 1 ? 0 : svdq::align256(size_t(groups) * size_t(N) * 4);
 }
 
@@ -671,13 +701,17 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
     if (dgate) j.add(nullptr, dgate, N, 0, each);
     return launch_joins(j, N, s);
   }
-  const int parts = grad_parts(rows);
+  if (dy16 && !dgate && awq_res_grad_fused(M, K, N))
+    return launch_awq_res_grad_rows(static_cast<const uint16_t*>(dY), Z, M, K, N, images, wt, act,
+                                    gate, dX, dZ, ws, s);
+  const int parts = grad_parts(M, N, images);
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
   // one workgroup's sums are the gradient
   const bool direct = images * parts == each;
   float* const part = !dgate ? nullptr : direct ? dgate : reinterpret_cast<float*>(w8);
-  hipLaunchKernelGGL(by_act<GradKernel>(act), dim3(unsigned((N + 511) / 512 * images * parts)),
-                     dim3(256), 0, s, dY, dy16, Z, gate, rows, parts, int(N), dZ, part);
+  hipLaunchKernelGGL(dy16 ? by_act<GradKernel>(act) : by_act<GradKernel32>(act),
+                     dim3(unsigned((N + 511) / 512 * images * parts)), dim3(256), 0, s, dY, Z, gate,
+                     rows, parts, int(N), dZ, part);
   SVDQ_TRY(check_launch("awq_res_grad"));
   if (dgate && !direct) j.add(part, dgate, N, images * parts / each, each);
   SVDQ_TRY(launch_joins(j, N, s));

@@ -65,6 +65,13 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
                                 int64_t N, int64_t images, AwqWeight w, svdq_act act, Vec gate,
                                 uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s);
 
+// At most 64 rows without dgate: dZ and dX in the product's own launches (awq_grad.hip),
+// workspace as awq_linear_grad_workspace
+bool awq_res_grad_fused(int64_t M, int64_t K, int64_t N);
+svdq_status launch_awq_res_grad_rows(const uint16_t* dY, const uint16_t* Z, int64_t M, int64_t K,
+                                     int64_t N, int64_t images, AwqWeight w, svdq_act act, Vec gate,
+                                     uint16_t* dX, uint16_t* dZ, void* ws, hipStream_t s);
+
 // Mixture of experts on AWQ weights, expert after expert (every one K N / 64 rows of 32
 // bytes of codes)
 size_t awq_moe_workspace(int64_t T, int64_t E, int64_t top, int64_t K, int64_t N);
