@@ -452,6 +452,48 @@ __global__ __launch_bounds__(svdq_gemm::NT) void grad_wide_kernel(svdq_gemm::Arg
     store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, p.rows, dX);
 }
 
+// the same with the last round of tiles split over the reduction
+__global__ __launch_bounds__(svdq_gemm::NT) void grad_split_kernel(svdq_gemm::Args p,
+                                                                   uint16_t* __restrict__ dX,
+                                                                   int64_t full, int S,
+                                                                   float* __restrict__ part) {
+  using namespace svdq_gemm;
+  __shared__ Stage st0, st1, st2, st3, st4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Work w = work_of(p, full, S);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  tile_product(p, w.m0, w.b0, st0, st1, st2, st3, st4, acc, w.first, w.count);
+  const int64_t row = (wave >> 2) * WM, col = (wave & 3) * WN;
+  float* const eb = epilogue_buffer<32 * (WN + 4)>(wave, st0, st1, st2);
+  const float none[CBL] = {0.f, 0.f};
+  if (w.split < 0)
+    store_wave_tile<RBL, CBL, true>(acc, none, eb, lane, w.m0 + row, w.b0 + col, p.M, p.rows, dX);
+  else
+    store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row, col, BM, BN, part + w.split * TILE);
+}
+
+// a workgroup takes 8 rows of a split tile, a thread 8 columns of one
+__global__ __launch_bounds__(256) void grad_join_kernel(const float* __restrict__ part, int S,
+                                                        int64_t full, int M, int K,
+                                                        uint16_t* __restrict__ dX) {
+  const int tile = blockIdx.x >> 5, row = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5);
+  const int col = (threadIdx.x & 31) * 8;
+  int64_t m0, k0;
+  svdq_gemm::tile_of(full + tile, (M + 255) / 256, (K + 255) / 256, m0, k0);
+  const int64_t m = m0 + row, k = k0 + col;
+  if (m >= M || k >= K) return;
+  const float* const p = part + int64_t(tile) * S * svdq_gemm::TILE + row * 256 + col;
+  v4f v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  for (int q = 0; q < S; ++q)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] += reinterpret_cast<const v4f*>(p + q * svdq_gemm::TILE)[i];
+  *reinterpret_cast<uint4*>(dX + m * K + k) =
+      make_uint4(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
+                 pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3]));
+}
+
 // -------------------------------------------------------- medium number of rows
 // B rows of a tile: 128 columns k of dX (two groups) over 64 n of one layer.
 // A thread takes 4 rows n and 8 k of each, and writes 8 pieces of 4 n.  The
@@ -630,6 +672,47 @@ svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int
   const Rows in{d, nullptr, nullptr, nullptr, nullptr, {}, 1};
   if (rest <= ROWS) return run_rows<PLAIN>(in, rest, K, N, &wt, x, xb, part, s);
   return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, s);
+}
+
+namespace {
+
+// the rounds of a product on M rows; S 1 where splitting the last one gains nothing
+svdq_gemm::Rounds product_rounds(int64_t M, int64_t K, int64_t N) {
+  const svdq_gemm::Rounds none{0, 0, 1};
+  if (M <= ROWS) return none;
+  const int64_t np = pad64(N);
+  const svdq_plan::Shape shape{np / 64, (K + 255) / 256, (K + 127) / 128, K * N};
+  double us;
+  svdq_plan::wide_rows(M, shape, &us);
+  const svdq_gemm::Rounds r = svdq_gemm::rounds(M, K, np / 32);
+  return r.S > 1 && svdq_plan::split_us(r, shape) < us ? r : none;
+}
+
+}  // namespace
+
+size_t awq_grad_product_workspace(int64_t M, int64_t K, int64_t N) {
+  const svdq_gemm::Rounds r = product_rounds(M, K, N);
+  return r.S == 1 ? awq_linear_grad_workspace(M, K, N)
+                  : transposed_bytes(K, N, 1) + svdq_gemm::rounds_bytes(r);
+}
+
+svdq_status launch_awq_grad_product(const uint16_t* dZ, int64_t M, int64_t K, int64_t N, AwqWeight wt,
+                                    uint16_t* dX, void* ws, hipStream_t s) {
+  const svdq_gemm::Rounds r = product_rounds(M, K, N);
+  if (r.S == 1) return launch_awq_linear_grad(dZ, M, K, N, wt, dX, SVDQ_BF16, ws, s);
+  const int64_t np = pad64(N);
+  uint16_t* const B = static_cast<uint16_t*>(ws);
+  float* const part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + transposed_bytes(K, N, 1));
+  hipLaunchKernelGGL(transpose_dequant_kernel, dim3(unsigned((np + 255) / 256 * (K / 64))), dim3(256),
+                     0, s, wt, int(N), np / 32, int64_t(0), B);
+  SVDQ_TRY(check_launch("transpose_dequant"));
+  const svdq_gemm::Args p{{dZ, dZ}, N, int(np / 64), 1, B, int(M), int(K)};
+  hipLaunchKernelGGL(grad_split_kernel, dim3(unsigned(r.full + r.left * r.S)), dim3(svdq_gemm::NT), 0,
+                     s, p, dX, r.full, r.S, part);
+  SVDQ_TRY(check_launch("grad_split"));
+  hipLaunchKernelGGL(grad_join_kernel, dim3(unsigned(r.left * 32)), dim3(256), 0, s, part, r.S, r.full,
+                     int(M), int(K), dX);
+  return check_launch("grad_join");
 }
 
 bool awq_res_grad_fused(int64_t M, int64_t K, int64_t N) {

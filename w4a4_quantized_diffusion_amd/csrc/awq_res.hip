@@ -389,6 +389,56 @@ __global__ __launch_bounds__(svdq_gemm::NT) void res_wide_kernel(svdq_gemm::Args
                               m0 + (wave >> 2) * WM, b0 + (wave & 3) * WN, p.M, p.rows);
 }
 
+template <int ACT>
+__global__ __launch_bounds__(svdq_gemm::NT) void res_split_kernel(svdq_gemm::Args p, ResEpilogue e,
+                                                                  int64_t full, int S,
+                                                                  float* __restrict__ part) {
+  using namespace svdq_gemm;
+  __shared__ Stage st0, st1, st2, st3, st4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Work w = work_of(p, full, S);
+  v16f acc[RBL][CBL];
+  zero_acc(acc);
+  tile_product(p, w.m0, w.b0, st0, st1, st2, st3, st4, acc, w.first, w.count);
+  const int64_t row = (wave >> 2) * WM, col = (wave & 3) * WN;
+  float* const eb = epilogue_buffer<32 * (WN + 4)>(wave, st0, st1, st2);
+  if (w.split < 0) {
+    res_epilogue<ACT, RBL, CBL>(e, acc, eb, lane, w.m0 + row, w.b0 + col, p.M, p.rows);
+  } else {
+    const float none[CBL] = {0.f, 0.f};
+    store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row, col, BM, BN, part + w.split * TILE);
+  }
+}
+
+// The split tiles' sums and the epilogue: a workgroup takes 8 rows of a tile, a thread 8
+// columns of one.
+template <int ACT>
+__global__ __launch_bounds__(256) void res_join_kernel(const float* __restrict__ part, int S,
+                                                       int64_t full, int M, int N, ResEpilogue e) {
+  const int tile = blockIdx.x >> 5, row = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5);
+  const int col = (threadIdx.x & 31) * 8;
+  int64_t m0, n0;
+  svdq_gemm::tile_of(full + tile, (M + 255) / 256, (N + 255) / 256, m0, n0);
+  const int64_t m = m0 + row, n = n0 + col;
+  if (m >= M || n >= N) return;
+  const float* const p = part + int64_t(tile) * S * svdq_gemm::TILE + row * 256 + col;
+  float z[8] = {};
+  for (int q = 0; q < S; ++q) {
+    const float4 a = *reinterpret_cast<const float4*>(p + q * svdq_gemm::TILE);
+    const float4 b = *reinterpret_cast<const float4*>(p + q * svdq_gemm::TILE + 4);
+    z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
+    z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+  }
+  if (e.bias) {
+    float b[8];
+    load_any<8>(e.bias, true, n, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += b[i];
+  }
+  emit<ACT, 8>(e, int(m), n, N, z);
+}
+
 // -------------------------------------------------------- medium number of rows
 // B rows of a tile: 128 rows of the weights, two threads to a row, 32 codes each.
 struct RowWeights {
@@ -459,9 +509,17 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void res_mid_kernel(svdq_mid::Args
 
 int64_t mid_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128); }
 
-int64_t wide_rows(int64_t M, int64_t K, int64_t N) {
+// the rows of the wide form, and whether its last round is split (then they are all)
+int64_t wide_rows(int64_t M, int64_t K, int64_t N, svdq_gemm::Rounds* split) {
+  split->S = 1;
   if (M <= ROWS) return 0;
-  return svdq_plan::wide_rows(M, {K / 64, (N + 255) / 256, (N + 127) / 128, K * N});
+  const svdq_plan::Shape shape{K / 64, (N + 255) / 256, (N + 127) / 128, K * N};
+  double us;
+  const int64_t w = svdq_plan::wide_rows(M, shape, &us);
+  const svdq_gemm::Rounds r = svdq_gemm::rounds(M, N, K / 32);
+  if (r.S == 1 || svdq_plan::split_us(r, shape) >= us) return w;
+  *split = r;
+  return M;
 }
 
 size_t weight_bytes(int64_t K, int64_t N) { return svdq_gemm::weight_bytes(N, K / 32); }
@@ -497,6 +555,14 @@ struct SumKernel {
 template <int ACT>
 struct MidKernel {
   static auto get() { return res_mid_kernel<ACT>; }
+};
+template <int ACT>
+struct SplitKernel {
+  static auto get() { return res_split_kernel<ACT>; }
+};
+template <int ACT>
+struct JoinKernel {
+  static auto get() { return res_join_kernel<ACT>; }
 };
 template <int ACT>
 struct WideKernel {
@@ -542,13 +608,21 @@ svdq_status mid(const Call& c, float* part) {
   return S == 1 ? SVDQ_OK : sum(c, part, S);
 }
 
-svdq_status wide(const Call& c, uint16_t* B) {
+svdq_status wide(const Call& c, uint16_t* B, const svdq_gemm::Rounds& r, float* part) {
   const int64_t quads = (c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS;
   hipLaunchKernelGGL(res_dequant_kernel, dim3(unsigned((c.N + 63) / 64 * quads)), dim3(256), 0, c.s,
                      c.w, int(c.K), int(c.N), B);
   SVDQ_TRY(svdq::check_launch("awq_res (dequant)"));
-  const int64_t tiles = (c.M + 255) / 256 * ((c.N + 255) / 256);
   svdq_gemm::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, B, int(c.M), int(c.N)};
+  if (r.S > 1) {
+    hipLaunchKernelGGL(by_act<SplitKernel>(c.act), dim3(unsigned(r.full + r.left * r.S)),
+                       dim3(svdq_gemm::NT), 0, c.s, p, c.e, r.full, r.S, part);
+    SVDQ_TRY(svdq::check_launch("awq_res (split)"));
+    hipLaunchKernelGGL(by_act<JoinKernel>(c.act), dim3(unsigned(r.left * 32)), dim3(256), 0, c.s, part,
+                       r.S, r.full, int(c.M), int(c.N), c.e);
+    return svdq::check_launch("awq_res (join)");
+  }
+  const int64_t tiles = (c.M + 255) / 256 * ((c.N + 255) / 256);
   hipLaunchKernelGGL(by_act<WideKernel>(c.act), dim3(unsigned(tiles)), dim3(svdq_gemm::NT), 0, c.s,
                      p, c.e);
   return svdq::check_launch("awq_res (wide)");
@@ -657,18 +731,21 @@ size_t grad_part_bytes(int64_t M, int64_t N, int64_t images) {
 namespace svdq {
 
 size_t awq_res_workspace(int64_t M, int64_t K, int64_t N) {
-  const int64_t w = wide_rows(M, K, N);
-  return (w ? weight_bytes(K, N) : 0) + part_bytes(M - w, K, N);
+  svdq_gemm::Rounds r;
+  const int64_t w = wide_rows(M, K, N, &r);
+  return (w ? weight_bytes(K, N) : 0) + (r.S > 1 ? rounds_bytes(r) : part_bytes(M - w, K, N));
 }
 
 svdq_status launch_awq_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, AwqWeight wt,
                            svdq_act act, const ResEpilogue& e, void* ws, hipStream_t s) {
-  const int64_t w = wide_rows(M, K, N), rest = M - w;
+  svdq_gemm::Rounds r;
+  const int64_t w = wide_rows(M, K, N, &r), rest = M - w;
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  float* const part = reinterpret_cast<float*>(w8 + (w ? weight_bytes(K, N) : 0));
   Call c{X, M, K, N, wt, act, e, s};
   if (w) {
     c.M = w;
-    SVDQ_TRY(wide(c, reinterpret_cast<uint16_t*>(w8)));
+    SVDQ_TRY(wide(c, reinterpret_cast<uint16_t*>(w8), r, part));
   }
   if (!rest) return SVDQ_OK;
   // the rows behind: every operand from row w on; `first` keeps the images' count
@@ -678,7 +755,6 @@ svdq_status launch_awq_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, A
   c.e.Y = static_cast<uint8_t*>(e.Y) + w * N * (e.y16 ? 2 : 4);
   if (e.R) c.e.R = static_cast<const uint8_t*>(e.R) + w * N * (e.r16 ? 2 : 4);
   if (e.Z) c.e.Z = e.Z + w * N;
-  float* const part = reinterpret_cast<float*>(w8 + (w ? weight_bytes(K, N) : 0));
   if (rest > ROWS) return mid(c, part);
   switch ((rest + 15) / 16) {
     case 1: return few<1>(c, part);
@@ -689,7 +765,7 @@ svdq_status launch_awq_res(const uint16_t* X, int64_t M, int64_t K, int64_t N, A
 }
 
 size_t awq_res_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t images) {
-  return grad_part_bytes(M, N, images) + awq_linear_grad_workspace(M, K, N);
+  return grad_part_bytes(M, N, images) + awq_grad_product_workspace(M, K, N);
 }
 
 svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, int64_t M, int64_t K,
@@ -715,8 +791,7 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
   SVDQ_TRY(check_launch("awq_res_grad"));
   if (dgate && !direct) j.add(part, dgate, N, images * parts / each, each);
   SVDQ_TRY(launch_joins(j, N, s));
-  return launch_awq_linear_grad(dZ, M, K, N, wt, dX, SVDQ_BF16,
-                                w8 + grad_part_bytes(M, N, images), s);
+  return launch_awq_grad_product(dZ, M, K, N, wt, dX, w8 + grad_part_bytes(M, N, images), s);
 }
 
 }  // namespace svdq

@@ -65,6 +65,12 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
                                 int64_t N, int64_t images, AwqWeight w, svdq_act act, Vec gate,
                                 uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s);
 
+// dX = dZ wd in bf16, as launch_awq_linear_grad, with a last round of tiles split where
+// that is faster (awq_grad.hip)
+size_t awq_grad_product_workspace(int64_t M, int64_t K, int64_t N);
+svdq_status launch_awq_grad_product(const uint16_t* dZ, int64_t M, int64_t K, int64_t N, AwqWeight w,
+                                    uint16_t* dX, void* ws, hipStream_t s);
+
 // At most 64 rows without dgate: dZ and dX in the product's own launches (awq_grad.hip),
 // workspace as awq_linear_grad_workspace
 bool awq_res_grad_fused(int64_t M, int64_t K, int64_t N);

@@ -97,10 +97,11 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // acc += the tile at (m0, b0), b0 a row of B.  All 512 threads call it.  The
 // stages are separate LDS objects, so that the compiler can tell the one a
-// transfer fills apart from the ones that are read.
+// transfer fills apart from the ones that are read.  `count` stages from `first` on (0:
+// all of them).
 __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t b0, Stage& st0,
                                              Stage& st1, Stage& st2, Stage& st3, Stage& st4,
-                                             v16f (&acc)[RBL][CBL]) {
+                                             v16f (&acc)[RBL][CBL], int first = 0, int count = 0) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -120,16 +121,16 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
     aoff[t] = 2 * uint32_t(min(int64_t(r), p.M - 1 - m0)) * uint32_t(p.width);
     boff[t] = 64 * uint32_t(min(int64_t(r), p.rows - 1 - b0)) + piece;
   }
-  const int seg = 2 * p.chunks, total = seg * p.segments;
+  const int seg = 2 * p.chunks, all = seg * p.segments, total = count ? count : all;
   const uint8_t* const a0 = reinterpret_cast<const uint8_t*>(p.A[0] + m0 * p.width);
   const uint8_t* const a1 = reinterpret_cast<const uint8_t*>(p.A[1] + m0 * p.width);
   const uint8_t* const bb =
-      reinterpret_cast<const uint8_t*>(p.B) + b0 / BN * total * int64_t(BLOCK_BYTES);
+      reinterpret_cast<const uint8_t*>(p.B) + b0 / BN * all * int64_t(BLOCK_BYTES);
   // transfer t of stage s: 0, 1 of A, 2, 3 of B
   const uint8_t *asrc, *bsrc;
   uint32_t apiece;
   auto dma_at = [&](int s) __attribute__((always_inline)) {
-    s = min(s, total - 1);
+    s = first + min(s, total - 1);
     const bool second = s >= seg;
     // pieces that would lie past A's width repeat its last one
     const int col = min(32 * (second ? s - seg : s), int(p.width) - 8);
@@ -220,6 +221,64 @@ __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int64_t 
   // the repeated last transfers, before the buffers are used for anything else
   __builtin_amdgcn_s_waitcnt(0x0070);
   __syncthreads();
+}
+
+// Tiles whose number is no multiple of the 256 compute units leave a last round that is
+// partly empty.  Where that is most of the chip, the last round's tiles are split over
+// the reduction as well: the first `full` workgroups take whole tiles, then S workgroups
+// take a tile of the `left` others each, into fp32 sums [left][S][256][256] that a launch
+// of its own joins.  4608 rows 4096 -> 12288 are 864 tiles, 3.4 rounds.
+struct Rounds {
+  int64_t full, left;
+  int S;                  // 1: nothing is split
+};
+
+constexpr int64_t UNITS = 256;
+constexpr int64_t TILE = int64_t(BM) * BN;
+
+inline Rounds rounds(int64_t M, int64_t rows, int64_t stages) {
+  const int64_t tiles = (M + BM - 1) / BM * ((rows + BN - 1) / BN);
+  Rounds r{tiles / UNITS * UNITS, tiles % UNITS, 1};
+  if (r.left) r.S = int(std::min<int64_t>({UNITS / r.left, 8, stages / 16}));
+  if (r.S <= 1) r = {tiles, 0, 1};
+  return r;
+}
+
+inline size_t rounds_bytes(const Rounds& r) { return size_t(r.left) * size_t(r.S) * TILE * 4; }
+
+// this workgroup's tile; of a split one also its number among them and its stages
+struct Work {
+  int64_t m0, b0;
+  int split, first, count;       // split -1: a whole tile
+};
+
+__device__ __forceinline__ void tile_of(int64_t t, int tiles_m, int tiles_n, int64_t& m0,
+                                        int64_t& b0) {
+  constexpr int GN = 8;
+  const int grp = int(t / (GN * tiles_m)), in = int(t - int64_t(grp) * (GN * tiles_m));
+  const int gn = min(GN, tiles_n - grp * GN);
+  m0 = int64_t(in / gn) * BM;
+  b0 = int64_t(grp * GN + in % gn) * BN;
+}
+
+__device__ __forceinline__ Work work_of(const Args& p, int64_t full, int S) {
+  Work w;
+  const int tm = (p.M + BM - 1) / BM, tn = (p.rows + BN - 1) / BN;
+  const int64_t t = blockIdx.x;
+  if (t < full) {
+    // a run of whole tiles for each XCD
+    tile_of((full & 7) == 0 ? (t & 7) * (full >> 3) + (t >> 3) : t, tm, tn, w.m0, w.b0);
+    w.split = -1;
+    w.first = w.count = 0;
+    return w;
+  }
+  const int i = int(t - full), slice = i % S, stages = 2 * p.chunks;
+  w.split = i / S;
+  tile_of(full + w.split, tm, tn, w.m0, w.b0);
+  w.first = int(int64_t(slice) * stages / S);
+  w.count = int(int64_t(slice + 1) * stages / S) - w.first;
+  w.split = i;
+  return w;
 }
 
 template <int R, int C>
@@ -436,8 +495,15 @@ inline double rest_us(int64_t rows, const Shape& p) {
   return rows == 0 ? 0 : rows <= 64 ? few_us(p) : mid_us(rows, p);
 }
 
+// all rows in the wide form with the last round split (gemm_bf16.h's Rounds); its join
+// writes and reads the sums
+inline double split_us(const svdq_gemm::Rounds& r, const Shape& p) {
+  return 9 + 1.72 * (double(r.full / svdq_gemm::UNITS) + 1.0 / r.S) * double(p.chunks) +
+         2.5625 * double(p.weights) / 5.2e6 + double(svdq_gemm::rounds_bytes(r)) * 2 / 4.5e6;
+}
+
 // rows of the wide form: 0, all, or whole tiles that leave the last round out
-inline int64_t wide_rows(int64_t M, const Shape& p) {
+inline int64_t wide_rows(int64_t M, const Shape& p, double* us = nullptr) {
   int64_t best = 0;
   double t = rest_us(M, p);
   auto consider = [&](int64_t m) {
@@ -447,6 +513,7 @@ inline int64_t wide_rows(int64_t M, const Shape& p) {
   consider(M);
   const int64_t whole = M / 256 * 256;
   for (int64_t i = 0; i < 32 && whole - 256 * i > 0; ++i) consider(whole - 256 * i);
+  if (us) *us = t;
   return best;
 }
 
