@@ -486,9 +486,21 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const float* __restrict_
   if (m >= M || k >= K) return;
   const float* const p = part + int64_t(tile) * S * svdq_gemm::TILE + row * 256 + col;
   v4f v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-  for (int q = 0; q < S; ++q)
+  // (two slices' loads at a time; one past the last counts as zeros)
+  for (int q = 0; q < S; q += 2) {
+    v4f u[2][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] += reinterpret_cast<const v4f*>(p + q * svdq_gemm::TILE)[i];
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        u[j][i] = reinterpret_cast<const v4f*>(p + min(q + j, S - 1) * svdq_gemm::TILE)[i];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] += q + j < S ? u[j][i][e] : 0.f;
+  }
   *reinterpret_cast<uint4*>(dX + m * K + k) =
       make_uint4(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
                  pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3]));

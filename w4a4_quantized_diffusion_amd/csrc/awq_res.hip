@@ -341,16 +341,20 @@ __global__ __launch_bounds__(NT, 4) void res_column_kernel(const uint16_t* __res
 }
 
 // ---------------------------------------------------------- many rows
-// The weights dequantized once into the workspace: 64 rows and four groups of 64 k (two
-// stages each) per workgroup, so that its loads are in flight together; four lanes take
-// one row, 8 k of each stage, so that a wave stores 1 KB in a row.
-constexpr int DEQUANT_GROUPS = 4;
+// The weights dequantized once into the workspace: 64 rows and two groups of 64 k (two
+// stages each) per workgroup; four lanes take one row, 8 k of each stage, so that a wave
+// stores 1 KB in a row.  Neighbouring workgroups go along K: a row block's stages are
+// consecutive in the workspace, while the same stage of other row blocks lies whole rows
+// of stages apart, in the same memory channels (12288 x 4096: 129 MB in 22.8 us, 5.7
+// TB/s; in the order of the rows 33).
+constexpr int DEQUANT_GROUPS = 2;
 
 __global__ __launch_bounds__(256) void res_dequant_kernel(svdq::AwqWeight w, int K, int N,
                                                           uint16_t* __restrict__ B) {
   const int row = threadIdx.x >> 2, piece = threadIdx.x & 3;
-  const int blocks = (N + 63) / 64, G = K / 64, g0 = blockIdx.x / blocks * DEQUANT_GROUPS;
-  const int64_t n = int64_t(blockIdx.x % blocks) * 64 + row;
+  const int G = K / 64, along = (G + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS;
+  const int g0 = blockIdx.x % along * DEQUANT_GROUPS;
+  const int64_t n = int64_t(blockIdx.x / along) * 64 + row;
   if (n >= N) return;
   uint32_t c[DEQUANT_GROUPS][2];
   uint16_t s[DEQUANT_GROUPS], z[DEQUANT_GROUPS];
@@ -424,11 +428,18 @@ __global__ __launch_bounds__(256) void res_join_kernel(const float* __restrict__
   if (m >= M || n >= N) return;
   const float* const p = part + int64_t(tile) * S * svdq_gemm::TILE + row * 256 + col;
   float z[8] = {};
-  for (int q = 0; q < S; ++q) {
-    const float4 a = *reinterpret_cast<const float4*>(p + q * svdq_gemm::TILE);
-    const float4 b = *reinterpret_cast<const float4*>(p + q * svdq_gemm::TILE + 4);
-    z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
-    z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+  // (two slices' loads at a time; one past the last counts as zeros)
+  for (int q = 0; q < S; q += 2) {
+    v4f v[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[k][i] = reinterpret_cast<const v4f*>(p + min(q + k, S - 1) * svdq_gemm::TILE)[i];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] += q + k < S ? v[k][i >> 2][i & 3] : 0.f;
   }
   if (e.bias) {
     float b[8];
@@ -609,8 +620,8 @@ svdq_status mid(const Call& c, float* part) {
 }
 
 svdq_status wide(const Call& c, uint16_t* B, const svdq_gemm::Rounds& r, float* part) {
-  const int64_t quads = (c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS;
-  hipLaunchKernelGGL(res_dequant_kernel, dim3(unsigned((c.N + 63) / 64 * quads)), dim3(256), 0, c.s,
+  const int64_t along = (c.K / 64 + DEQUANT_GROUPS - 1) / DEQUANT_GROUPS;
+  hipLaunchKernelGGL(res_dequant_kernel, dim3(unsigned((c.N + 63) / 64 * along)), dim3(256), 0, c.s,
                      c.w, int(c.K), int(c.N), B);
   SVDQ_TRY(svdq::check_launch("awq_res (dequant)"));
   svdq_gemm::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, B, int(c.M), int(c.N)};

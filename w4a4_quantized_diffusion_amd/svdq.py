@@ -33,6 +33,14 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _U32 = ctypes.c_uint32
+
+
+class Vec(ctypes.Structure):
+    """svdq_vec"""
+    _fields_ = [("data", _P), ("dtype", ctypes.c_int), ("ld", _I64)]
+
+
+_V = ctypes.POINTER(Vec)               # (takes a Vec, or None)
 _SIG = {
     "svdq_last_error": (ctypes.c_char_p, []),
     "svdq_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32, ctypes.c_int]),
@@ -92,7 +100,7 @@ _SIG = {
     # X, x_dtype, H, h_dtype, M, D, images, kind, eps, post, gate, weight, scale,
     # shift, X_out, Y, y_dtype, stream
     "svdq_block_norm": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int, _I64, _I64, _I64,
-                                        ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P,
+                                        ctypes.c_int, ctypes.c_float, _V, _V, _V, _V, _V, _P, _P,
                                         ctypes.c_int, _P]),
     "svdq_block_norm_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     # dY, y_dtype, dX_out, X, x_dtype, H, h_dtype, M, D, images, kind, eps, post, gate,
@@ -100,19 +108,19 @@ _SIG = {
     # workspace_bytes, stream
     "svdq_block_norm_grad": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int, _P,
                                              ctypes.c_int, _I64, _I64, _I64, ctypes.c_int,
-                                             ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                             ctypes.c_float, _V, _V, _V, _V, _V, _P, _P, _P, _P,
                                              _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "awq_linear_w4a16_res_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     # X, M, K, N, group, q, scales, zeros, bias, act, gate, images, R, r_dtype, Y,
     # y_dtype, Z_out, workspace, workspace_bytes, stream
     "awq_linear_w4a16_res": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P,
-                                             ctypes.c_int, _P, _I64, _P, ctypes.c_int, _P,
+                                             ctypes.c_int, _V, _I64, _P, ctypes.c_int, _P,
                                              ctypes.c_int, _P, _P, ctypes.c_size_t, _P]),
     "awq_linear_w4a16_res_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     # dY, dy_dtype, Z, M, K, N, group, q, scales, zeros, act, gate, images, dX, dZ,
     # dgate, workspace, workspace_bytes, stream
     "awq_linear_w4a16_res_grad": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I64, _I64, _I32, _P,
-                                                  _P, _P, ctypes.c_int, _P, _I64, _P, _P, _P, _P,
+                                                  _P, _P, ctypes.c_int, _V, _I64, _P, _P, _P, _P,
                                                   ctypes.c_size_t, _P]),
     "awq_moe_w4a16_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32, _I64, _I64]),
     # X, logits, logits_dtype, T, E, top, K, N, group, gate q / scales / zeros, up,
@@ -405,6 +413,8 @@ def _raw_stream(dev):
 
 # the same handle without building a Stream object, where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+# (the binding is reached with a device tensor only, so the device is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _arg(t, name, shape, dtype, dev):
@@ -452,7 +462,7 @@ def _ws(workspace, need, X, dev):
 
 def _run(dev, fn, *args):
     """Call fn(*args, stream) on device `dev` and its current stream."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -584,50 +594,68 @@ def awq_linear_w4a16_grad(dY, layer, dx_dtype=torch.bfloat16, workspace=None, dX
 
 # ------------------------------------------------- norms around a block
 
-class Vec(ctypes.Structure):
-    """svdq_vec"""
-    _fields_ = [("data", _P), ("dtype", ctypes.c_int), ("ld", _I64)]
-
-
 _VECTORS = ("post", "gate", "weight", "scale", "shift")
 
 
-def _vecs(vectors, M, D, dev, names=_VECTORS):
-    """(images, [svdq_vec or None]) of a call's vectors: [D], or [images, D] with the
+def _vec(v, name, M, D, dev, images):
+    """(images of the call so far, svdq_vec) of one vector: [D], or [images, D] with the
     rows at any distance."""
+    dt = _DT.get(v.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {v.dtype}")
+    if v.get_device() != dev:
+        raise ValueError(f"{name} is on {v.device}, expected cuda:{dev}")
+    shape, stride = v.shape, v.stride()
+    if not 1 <= len(shape) <= 2 or shape[-1] != D or shape[0] == 0:
+        raise ValueError(f"{name} must have shape [{D}] or [images, {D}], got {tuple(shape)}")
+    if D > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the values of a row must be adjacent")
+    ld = 0
+    if len(shape) == 2 and shape[0] > 1:
+        n, ld = shape[0], stride[0]
+        if images != 1 and n != images:
+            raise ValueError(f"{name} has {n} rows, another vector {images}")
+        if M % n:
+            raise ValueError(f"{name} has {n} rows, which do not divide the {M} rows of x")
+        if ld < D:
+            raise ValueError(f"{name}: its rows overlap")
+        images = n
+    return images, Vec(v.data_ptr(), dt, ld)
+
+
+def _vecs(vectors, M, D, dev, names=_VECTORS):
+    """(images, [svdq_vec or None]) of a call's vectors."""
     images, out = 1, []
     for name, v in zip(names, vectors):
-        if v is None:
-            out.append(None)
-            continue
-        if v.dtype not in _DT:
-            raise TypeError(f"{name} must be float32 or bfloat16, got {v.dtype}")
-        if v.get_device() != dev:
-            raise ValueError(f"{name} is on {v.device}, expected cuda:{dev}")
-        shape = v.shape
-        if not 1 <= len(shape) <= 2 or shape[-1] != D or shape[0] == 0:
-            raise ValueError(f"{name} must have shape [{D}] or [images, {D}], got {tuple(shape)}")
-        if D > 1 and v.stride(-1) != 1:
-            raise ValueError(f"{name}: the values of a row must be adjacent")
-        ld = 0
-        if len(shape) == 2 and shape[0] > 1:
-            n = shape[0]
-            if images != 1 and n != images:
-                raise ValueError(f"{name} has {n} rows, another vector {images}")
-            if M % n:
-                raise ValueError(f"{name} has {n} rows, which do not divide the {M} rows of x")
-            images, ld = n, v.stride(0)
-            if ld < D:
-                raise ValueError(f"{name}: its rows overlap")
-        out.append(Vec(v.data_ptr(), _DT[v.dtype], ld))
+        if v is not None:
+            images, v = _vec(v, name, M, D, dev, images)
+        out.append(v)
     return images, out
 
 
-def _matrix(t, name, like, dev):
-    """A float32 or bfloat16 operand [M, D] -> (address, dtype)."""
-    if t.dtype not in _DT:
+def _matrix(t, name, shape, dev):
+    """A float32 or bfloat16 operand -> (address, dtype)."""
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return _arg(t, name, like, t.dtype, dev), _DT[t.dtype]
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), dt
+
+
+def _norm_rows(x):
+    """(M, D, device index, address, dtype) of a norm's first operand."""
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must have shape [M, D], got {tuple(shape)}")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x: expected a device tensor")
+    return (*shape, dev, *_matrix(x, "x", shape, dev))
 
 
 def svdq_block_norm(x, h=None, kind="layer", eps=1e-6, post=None, gate=None, weight=None,
@@ -638,24 +666,27 @@ def svdq_block_norm(x, h=None, kind="layer", eps=1e-6, post=None, gate=None, wei
     [images, D] (one row for every M / images rows of x, at any row distance).
     Returns (x', y), x' in x's type, or y alone without h."""
     l = lib()
-    if x.dim() != 2:
-        raise ValueError(f"x must have shape [M, D], got {tuple(x.shape)}")
-    M, dev = _rows(x, "x", x.shape[1])
-    D = x.shape[1]
-    xp, xt = _matrix(x, "x", x.shape, dev)
+    M, D, dev, xp, xt = _norm_rows(x)
+    shape = x.shape
     images, v = _vecs((post, gate, weight, scale, shift), M, D, dev)
     hp = op = None
     ht = F32
     if h is not None:
-        hp, ht = _matrix(h, "h", (M, D), dev)
-        X_out = _out(X_out, "X_out", (M, D), x.dtype, x, dev)
+        hp, ht = _matrix(h, "h", shape, dev)
+        if X_out is None:
+            X_out = torch.empty_like(x)
+        else:
+            _arg(X_out, "X_out", shape, x.dtype, dev)
         op = X_out.data_ptr()
     elif X_out is not None:
         raise ValueError("X_out goes with h")
     yt = _out_dtype(Y, y_dtype, "Y")
-    Y = _out(Y, "Y", (M, D), yt, x, dev)
-    _run(dev, l.svdq_block_norm, xp, xt, hp, ht, M, D, images, _NORM[kind], eps,
-         *(e and ctypes.byref(e) for e in v), op, Y.data_ptr(), _DT[yt])
+    if Y is None and yt is x.dtype:
+        Y = torch.empty_like(x)
+    else:
+        Y = _out(Y, "Y", shape, yt, x, dev)
+    _run(dev, l.svdq_block_norm, xp, xt, hp, ht, M, D, images, _NORM[kind], eps, *v, op, Y.data_ptr(),
+         _DT[yt])
     return Y if h is None else (X_out, Y)
 
 
@@ -672,28 +703,24 @@ def svdq_block_norm_grad(dy, x, h=None, dx_out=None, kind="layer", eps=1e-6, pos
     vectors' shapes; None where there is no input, or `need` (of the five vectors)
     says no."""
     l = lib()
-    if x.dim() != 2:
-        raise ValueError(f"x must have shape [M, D], got {tuple(x.shape)}")
-    M, dev = _rows(x, "x", x.shape[1])
-    D = x.shape[1]
-    xp, xt = _matrix(x, "x", x.shape, dev)
-    dyp, dyt = _matrix(dy, "dy", (M, D), dev)
+    M, D, dev, xp, xt = _norm_rows(x)
+    shape = x.shape
+    dyp, dyt = _matrix(dy, "dy", shape, dev)
     vectors = (post, gate, weight, scale, shift)
     images, v = _vecs(vectors, M, D, dev)
     hp = dhp = dh = None
     ht = F32
     if h is not None:
-        hp, ht = _matrix(h, "h", (M, D), dev)
+        hp, ht = _matrix(h, "h", shape, dev)
         dh = torch.empty_like(h)
         dhp = dh.data_ptr()
-    dop = None if dx_out is None else _arg(dx_out, "dx_out", (M, D), x.dtype, dev)
+    dop = None if dx_out is None else _arg(dx_out, "dx_out", shape, x.dtype, dev)
     dx = torch.empty_like(x)
     grads = [x.new_empty(t.shape, dtype=torch.float32) if t is not None and n else None
              for t, n in zip(vectors, need)]
     keep, ws, nws = _ws(workspace, l.svdq_block_norm_grad_workspace_bytes(M, D, images), x, dev)
     _run(dev, l.svdq_block_norm_grad, dyp, dyt, dop, xp, xt, hp, ht, M, D, images, _NORM[kind], eps,
-         *(e and ctypes.byref(e) for e in v), dx.data_ptr(), dhp,
-         *(None if t is None else t.data_ptr() for t in grads), ws, nws)
+         *v, dx.data_ptr(), dhp, *[None if t is None else t.data_ptr() for t in grads], ws, nws)
     return (dx, dh, *grads)
 
 
@@ -722,7 +749,7 @@ def awq_linear_w4a16_res(X, layer, bias=None, act="none", gate=None, residual=No
     b = None if bias is None else _arg(bias, "bias", (N,), torch.bfloat16, dev)
     keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_res_workspace_bytes(M, K, N), X, dev)
     _run(dev, l.awq_linear_w4a16_res, x, M, K, N, layer["group"], *_awq_args(layer, K, N, dev), b,
-         _ACT_OR_NONE[act], g and ctypes.byref(g), images, r, rt, Y.data_ptr(), _DT[yt],
+         _ACT_OR_NONE[act], g, images, r, rt, Y.data_ptr(), _DT[yt],
          Z.data_ptr() if save else None, ws, nws)
     return (Y, Z) if save else Y
 
@@ -751,7 +778,7 @@ def awq_linear_w4a16_res_grad(dY, Z, layer, act="none", gate=None, workspace=Non
     keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_res_grad_workspace_bytes(M, K, N, images), dY,
                         dev)
     _run(dev, l.awq_linear_w4a16_res_grad, d, dt, z, M, K, N, layer["group"],
-         *_awq_args(layer, K, N, dev), _ACT_OR_NONE[act], g and ctypes.byref(g), images,
+         *_awq_args(layer, K, N, dev), _ACT_OR_NONE[act], g, images,
          dX.data_ptr(), dZ.data_ptr(), None if dgate is None else dgate.data_ptr(), ws, nws)
     return dX, dZ, dgate
 
