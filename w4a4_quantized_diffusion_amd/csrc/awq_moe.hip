@@ -640,15 +640,20 @@ struct Plan {
   int S;
 };
 
-Plan plan(int64_t T, int64_t E, int64_t top, int64_t K, int64_t N) {
+// Measured, us.  16 rows at a time against 32 (tokens an expert): 64 tokens, 64 experts, 8
+// each, 2048 x 768 (8) 61 / 67; 61 tokens, 40, 6, 4096 x 1408 (9) 116 / 125; 64 tokens, 16,
+// 4, 4096 x 1024 (16) 64 / 53; 64 tokens, 8, 2, 4096 x 2048 (16) 65 / 53.
+// 16 columns of the down-projection a workgroup against 32 with slices: one token, 4 of 32
+// experts, 2048 x 1024 15.1 / 18.0 (the third launch), 2 of 8, 8192 x 2048 29.6 / 28.4 (K
+// of 8192 needs no slices); 8 tokens, 2 of 8, 1024 x 512 14.4 / 13.5; 16 tokens, 8 of 64,
+// 2048 x 768 64 / 51; 64 tokens, 8 of 256, 2048 x 256 89 / 76.
+Plan plan(int64_t T, int64_t E, int64_t top, int64_t K) {
   Plan p{};
-  // 32 rows at a time where that many tokens go to an expert
-  p.two_rows = T * top > 16 * E;
+  p.two_rows = T * top > 12 * E;
+  p.two_columns = T > 1 || K >= 8192;
   p.S = 1;
-  if (std::min(E, T * top) * N >= 16384) {
-    p.two_columns = true;
+  if (p.two_columns)
     while (p.S < MAX_SLICES && p.S * (K / 32) < 256) p.S *= 2;
-  }
   return p;
 }
 
@@ -660,7 +665,7 @@ size_t h_bytes(int64_t T, int64_t top, int64_t N) {
 namespace svdq {
 
 size_t awq_moe_workspace(int64_t T, int64_t E, int64_t top, int64_t K, int64_t N) {
-  const Plan p = plan(T, E, top, K, N);
+  const Plan p = plan(T, E, top, K);
   return align256(sizeof(Route)) + h_bytes(T, top, N) +
          (p.S == 1 ? 0 : align256(size_t(p.S) * size_t(T) * size_t(K) * 4));
 }
@@ -670,7 +675,7 @@ svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int6
                            AwqWeight down, svdq_act act, bool renorm, uint16_t* Y, int32_t* ids,
                            float* weights, void* ws, hipStream_t s) {
   const int64_t rows = K * N / 64;
-  const Plan p = plan(T, E, top, K, N);
+  const Plan p = plan(T, E, top, K);
   uint8_t* const h = static_cast<uint8_t*>(ws) + align256(sizeof(Route));
   float* const part = reinterpret_cast<float*>(h + h_bytes(T, top, N));
   const Moe a{X, logits, l16, renorm, int(T), int(E), int(top), int(K), int(N),

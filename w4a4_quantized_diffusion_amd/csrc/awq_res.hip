@@ -146,9 +146,14 @@ Split split(int64_t M, int64_t K, int64_t N) {
   return p;
 }
 
-// every 16 columns read all of X in one launch: N / 16 times 2 M K bytes from the L2
+// Whether few rows take one launch, where every 16 columns read all of X from the L2 (2 M
+// K N / 16 bytes) and a wave's rows of X grow with M K.  Measured, one launch against two,
+// us: 2048 -> 2048 1 row 3.8 / 6.1, 48 rows 8.4 / 8.9, 64 rows 10.3 / 9.8; 4096 -> 4096 24
+// rows 9.7 / 10.4, 33 rows 15.2 / 11.2; 2048 -> 8192 24 rows 9.8 / 10.5, 33 rows 12.5 /
+// 11.9; 8192 -> 2048 8 rows 9.2 / 10.2, 16 rows 11.9 / 10.8; 4096 -> 12288 8 rows 12.4 /
+// 13.9, 16 rows 16.3 / 14.6, 64 rows 48 / 23.5; 12288 -> 4096 8 rows 12.4 / 12.9.
 bool one_launch(int64_t M, int64_t K, int64_t N) {
-  return M * N <= (int64_t(1) << 30) / K && !(M > 16 && K >= 4096 && N <= 1024);
+  return M * K <= 3 << 15 && M * K <= (27 << 24) / N;
 }
 
 // One chunk of 64 k of 16 rows of the weights: lane group j holds the codes

@@ -369,10 +369,16 @@ __device__ __forceinline__ void vector(const Vec& v, const Cut<V, C, TAIL>& cut,
   }
 }
 
-template <int V, int C, int TAIL, int T, bool LAYER, bool POST_NORM>
-__global__ __launch_bounds__(512, C == 1 ? 4 : 2) void block_norm_grad_kernel(svdq::BlockNorm a,
-                                                               svdq::BlockNormGrad g) {
+//
+// LONG: rows of more than 8192, in 1024 threads, where 128 registers a thread do not hold
+// the two factors too: they lie in LDS (2304 rows of 12288, everything in use: X us; with
+// all in registers, spilled, 426, and in 512 threads of four pieces 714).
+
+template <int V, int C, int TAIL, int T, bool LAYER, bool POST_NORM, bool LONG>
+__global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void block_norm_grad_kernel(
+    svdq::BlockNorm a, svdq::BlockNormGrad g) {
   __shared__ __align__(16) float lds[2][2][MAX_WAVES];
+  extern __shared__ __align__(16) float factors[];   // LONG: [2][C][threads][V]
   Sums sum(lds);
   const int D = int(a.D);
   const int64_t image = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
@@ -381,82 +387,127 @@ __global__ __launch_bounds__(512, C == 1 ? 4 : 2) void block_norm_grad_kernel(sv
   const float inv = 1.f / float(D);
   const Cut<V, C, TAIL> cut(D);
   // B's factor and the norm's: gate post, weight (1 + scale)
-  Row<V, C> gp, wm, accA, accB, accS;
+  constexpr int GP = 0, WM = 1;
+  Row<V, C> held[LONG ? 1 : 2], accA, accB, accS;
+  auto place = [&](int which, int c) __attribute__((always_inline)) {
+    return reinterpret_cast<float4*>(factors + ((which * C + c) * int(blockDim.x) + int(threadIdx.x)) * V);
+  };
+  auto factor = [&](int which, int c, float (&f)[V]) __attribute__((always_inline)) {
+    if constexpr (LONG) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 v = place(which, c)[i / 4];
+        f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = held[which].v[c][i];
+    }
+  };
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     float u[V], v[V];
+    auto keep = [&](int which) __attribute__((always_inline)) {
+      if constexpr (LONG) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) place(which, c)[i / 4] = make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) held[which].v[c][i] = u[i];
+      }
+    };
     vector(a.gate, cut, image, c, 1.f, u);
     vector(a.post, cut, image, c, 1.f, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) gp.v[c][i] = u[i] * v[i];
+    for (int i = 0; i < V; ++i) u[i] *= v[i];
+    keep(GP);
     vector(a.weight, cut, image, c, 1.f, u);
     vector(a.scale, cut, image, c, 0.f, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      wm.v[c][i] = u[i] * (1.f + v[i]);
+      u[i] *= 1.f + v[i];
       accA.v[c][i] = accB.v[c][i] = accS.v[c][i] = 0.f;
     }
+    keep(WM);
   }
   const bool x16 = type16<T>(X16, a.x16), h16 = type16<T>(H16, a.h16), y16 = type16<T>(Y16, g.y16);
   Raw<V> xr[C], hr[C], dyr[C], dxr[C];
-  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+  // the row's loads, and what they bring: elements past D are zeros
+  auto fetch_in = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       load(xr[c], cut, c, a.X, x16, row * D);
       if (a.H) load(hr[c], cut, c, a.H, h16, row * D);
-      load(dyr[c], cut, c, g.dY, y16, row * D);
-      if (g.dX_out) load(dxr[c], cut, c, g.dX_out, x16, row * D);
     }
   };
-  // (with four pieces a thread the registers do not hold two rows)
-  constexpr bool AHEAD = C <= 2;
-  if (AHEAD) fetch(r0);
-  for (int64_t row = r0; row < r1; ++row) {
-    if (!AHEAD) fetch(row);
-    Row<V, C> t, n, dy, d;
+  auto fetch_dy = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) load(dyr[c], cut, c, g.dY, y16, row * D);
+  };
+  auto fetch_dx = [&](int64_t row) __attribute__((always_inline)) {
+    if (g.dX_out)
+#pragma unroll
+      for (int c = 0; c < C; ++c) load(dxr[c], cut, c, g.dX_out, x16, row * D);
+  };
+  auto take = [&](Row<V, C>& v, const Raw<V> (&raw)[C], bool given, bool b16)
+      __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      value(xr[c], x16, n.v[c]);
-      value(dyr[c], y16, dy.v[c]);
-      if (a.H)
-        value(hr[c], h16, t.v[c]);
+      if (given)
+        value(raw[c], b16, v.v[c]);
       else
 #pragma unroll
-        for (int i = 0; i < V; ++i) t.v[c][i] = 0.f;
-      if (g.dX_out)
-        value(dxr[c], x16, d.v[c]);
-      else
+        for (int i = 0; i < V; ++i) v.v[c][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) d.v[c][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const bool in = cut.in(c, i);
-        t.v[c][i] = in ? t.v[c][i] : 0.f;
-        n.v[c][i] = in ? n.v[c][i] : 0.f;
-        dy.v[c][i] = in ? dy.v[c][i] : 0.f;
-        d.v[c][i] = in ? d.v[c][i] : 0.f;
-      }
+      for (int i = 0; i < V; ++i) v.v[c][i] = cut.in(c, i) ? v.v[c][i] : 0.f;
     }
-    if (AHEAD) fetch(min(row + 1, r1 - 1));
+  };
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    fetch_in(row);
+    fetch_dy(row);
+    fetch_dx(row);
+  };
+  // (a long row's gradients come when they are needed, and nothing of the next one)
+  if (!LONG) fetch(r0);
+  for (int64_t row = r0; row < r1; ++row) {
+    Row<V, C> t, n, dy, d;
+    if (LONG) fetch_in(row);
+    take(n, xr, true, x16);
+    take(t, hr, a.H != nullptr, h16);
+    if (!LONG) {
+      take(dy, dyr, true, y16);
+      take(d, dxr, g.dX_out != nullptr, x16);
+      fetch(min(row + 1, r1 - 1));
+    }
     float rh = 1.f;
     if (POST_NORM) rh = normalize(t, cut, LAYER, D, a.eps, sum);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float f[V];
+      factor(GP, c, f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) n.v[c][i] = fmaf(gp.v[c][i], t.v[c][i], n.v[c][i]);
+      for (int i = 0; i < V; ++i) n.v[c][i] = fmaf(f[i], t.v[c][i], n.v[c][i]);
+    }
+    if (LONG) fetch_dy(row);
     const float r = normalize(n, cut, LAYER, D, a.eps, sum);
+    if (LONG) take(dy, dyr, true, y16);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float f[V];
+      factor(WM, c, f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         accS.v[c][i] += dy.v[c][i];
         accA.v[c][i] = fmaf(dy.v[c][i], n.v[c][i], accA.v[c][i]);
-        dy.v[c][i] *= wm.v[c][i];
+        dy.v[c][i] *= f[i];
         s1 += dy.v[c][i];
         s2 = fmaf(dy.v[c][i], n.v[c][i], s2);
       }
+    }
+    if (LONG) fetch_dx(row);
     sum(s1, s2);
+    if (LONG) take(d, dxr, g.dX_out != nullptr, x16);
     const float m1 = LAYER ? s1 * inv : 0.f, m2 = s2 * inv;
     s1 = s2 = 0.f;
 #pragma unroll
@@ -468,9 +519,11 @@ __global__ __launch_bounds__(512, C == 1 ? 4 : 2) void block_norm_grad_kernel(sv
         accB.v[c][i] = fmaf(d.v[c][i], t.v[c][i], accB.v[c][i]);
       }
       store(cut, c, g.dX, x16, row * D, d.v[c]);
+      float f[V];
+      factor(GP, c, f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        d.v[c][i] *= gp.v[c][i];
+        d.v[c][i] *= f[i];
         s1 += d.v[c][i];
         s2 = fmaf(d.v[c][i], t.v[c][i], s2);
       }
@@ -570,15 +623,18 @@ auto norm_of(int C, int types) {
                               : block_norm_kernel<V, 1, TAIL, ANY>;
 }
 
-template <int C, int TAIL, int T>
+template <int C, int TAIL, int T, bool LONG = false>
 auto grad_of(bool layer, bool post) {
-  return layer ? post ? block_norm_grad_kernel<V, C, TAIL, T, true, true>
-                      : block_norm_grad_kernel<V, C, TAIL, T, true, false>
-         : post ? block_norm_grad_kernel<V, C, TAIL, T, false, true>
-                : block_norm_grad_kernel<V, C, TAIL, T, false, false>;
+  return layer ? post ? block_norm_grad_kernel<V, C, TAIL, T, true, true, LONG>
+                      : block_norm_grad_kernel<V, C, TAIL, T, true, false, LONG>
+         : post ? block_norm_grad_kernel<V, C, TAIL, T, false, true, LONG>
+                : block_norm_grad_kernel<V, C, TAIL, T, false, false, LONG>;
 }
 auto grad_of(const Shape& p, int types, bool layer, bool post) {
-  if (p.C == 4) return grad_of<4, MOVED, ANY>(layer, post);
+  if (p.NT > GRAD_THREADS)
+    return p.tail != FULL                ? grad_of<2, MOVED, ANY, true>(layer, post)
+           : types == (X16 | H16 | Y16) ? grad_of<2, FULL, X16 | H16 | Y16, true>(layer, post)
+                                         : grad_of<2, FULL, ANY, true>(layer, post);
   if (p.C == 2)
     return p.tail == FULL ? grad_of<2, FULL, ANY>(layer, post) : grad_of<2, MOVED, ANY>(layer, post);
   if (p.tail == TINY) return grad_of<1, TINY, ANY>(layer, post);
@@ -598,7 +654,8 @@ int types_of(const svdq::BlockNorm& a, bool y16) {
   return (a.x16 ? X16 : 0) | (h16 ? H16 : 0) | (y16 ? Y16 : 0);
 }
 
-Shape grad_shape(int64_t D) { return shape(D, GRAD_THREADS); }
+// (two pieces a thread of 512 threads, beyond that two of up to 1024)
+Shape grad_shape(int64_t D) { return shape(D, D > 2 * GRAD_THREADS * V ? 1024 : GRAD_THREADS); }
 
 // Workgroups an image: 16 waves to a compute unit in all
 int64_t grad_parts(int64_t M, int64_t D, int64_t images) {
@@ -657,7 +714,14 @@ svdq_status launch_block_norm_grad(const BlockNorm& a, BlockNormGrad g, int64_t 
   if (M) {
     const Shape p = grad_shape(a.D);
     auto k = grad_of(p, types_of(a, g.y16), a.layer, a.post.p != nullptr);
-    hipLaunchKernelGGL(k, dim3(unsigned(images * g.parts)), dim3(p.NT), 0, s, a, g);
+    // (the most that any D asks for: the attribute is the function's, and a host thread
+    // with a smaller one must not lower it between another's two steps)
+    const size_t lds = p.NT > GRAD_THREADS ? size_t(2) * p.C * p.NT * V * 4 : 0;
+    if (lds)
+      SVDQ_CHECK_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                         hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         2 * 2 * 1024 * V * 4));
+    hipLaunchKernelGGL(k, dim3(unsigned(images * g.parts)), dim3(p.NT), lds, s, a, g);
     SVDQ_TRY(check_launch("block_norm_grad"));
   }
   return launch_joins(j, a.D, s);
