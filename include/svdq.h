@@ -479,8 +479,9 @@ svdq_status awq_linear_w4a16_res_grad(const void* dY, svdq_dtype dy_dtype, const
  * awq_quantize_weights writes them, one behind the other; of down: E layers [K, N].
  * ids int32 [T, top] and weights f32 [T, top] receive e_j and p_j (NULL: not wanted).
  * A logit of -infinity keeps an expert out as long as others are left (its p is 0); a
- * token whose logits are all -infinity has p = 0, and a NaN counts as the largest
- * logit and makes its token's p and Y NaN.  An infinity or NaN in X stays in its token.
+ * token whose logits are all -infinity has p = 0; a NaN counts as the largest logit, and
+ * it or +infinity makes its token's p and Y NaN.  An infinity or NaN in X stays in its
+ * token.
  * 0 <= T <= 64, E <= 256, 1 <= top <= min(E, 16) (more: SVDQ_ERR_UNSUPPORTED),
  * K % 64 == 0, N % 64 == 0, group == 64.  Workspace as for the weight-only operators. */
 size_t awq_moe_w4a16_workspace_bytes(int64_t T, int64_t E, int32_t top, int64_t K, int64_t N);

@@ -371,3 +371,41 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         for a, b in zip(want, held):
             assert torch.equal(a, b), i
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^31 elements: the last rows as in a small call."""
+    m, d = 270000, 8192
+    x, h = (torch.empty((m, d), dtype=BF, device="cuda").normal_() for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    scale = draw(g, (2, d), BF, 0.3)
+    xo, y = svdq.svdq_block_norm(x, h, "rms", scale=scale)
+    a, b = svdq.svdq_block_norm(x[-5:], h[-5:], "rms", scale=scale[1])
+    assert torch.equal(xo[-5:], a) and torch.equal(y[-5:], b)
+    a, b = svdq.svdq_block_norm(x[:5], h[:5], "rms", scale=scale[0])
+    assert torch.equal(xo[:5], a) and torch.equal(y[:5], b)
+    del xo
+    dx, dh, _, _, _, dscale, _ = svdq.svdq_block_norm_grad(y, x, h, h, "rms", scale=scale)
+    small = svdq.svdq_block_norm_grad(y[-5:].contiguous(), x[-5:], h[-5:], h[-5:], "rms",
+                                      scale=scale[1])
+    assert torch.equal(dx[-5:], small[0]) and torch.equal(dh[-5:], small[1])
+    assert torch.isfinite(dscale).all()
+
+
+def test_gradient_without_the_stream_s():
+    """dx_out None with h counts as zeros."""
+    p = problem(7, 264, "layer")
+    p["dx_out"] = torch.zeros_like(p["x"])
+    want = call_grad(p)
+    p["dx_out"] = None
+    for a, b in zip(want, call_grad(p)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [4100, 5120, 9000, 12288, 16384])
+def test_long_rows_of_every_type(d):
+    """Two pieces a thread and factors in LDS, whole and with a moved last piece."""
+    for xt, ht, yt in ((BF, BF, BF), (F32, BF, F32), (F32, F32, BF)):
+        p = problem(6, d, "layer" if xt is BF else "rms", 2, xt, ht, yt, F32)
+        check_forward(p)
+        check_grad(p)

@@ -152,6 +152,33 @@ def test_large_logits():
     check_all(p, renorm=False)
 
 
+def test_infinite_logits():
+    """+infinity is a tie for the first place or alone there, and makes its token NaN as
+    the softmax does; the other tokens are not touched."""
+    p = problem(5, 10, 3, 128, 64)
+    clean, _, cw = call(p, routing=True)
+    p["logits"][1, 4] = float("inf")
+    p["logits"][3, [2, 6]] = float("inf")
+    for renorm in (True, False):
+        y, ids, w = call(p, renorm=renorm, routing=True)
+        assert ids[1, 0] == 4 and ids[3, :2].tolist() == [2, 6]
+        assert torch.isnan(w[1]).any() and torch.isnan(y[1]).all() and torch.isnan(y[3]).all()
+        if renorm:
+            for r in (0, 2, 4):
+                assert torch.equal(y[r], clean[r]) and torch.equal(w[r], cw[r])
+
+
+def test_weights_past_32_bits():
+    """Experts whose codes lie more than 2^32 bytes behind the first one's."""
+    e, k, n = 130, 4096, 16384
+    p = problem(3, e, 2, k, n)
+    p["logits"] -= 100
+    p["logits"][0, [129, 3]] = 1.0
+    p["logits"][1, [128, 127]] = 2.0
+    p["logits"][2, [0, 129]] = torch.tensor([3.0, 1.0], device="cuda")
+    check_all(p)
+
+
 def test_masked_tokens():
     """A token without an expert has weights of zero and a row of zeros; a NaN stays in
     its token."""

@@ -289,3 +289,68 @@ def test_stream_graph_and_same_bits(m):
         torch.cuda.synchronize()
         for a, b in zip(want, held):
             assert torch.equal(a, b), i
+
+
+def split_bytes(m, rows, stages, weights):
+    """The workspace of a product whose last round of 256 x 256 tiles is split over the
+    reduction: the dequantized weights and S fp32 tiles for each left over."""
+    left = -(-m // 256) * -(-rows // 256) % 256
+    return weights + left * min(256 // left, 8, stages // 16) * 256 * 256 * 4
+
+
+# no whole round before the split tiles, and three; ragged edges in both directions
+@pytest.mark.parametrize("m,k,n,images", [(1467, 8192, 4112, 3), (4599, 4096, 12304, 9)])
+def test_split_rounds(m, k, n, images):
+    weights = -(-n // 256) * (k // 32) * 16384
+    assert svdq.awq_linear_w4a16_res_workspace_bytes(m, k, n) == split_bytes(m, n, k // 32, weights)
+    check_forward(problem(m, k, n, images, gate=F32), "silu")
+    check_forward(problem(m, k, n, gate=None, res=F32, bias=False), "none", F32, save=False)
+
+
+@pytest.mark.parametrize("m,k,n,images", [(2310, 2048, 4112, 2), (1200, 4096, 12304, 3),
+                                          (4608, 1024, 4096, 2)])
+def test_grad_split_rounds(m, k, n, images):
+    pad = -(-n // 64) * 64
+    weights = -(-k // 256) * (pad // 32) * 16384
+    both = svdq.awq_linear_w4a16_res_grad_workspace_bytes(m, k, n, images)
+    assert both > split_bytes(m, k, pad // 32, weights)
+    assert both < split_bytes(m, k, pad // 32, weights) + (64 << 20)
+    check_grad(m, k, n, images, "gelu")
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("m,images", [(1, 1), (20, 4), (64, 2)])
+def test_grad_of_few_rows_with_and_without_dgate(act, m, images):
+    """Without dgate dZ is formed in the product's launch: the same bits."""
+    for gate in (BF, F32):
+        p = problem(m, 512, 1040, images, gate=gate)
+        dy, z = bf((m, 1040), 3), bf((m, 1040), 4, 1.5)
+        full = svdq.awq_linear_w4a16_res_grad(dy, z, p["w"][0], act, p["gate"])
+        some = svdq.awq_linear_w4a16_res_grad(dy, z, p["w"][0], act, p["gate"], need_dgate=False)
+        assert torch.equal(full[0], some[0]) and torch.equal(full[1], some[1]) and some[2] is None
+
+
+def test_offsets_past_32_bits():
+    """Y, R and Z of more than 2^31 elements; the gate of the last image."""
+    m, k, n = 140000, 64, 16384
+    lay, w = awq_layer(n, k, 3)
+    x = bf((m, k), 1)
+    r = torch.empty((m, n), dtype=BF, device="cuda").normal_()
+    gate = bf((2, n), 2)
+    y, z = svdq.awq_linear_w4a16_res(x, lay, act="silu", gate=gate, residual=r, save=True)
+    at = torch.tensor([0, 69999, 70000, 131071, 131072, m - 1], device="cuda")
+    ref = x[at].double() @ w.t()
+    tol = k * U * (x[at].double().abs() @ w.abs().t())
+    check(z[at], ref, tol + half_step(ref, BF), "Z")
+    g = gate[(at >= 70000).long()].double()
+    a = act64(ref, "silu")[0] * g
+    out = a + r[at].double()
+    check(y[at], out, (1.13 * tol + 16 * U * ref.abs()) * g.abs() + 4 * U * (a.abs() + out.abs())
+          + half_step(out, BF), "Y")
+    dx, dz, dgate = svdq.awq_linear_w4a16_res_grad(r, z, lay, "silu", gate)
+    d = r[at].double() * g * act64(z[at].double(), "silu")[1]
+    check(dz[at], d, 16 * U * (r[at].double() * g).abs() * (1 + z[at].double().abs())
+          + half_step(d, BF), "dZ")
+    d = dz[at].double()
+    check(dx[at], d @ w, n * U * (d.abs() @ w.abs()) + half_step(d @ w, BF), "dX")
+    assert torch.isfinite(dgate).all() and dgate.abs().sum() > 0
