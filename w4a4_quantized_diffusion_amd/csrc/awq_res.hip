@@ -789,8 +789,9 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
                                 uint16_t* dX, uint16_t* dZ, float* dgate, void* ws, hipStream_t s) {
   const int64_t rows = M / images, each = gate.ld ? images : 1;
   Joins j{};
+  j.images = images;
   if (M == 0) {
-    if (dgate) j.add(nullptr, dgate, N, 0, each);
+    if (dgate) j.add(nullptr, dgate, each);
     return launch_joins(j, N, s);
   }
   if (dy16 && !dgate && awq_res_grad_fused(M, K, N))
@@ -805,7 +806,8 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
                      dim3(unsigned((N + 511) / 512 * images * parts)), dim3(256), 0, s, dY, Z, gate,
                      rows, parts, int(N), dZ, part);
   SVDQ_TRY(check_launch("awq_res_grad"));
-  if (dgate && !direct) j.add(part, dgate, N, images * parts / each, each);
+  j.parts = parts;
+  if (dgate && !direct) j.add(part, dgate, each);
   SVDQ_TRY(launch_joins(j, N, s));
   return launch_awq_grad_product(dZ, M, K, N, wt, dX, w8 + grad_part_bytes(M, N, images), s);
 }

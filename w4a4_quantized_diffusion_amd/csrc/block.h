@@ -26,22 +26,29 @@ struct BlockNormGrad {
   void *dX, *dH;
   bool y16;
   int64_t parts;          // workgroups an image
-  float* part[5];         // partial sums of the vectors' gradients [workgroups][D]
+  float* grad[5];         // gradients of vectors that are one workgroup's sums [workgroups][D]
+  float* sums[3];         // the workgroups' A, B and S [workgroups][D], for the others
 };
 
-// Sums of partial results, up to five in one launch: to[i][D] = the sum over parts
-// i parts .. of from [each parts][D], in a fixed order; zeros for no parts
+// Sums of partial results, up to five in one launch: to[i][D] = the sum over the parts of
+// image i (`parts` an image) of from [images parts][D], or the sum over all of them where
+// `each` is 1, times the image's factor vector + add (1 if there is none).  In a fixed
+// order; zeros for no parts.
 struct Joins {
   int count;
+  int64_t parts, images;
   const float* from[5];
   float* to[5];
-  int64_t parts[5], blocks[5];
+  Vec factor[5];
+  float plus[5];
+  int64_t each[5];
 
-  void add(const float* f, float* t, int64_t D, int64_t p, int64_t each) {
+  void add(const float* f, float* t, int64_t e, const Vec& v = {nullptr, 0, false}, float p = 0.f) {
     from[count] = f;
     to[count] = t;
-    parts[count] = p;
-    blocks[count++] = (D + 63) / 64 * each;
+    each[count] = e;
+    factor[count] = v;
+    plus[count++] = p;
   }
 };
 svdq_status launch_joins(const Joins& j, int64_t D, hipStream_t s);

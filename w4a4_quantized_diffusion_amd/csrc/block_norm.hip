@@ -353,7 +353,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(svdq::BlockNorm a, int
 // three sums a column, A = sum dY n, B = sum g n(H) (or g H) and S = sum dY, hold all
 // five gradients: dweight = (1 + scale) A, dscale = weight A, dgate = post B, dpost =
 // gate B, dshift = S.  The next row's loads are in flight while one is worked on.  The
-// workgroups' gradients are joined by a second launch in a fixed order.
+// workgroups' sums are joined, and multiplied, by a second launch in a fixed order.
 
 enum { POST, GATE, WEIGHT, SCALE, SHIFT, VECTORS };
 
@@ -542,28 +542,32 @@ __global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void blo
       store(cut, c, g.dH, h16, row * D, d.v[c]);
     }
   }
-  // each gradient: a sum times the vector it shares its product with
-  auto put = [&](int k, const Row<V, C>& acc, const Vec& other, float none, float add)
+  // each gradient is a sum times the vector it shares its product with: here where no
+  // other workgroup has part in it, else in the join
+  auto put = [&](float* to, const Row<V, C>& acc, const Vec& other, float none, float add)
       __attribute__((always_inline)) {
-    if (!g.part[k]) return;
+    if (!to) return;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float f[V];
       vector(other, cut, image, c, none, f);
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = acc.v[c][i] * (f[i] + add);
-      store(cut, c, g.part[k], false, int64_t(blockIdx.x) * D, f);
+      store(cut, c, to, false, int64_t(blockIdx.x) * D, f);
     }
   };
-  put(POST, accB, a.gate, 1.f, 0.f);
-  put(GATE, accB, a.post, 1.f, 0.f);
-  put(WEIGHT, accA, a.scale, 0.f, 1.f);
-  put(SCALE, accA, a.weight, 1.f, 0.f);
-  put(SHIFT, accS, Vec{nullptr, 0, false}, 1.f, 0.f);
+  const Vec one{nullptr, 0, false};
+  put(g.grad[POST], accB, a.gate, 1.f, 0.f);
+  put(g.grad[GATE], accB, a.post, 1.f, 0.f);
+  put(g.grad[WEIGHT], accA, a.scale, 0.f, 1.f);
+  put(g.grad[SCALE], accA, a.weight, 1.f, 0.f);
+  put(g.grad[SHIFT], accS, one, 1.f, 0.f);
+  put(g.sums[0], accA, one, 1.f, 0.f);
+  put(g.sums[1], accB, one, 1.f, 0.f);
+  put(g.sums[2], accS, one, 1.f, 0.f);
 }
 
-// For up to five sums at once: out[i] = the sum over the parts of image i (all of them
-// where a vector is shared).  64 columns and 16 waves a workgroup.
+// 64 columns and 16 waves a workgroup
 __global__ __launch_bounds__(1024) void join_kernel(svdq::Joins j, int64_t total, int D) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63;
@@ -572,24 +576,40 @@ __global__ __launch_bounds__(1024) void join_kernel(svdq::Joins j, int64_t total
   for (int64_t block = blockIdx.x; block < total; block += gridDim.x) {
     int64_t b = block;
     int k = 0;
-    while (k + 1 < j.count && b >= j.blocks[k]) b -= j.blocks[k++];
-    const int64_t image = b / across, parts = j.parts[k];
+    while (k + 1 < j.count && b >= j.each[k] * across) b -= j.each[k++] * across;
+    const int64_t image = b / across, n = j.each[k] == 1 ? j.images * j.parts : j.parts;
     const int col = int(b % across) * 64 + lane;
+    const Vec f = j.factor[k];
+    auto factor = [&](int64_t i) __attribute__((always_inline)) {
+      if (!f.p) return 1.f;
+      const int64_t at = i * f.ld + col;
+      return j.plus[k] + (f.b16 ? bf16_to_f32(static_cast<const uint16_t*>(f.p)[at])
+                                : static_cast<const float*>(f.p)[at]);
+    };
+    // where the factor changes along the sum, image by image
+    const bool vary = f.p && f.ld && j.each[k] == 1 && j.images > 1;
+    const int64_t each = vary ? j.parts : n, runs = vary ? j.images : 1;
     float s = 0.f;
     if (col < D) {
-      const float* const p = j.from[k] + image * parts * D + col;
-      int64_t i = wave;
-      for (; i + 48 < parts; i += 64) {
-        const float v0 = p[i * D], v1 = p[(i + 16) * D], v2 = p[(i + 32) * D], v3 = p[(i + 48) * D];
-        s += (v0 + v1) + (v2 + v3);
+      const float* p = j.from[k] + image * n * D + col;
+      for (int64_t r = 0; r < runs; ++r, p += each * D) {
+        float t = 0.f;
+        int64_t i = wave;
+        for (; i + 112 < each; i += 128) {
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = p[(i + 16 * q) * D];
+          t += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+        for (; i < each; i += 16) t += p[i * D];
+        s += vary ? t * factor(r) : t;
       }
-      for (; i < parts; i += 16) s += p[i * D];
     }
     red[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && col < D) {
       for (int w = 1; w < 16; ++w) s += red[w][lane];
-      j.to[k][image * D + col] = s;
+      j.to[k][image * D + col] = vary || n == 0 ? s : s * factor(image);
     }
     __syncthreads();
   }
@@ -669,7 +689,7 @@ namespace svdq {
 
 svdq_status launch_joins(const Joins& j, int64_t D, hipStream_t s) {
   int64_t blocks = 0;
-  for (int k = 0; k < j.count; ++k) blocks += j.blocks[k];
+  for (int k = 0; k < j.count; ++k) blocks += (D + 63) / 64 * j.each[k];
   if (!blocks) return SVDQ_OK;
   hipLaunchKernelGGL(join_kernel, dim3(unsigned(std::min(blocks, MOST_GROUPS))), dim3(1024), 0, s, j,
                      blocks, int(D));
@@ -690,26 +710,36 @@ svdq_status launch_block_norm(const BlockNorm& a, int64_t M, void* X_out, void* 
 
 size_t block_norm_grad_workspace(int64_t M, int64_t D, int64_t images) {
   if (M == 0) return 0;
-  return align256(size_t(VECTORS) * size_t(images * grad_parts(M, D, images)) * size_t(D) * 4);
+  return align256(size_t(3) * size_t(images * grad_parts(M, D, images)) * size_t(D) * 4);
 }
 
 svdq_status launch_block_norm_grad(const BlockNorm& a, BlockNormGrad g, int64_t M, int64_t images,
                                    float* const (&out)[5], void* ws, hipStream_t s) {
   g.parts = M ? grad_parts(M, a.D, images) : 0;
+  const int64_t groups = images * g.parts;
   const Vec* const vs[VECTORS] = {&a.post, &a.gate, &a.weight, &a.scale, &a.shift};
+  // the sum of each gradient, and the vector it is multiplied by
+  constexpr int SUM[VECTORS] = {1, 1, 0, 0, 2};
+  const Vec factor[VECTORS] = {a.gate, a.post, a.scale, a.weight, {nullptr, 0, false}};
   float* at = static_cast<float*>(ws);
   Joins j{};
+  j.parts = g.parts;
+  j.images = images;
+  for (int k = 0; k < 3; ++k) g.sums[k] = nullptr;
   for (int k = 0; k < VECTORS; ++k) {
-    g.part[k] = nullptr;
+    g.grad[k] = nullptr;
     if (!out[k]) continue;
     const int64_t each = vs[k]->ld ? images : 1;
-    if (images * g.parts == each) {       // one workgroup's sums are the gradient
-      g.part[k] = out[k];
+    if (groups == each) {                 // one workgroup's sums are the gradient
+      g.grad[k] = out[k];
       continue;
     }
-    g.part[k] = at;
-    at += images * g.parts * a.D;
-    j.add(g.part[k], out[k], a.D, images * g.parts / each, each);
+    float*& sum = g.sums[SUM[k]];
+    if (!sum) {
+      sum = at;
+      at += groups * a.D;
+    }
+    j.add(sum, out[k], each, factor[k], k == WEIGHT ? 1.f : 0.f);
   }
   if (M) {
     const Shape p = grad_shape(a.D);
