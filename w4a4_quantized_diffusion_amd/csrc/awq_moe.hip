@@ -275,7 +275,7 @@ __device__ __forceinline__ void lds_barrier() {
 // A workgroup's 8 waves take the chunks of K in turn, D of them at a time, and their sums
 // meet in LDS.  The workgroups go on from item to item with the next item's loads in
 // flight.  (One token runs through the code once: a loop that also unrolled the ends of
-// the items took 12 us instead of X for it, most of it waiting for instructions.)
+// the items took 12 us instead of 9 for it, most of that waiting for instructions.)
 
 constexpr int UP_WAVES = 8;
 
@@ -455,7 +455,7 @@ constexpr int MAX_SLICES = 8;
 
 template <int MT, int CT>
 __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe a) {
-  constexpr int D = MT * CT == 4 ? 2 : MT == 1 && CT == 1 ? 4 : 3;
+  constexpr int D = MT * CT == 1 ? 4 : 2;   // (with 32 columns 2, 3, 4 and 6 take 44-48 us)
   constexpr int W = 16 * CT;
   __shared__ Route r;
   extern __shared__ __align__(16) float sums[];     // [wave][T][W]
