@@ -318,6 +318,17 @@ def test_grad_split_rounds(m, k, n, images):
     check_grad(m, k, n, images, "gelu")
 
 
+# a long reduction with few tiles: `slices` of it, joined in two turns or more
+@pytest.mark.parametrize("m,length,width,slices",
+                         [(65, 8192, 128, 16), (66, 11264, 64, 22), (200, 16384, 192, 32)])
+def test_many_slices(m, length, width, slices):
+    assert svdq.awq_linear_w4a16_res_workspace_bytes(m, length, width) == slices * m * width * 4
+    check_forward(problem(m, length, width, gate=F32), "gelu")
+    check_forward(problem(m, length, width, gate=None, res=F32, bias=False), "none", F32, save=False)
+    assert svdq.awq_linear_w4a16_res_grad_workspace_bytes(m, width, length, 1) >= slices * m * width * 4
+    check_grad(m, width, length, 1, "gelu")
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("m,images", [(1, 1), (20, 4), (64, 2)])
 def test_grad_of_few_rows_with_and_without_dgate(act, m, images):

@@ -333,16 +333,19 @@ __global__ __launch_bounds__(64) void grad_sum_kernel(const float* __restrict__ 
                                                       bool xbf16) {
   const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
   if (i >= total) return;
-  // all loads first; a slice past the last counts as zeros
-  v4f v[MAX_SLICES], p = {0, 0, 0, 0};
+  v4f p = {0, 0, 0, 0};
+  for (int q0 = 0; q0 < S; q0 += MAX_SLICES) {
+    // all loads first; a slice past the last counts as zeros
+    v4f v[MAX_SLICES];
 #pragma unroll
-  for (int q = 0; q < MAX_SLICES; ++q)
-    v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q, S - 1)) * total + i];
-  __builtin_amdgcn_sched_barrier(0);
+    for (int q = 0; q < MAX_SLICES; ++q)
+      v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q0 + q, S - 1)) * total + i];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int q = 0; q < MAX_SLICES; ++q)
+    for (int q = 0; q < MAX_SLICES; ++q)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] += q < S ? v[q][e] : 0.f;
+      for (int e = 0; e < 4; ++e) p[e] += q0 + q < S ? v[q][e] : 0.f;
+  }
   if (xbf16)
     static_cast<uint2*>(dX)[i] = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
   else
@@ -603,16 +606,19 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
     store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, K, dX);
 }
 
-int mid_slices(int64_t M, int64_t K, int64_t N, int layers) {
-  return svdq_mid::slices((M + 127) / 128 * ((K + 127) / 128), (N + 63) / 64 * layers);
+// `fine`: the product of the layer with an epilogue.  The older products keep the slices
+// that they have had, and with them their results to the bit.
+int mid_slices(int64_t M, int64_t K, int64_t N, int layers, bool fine) {
+  const int64_t tiles = (M + 127) / 128 * ((K + 127) / 128), chunks = (N + 63) / 64 * layers;
+  return fine ? svdq_mid::fine_slices(tiles, chunks) : svdq_mid::slices(tiles, chunks);
 }
 
 // dX = A0 wd0 [+ A1 wd1]
 svdq_status launch_mid(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWeight* w,
                        int layers, int64_t M, int64_t K, int64_t N, void* dX, bool xbf16,
-                       float* part, hipStream_t s) {
+                       float* part, bool fine, hipStream_t s) {
   const int64_t tiles = (M + 127) / 128 * ((K + 127) / 128);
-  const int S = mid_slices(M, K, N, layers);
+  const int S = mid_slices(M, K, N, layers, fine);
   svdq_mid::Args p{{A0, A1}, N, int((N + 63) / 64), layers, int(M)};
   hipLaunchKernelGGL(grad_mid_kernel, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, s, p, w[0],
                      w[layers - 1], int(K), int(N), S, int(tiles), dX, xbf16, part);
@@ -633,9 +639,10 @@ size_t transposed_bytes(int64_t K, int64_t N, int layers) {
 }
 
 // bytes of the partial sums of `rows` rows
-size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers) {
+size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers, bool fine = false) {
   if (rows == 0) return 0;
-  const int S = rows <= ROWS ? split(rows, K, N, layers).slices : mid_slices(rows, K, N, layers);
+  const int S =
+      rows <= ROWS ? split(rows, K, N, layers).slices : mid_slices(rows, K, N, layers, fine);
   return S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(K) * 4);
 }
 
@@ -656,13 +663,31 @@ svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqW
   return svdq::check_launch("grad_wide");
 }
 
+size_t linear_grad_bytes(int64_t M, int64_t K, int64_t N, bool fine) {
+  const int64_t w = wide_rows(M, K, N, 1);
+  return (w ? transposed_bytes(K, N, 1) : 0) + part_bytes(M - w, K, N, 1, fine);
+}
+
+svdq_status linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N, svdq::AwqWeight wt,
+                        void* dX, bool xb, void* ws, bool fine, hipStream_t s) {
+  const int64_t w = wide_rows(M, K, N, 1), rest = M - w;
+  uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  if (w) SVDQ_TRY(launch_wide(dY, dY, &wt, 1, w, K, N, dX, xb, reinterpret_cast<uint16_t*>(w8), s));
+  if (!rest) return SVDQ_OK;
+  float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 1) : 0));
+  const uint16_t* const d = dY + w * N;
+  void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
+  const Rows in{d, nullptr, nullptr, nullptr, nullptr, {}, 1};
+  if (rest <= ROWS) return run_rows<PLAIN>(in, rest, K, N, &wt, x, xb, part, s);
+  return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, fine, s);
+}
+
 }  // namespace
 
 namespace svdq {
 
 size_t awq_linear_grad_workspace(int64_t M, int64_t K, int64_t N) {
-  const int64_t w = wide_rows(M, K, N, 1);
-  return (w ? transposed_bytes(K, N, 1) : 0) + part_bytes(M - w, K, N, 1);
+  return linear_grad_bytes(M, K, N, false);
 }
 
 size_t awq_gated_grad_workspace(int64_t M, int64_t K, int64_t N) {
@@ -673,17 +698,7 @@ size_t awq_gated_grad_workspace(int64_t M, int64_t K, int64_t N) {
 svdq_status launch_awq_linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
                                    AwqWeight wt, void* dX, svdq_dtype x_dt, void* ws,
                                    hipStream_t s) {
-  const int64_t w = wide_rows(M, K, N, 1), rest = M - w;
-  const bool xb = x_dt == SVDQ_BF16;
-  uint8_t* const w8 = static_cast<uint8_t*>(ws);
-  if (w) SVDQ_TRY(launch_wide(dY, dY, &wt, 1, w, K, N, dX, xb, reinterpret_cast<uint16_t*>(w8), s));
-  if (!rest) return SVDQ_OK;
-  float* const part = reinterpret_cast<float*>(w8 + (w ? transposed_bytes(K, N, 1) : 0));
-  const uint16_t* const d = dY + w * N;
-  void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
-  const Rows in{d, nullptr, nullptr, nullptr, nullptr, {}, 1};
-  if (rest <= ROWS) return run_rows<PLAIN>(in, rest, K, N, &wt, x, xb, part, s);
-  return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, s);
+  return linear_grad(dY, M, K, N, wt, dX, x_dt == SVDQ_BF16, ws, false, s);
 }
 
 namespace {
@@ -704,14 +719,14 @@ svdq_gemm::Rounds product_rounds(int64_t M, int64_t K, int64_t N) {
 
 size_t awq_grad_product_workspace(int64_t M, int64_t K, int64_t N) {
   const svdq_gemm::Rounds r = product_rounds(M, K, N);
-  return r.S == 1 ? awq_linear_grad_workspace(M, K, N)
+  return r.S == 1 ? linear_grad_bytes(M, K, N, true)
                   : transposed_bytes(K, N, 1) + svdq_gemm::rounds_bytes(r);
 }
 
 svdq_status launch_awq_grad_product(const uint16_t* dZ, int64_t M, int64_t K, int64_t N, AwqWeight wt,
                                     uint16_t* dX, void* ws, hipStream_t s) {
   const svdq_gemm::Rounds r = product_rounds(M, K, N);
-  if (r.S == 1) return launch_awq_linear_grad(dZ, M, K, N, wt, dX, SVDQ_BF16, ws, s);
+  if (r.S == 1) return linear_grad(dZ, M, K, N, wt, dX, true, ws, true, s);
   const int64_t np = pad64(N);
   uint16_t* const B = static_cast<uint16_t*>(ws);
   float* const part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + transposed_bytes(K, N, 1));
@@ -767,7 +782,7 @@ svdq_status launch_awq_gated_grad(const uint16_t* dH, const uint16_t* G, const u
     SVDQ_TRY(launch_wide(dG, dU, wt, 2, w, K, N, dX, true, reinterpret_cast<uint16_t*>(w8), s));
   if (!rest || fused) return SVDQ_OK;
   if (rest <= ROWS) return run_rows<PLAIN_PAIR>(in, rest, K, N, wt, x, true, part, s);
-  return launch_mid(in.dG, in.dU, wt, 2, rest, K, N, x, true, part, s);
+  return launch_mid(in.dG, in.dU, wt, 2, rest, K, N, x, true, part, false, s);
 }
 
 }  // namespace svdq

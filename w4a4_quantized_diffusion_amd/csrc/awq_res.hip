@@ -255,19 +255,22 @@ __global__ __launch_bounds__(64) void res_sum_kernel(const float* __restrict__ p
   const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x, total = int64_t(M) * N / 4;
   if (i >= total) return;
   const int64_t m = 4 * i / N, n = 4 * i - m * N;
-  // all loads first; a slice past the last counts as zeros
-  v4f v[SUM_SLICES];
-#pragma unroll
-  for (int q = 0; q < SUM_SLICES; ++q)
-    v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q, S - 1)) * total + i];
   float z[4] = {}, b[4] = {};
-  if (e.bias) load_any<4>(e.bias, true, n, b);
+  for (int q0 = 0; q0 < S; q0 += SUM_SLICES) {
+    // all loads first; a slice past the last counts as zeros
+    v4f v[SUM_SLICES];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+    for (int q = 0; q < SUM_SLICES; ++q)
+      v[q] = reinterpret_cast<const v4f*>(part)[int64_t(min(q0 + q, S - 1)) * total + i];
+    __builtin_amdgcn_sched_barrier(0);
+    if (q0 == 0 && e.bias) load_any<4>(e.bias, true, n, b);
 #pragma unroll
-    for (int q = 0; q < SUM_SLICES; ++q) z[k] += q < S ? v[q][k] : 0.f;
-    z[k] += b[k];
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int q = 0; q < SUM_SLICES; ++q) z[k] += q0 + q < S ? v[q][k] : 0.f;
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) z[k] += b[k];
   emit<ACT, 4>(e, int(m), n, N, z);
 }
 
@@ -525,6 +528,10 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void res_mid_kernel(svdq_mid::Args
 
 int64_t mid_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128); }
 
+int mid_slices(int64_t M, int64_t K, int64_t N) {
+  return svdq_mid::fine_slices(mid_tiles(M, N), K / 64);
+}
+
 // the rows of the wide form, and whether its last round is split (then they are all)
 int64_t wide_rows(int64_t M, int64_t K, int64_t N, svdq_gemm::Rounds* split) {
   split->S = 1;
@@ -544,7 +551,7 @@ size_t weight_bytes(int64_t K, int64_t N) { return svdq_gemm::weight_bytes(N, K 
 size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
   if (rows == 0 || (rows <= ROWS && one_launch(rows, K, N))) return 0;
   const int S = rows <= ROWS ? split(rows, K, N).slices
-                             : svdq_mid::slices(mid_tiles(rows, N), K / 64);
+                             : mid_slices(rows, K, N);
   return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(N) * 4);
 }
 
@@ -616,7 +623,7 @@ svdq_status few(const Call& c, float* part) {
 
 svdq_status mid(const Call& c, float* part) {
   const int64_t tiles = mid_tiles(c.M, c.N);
-  const int S = svdq_mid::slices(tiles, c.K / 64);
+  const int S = mid_slices(c.M, c.K, c.N);
   svdq_mid::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, int(c.M)};
   hipLaunchKernelGGL(by_act<MidKernel>(c.act), dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0,
                      c.s, p, c.w, int(c.N), S, int(tiles), c.e, part);

@@ -336,6 +336,16 @@ inline int slices(int64_t tiles, int64_t chunks) {
                                 std::max<int64_t>(1, chunks / 4)}));
 }
 
+// The same with 16 to 32 slices, of at least eight chunks each, where the tiles leave
+// room for them: 65 rows 8192 -> 512 14.1 us (with 8 slices 18.7), 128 rows 12288 -> 2048
+// 22.0 (27.1).  Slices of four chunks: 65 rows 4096 -> 4096 21.6 us and with 8 slices 17.6,
+// since their sums are 16 MB; 9 to 15 slices, which the second launch loads in two turns
+// as well, gain nothing (10 of 333 rows 8192 -> 2064: 32.6 us, 8: 31.9).
+inline int fine_slices(int64_t tiles, int64_t chunks) {
+  const int64_t S = std::min<int64_t>({512 / tiles, 32, chunks / 8});
+  return S < 16 ? slices(tiles, chunks) : int(S);
+}
+
 // Weights: fetch<set>(chunk) loads this thread's share of a chunk's B rows into
 // one of two register sets, put<set, q>(b) dequantizes quarter q of it and (at
 // the latest in quarter 3) writes it to LDS, slot(row, piece) is where piece
