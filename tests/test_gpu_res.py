@@ -318,6 +318,14 @@ def test_grad_split_rounds(m, k, n, images):
     check_grad(m, k, n, images, "gelu")
 
 
+# few rows and a long reduction: 9 to 16 slices, joined in two turns
+@pytest.mark.parametrize("m,k,n,slices", [(18, 5632, 64, 11), (64, 8192, 144, 16), (33, 4672, 16, 9)])
+def test_many_slices_of_few_rows(m, k, n, slices):
+    assert svdq.awq_linear_w4a16_res_workspace_bytes(m, k, n) == -(-slices * m * n * 4 // 256) * 256
+    check_forward(problem(m, k, n, gate=F32), "silu")
+    check_forward(problem(m, k, n, gate=None, res=F32, bias=False), "none", F32, save=False)
+
+
 # a long reduction with few tiles: `slices` of it, joined in two turns or more
 @pytest.mark.parametrize("m,length,width,slices",
                          [(65, 8192, 128, 16), (66, 11264, 64, 22), (200, 16384, 192, 32)])

@@ -138,11 +138,15 @@ struct Split {
   int blocks, slices;
 };
 
+// Up to 8 slices, as many as the second launch loads at once, and up to 16 of at least
+// eight chunks each: 64 rows 16384 -> 4096 32.7 -> 24.5 us, 17 rows 8192 -> 512 10.2 -> 8.7;
+// with slices of four chunks 33 rows 4096 -> 4096 take 12.5 us instead of 11.4.
 Split split(int64_t M, int64_t K, int64_t N) {
   Split p;
   p.blocks = int((N + 16 * WAVES - 1) / (16 * WAVES));
   p.slices = int(std::min<int64_t>(
-      {K / 64, SUM_SLICES, std::max<int64_t>(1, 512 / p.blocks)}));
+      {K / 64, std::max<int64_t>(SUM_SLICES, std::min<int64_t>(16, K / 512)),
+       std::max<int64_t>(1, 512 / p.blocks)}));
   return p;
 }
 
@@ -150,8 +154,9 @@ Split split(int64_t M, int64_t K, int64_t N) {
 // K N / 16 bytes) and a wave's rows of X grow with M K.  Measured, one launch against two,
 // us: 2048 -> 2048 1 row 3.8 / 6.1, 48 rows 8.4 / 8.9, 64 rows 10.3 / 9.8; 4096 -> 4096 24
 // rows 9.7 / 10.4, 33 rows 15.2 / 11.2; 2048 -> 8192 24 rows 9.8 / 10.5, 33 rows 12.5 /
-// 11.9; 8192 -> 2048 8 rows 9.2 / 10.2, 16 rows 11.9 / 10.8; 4096 -> 12288 8 rows 12.4 /
-// 13.9, 16 rows 16.3 / 14.6, 64 rows 48 / 23.5; 12288 -> 4096 8 rows 12.4 / 12.9.
+// 11.9; 8192 -> 2048 8 rows 9.3 / 9.2, 12 rows 10.6 / 9.3; 4096 -> 12288 8 rows 12.4 /
+// 13.9, 16 rows 16.3 / 14.6, 64 rows 48 / 23.5; 12288 -> 4096 8 rows 12.3 / 13.1, 12 rows
+// 13.3 / 13.2.
 bool one_launch(int64_t M, int64_t K, int64_t N) {
   return M * K <= 3 << 15 && M * K <= (27 << 24) / N;
 }
