@@ -5,11 +5,11 @@
 //
 // Wg, Wu [E][N, K], Wd [E][K, N] in the AWQ format.  Two launches: the first forms
 // H = act(G) * U for every chosen (token, expert) pair, a slot, the second the
-// down-projections and their weighted sum.  Both route for themselves: every workgroup
-// finds the choices of all tokens in LDS from the logits (at most 64 x 256), about a
-// microsecond, where a launch of its own would cost two to three.  The bound is
-// reading the chosen experts' weights; slots are sorted by expert, so that each expert's
-// weights are read once for all of its tokens.
+// down-projections and their weighted sum; a third adds the sums of slices, where there
+// are some.  Every workgroup of the first finds the choices of all tokens in LDS from the
+// logits (at most 64 x 256), about a microsecond, where a launch of its own would cost two
+// to three, and leaves them to the second.  Slots are sorted by expert, so that each
+// expert's weights are read once for all of its tokens.
 //
 // H enters the second product rounded to bf16 (the MFMAs' type, and what two separate
 // layers would hand on); all sums and the weights are fp32, and no atomics touch them:
@@ -276,6 +276,13 @@ __device__ __forceinline__ void lds_barrier() {
 // meet in LDS.  The workgroups go on from item to item with the next item's loads in
 // flight.  (One token runs through the code once: a loop that also unrolled the ends of
 // the items took 12 us instead of 9 for it, most of that waiting for instructions.)
+//
+// Measured: 61 tokens, 6 of 40 experts, 4096 x 1408: 245 MB of codes and scales in 67-77
+// us, 3.2-3.7 TB/s.  The vector units are busy 57% of the cycles, with 2.4-3 instructions
+// a code for the dequantization and the routing of operands; a copy of the kernel that only
+// loads takes 55 us, and what is left between is the two not overlapping fully.  Three and four
+// chunks ahead, 4 or 16 waves a workgroup and 6 waves a SIMD gain nothing; a workgroup per
+// item instead of 512 that go on takes 97 us.
 
 constexpr int UP_WAVES = 8;
 
@@ -449,6 +456,10 @@ __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
 // joined in order.  A wave goes on from expert to expert with the next one's loads in
 // flight.  With S > 1 a third launch adds the slices' sums (the workgroup of a column
 // block that ends last could, but its fences write the L2 back and took 9 us).
+//
+// Measured: 61 tokens as above 123 MB in 42-44 us, 2.9 TB/s, and 4-5 for the sums; one token
+// 5.8 us.  A copy that only loads takes 30 us; the rest is the dequantization, an expert's
+// sums in LDS and the fewer bytes in flight at their turn.
 
 constexpr int DOWN_WAVES = 16;
 constexpr int MAX_SLICES = 8;

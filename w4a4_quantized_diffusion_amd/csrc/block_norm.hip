@@ -13,6 +13,11 @@
 // fp32; the variance is summed from the differences to the mean (a second sum over
 // registers, where sum v^2 - mean^2 would lose the digits of a large mean).  x' enters
 // the norm as the fp32 sum, before it is rounded to X's type.
+//
+// Measured: 9216 rows of 4096, layer norm, gate, scale and shift, bf16: 302 MB in 55.6 us,
+// 5.4 TB/s (a large copy: 5.3).  333 rows of 5455, fp32 and bf16, with a post norm 10.4 us,
+// 2.4 TB/s: 1.3 rounds of workgroups, each a chain of loads, four sums over the
+// workgroup and stores that few others hide.  One row 2.6 us, a launch.
 
 #include "block.h"
 
@@ -354,6 +359,15 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(svdq::BlockNorm a, int
 // five gradients: dweight = (1 + scale) A, dscale = weight A, dgate = post B, dpost =
 // gate B, dshift = S.  The next row's loads are in flight while one is worked on.  The
 // workgroups' sums are joined, and multiplied, by a second launch in a fixed order.
+//
+// Measured: 9216 rows of 4096, post norm and all five gradients, bf16: 453 MB in 102 us,
+// 4.4 TB/s, and 10 us for the join.  Between memory and the chain of a row: two or four
+// sums over the workgroup follow one another in each row, and the registers of a row,
+// the next row and the column sums leave two workgroups a compute unit to hide
+// them.  (Five column sums
+// spilled: 436 us with them; 175 with three; 111 with the sums over the workgroup in row
+// operations of the lanes and the switched-off parts compiled out.)  20 rows of 2048 take
+// 4.5 us and the join 3.4.
 
 enum { POST, GATE, WEIGHT, SCALE, SHIFT, VECTORS };
 
@@ -566,7 +580,9 @@ __global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void blo
   put(g.sums[2], accS, one, 1.f, 0.f);
 }
 
-// 64 columns and 16 waves a workgroup
+// 64 columns and 16 waves a workgroup; every wave adds its share of the parts, one after
+// the other, and the waves' sums meet in LDS.  The fixed order is what two calls with the
+// same bits need (atomics on the gradients would be one launch).
 __global__ __launch_bounds__(1024) void join_kernel(svdq::Joins j, int64_t total, int D) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63;
