@@ -337,7 +337,11 @@ class AWQLinear(nn.Module):
     layer's own kernels, each part optional: act "silu" or "gelu" (tanh form), gate [N] or
     one row per image ([images, N] for x [images, ..., K]), residual of the output's
     shape in fp32 or bf16, whose type the output then has.  Differentiable in x, gate and
-    residual."""
+    residual.
+
+    Forward and backward can be captured into a graph together.  A backward pass
+    that is captured needs leaves of its own: torch ends the process when an eager
+    graph of the same leaves is still alive then."""
 
     def __init__(self, layer, bias=None):
         super().__init__()
