@@ -337,6 +337,22 @@ def test_many_slices(m, length, width, slices):
     check_grad(m, width, length, 1, "gelu")
 
 
+# two sets of waves a tile, with as many chunks and one less; `sums` slices (0: no second
+# launch), of two chunks and more
+@pytest.mark.parametrize("m,k,n,sums", [(130, 704, 400, 5), (390, 960, 8064, 0), (150, 1088, 2048, 4),
+                                        (333, 8192, 2064, 5), (257, 12352, 1040, 9)])
+def test_two_sets_of_waves(m, k, n, sums):
+    assert svdq.awq_linear_w4a16_res_workspace_bytes(m, k, n) == -(-sums * m * n * 4 // 256) * 256
+    check_forward(problem(m, k, n, gate=F32), "silu")
+    check_forward(problem(m, k, n, gate=None, res=F32, bias=False), "none", F32, save=False)
+    p = problem(m, k, n)
+    want = call(p, "gelu")
+    p["x"][m // 2, k // 2] = float("inf")
+    got = call(p, "gelu")
+    keep = torch.arange(m, device=got.device) != m // 2
+    assert torch.equal(got[keep], want[keep]) and not got[m // 2].isfinite().any()
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("m,images", [(1, 1), (20, 4), (64, 2)])
 def test_grad_of_few_rows_with_and_without_dgate(act, m, images):

@@ -483,8 +483,9 @@ struct RowWeights {
   uint4 c[2];
   uint16_t cs[2], cz[2];
 
-  __device__ __forceinline__ RowWeights(const svdq::AwqWeight& w, int N, int64_t n0)
-      : N(N), row(int(threadIdx.x) >> 1), half(threadIdx.x & 1) {
+  __device__ __forceinline__ RowWeights(const svdq::AwqWeight& w, int N, int64_t n0,
+                                        int tid = int(threadIdx.x))
+      : N(N), row(tid >> 1), half(tid & 1) {
     const int64_t nr = min(n0 + row, int64_t(N) - 1);
     q = w.q + nr * 32 + 16 * half;
     s = w.s + nr;
@@ -547,17 +548,60 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void res_mid_kernel(svdq_mid::Args
                                    part + int64_t(slice) * p.M * N);
 }
 
+// The same tile by two such sets of four waves, each with half of a slice's chunks and LDS
+// of its own.
+template <int ACT>
+__global__ __launch_bounds__(2 * svdq_mid::NT, 2) void res_twin_kernel(svdq_mid::Args p,
+                                                                       svdq::AwqWeight wt, int N,
+                                                                       int S, int tiles,
+                                                                       ResEpilogue e,
+                                                                       float* __restrict__ part) {
+  using namespace svdq_mid;
+  __shared__ ChunkA a0[2], a1[2], a2[2];
+  __shared__ ChunkB b0[2], b1[2];
+  const int lane = threadIdx.x & 63, tid = threadIdx.x & (svdq_mid::NT - 1);
+  const int half = __builtin_amdgcn_readfirstlane(threadIdx.x / svdq_mid::NT);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slice = blockIdx.x / tiles;
+  int64_t m0, n0;
+  tile_at(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (N + BN - 1) / BN, BM, BN, m0, n0);
+  v16f acc[RBL][CBL], sum[1][CBL];
+  zero_acc(acc);
+  RowWeights w(wt, N, n0, tid);
+  const int c0 = int(int64_t(slice) * p.chunks / S), c2 = int(int64_t(slice + 1) * p.chunks / S);
+  const int c1 = (c0 + c2 + 1) / 2;
+  tile_product(p, m0, half ? c1 : c0, half ? c2 : c1, w, a0[half], a1[half], a2[half], b0[half],
+               b1[half], acc, tid);
+  // a barrier a chunk, which the half with one chunk less makes up for
+  if (half && c2 - c1 < c1 - c0) __builtin_amdgcn_s_barrier();
+  add_halves(acc, half, wave, lane, b0, b1, sum);
+  const int64_t row0 = m0 + (wave >> 1) * 64 + 32 * half, col0 = n0 + (wave & 1) * 64;
+  // 32 x 68 floats, in an LDS object of the wave's own
+  __syncthreads();
+  float* const eb = reinterpret_cast<float*>(wave == 0   ? &a0[half].v
+                                              : wave == 1 ? &a1[half].v
+                                              : wave == 2 ? &a2[half].v
+                                                          : &b0[half].v);
+  if (S == 1) {
+    res_epilogue<ACT, 1, CBL>(e, sum, eb, lane, row0, col0, p.M, N);
+    return;
+  }
+  const float none[CBL] = {0.f, 0.f};
+  store_wave_tile<1, CBL, false>(sum, none, eb, lane, row0, col0, p.M, N,
+                                 part + int64_t(slice) * p.M * N);
+}
+
 int64_t mid_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128); }
 
-int mid_slices(int64_t M, int64_t K, int64_t N) {
-  return svdq_mid::fine_slices(mid_tiles(M, N), K / 64);
+svdq_plan::Shape shape_of(int64_t K, int64_t N) {
+  return {K / 64, (N + 255) / 256, (N + 127) / 128, K * N, true};
 }
 
 // the rows of the wide form, and whether its last round is split (then they are all)
 int64_t wide_rows(int64_t M, int64_t K, int64_t N, svdq_gemm::Rounds* split) {
   split->S = 1;
   if (M <= ROWS) return 0;
-  const svdq_plan::Shape shape{K / 64, (N + 255) / 256, (N + 127) / 128, K * N};
+  const svdq_plan::Shape shape = shape_of(K, N);
   double us;
   const int64_t w = svdq_plan::wide_rows(M, shape, &us);
   const svdq_gemm::Rounds r = svdq_gemm::rounds(M, N, K / 32);
@@ -572,7 +616,7 @@ size_t weight_bytes(int64_t K, int64_t N) { return svdq_gemm::weight_bytes(N, K 
 size_t part_bytes(int64_t rows, int64_t K, int64_t N) {
   if (rows == 0 || (rows <= ROWS && one_launch(rows, K, N))) return 0;
   const int S = rows <= ROWS ? split(rows, K, N).slices
-                             : mid_slices(rows, K, N);
+                             : svdq_plan::medium(rows, shape_of(K, N)).S;
   return rows > ROWS && S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(N) * 4);
 }
 
@@ -599,6 +643,10 @@ struct SumKernel {
 template <int ACT>
 struct MidKernel {
   static auto get() { return res_mid_kernel<ACT>; }
+};
+template <int ACT>
+struct TwinKernel {
+  static auto get() { return res_twin_kernel<ACT>; }
 };
 template <int ACT>
 struct SplitKernel {
@@ -644,10 +692,12 @@ svdq_status few(const Call& c, float* part) {
 
 svdq_status mid(const Call& c, float* part) {
   const int64_t tiles = mid_tiles(c.M, c.N);
-  const int S = mid_slices(c.M, c.K, c.N);
+  const svdq_plan::Medium f = svdq_plan::medium(c.M, shape_of(c.K, c.N));
+  const int S = f.S;
   svdq_mid::Args p{{c.X, c.X}, c.K, int(c.K / 64), 1, int(c.M)};
-  hipLaunchKernelGGL(by_act<MidKernel>(c.act), dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0,
-                     c.s, p, c.w, int(c.N), S, int(tiles), c.e, part);
+  auto k = f.twin ? by_act<TwinKernel>(c.act) : by_act<MidKernel>(c.act);
+  hipLaunchKernelGGL(k, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT * (f.twin ? 2 : 1)), 0, c.s, p,
+                     c.w, int(c.N), S, int(tiles), c.e, part);
   SVDQ_TRY(svdq::check_launch("awq_res (mid)"));
   return S == 1 ? SVDQ_OK : sum(c, part, S);
 }

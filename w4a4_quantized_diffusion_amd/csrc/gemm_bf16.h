@@ -346,6 +346,37 @@ inline int fine_slices(int64_t tiles, int64_t chunks) {
   return S < 16 ? slices(tiles, chunks) : int(S);
 }
 
+// Two halves of four waves each, whose accumulators hold the sums over two parts of the
+// reduction, add them up: half 0 keeps rows 0..31 of each wave's 64 and half 1 the others,
+// in acc[0].  Each hands the rest on through its `b0` and `b1`.
+__device__ __forceinline__ void add_halves(v16f (&acc)[RBL][CBL], int half, int wave, int lane,
+                                           ChunkB (&b0)[2], ChunkB (&b1)[2], v16f (&out)[1][CBL]) {
+  // 8 KB a wave, two waves to an object
+  auto at = [&](int h, int k) __attribute__((always_inline)) -> v4f* {
+    return reinterpret_cast<v4f*>(wave < 2 ? b0[h].v : b1[h].v) + (wave & 1) * 512 + k * 64 + lane;
+  };
+#pragma unroll
+  for (int j = 0; j < CBL; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v4f v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = half ? acc[0][j][4 * k + e] : acc[1][j][4 * k + e];
+      *at(half, 4 * j + k) = v;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < CBL; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const v4f v = *at(half ^ 1, 4 * j + k);
+      // (half 0's sum first, in both halves)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        out[0][j][4 * k + e] = half ? v[e] + acc[1][j][4 * k + e] : acc[0][j][4 * k + e] + v[e];
+    }
+}
+
 // Weights: fetch<set>(chunk) loads this thread's share of a chunk's B rows into
 // one of two register sets, put<set, q>(b) dequantizes quarter q of it and (at
 // the latest in quarter 3) writes it to LDS, slot(row, piece) is where piece
@@ -358,8 +389,9 @@ using I3 = std::integral_constant<int, 3>;
 template <class Weights>
 __device__ __forceinline__ void tile_product(const Args& p, int64_t m0, int c0, int c1, Weights& w,
                                              ChunkA& a0, ChunkA& a1, ChunkA& a2, ChunkB& b0,
-                                             ChunkB& b1, v16f (&acc)[RBL][CBL]) {
-  const int tid = threadIdx.x, lane = tid & 63;
+                                             ChunkB& b1, v16f (&acc)[RBL][CBL],
+                                             int tid = int(threadIdx.x)) {
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int h = lane >> 5, r32 = lane & 31;
@@ -484,6 +516,7 @@ struct Shape {
   int64_t chunks;         // of the reduction
   int64_t wide_n, mid_n;  // tiles across
   int64_t weights;        // 4-bit weights of the call
+  bool twin = false;      // whether a medium number of rows has the choice of medium()
 };
 
 inline double few_us(const Shape& p) { return 6 + 0.5625 * double(p.weights) / 4.5e6; }
@@ -495,6 +528,35 @@ inline double mid_us(int64_t rows, const Shape& p) {
   return S == 1 ? t : t + 3 + 8.0 * S * double(rows) * double(p.mid_n) * 128 / 4.5e6;
 }
 
+// A medium number of rows where a tile may also go to two sets of four waves, each with
+// half of a slice's chunks, which meet in LDS: as many waves, and half the partial sums
+// or none.  500 rows 1024 -> 8192 take 19.0 us so and 29.8 in twice as many workgroups of one
+// set, 333 rows 2048 -> 8192 27.3 and 31.7, 900 rows 4096 -> 4096 48.3 and 54.2; but 333 rows
+// 4096 -> 4096, whose 96 tiles in two slices fill three quarters of the chip, 29.9 and
+// 28.3, and more tiles than compute units leave the last round emptier: 400 rows 2048 ->
+// 16384 53.7 and 48.9.  The constants are fitted to such pairs: a chunk 1.25 us with two
+// sets on a compute unit, 0.9 with one, two chunks of a twin 1.35.
+struct Medium {
+  int S;
+  bool twin;
+  double us;
+};
+
+inline Medium medium(int64_t rows, const Shape& p) {
+  const int64_t tiles = (rows + 127) / 128 * p.mid_n;
+  const double sums = 8.0 * double(rows) * double(p.mid_n) * 128 / 4.5e6, c = double(p.chunks);
+  const int S = svdq_mid::fine_slices(tiles, p.chunks);
+  Medium m{S, false, (S == 1 ? 3 : 6 + S * sums) +
+                         (tiles * S <= 256 ? 0.9 : 1.25) * double((tiles * S + 511) / 512) * c / S};
+  // (a slice has a chunk for each set)
+  const int most = int(std::min<int64_t>({256 / tiles, 16, p.chunks / 2}));
+  for (int s = 1; s <= most; ++s) {
+    const double us = (s == 1 ? 5 : 8 + s * sums) + 0.675 * c / s;
+    if (us < m.us) m = {s, true, us};
+  }
+  return m;
+}
+
 inline double wide_us(int64_t rows, const Shape& p) {
   const int64_t tiles = (rows + 255) / 256 * p.wide_n;
   return 6 + 1.72 * double((tiles + 255) / 256) * double(p.chunks) +
@@ -502,7 +564,10 @@ inline double wide_us(int64_t rows, const Shape& p) {
 }
 
 inline double rest_us(int64_t rows, const Shape& p) {
-  return rows == 0 ? 0 : rows <= 64 ? few_us(p) : mid_us(rows, p);
+  return rows == 0     ? 0
+         : rows <= 64 ? few_us(p)
+         : p.twin     ? medium(rows, p).us
+                      : mid_us(rows, p);
 }
 
 // all rows in the wide form with the last round split (gemm_bf16.h's Rounds); its join
