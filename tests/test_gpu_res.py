@@ -353,6 +353,13 @@ def test_two_sets_of_waves(m, k, n, sums):
     assert torch.equal(got[keep], want[keep]) and not got[m // 2].isfinite().any()
 
 
+@pytest.mark.parametrize("m,k,n,images", [(130, 384, 704, 2), (390, 8064, 960, 3), (333, 2048, 8208, 1),
+                                          (150, 2048, 1104, 1)])
+def test_grad_two_sets_of_waves(m, k, n, images):
+    check_grad(m, k, n, images, "gelu")
+    check_grad(m, k, n, images, "none", dyt=F32, gate=None)
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("m,images", [(1, 1), (20, 4), (64, 2)])
 def test_grad_of_few_rows_with_and_without_dgate(act, m, images):

@@ -529,9 +529,8 @@ struct GradWeights {
   v8i o0, o1;               // rows 0, 1 and rows 2, 3
 
   __device__ __forceinline__ GradWeights(const svdq::AwqWeight& a, const svdq::AwqWeight& b, int K,
-                                         int N, int chunks, int64_t k0)
+                                         int N, int chunks, int64_t k0, int t = int(threadIdx.x))
       : wa(a), wb(b), N(N), chunks(chunks) {
-    const int t = threadIdx.x;
     j = t & 7;
     quad = (t >> 3) & 15;
     kr = 64 * (t >> 7) + 8 * j;
@@ -608,32 +607,79 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void grad_mid_kernel(
     store_wave_tile<RBL, CBL, false>(acc, none, eb, lane, row0, col0, p.M, K, dX);
 }
 
-// `fine`: the product of the layer with an epilogue.  The older products keep the slices
+// The same tile of one layer's product by two such sets of four waves, each with half of a
+// slice's chunks and LDS of its own; dX in bf16.
+__global__ __launch_bounds__(2 * svdq_mid::NT, 2) void grad_twin_kernel(
+    svdq_mid::Args p, svdq::AwqWeight wa, int K, int N, int S, int tiles, void* __restrict__ dX,
+    float* __restrict__ part) {
+  using namespace svdq_mid;
+  __shared__ ChunkA a0[2], a1[2], a2[2];
+  __shared__ ChunkB b0[2], b1[2];
+  const int lane = threadIdx.x & 63, tid = threadIdx.x & (svdq_mid::NT - 1);
+  const int half = __builtin_amdgcn_readfirstlane(threadIdx.x / svdq_mid::NT);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slice = blockIdx.x / tiles;
+  int64_t m0, k0;
+  tile_at(int(blockIdx.x % tiles), (p.M + BM - 1) / BM, (K + BN - 1) / BN, BM, BN, m0, k0);
+  v16f acc[RBL][CBL], sum[1][CBL];
+  zero_acc(acc);
+  GradWeights w(wa, wa, K, N, p.chunks, k0, tid);
+  const int c0 = int(int64_t(slice) * p.chunks / S), c2 = int(int64_t(slice + 1) * p.chunks / S);
+  const int c1 = (c0 + c2 + 1) / 2;
+  tile_product(p, m0, half ? c1 : c0, half ? c2 : c1, w, a0[half], a1[half], a2[half], b0[half],
+               b1[half], acc, tid);
+  // a barrier a chunk, which the half with one chunk less makes up for
+  if (half && c2 - c1 < c1 - c0) __builtin_amdgcn_s_barrier();
+  add_halves(acc, half, wave, lane, b0, b1, sum);
+  const int64_t row0 = m0 + (wave >> 1) * 64 + 32 * half, col0 = k0 + (wave & 1) * 64;
+  __syncthreads();
+  float* const eb = reinterpret_cast<float*>(wave == 0   ? &a0[half].v
+                                              : wave == 1 ? &a1[half].v
+                                              : wave == 2 ? &a2[half].v
+                                                          : &b0[half].v);
+  const float none[CBL] = {0.f, 0.f};
+  if (S > 1)
+    store_wave_tile<1, CBL, false>(sum, none, eb, lane, row0, col0, p.M, K,
+                                   part + int64_t(slice) * p.M * K);
+  else
+    store_wave_tile<1, CBL, true>(sum, none, eb, lane, row0, col0, p.M, K, dX);
+}
+
+svdq_plan::Shape shape_of(int64_t K, int64_t N, int layers, bool twin) {
+  const int64_t chunks = (N + 63) / 64 * layers;
+  return {chunks, (K + 255) / 256, (K + 127) / 128, layers * K * N, twin};
+}
+
+// `twin`: the product of the layer with an epilogue.  The older products keep the slices
 // that they have had, and with them their results to the bit.
-int mid_slices(int64_t M, int64_t K, int64_t N, int layers, bool fine) {
-  const int64_t tiles = (M + 127) / 128 * ((K + 127) / 128), chunks = (N + 63) / 64 * layers;
-  return fine ? svdq_mid::fine_slices(tiles, chunks) : svdq_mid::slices(tiles, chunks);
+svdq_plan::Medium medium(int64_t M, int64_t K, int64_t N, int layers, bool twin) {
+  const svdq_plan::Shape shape = shape_of(K, N, layers, twin);
+  if (twin) return svdq_plan::medium(M, shape);
+  return {svdq_mid::slices((M + 127) / 128 * shape.mid_n, shape.chunks), false, 0};
 }
 
 // dX = A0 wd0 [+ A1 wd1]
 svdq_status launch_mid(const uint16_t* A0, const uint16_t* A1, const svdq::AwqWeight* w,
                        int layers, int64_t M, int64_t K, int64_t N, void* dX, bool xbf16,
-                       float* part, bool fine, hipStream_t s) {
+                       float* part, bool twin, hipStream_t s) {
   const int64_t tiles = (M + 127) / 128 * ((K + 127) / 128);
-  const int S = mid_slices(M, K, N, layers, fine);
+  const svdq_plan::Medium f = medium(M, K, N, layers, twin);
+  const int S = f.S;
   svdq_mid::Args p{{A0, A1}, N, int((N + 63) / 64), layers, int(M)};
-  hipLaunchKernelGGL(grad_mid_kernel, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, s, p, w[0],
-                     w[layers - 1], int(K), int(N), S, int(tiles), dX, xbf16, part);
+  if (f.twin)
+    hipLaunchKernelGGL(grad_twin_kernel, dim3(unsigned(tiles * S)), dim3(2 * svdq_mid::NT), 0, s, p,
+                       w[0], int(K), int(N), S, int(tiles), dX, part);
+  else
+    hipLaunchKernelGGL(grad_mid_kernel, dim3(unsigned(tiles * S)), dim3(svdq_mid::NT), 0, s, p, w[0],
+                       w[layers - 1], int(K), int(N), S, int(tiles), dX, xbf16, part);
   SVDQ_TRY(svdq::check_launch("awq_grad (mid)"));
   return S == 1 ? SVDQ_OK : launch_sum(part, S, M, K, dX, xbf16, s);
 }
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-int64_t wide_rows(int64_t M, int64_t K, int64_t N, int layers) {
-  if (M <= ROWS) return 0;
-  return svdq_plan::wide_rows(
-      M, {pad64(N) / 64 * layers, (K + 255) / 256, (K + 127) / 128, layers * K * N});
+int64_t wide_rows(int64_t M, int64_t K, int64_t N, int layers, bool twin = false) {
+  return M <= ROWS ? 0 : svdq_plan::wide_rows(M, shape_of(K, N, layers, twin));
 }
 
 size_t transposed_bytes(int64_t K, int64_t N, int layers) {
@@ -641,10 +687,10 @@ size_t transposed_bytes(int64_t K, int64_t N, int layers) {
 }
 
 // bytes of the partial sums of `rows` rows
-size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers, bool fine = false) {
+size_t part_bytes(int64_t rows, int64_t K, int64_t N, int layers, bool twin = false) {
   if (rows == 0) return 0;
   const int S =
-      rows <= ROWS ? split(rows, K, N, layers).slices : mid_slices(rows, K, N, layers, fine);
+      rows <= ROWS ? split(rows, K, N, layers).slices : medium(rows, K, N, layers, twin).S;
   return S == 1 ? 0 : svdq::align256(size_t(S) * size_t(rows) * size_t(K) * 4);
 }
 
@@ -665,14 +711,14 @@ svdq_status launch_wide(const uint16_t* A0, const uint16_t* A1, const svdq::AwqW
   return svdq::check_launch("grad_wide");
 }
 
-size_t linear_grad_bytes(int64_t M, int64_t K, int64_t N, bool fine) {
-  const int64_t w = wide_rows(M, K, N, 1);
-  return (w ? transposed_bytes(K, N, 1) : 0) + part_bytes(M - w, K, N, 1, fine);
+size_t linear_grad_bytes(int64_t M, int64_t K, int64_t N, bool twin) {
+  const int64_t w = wide_rows(M, K, N, 1, twin);
+  return (w ? transposed_bytes(K, N, 1) : 0) + part_bytes(M - w, K, N, 1, twin);
 }
 
 svdq_status linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N, svdq::AwqWeight wt,
-                        void* dX, bool xb, void* ws, bool fine, hipStream_t s) {
-  const int64_t w = wide_rows(M, K, N, 1), rest = M - w;
+                        void* dX, bool xb, void* ws, bool twin, hipStream_t s) {
+  const int64_t w = wide_rows(M, K, N, 1, twin), rest = M - w;
   uint8_t* const w8 = static_cast<uint8_t*>(ws);
   if (w) SVDQ_TRY(launch_wide(dY, dY, &wt, 1, w, K, N, dX, xb, reinterpret_cast<uint16_t*>(w8), s));
   if (!rest) return SVDQ_OK;
@@ -681,7 +727,7 @@ svdq_status linear_grad(const uint16_t* dY, int64_t M, int64_t K, int64_t N, svd
   void* const x = static_cast<uint8_t*>(dX) + w * K * (xb ? 2 : 4);
   const Rows in{d, nullptr, nullptr, nullptr, nullptr, {}, 1};
   if (rest <= ROWS) return run_rows<PLAIN>(in, rest, K, N, &wt, x, xb, part, s);
-  return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, fine, s);
+  return launch_mid(d, d, &wt, 1, rest, K, N, x, xb, part, twin, s);
 }
 
 }  // namespace
@@ -710,7 +756,7 @@ svdq_gemm::Rounds product_rounds(int64_t M, int64_t K, int64_t N) {
   const svdq_gemm::Rounds none{0, 0, 1};
   if (M <= ROWS) return none;
   const int64_t np = pad64(N);
-  const svdq_plan::Shape shape{np / 64, (K + 255) / 256, (K + 127) / 128, K * N};
+  const svdq_plan::Shape shape = shape_of(K, N, 1, true);
   double us;
   svdq_plan::wide_rows(M, shape, &us);
   const svdq_gemm::Rounds r = svdq_gemm::rounds(M, K, np / 32);

@@ -535,7 +535,7 @@ inline double mid_us(int64_t rows, const Shape& p) {
 // 4096 -> 4096, whose 96 tiles in two slices fill three quarters of the chip, 29.9 and
 // 28.3, and more tiles than compute units leave the last round emptier: 400 rows 2048 ->
 // 16384 53.7 and 48.9.  The constants are fitted to such pairs: a chunk 1.25 us with two
-// sets on a compute unit, 0.9 with one, two chunks of a twin 1.35.
+// sets on a compute unit, 0.9 with one, two chunks of a twin 1.35, the sums of slices 6 TB/s.
 struct Medium {
   int S;
   bool twin;
@@ -544,7 +544,7 @@ struct Medium {
 
 inline Medium medium(int64_t rows, const Shape& p) {
   const int64_t tiles = (rows + 127) / 128 * p.mid_n;
-  const double sums = 8.0 * double(rows) * double(p.mid_n) * 128 / 4.5e6, c = double(p.chunks);
+  const double sums = 8.0 * double(rows) * double(p.mid_n) * 128 / 6e6, c = double(p.chunks);
   const int S = svdq_mid::fine_slices(tiles, p.chunks);
   Medium m{S, false, (S == 1 ? 3 : 6 + S * sums) +
                          (tiles * S <= 256 ? 0.9 : 1.25) * double((tiles * S + 511) / 512) * c / S};
