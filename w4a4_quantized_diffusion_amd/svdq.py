@@ -7,6 +7,7 @@ the library is not built this module raises; there is no fallback.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -20,6 +21,7 @@ LOWRANK_GIVEN = 1
 
 _PREC = {"int4": INT4, "nvfp4": NVFP4, INT4: INT4, NVFP4: NVFP4}
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
+_U8, _I16 = torch.uint8, torch.int16
 SILU, GELU = 0, 1
 _ACT = {"silu": SILU, "gelu": GELU, SILU: SILU, GELU: GELU}
 NO_ACT = 2
@@ -431,6 +433,26 @@ def _arg(t, name, shape, dtype, dev):
     return t.data_ptr()
 
 
+def _triple(q, s, z, shape, dev, which):
+    """The addresses of an AWQ weight's codes, scales and zeros, as _arg would check them
+    (one by one that is a fifth of a small call's time on the host)."""
+    groups = shape[:-1]
+    if not (q.dtype is _U8 and s.dtype is _I16 and z.dtype is _I16 and q.shape == shape
+            and s.shape == groups and z.shape == groups
+            and q.get_device() == s.get_device() == z.get_device() == dev
+            and q.is_contiguous() and s.is_contiguous() and z.is_contiguous()):
+        _arg(q, "q" + which, shape, _U8, dev)
+        _arg(s, "scales" + which, groups, _I16, dev)
+        _arg(z, "zeros" + which, groups, _I16, dev)
+    return q.data_ptr(), s.data_ptr(), z.data_ptr()
+
+
+@functools.lru_cache(1024)
+def _need(l, name, *sizes):
+    """What the library's `name` says of the bytes of a workspace: a function of the sizes."""
+    return getattr(l, name)(*sizes)
+
+
 def _rows(X, name, width):
     """(M, device index) of a call's first operand [M, width]."""
     if X.dim() != 2 or X.shape[1] != width:
@@ -474,10 +496,7 @@ def _run(dev, fn, *args):
 def _awq_args(layer, K, N, dev, which=""):
     if layer["K"] != K or layer["N"] != N:
         raise ValueError(f"layer{which} is {layer['N']} x {layer['K']}, expected {N} x {K}")
-    g = K // 64
-    return (_arg(layer["q"], "q" + which, (g, N, 32), torch.uint8, dev),
-            _arg(layer["scales"], "scales" + which, (g, N), torch.int16, dev),
-            _arg(layer["zeros"], "zeros" + which, (g, N), torch.int16, dev))
+    return _triple(layer["q"], layer["scales"], layer["zeros"], (K // 64, N, 32), dev, which)
 
 
 def _out_dtype(Y, dtype, name):
@@ -718,7 +737,7 @@ def svdq_block_norm_grad(dy, x, h=None, dx_out=None, kind="layer", eps=1e-6, pos
     dx = torch.empty_like(x)
     grads = [x.new_empty(t.shape, dtype=torch.float32) if t is not None and n else None
              for t, n in zip(vectors, need)]
-    keep, ws, nws = _ws(workspace, l.svdq_block_norm_grad_workspace_bytes(M, D, images), x, dev)
+    keep, ws, nws = _ws(workspace, _need(l, "svdq_block_norm_grad_workspace_bytes", M, D, images), x, dev)
     _run(dev, l.svdq_block_norm_grad, dyp, dyt, dop, xp, xt, hp, ht, M, D, images, _NORM[kind], eps,
          *v, dx.data_ptr(), dhp, *[None if t is None else t.data_ptr() for t in grads], ws, nws)
     return (dx, dh, *grads)
@@ -747,7 +766,7 @@ def awq_linear_w4a16_res(X, layer, bias=None, act="none", gate=None, residual=No
     Y = _out(Y, "Y", (M, N), yt, X, dev)
     Z = X.new_empty((M, N)) if save else None
     b = None if bias is None else _arg(bias, "bias", (N,), torch.bfloat16, dev)
-    keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_res_workspace_bytes(M, K, N), X, dev)
+    keep, ws, nws = _ws(workspace, _need(l, "awq_linear_w4a16_res_workspace_bytes", M, K, N), X, dev)
     _run(dev, l.awq_linear_w4a16_res, x, M, K, N, layer["group"], *_awq_args(layer, K, N, dev), b,
          _ACT_OR_NONE[act], g, images, r, rt, Y.data_ptr(), _DT[yt],
          Z.data_ptr() if save else None, ws, nws)
@@ -775,8 +794,8 @@ def awq_linear_w4a16_res_grad(dY, Z, layer, act="none", gate=None, workspace=Non
     dgate = None
     if gate is not None and need_dgate:
         dgate = dY.new_empty(gate.shape, dtype=torch.float32)
-    keep, ws, nws = _ws(workspace, l.awq_linear_w4a16_res_grad_workspace_bytes(M, K, N, images), dY,
-                        dev)
+    need = _need(l, "awq_linear_w4a16_res_grad_workspace_bytes", M, K, N, images)
+    keep, ws, nws = _ws(workspace, need, dY, dev)
     _run(dev, l.awq_linear_w4a16_res_grad, d, dt, z, M, K, N, layer["group"],
          *_awq_args(layer, K, N, dev), _ACT_OR_NONE[act], g, images,
          dX.data_ptr(), dZ.data_ptr(), None if dgate is None else dgate.data_ptr(), ws, nws)
@@ -793,10 +812,7 @@ def _experts_args(lay, E, K, N, dev, which):
     if lay["E"] != E or lay["K"] != K or lay["N"] != N:
         raise ValueError(f"{which} is {lay['E']} x {lay['N']} x {lay['K']}, expected "
                          f"{E} x {N} x {K}")
-    g = K // 64
-    return (_arg(lay["q"], "q_" + which, (E, g, N, 32), torch.uint8, dev),
-            _arg(lay["scales"], "scales_" + which, (E, g, N), torch.int16, dev),
-            _arg(lay["zeros"], "zeros_" + which, (E, g, N), torch.int16, dev))
+    return _triple(lay["q"], lay["scales"], lay["zeros"], (E, K // 64, N, 32), dev, "_" + which)
 
 
 def awq_moe_w4a16(X, logits, gate, up, down, top, act="silu", renorm=True, routing=False,
@@ -817,7 +833,7 @@ def awq_moe_w4a16(X, logits, gate, up, down, top, act="silu", renorm=True, routi
         ids = X.new_empty((T, top), dtype=torch.int32)
         w = X.new_empty((T, top), dtype=torch.float32)
         ip, wp = ids.data_ptr(), w.data_ptr()
-    keep, ws, nws = _ws(workspace, l.awq_moe_w4a16_workspace_bytes(T, E, top, K, N), X, dev)
+    keep, ws, nws = _ws(workspace, _need(l, "awq_moe_w4a16_workspace_bytes", T, E, top, K, N), X, dev)
     _run(dev, l.awq_moe_w4a16, x, lg, lt, T, E, top, K, N, gate["group"],
          *_experts_args(gate, E, K, N, dev, "gate"), *_experts_args(up, E, K, N, dev, "up"),
          *_experts_args(down, E, N, K, dev, "down"), _ACT[act], 1 if renorm else 0, Y.data_ptr(),
