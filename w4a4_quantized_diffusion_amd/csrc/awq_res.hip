@@ -512,9 +512,8 @@ struct RowWeights {
   }
 };
 
-// 333 rows 8192 -> 2064 in 8 slices of 51 tiles: 25 us (0.44 PFLOP/s) and 6 for the sums.
-// Dequantization and MFMAs add up on a SIMD, 408 workgroups fill 80% of the places, and 22
-// MB of partial sums are written and read; 5, 6, 7 and 10 slices take as long or longer.
+// One set of four waves a tile (svdq_plan::medium says when): 333 rows 4096 -> 4096 28.3 us
+// with the sums (0.39 PFLOP/s).
 template <int ACT>
 __global__ __launch_bounds__(svdq_mid::NT, 2) void res_mid_kernel(svdq_mid::Args p,
                                                                   svdq::AwqWeight wt, int N, int S,
@@ -549,7 +548,12 @@ __global__ __launch_bounds__(svdq_mid::NT, 2) void res_mid_kernel(svdq_mid::Args
 }
 
 // The same tile by two such sets of four waves, each with half of a slice's chunks and LDS
-// of its own.
+// of its own.  333 rows 8192 -> 2064 in 5 slices of 51 tiles: 22-24 us (0.47-0.51 PFLOP/s)
+// and 5 for the sums; one set a workgroup in 8 slices took 25 and 6.  Copies of the loop
+// that only load take 13 us less the sums, and without the dequantization, the MFMAs or the LDS
+// reads alone 6, 5 and 4 less: loads, vector, matrix and LDS work share a SIMD's two waves
+// without hiding one another fully.  Runs of tiles for each XCD gain 5% at some sizes and
+// cost 15% at others.
 template <int ACT>
 __global__ __launch_bounds__(2 * svdq_mid::NT, 2) void res_twin_kernel(svdq_mid::Args p,
                                                                        svdq::AwqWeight wt, int N,

@@ -15,7 +15,7 @@
 // the norm as the fp32 sum, before it is rounded to X's type.
 //
 // Measured: 9216 rows of 4096, layer norm, gate, scale and shift, bf16: 302 MB in 55.6 us,
-// 5.4 TB/s (a large copy: 5.3).  333 rows of 5455, fp32 and bf16, with a post norm 10.4 us,
+// 5.4 TB/s (a large copy: 5.3).  333 rows of 5455, an fp32 stream, with a post norm 10.4 us,
 // 2.4 TB/s: 1.3 rounds of workgroups, each a chain of loads, four sums over the
 // workgroup and stores that few others hide.  One row 2.6 us, a launch.
 
