@@ -277,8 +277,8 @@ __device__ __forceinline__ void lds_barrier() {
 // flight.  (One token runs through the code once: a loop that also unrolled the ends of
 // the items took 12 us instead of 9 for it, most of that waiting for instructions.)
 //
-// Measured: 61 tokens, 6 of 40 experts, 4096 x 1408: 245 MB of codes and scales in 67-77
-// us, 3.2-3.7 TB/s.  The vector units are busy 57% of the cycles, with 2.4-3 instructions
+// Measured: 61 tokens, 6 of 40 experts, 4096 x 1408: 260 MB of codes and scales in 67-72
+// us, 3.6-3.9 TB/s.  The vector units are busy 57% of the cycles, with 2.4-3 instructions
 // a code for the dequantization and the routing of operands; a copy of the kernel that only
 // loads takes 55 us, and what is left between is the two not overlapping fully.  Three and four
 // chunks ahead, 4 or 16 waves a workgroup and 6 waves a SIMD gain nothing; a workgroup per
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
 // flight.  With S > 1 a third launch adds the slices' sums (the workgroup of a column
 // block that ends last could, but its fences write the L2 back and took 9 us).
 //
-// Measured: 61 tokens as above 123 MB in 42-44 us, 2.9 TB/s, and 4-5 for the sums; one token
+// Measured: 61 tokens as above 130 MB in 42-44 us, 3.0 TB/s, and 4-5 for the sums; one token
 // 5.8 us.  A copy that only loads takes 30 us; the rest is the dequantization, an expert's
 // sums in LDS and the fewer bytes in flight at their turn.
 
