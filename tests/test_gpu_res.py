@@ -353,6 +353,37 @@ def test_two_sets_of_waves(m, k, n, sums):
     assert torch.equal(got[keep], want[keep]) and not got[m // 2].isfinite().any()
 
 
+@pytest.mark.parametrize("m,k,n", [(333, 8192, 2064), (390, 960, 8064), (64, 8192, 144), (65, 8192, 128)])
+def test_two_at_once_and_replayed(m, k, n):
+    """Calls on two streams and in a graph that share nothing but their inputs."""
+    p = problem(m, k, n)
+    dy, z = bf((m, n), 8), bf((m, n), 9)
+    both = lambda: (call(p, "gelu"),) + svdq.awq_linear_w4a16_res_grad(dy, z, p["w"][0], "gelu",
+                                                                       p["gate"])
+    want = both()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(both())
+    torch.cuda.synchronize()
+    for other in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for i in range(3):
+        p["x"].copy_(torch.roll(p["x"], 1, 1))
+        dy.copy_(torch.roll(dy, 1, 1))
+        graph.replay()
+        want = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), i
+
+
 @pytest.mark.parametrize("m,k,n,images", [(130, 384, 704, 2), (390, 8064, 960, 3), (333, 2048, 8208, 1),
                                           (150, 2048, 1104, 1)])
 def test_grad_two_sets_of_waves(m, k, n, images):
