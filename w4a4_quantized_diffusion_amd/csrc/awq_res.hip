@@ -730,7 +730,7 @@ svdq_status wide(const Call& c, uint16_t* B, const svdq_gemm::Rounds& r, float* 
 // A wave takes 512 columns, 8 to a lane, and every fourth pair of rows of a workgroup's;
 // the workgroup's sums for dgate meet in LDS and, where an image has more workgroups than
 // one, in a second launch in a fixed order.  Memory bound: 4608 rows of 12288, 340 MB, 66
-// us, 5.2 TB/s, and 7 for the sums.
+// us, 5.2 TB/s, and 5 for the sums.
 
 constexpr int PAIR = 2;                  // rows whose loads a wave has in flight together
 

@@ -361,13 +361,13 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(svdq::BlockNorm a, int
 // workgroups' sums are joined, and multiplied, by a second launch in a fixed order.
 //
 // Measured: 9216 rows of 4096, post norm and all five gradients, bf16: 453 MB in 102 us,
-// 4.4 TB/s, and 10 us for the join.  Between memory and the chain of a row: two or four
+// 4.4 TB/s, and 8 us for the join.  Between memory and the chain of a row: two or four
 // sums over the workgroup follow one another in each row, and the registers of a row,
 // the next row and the column sums leave two workgroups a compute unit to hide
 // them.  (Five column sums
 // spilled: 436 us with them; 175 with three; 111 with the sums over the workgroup in row
 // operations of the lanes and the switched-off parts compiled out.)  20 rows of 2048 take
-// 4.5 us and the join 3.4.
+// 4.5 us and the join 3.6.
 
 enum { POST, GATE, WEIGHT, SCALE, SHIFT, VECTORS };
 
@@ -580,11 +580,15 @@ __global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void blo
   put(g.sums[2], accS, one, 1.f, 0.f);
 }
 
-// 64 columns and 16 waves a workgroup; every wave adds its share of the parts, one after
+constexpr int JOIN_WAVES = 8;
+
+// 64 columns and 8 waves a workgroup; every wave adds its share of the parts, one after
 // the other, and the waves' sums meet in LDS.  The fixed order is what two calls with the
 // same bits need (atomics on the gradients would be one launch).
-__global__ __launch_bounds__(1024) void join_kernel(svdq::Joins j, int64_t total, int D) {
-  __shared__ float red[16][64];
+// 512 parts of 4096 columns in five sums 8.4 us (16 waves 10.2, 4 waves 9.2), 72 parts of
+// 12288 5.3 (7.0, 5.3), 20 parts of 2048 3.8 (3.7, 4.4).
+__global__ __launch_bounds__(64 * JOIN_WAVES) void join_kernel(svdq::Joins j, int64_t total, int D) {
+  __shared__ float red[JOIN_WAVES][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int across = (D + 63) / 64;
@@ -610,20 +614,20 @@ __global__ __launch_bounds__(1024) void join_kernel(svdq::Joins j, int64_t total
       for (int64_t r = 0; r < runs; ++r, p += each * D) {
         float t = 0.f;
         int64_t i = wave;
-        for (; i + 112 < each; i += 128) {
+        for (; i + 7 * JOIN_WAVES < each; i += 8 * JOIN_WAVES) {
           float v[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = p[(i + 16 * q) * D];
+          for (int q = 0; q < 8; ++q) v[q] = p[(i + JOIN_WAVES * q) * D];
           t += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
-        for (; i < each; i += 16) t += p[i * D];
+        for (; i < each; i += JOIN_WAVES) t += p[i * D];
         s += vary ? t * factor(r) : t;
       }
     }
     red[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && col < D) {
-      for (int w = 1; w < 16; ++w) s += red[w][lane];
+      for (int w = 1; w < JOIN_WAVES; ++w) s += red[w][lane];
       j.to[k][image * D + col] = vary || n == 0 ? s : s * factor(image);
     }
     __syncthreads();
@@ -706,8 +710,8 @@ svdq_status launch_joins(const Joins& j, int64_t D, hipStream_t s) {
   int64_t blocks = 0;
   for (int k = 0; k < j.count; ++k) blocks += (D + 63) / 64 * j.each[k];
   if (!blocks) return SVDQ_OK;
-  hipLaunchKernelGGL(join_kernel, dim3(unsigned(std::min(blocks, MOST_GROUPS))), dim3(1024), 0, s, j,
-                     blocks, int(D));
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned(std::min(blocks, MOST_GROUPS))),
+                     dim3(64 * JOIN_WAVES), 0, s, j, blocks, int(D));
   return check_launch("join");
 }
 
