@@ -124,6 +124,9 @@ __device__ __forceinline__ void value(const Raw<V>& r, bool b16, float (&v)[V]) 
   }
 }
 
+// (Ordinary stores.  Non-temporal ones make the kernel alone up to a fifth faster, 9216 rows of
+// 2048 31.0 -> 25.4 us, but the product that reads its output loses more: norm, product and
+// product on 4608 rows of 4096 together 335 us and 341 so, on 64 rows 34.8 and 36.3.)
 template <int V, int C, int TAIL>
 __device__ __forceinline__ void store(const Cut<V, C, TAIL>& cut, int c, void* p, bool b16,
                                       int64_t first, const float (&v)[V]) {
