@@ -52,6 +52,8 @@ __device__ __forceinline__ int64_t gate_at(const ResEpilogue& e, int m, int64_t 
 }
 
 // V (4 or 8) neighbouring outputs of row m from column n on: z = acc + bias
+// (Non-temporal stores: many rows alone 1-10% faster, 4300 rows 1024 -> 4096 60.5 us for 67,
+// and blocks of norm and products one behind the other as fast as with ordinary ones.)
 template <int ACT, int V>
 __device__ __forceinline__ void emit(const ResEpilogue& e, int m, int64_t n, int64_t N,
                                      float (&z)[V]) {
