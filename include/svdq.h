@@ -392,8 +392,9 @@ svdq_status awq_linear_w4a16_grad(const uint16_t* dY, int64_t M, int64_t K, int6
  *   x' = X + gate * t                 (x' = X without H; gate counts as 1 if absent)
  *   Y  = n(x') * weight * (1 + scale) + shift      (absent: 1, 0 and 0)
  * n(v) along a row of D: SVDQ_LAYER_NORM (v - mean v) / sqrt(var v + eps) (var over
- * D values), SVDQ_RMS_NORM v / sqrt(mean v^2 + eps).  All of it is fp32 until X_out
- * (x') and Y are rounded, once each; Y comes from the unrounded x'.
+ * D values), SVDQ_RMS_NORM v / sqrt(mean v^2 + eps).  All of it is fp32 (the mean's
+ * sum: 64 bits) until X_out (x') and Y are rounded, once each; Y comes from the
+ * unrounded x'.
  * X, X_out [M, D] x_dtype, H [M, D] h_dtype, Y [M, D] y_dtype, contiguous, DEVICE,
  * aligned to their elements (16-byte addresses and D % 8 == 0 run fastest).  H and
  * X_out are both given or both NULL.  Each vector is NULL or a svdq_vec (HOST struct):

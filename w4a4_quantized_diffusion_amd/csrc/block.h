@@ -18,6 +18,7 @@ struct BlockNorm {
   bool x16, h16, layer;
   int64_t D, images, rows;  // rows of one image
   float eps;
+  double per;             // 1 / D
   Vec post, gate, weight, scale, shift;
 };
 

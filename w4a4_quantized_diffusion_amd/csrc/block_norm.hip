@@ -10,9 +10,12 @@
 //
 // One workgroup takes one row at a time and keeps it in registers between the
 // sums, so every matrix is read and written once: the bound is memory.  Sums are
-// fp32; the variance is summed from the differences to the mean (a second sum over
-// registers, where sum v^2 - mean^2 would lose the digits of a large mean).  x' enters
-// the norm as the fp32 sum, before it is rounded to X's type.
+// fp32, but for the mean's, which is 64 bits wide: an error of the mean of a few units of
+// its last place is in every n of the row, r times it, and no small one where the mean is
+// large against the deviation; and 2^14 equal values sum up exactly, so that their
+// differences are zeros.  The variance is summed from the differences to the mean (a
+// second sum over registers, where sum v^2 - mean^2 would lose the digits of a large
+// mean).  x' enters the norm as the fp32 sum, before it is rounded to X's type.
 //
 // Measured: 9216 rows of 4096, layer norm, gate, scale and shift, bf16: 302 MB in 55.6 us,
 // 5.4 TB/s (a large copy: 5.3).  333 rows of 5455, an fp32 stream, with a post norm 10.4 us,
@@ -162,10 +165,31 @@ __device__ __forceinline__ float row_sum(float v) {
   return add_dpp<0x118>(add_dpp<0x114>(add_dpp<0x112>(add_dpp<0x111>(v))));
 }
 
+// the same in 64 bits
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double add_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(b)), CTRL, ROWS, 0xF, true));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(b >> 32)), CTRL, ROWS, 0xF, true));
+  return v + __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double row_sum(double v) {
+  return add_dpp<0x118>(add_dpp<0x114>(add_dpp<0x112>(add_dpp<0x111>(v))));
+}
+__device__ __forceinline__ double lane_of(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(b)), l));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(b >> 32)), l));
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
 // the sum over a wave, in every lane (row_bcast 15 and 31 join the rows)
 __device__ __forceinline__ float wave_sum(float v) {
   v = add_dpp<0x143, 0xC>(add_dpp<0x142, 0xA>(row_sum(v)));
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  return lane_of(add_dpp<0x143, 0xC>(add_dpp<0x142, 0xA>(row_sum(v))), 63);
 }
 
 // Sums over a workgroup, in every thread: of the waves, then of the waves' sums, which 16
@@ -209,6 +233,20 @@ struct Sums {
     __syncthreads();
     a = from(read(), 15);
   }
+  // (the halves of a wave's sum in the two sets)
+  __device__ __forceinline__ void operator()(double& a) {
+    a = wave_sum(a);
+    if (waves == 1) return;
+    turn ^= 1;
+    const uint64_t b = __builtin_bit_cast(uint64_t, a);
+    uint32_t(*const w)[MAX_WAVES] = reinterpret_cast<uint32_t(*)[MAX_WAVES]>(red[turn]);
+    w[0][wave] = uint32_t(b);
+    w[1][wave] = uint32_t(b >> 32);
+    __syncthreads();
+    const int i = lane & 15;
+    const uint64_t v = uint64_t(w[1][i]) << 32 | w[0][i];
+    a = lane_of(row_sum(i < waves ? __builtin_bit_cast(double, v) : 0.), 15);
+  }
 };
 
 template <int V, int C>
@@ -219,20 +257,24 @@ struct Row {
 // v -> n(v); returns 1 / deviation.  Elements past D hold zeros before and after.
 template <int V, int C, int TAIL>
 __device__ __forceinline__ float normalize(Row<V, C>& r, const Cut<V, C, TAIL>& cut, bool layer, int D,
-                                           float eps, Sums& sum) {
+                                           double per, float eps, Sums& sum) {
   const float inv = 1.f / float(D);
   if (layer) {
-    float s = 0.f;
+    double s = 0.;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += r.v[c][i];
+      for (int i = 0; i < V; ++i) s += double(r.v[c][i]);
     sum(s);
-    const float mean = s * inv;
+    // s / D: the product with the reciprocal, and what it leaves of s (a sum of D equal
+    // values gives the value); in two fp32 numbers, of which v - hi takes the first exactly
+    // where the mean is large against the differences
+    const double q = s * per, mean = fma(fma(-q, double(D), s), per, q);
+    const float hi = float(mean), lo = float(mean - double(hi));
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < V; ++i) r.v[c][i] = cut.in(c, i) ? r.v[c][i] - mean : 0.f;
+      for (int i = 0; i < V; ++i) r.v[c][i] = cut.in(c, i) ? (r.v[c][i] - hi) - lo : 0.f;
   }
   float s = 0.f;
 #pragma unroll
@@ -284,7 +326,7 @@ __device__ __forceinline__ void norm_row(const svdq::BlockNorm& a, int64_t row, 
       for (int i = 0; i < V; ++i) t.v[c][i] = cut.in(c, i) ? t.v[c][i] : 0.f;
     }
     if (a.post.p) {
-      normalize(t, cut, a.layer, D, a.eps, sum);
+      normalize(t, cut, a.layer, D, a.per, a.eps, sum);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float f[V];
@@ -312,7 +354,7 @@ __device__ __forceinline__ void norm_row(const svdq::BlockNorm& a, int64_t row, 
 #pragma unroll
     for (int i = 0; i < V; ++i) xn.v[c][i] = cut.in(c, i) ? xn.v[c][i] : 0.f;
   }
-  normalize(xn, cut, a.layer, D, a.eps, sum);
+  normalize(xn, cut, a.layer, D, a.per, a.eps, sum);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (C > 1) behind(c);
@@ -496,7 +538,7 @@ __global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void blo
       fetch(min(row + 1, r1 - 1));
     }
     float rh = 1.f;
-    if (POST_NORM) rh = normalize(t, cut, LAYER, D, a.eps, sum);
+    if (POST_NORM) rh = normalize(t, cut, LAYER, D, a.per, a.eps, sum);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float f[V];
@@ -505,7 +547,7 @@ __global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void blo
       for (int i = 0; i < V; ++i) n.v[c][i] = fmaf(f[i], t.v[c][i], n.v[c][i]);
     }
     if (LONG) fetch_dy(row);
-    const float r = normalize(n, cut, LAYER, D, a.eps, sum);
+    const float r = normalize(n, cut, LAYER, D, a.per, a.eps, sum);
     if (LONG) take(dy, dyr, true, y16);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll

@@ -801,7 +801,7 @@ svdq_status svdq_block_norm(const void* X, svdq_dtype x_dtype, const void* H, sv
   TRY(check_norm(M, D, images, kind, eps));
   if (M == 0) return SVDQ_OK;
   svdq::BlockNorm a{X, H, x_dtype == SVDQ_BF16, h_dtype == SVDQ_BF16, kind == SVDQ_LAYER_NORM, D,
-                    images, M / images, eps};
+                    images, M / images, eps, 1. / double(D)};
   Span spans[9];
   TRY(check_ptr(X, "X", elem(x_dtype)));
   TRY(take_vecs({post, gate, weight, scale, shift}, H != nullptr, D, images, a, spans));
@@ -841,7 +841,7 @@ svdq_status svdq_block_norm_grad(const void* dY, svdq_dtype y_dtype, const void*
   if (H || dH) TRY(check_dtype(h_dtype, "h_dtype"));
   TRY(check_norm(M, D, images, kind, eps));
   svdq::BlockNorm a{X, H, x_dtype == SVDQ_BF16, h_dtype == SVDQ_BF16, kind == SVDQ_LAYER_NORM, D,
-                    images, M / images, eps};
+                    images, M / images, eps, 1. / double(D)};
   const svdq::BlockNormGrad g{dY, dX_out, dX, dH, y_dtype == SVDQ_BF16};
   Span spans[17];
   // (without rows there is no H to go by)
