@@ -652,7 +652,8 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void join_kernel(svdq::Joins j, in
     };
     // where the factor changes along the sum, image by image
     const bool vary = f.p && f.ld && j.each[k] == 1 && j.images > 1;
-    const int64_t each = vary ? j.parts : n, runs = vary ? j.images : 1;
+    // (no parts: no factors either, of which one may be infinite)
+    const int64_t each = vary ? j.parts : n, runs = n == 0 ? 0 : vary ? j.images : 1;
     float s = 0.f;
     if (col < D) {
       const float* p = j.from[k] + image * n * D + col;
