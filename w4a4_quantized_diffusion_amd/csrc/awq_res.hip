@@ -894,10 +894,20 @@ svdq_status launch_awq_res_grad(const void* dY, bool dy16, const uint16_t* Z, in
   // one workgroup's sums are the gradient
   const bool direct = images * parts == each;
   float* const part = !dgate ? nullptr : direct ? dgate : reinterpret_cast<float*>(w8);
-  hipLaunchKernelGGL(dy16 ? by_act<GradKernel>(act) : by_act<GradKernel32>(act),
-                     dim3(unsigned((N + 511) / 512 * images * parts)), dim3(256), 0, s, dY, Z, gate,
-                     rows, parts, int(N), dZ, part);
-  SVDQ_TRY(check_launch("awq_res_grad"));
+  auto k = dy16 ? by_act<GradKernel>(act) : by_act<GradKernel32>(act);
+  // a launch of at most 2^23 workgroups (a grid has fewer than 2^32 threads): 2^20 images
+  // of one row take several from 8 x 512 columns on
+  const int64_t blocks = (N + 511) / 512, most = (int64_t(1) << 23) / (blocks * parts);
+  const int64_t step = std::max<int64_t>(1, most);
+  for (int64_t i = 0; i < images; i += step) {
+    const int64_t n = std::min(step, images - i), at = i * rows * N;
+    Vec g = gate;
+    if (g.p) g.p = static_cast<const uint8_t*>(g.p) + i * g.ld * (g.b16 ? 2 : 4);
+    hipLaunchKernelGGL(k, dim3(unsigned(blocks * n * parts)), dim3(256), 0, s,
+                       static_cast<const uint8_t*>(dY) + at * (dy16 ? 2 : 4), Z ? Z + at : nullptr, g,
+                       rows, parts, int(N), dZ + at, part ? part + i * parts * N : nullptr);
+    SVDQ_TRY(check_launch("awq_res_grad"));
+  }
   j.parts = parts;
   if (dgate && !direct) j.add(part, dgate, each);
   SVDQ_TRY(launch_joins(j, N, s));
