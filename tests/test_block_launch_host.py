@@ -144,3 +144,36 @@ def test_res_grad_launches_fit(record, images, rows, n, dgate):
             assert gate == (6 << 40) + done * n * 2
             done += groups // (blocks * parts)
         assert done == images
+
+
+CALLS = [["norm_grad", [m, d, images, dt]] for m, d, images in ((6, 8200, 2), (4, 16384, 1), (9, 12288, 3))
+         for dt in (0, 1)]
+CALLS += [["moe", a] for a in ([64, 8, 2, 4096, 128], [40, 64, 8, 2048, 256], [64, 2, 2, 8192, 64],
+                               [50, 40, 6, 1024, 192], [33, 4, 2, 8256, 64], [1, 8, 2, 8192, 128])]
+
+
+def test_lds_attribute_is_one_value_per_function(record):
+    """Functions that need more than 64 KB of dynamic LDS get one value of the attribute,
+    whatever the call's size: two host threads with calls of two sizes cannot lower it
+    between each other's setting and launch."""
+    values, large = {}, set()
+    for launches in record(CALLS + CALLS[::-1]):
+        for kernel, _, _, shm, attr, _ in launches:
+            assert shm <= (attr if attr is not None else 64 << 10) <= 160 << 10, kernel
+            if attr is not None:
+                values.setdefault(kernel, set()).add(attr)
+            if shm > 64 << 10:
+                large.add(kernel)
+    assert all(len(v) == 1 for v in values.values()), values
+    assert any("block_norm_grad" in k for k in large) and any("moe_down" in k for k in large)
+
+
+def test_moe_forms(record):
+    """Wide layers need no slices: two launches, 32 columns a workgroup of the second."""
+    for k, launches in ((8192, 2), (8256, 2), (4096, 3)):
+        for t in (5, 64):
+            got, = record([["moe", [t, 8, 2, k, 128]]])
+            assert len(got) == launches
+            assert "moe_down_kernel" in got[1][0] and got[1][1] == k // 32 * (1 if launches == 2 else 2)
+    got, = record([["moe", [1, 8, 2, 8192, 128]]])
+    assert len(got) == 2 and got[1][1] == 8192 // 32
