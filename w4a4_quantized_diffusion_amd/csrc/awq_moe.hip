@@ -702,10 +702,10 @@ svdq_status launch_awq_moe(const uint16_t* X, const void* logits, bool l16, int6
   SVDQ_TRY(check_launch("awq_moe (up)"));
   const int W = p.two_columns ? 32 : 16;
   const size_t lds = size_t(DOWN_WAVES) * size_t(T) * size_t(W) * 4;
-  auto down_kernel = p.two_columns
-                         ? p.two_rows ? moe_down_kernel<2, 2> : moe_down_kernel<1, 2>
-                     : p.two_rows ? moe_down_kernel<2, 1>
-                                  : moe_down_kernel<1, 1>;
+  // (one token has no two rows of an expert)
+  auto down_kernel = !p.two_columns ? moe_down_kernel<1, 1>
+                     : p.two_rows   ? moe_down_kernel<2, 2>
+                                    : moe_down_kernel<1, 2>;
   // (the most that any call asks for: the attribute is the function's, and a host
   // thread with fewer tokens must not lower it between another's two steps)
   if (lds + sizeof(Route) > (64 << 10))
