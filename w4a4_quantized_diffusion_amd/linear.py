@@ -278,14 +278,34 @@ def _reverse_only(x):
         raise RuntimeError("this layer has no forward-mode derivative")
 
 
-def _vector(v, name, width):
+def _check_rows(rows, name, lead):
+    """Refuse a vector whose rows [*rows] are not those of the first dimensions of x
+    [*lead, K], side by side or as one number."""
+    given = tuple(rows)
+    while rows and rows[-1] == 1:
+        rows = rows[:-1]
+    if not rows or sum(d != 1 for d in lead) <= 1:
+        return               # (one dimension's rows are cut into runs, which the library checks)
+    n = 1
+    for d in lead:
+        n *= d
+        if len(rows) == 1 and rows[0] == n:
+            return
+    if len(rows) == 1 or rows != lead[:len(rows)]:
+        raise ValueError(f"{name}: its rows {given} are not the first dimensions of {tuple(lead)}")
+
+
+def _vector(v, name, width, lead):
     """A modulation vector [D], [images, D] or [images, 1, D] as the library takes it
-    (rows of adjacent values)."""
+    (rows of adjacent values), for x [*lead, K]."""
     if v is None:
         return None
     if v.dim() == 0 or v.shape[-1] != width:
         raise ValueError(f"{name}: expected [..., {width}], got {tuple(v.shape)}")
     if v.dim() > 1:
+        rows = v.shape[:-1]
+        if rows[:1] != lead[:1] or rows[1:].numel() != 1:
+            _check_rows(rows, name, lead)
         v = v.reshape(-1, width)
     if width > 1 and v.stride(-1) != 1 or v.dim() == 2 and len(v) > 1 and v.stride(0) < width:
         v = v.contiguous()
@@ -335,9 +355,9 @@ class AWQLinear(nn.Module):
 
     forward(x, act, gate, residual) computes residual + gate * act(layer(x)) in the
     layer's own kernels, each part optional: act "silu" or "gelu" (tanh form), gate [N] or
-    one row per image ([images, N] for x [images, ..., K]), residual of the output's
-    shape in fp32 or bf16, whose type the output then has.  Differentiable in x, gate and
-    residual.
+    one row per image ([images, N] or [images, 1, N] for x [images, ..., K]; [tokens, N] for
+    all tokens of all images, in order), residual of the output's shape in fp32 or bf16,
+    whose type the output then has.  Differentiable in x, gate and residual.
 
     Forward and backward can be captured into a graph together.  A backward pass
     that is captured needs leaves of its own: torch ends the process when an eager
@@ -367,7 +387,7 @@ class AWQLinear(nn.Module):
     def _res(self, x, act, gate, residual):
         lead, n = x.shape[:-1], self.out_features
         x2 = _rows(x, self.in_features)
-        gate = _vector(gate, "gate", n)
+        gate = _vector(gate, "gate", n, lead)
         y_dtype = torch.bfloat16
         if residual is not None:
             if residual.shape != (*lead, n):
@@ -610,9 +630,9 @@ class BlockNorm(nn.Module):
     the RMS norm ("rms") over the last dimension of `dim`.  weight and post are given as
     tensors (or None) and become parameters; gate, scale and shift, each optional, are
     [dim], or one row per image ([images, dim] or [images, 1, dim] for x [images, ...,
-    dim]; slices of a modulation layer's output are read where they lie).  x and h fp32 or
-    bf16, x' in x's type, y in `y_dtype`.  Differentiable once in everything, in reverse
-    mode.
+    dim]; slices of a modulation layer's output are read where they lie), or per token
+    (x's own shape).  x and h fp32 or bf16, x' in x's type, y in `y_dtype`.
+    Differentiable once in everything, in reverse mode.
 
     Forward and backward can be captured into a graph together.  A backward pass
     that is captured needs leaves of its own: torch ends the process when an eager
@@ -640,11 +660,11 @@ class BlockNorm(nn.Module):
             raise ValueError("a gate and a post norm go with h")
         if h is not None and h.shape != x.shape:
             raise ValueError(f"h: expected {tuple(x.shape)}, got {tuple(h.shape)}")
-        lead = x.shape
+        lead = x.shape[:-1]
         x2 = _norm_rows(x, self.dim)
         h2 = None if h is None else _norm_rows(h, self.dim)
-        vectors = [self.post, _vector(gate, "gate", self.dim), self.weight,
-                   _vector(scale, "scale", self.dim), _vector(shift, "shift", self.dim)]
+        vectors = [self.post, _vector(gate, "gate", self.dim, lead), self.weight,
+                   _vector(scale, "scale", self.dim, lead), _vector(shift, "shift", self.dim, lead)]
         inputs = [t for t in (x2, h2, *vectors) if t is not None]
         for t in inputs:
             _reverse_only(t)
@@ -653,8 +673,8 @@ class BlockNorm(nn.Module):
         else:
             out = svdq.svdq_block_norm(x2, h2, self.kind, self.eps, *vectors, self.y_dtype)
         if h is None:
-            return out.reshape(lead)
-        return out[0].reshape(lead), out[1].reshape(lead)
+            return out.reshape(x.shape)
+        return out[0].reshape(x.shape), out[1].reshape(x.shape)
 
     def extra_repr(self):
         return (f"{self.dim}, kind={self.kind}, eps={self.eps}, weight={self.weight is not None}, "
