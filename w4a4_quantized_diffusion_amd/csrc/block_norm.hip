@@ -655,8 +655,28 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void join_kernel(svdq::Joins j, in
     // (no parts: no factors either, of which one may be infinite)
     const int64_t each = vary ? j.parts : n, runs = n == 0 ? 0 : vary ? j.images : 1;
     float s = 0.f;
-    if (col < D) {
-      const float* p = j.from[k] + image * n * D + col;
+    const float* p = j.from[k] + image * n * D + col;
+    if (col < D && vary && j.parts < j.images) {
+      // many images: the waves take them in turn, eight at a time.  The steps that follow one
+      // another are images / 64 times parts here and images times parts / 64 below.
+      // The whole backward pass on 4608 rows of 4096, every gradient, so and in the order
+      // below: 4608 images 494 us and 3470, 512 95 and 327, 64 and 128 within 5%.
+      for (int64_t r = wave; r < runs; r += 8 * JOIN_WAVES) {
+        float t[8], g[8];
+        int64_t at[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          at[q] = min(r + JOIN_WAVES * q, runs - 1);
+          g[q] = factor(at[q]);
+          t[q] = 0.f;
+        }
+        for (int64_t i = 0; i < each; ++i)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) t[q] += p[(at[q] * each + i) * D];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += r + JOIN_WAVES * q < runs ? t[q] * g[q] : 0.f;
+      }
+    } else if (col < D) {
       for (int64_t r = 0; r < runs; ++r, p += each * D) {
         float t = 0.f;
         int64_t i = wave;
