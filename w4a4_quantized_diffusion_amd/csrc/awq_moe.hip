@@ -277,6 +277,9 @@ __device__ __forceinline__ void lds_barrier() {
 // flight.  (One token runs through the code once: a loop that also unrolled the ends of
 // the items took 12 us instead of 9 for it, most of that waiting for instructions.)
 //
+// One token of 4 experts with N 1024 is 128 items: a workgroup each on half of the compute
+// units.
+//
 // Measured: 61 tokens, 6 of 40 experts, 4096 x 1408: 260 MB of codes and scales in 67-72
 // us, 3.6-3.9 TB/s.  The vector units are busy 57% of the cycles, with 2.4-3 instructions
 // a code for the dequantization and the routing of operands; a copy of the kernel that only
@@ -457,8 +460,8 @@ __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
 // flight.  With S > 1 a third launch adds the slices' sums (the workgroup of a column
 // block that ends last could, but its fences write the L2 back and took 9 us).
 //
-// Measured: 61 tokens as above 130 MB in 42-44 us, 3.0 TB/s, and 4-5 for the sums; one token
-// 5.8 us.  A copy that only loads takes 30 us; the rest is the dequantization, an expert's
+// Measured: 61 tokens as above 130 MB in 42-45 us, 3.0 TB/s, and 4-5 for the sums; one token
+// 5.7-6.8 us, in 128 workgroups for K 2048.  A copy that only loads takes 30 us; the rest is the dequantization, an expert's
 // sums in LDS and the fewer bytes in flight at their turn.
 
 constexpr int DOWN_WAVES = 16;
@@ -466,7 +469,8 @@ constexpr int MAX_SLICES = 8;
 
 template <int MT, int CT>
 __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe a) {
-  constexpr int D = MT * CT == 1 ? 4 : 2;   // (with 32 columns 2, 3, 4 and 6 take 44-48 us)
+  // (with 32 columns 3, 4 and 6 take up to 4 us more for the 61 tokens)
+  constexpr int D = MT * CT == 1 ? 4 : 2;
   constexpr int W = 16 * CT;
   __shared__ Route r;
   extern __shared__ __align__(16) float sums[];     // [wave][T][W]

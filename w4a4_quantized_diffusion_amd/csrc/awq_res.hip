@@ -191,9 +191,12 @@ __device__ __forceinline__ void operands(const Codes& c, bool live, v8bf (&b)[2]
 }
 
 // A workgroup's 8 waves take 16 columns each and one of S slices of K, whose part of X they
-// share in LDS; a wave's weights are four chunks ahead in registers.  Memory bound where the
-// columns are many: 64 rows 4096 -> 12288 23.5 us with the second launch, 28 MB of weights
-// and 16 MB of partial sums, written and read.
+// share in LDS; a wave's weights are four chunks ahead in registers.  64 rows 4096 -> 12288
+// take 23 us with the second launch: 28 MB of weights, and 16 MB of partial sums written
+// and read, 2.7 TB/s, half of a copy's rate; 16 rows 14.5.  Not memory: a piece of X is
+// loaded, written to LDS, waited for and multiplied before the next one begins.  LDS_X holds
+// 8 chunks of up to 63 rows and 4 of 64, which then take twice the pieces: 63 and 64 rows
+// 4096 -> 12288 22.5-23.1 and 22.6-23.0 us, 4096 -> 4096 14.7 and 15.4.
 template <int MT>
 __global__ __launch_bounds__(NT, 4) void res_slice_kernel(const uint16_t* __restrict__ X, int M,
                                                           int K, int N, svdq::AwqWeight w, int S,

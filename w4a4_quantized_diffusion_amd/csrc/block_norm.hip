@@ -17,10 +17,20 @@
 // second sum over registers, where sum v^2 - mean^2 would lose the digits of a large
 // mean).  x' enters the norm as the fp32 sum, before it is rounded to X's type.
 //
-// Measured: 9216 rows of 4096, layer norm, gate, scale and shift, bf16: 302 MB in 55.6 us,
-// 5.4 TB/s (a large copy: 5.3).  333 rows of 5455, an fp32 stream, with a post norm 10.4 us,
-// 2.4 TB/s: 1.3 rounds of workgroups, each a chain of loads, four sums over the
-// workgroup and stores that few others hide.  One row 2.6 us, a launch.
+// Measured: 9216 rows of 4096, layer norm, gate, scale and shift, bf16: 302 MB in 56-61 us,
+// 5.0-5.4 TB/s (a large copy: 5.3); with a post norm 73: two sums more in a row's chain.
+// 333 rows of 5455, an fp32 stream, RMS norms before and after, 9.7-10.4 us, 2.4-2.6 TB/s:
+// all rows are resident at once, one or two workgroups of 11 waves to a compute unit, and
+// nothing follows that would hide a row's chain of loads, two sums over the workgroup and
+// stores (one row takes 4.4, 128 rows 5.6, 256 7.6, 512 11.0).  One row of 4096 2.5-3 us, a
+// launch.  Rows of a few hundred values leave most lanes idle: 9216 rows of 64 take 10.5 us
+// as 9216 of 512 do.
+//
+// The 64-bit sum of the mean adds about 0.1 us to each sum of a row's chain: 9216 rows of
+// 4096 60.5 -> 61.3 us, with a post norm 68.6 -> 73.2, 4608 rows of 8192 with one 101 ->
+// 111, and within 2% in the backward pass from 2048 columns and 9216 rows on.  The adds in
+// a thread cost nothing of that (in fp32, or in pairs: the same times); the row operations
+// and the turn through LDS do.
 
 #include "block.h"
 
@@ -405,14 +415,14 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(svdq::BlockNorm a, int
 // gate B, dshift = S.  The next row's loads are in flight while one is worked on.  The
 // workgroups' sums are joined, and multiplied, by a second launch in a fixed order.
 //
-// Measured: 9216 rows of 4096, post norm and all five gradients, bf16: 453 MB in 102 us,
+// Measured: 9216 rows of 4096, post norm and all five gradients, bf16: 453 MB in 102-104 us,
 // 4.4 TB/s, and 8 us for the join.  Between memory and the chain of a row: two or four
 // sums over the workgroup follow one another in each row, and the registers of a row,
 // the next row and the column sums leave two workgroups a compute unit to hide
 // them.  (Five column sums
 // spilled: 436 us with them; 175 with three; 111 with the sums over the workgroup in row
 // operations of the lanes and the switched-off parts compiled out.)  20 rows of 2048 take
-// 4.5 us and the join 3.6.
+// 4.5 us and the join 3.8.
 
 enum { POST, GATE, WEIGHT, SCALE, SHIFT, VECTORS };
 
@@ -429,8 +439,14 @@ __device__ __forceinline__ void vector(const Vec& v, const Cut<V, C, TAIL>& cut,
 }
 
 // LONG: rows of more than 8192, in 1024 threads, where 128 registers a thread do not hold
-// the two factors too: they lie in LDS (2304 rows of 12288, everything in use: 232 us; with
-// all in registers, spilled, 426, and in 512 threads of four pieces 714).
+// the two factors too: they lie in LDS (with them in registers 2304 rows of 12288 took 1.8
+// times as long, in 512 threads of four pieces 3 times).  The rest does not fit either: of
+// x', t, dY, dX' and three sums of 16 columns each the compiler spills 86 to 218 registers,
+// 250 to 450 bytes of scratch a lane, fewest for whole rows in bf16.  That traffic is what
+// these rows take: everything in use, bf16, 2304 rows of 12288 262-290 us and the join 12 (340
+// MB, 64 us at a copy's rate), of 16384 305 and 14, 4096 of 9216 380 and 10; in fp32, or with
+// an odd end, 12288 columns 375-390.  The forms for 4097 to 8192 columns with an odd end and
+// some one-piece forms of fp32 or unknown types spill up to 9 (fewer than 8 columns: 25).
 
 template <int V, int C, int TAIL, int T, bool LAYER, bool POST_NORM, bool LONG>
 __global__ __launch_bounds__(LONG ? 1024 : 512, C == 1 || LONG ? 4 : 2) void block_norm_grad_kernel(
@@ -718,7 +734,11 @@ Shape shape(int64_t D, int most) {
 }
 
 // The types that a model's stream meets are known to the kernel: all bf16, an fp32
-// stream with bf16 or fp32 blocks.  Others, and rows too short or long to matter, take ANY.
+// stream with bf16 or fp32 blocks.  Others take ANY, and so do rows of two pieces a thread,
+// forward from 8193 columns on and backward from 4097, but for whole bf16 rows of more than
+// 8192 backward: forms of their own for these are not built, nor measured against ANY.
+// With it, everything in use, bf16: backward 7372 rows of 5120 134 us and the join 14, 4608
+// of 8192 109 and 12 (86 at a copy's rate); forward 2304 of 12288 76 (43).
 template <int TAIL>
 auto norm_of(int C, int types) {
   if (C > 1) return block_norm_kernel<V, 2, TAIL, ANY>;
@@ -762,7 +782,9 @@ int types_of(const svdq::BlockNorm& a, bool y16) {
 // (two pieces a thread of 512 threads, beyond that two of up to 1024)
 Shape grad_shape(int64_t D) { return shape(D, D > 2 * GRAD_THREADS * V ? 1024 : GRAD_THREADS); }
 
-// Workgroups an image: 16 waves to a compute unit in all
+// Workgroups an image: 16 waves to a compute unit in all, and at most 1024 workgroups, which
+// leaves rows of up to 1024 columns 8 waves and up to 512 columns 4 (9216 rows of 64 take 20
+// us and the join 8, of 512 26 in all)
 int64_t grad_parts(int64_t M, int64_t D, int64_t images) {
   const int64_t rows = M / images, groups = 256 * (1024 / grad_shape(D).NT);
   return std::max<int64_t>(1, std::min(rows, std::min<int64_t>(groups, 1024) / images));

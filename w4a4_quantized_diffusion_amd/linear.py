@@ -336,6 +336,9 @@ class _AWQResFn(torch.autograd.Function):
         dx = dgate = None
         if need_x or need_gate:
             d = _rows(dy, lay["N"])
+            # (dY is dZ then, and needs no copy.  Against the other call, which copies it,
+            # us: 500 rows of K 8192, N 1024 34.5 / 19.5, of K 1024, N 8192 23.8 / 28.4, 900 of
+            # 4096 both 58 / 54, 4608 of K 4096, N 12288 420 / 432)
             if ctx.act == "none" and gate is None and d.dtype == torch.bfloat16:
                 dx = svdq.awq_linear_w4a16_grad(d, lay)
             else:
