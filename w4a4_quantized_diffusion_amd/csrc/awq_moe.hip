@@ -461,8 +461,9 @@ __global__ __launch_bounds__(64 * UP_WAVES, 4) void moe_up_kernel(Moe a) {
 // block that ends last could, but its fences write the L2 back and took 9 us).
 //
 // Measured: 61 tokens as above 130 MB in 42-45 us, 3.0 TB/s, and 4-5 for the sums; one token
-// 5.7-6.8 us, in 128 workgroups for K 2048.  A copy that only loads takes 30 us; the rest is the dequantization, an expert's
-// sums in LDS and the fewer bytes in flight at their turn.
+// 5.7-6.8 us, in 128 workgroups for K 2048.  A copy that only loads takes 30 us for the 61;
+// the rest is the dequantization, an expert's sums in LDS and the fewer bytes in flight at
+// their turn.
 
 constexpr int DOWN_WAVES = 16;
 constexpr int MAX_SLICES = 8;
